@@ -417,8 +417,15 @@ def _beam(state, case):
     swap = copies[:, None] & (spot == (lens // page)[:, None])
     refs = refs - tally(last_page, copies) + tally(copied, copies) + tally(fresh.clamp(max=n - 1), new)
     table = torch.where(new, fresh, torch.where(swap, copied[:, None], table))
-    src, dst = last_page[copies].long(), copied[copies].long()
-    state["pool"][:, dst] = state["pool"][:, src]
+    src, dst, held = last_page[copies].long(), copied[copies].long(), (lens % page)[copies]
+    # only the rows that the sequence holds: their bytes in the record's four parts
+    _, _, d = HEADS[case["heads"]]
+    each, side = d * case["bits"] // 8, 4 * (d // case["group"])
+    at = torch.arange(state["pool"].shape[-1], device="cuda")
+    rest = at - 2 * page * each
+    slot = torch.where(rest < 0, at % (page * each) // each, rest % (page * side) // side)
+    pool = state["pool"]
+    pool[:, dst] = torch.where(slot < held[:, None, None], pool[:, src], pool[:, dst])
     grown = _status(0, 0, need.sum(), copies.sum())
     return {"refs": refs, "table": table, "lens": lens + state["add"], "status": [freed, forked, grown], "pool": state["pool"].view(torch.int64)}
 
@@ -430,7 +437,7 @@ def _compact(state, case):
     live = refs > 0
     count = live.sum()
     holes = (~live & (page < count)).nonzero()[:, 0]
-    movers = (live & (page >= count)).nonzero()[:, 0]
+    movers = (live & (page >= count)).nonzero()[:, 0].flip(0)  # the last live page fills the first hole
     to = page.clone()
     to[movers] = holes
     fresh = refs.clone()
@@ -459,9 +466,9 @@ def work(case):
     if case["kind"] == "beam":
         rows = case["requests"] * case["width"]
         each = case["page"] * row * case["layers"]
-        # the losers' rows and their winners' partial pages are shared: one copy for each loser
+        # the losers' rows and their winners' partial pages are shared: one copy for each loser, of half a page on average
         held = 0.75 * case["prompt"] / case["page"] + 0.5 * case["generated"] / case["page"] + 1
-        return {"bytes": case["requests"] * (case["width"] // 2) * 2 * each * (1 - 1 / case["page"]) + rows * 8 * held + 8 * rows, "flops": 0}
+        return {"bytes": case["requests"] * (case["width"] // 2) * each * (1 - 1 / case["page"]) + rows * 8 * held + 8 * rows, "flops": 0}
     each = case["page"] * row * case["layers"]
     moved = _live(case) * (case["n_pages"] - _live(case)) / case["n_pages"]
     return {"bytes": moved * 2 * each + 8 * case["n_pages"] + 8 * _live(case) * 1.25, "flops": 0}
