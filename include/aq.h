@@ -305,6 +305,198 @@ aq_status aq_attention_decode_static(int dtype, const void *q_dev, const uint32_
 int aq_attention_describe_ws(int64_t H, int64_t KV, int64_t N, int64_t D, int bits,
                              int group_size, size_t workspace_bytes, char *buf, int buflen);
 
+/*
+ * A paged KV cache in the affine format: a pool of pages
+ * [layers][n_pages][KV][record].  The record of one page and one KV head
+ * holds `page` cached rows of K and of V, in this order:
+ *   K codes [page][D*bits/32] uint32 (each row packed as aq_pack packs one),
+ *   V codes, the same,
+ *   K (scale, bias) fp16 pairs [page][D/group_size],
+ *   V (scale, bias) fp16 pairs, the same,
+ * aq_cache_record_bytes bytes together.  A sequence is a row of a page table
+ * (int32 [B][max_pages], page numbers; token j of row b is slot j % page of
+ * page table[b][j / page]) and a length (int32 [B]); one table serves every
+ * layer.  refs (int32 [n_pages]) counts the table rows that hold a page, 0
+ * for a free one.  The caller owns all of them; the pages need no initial
+ * value, refs starts as zeros, lens as zeros.  The pages, tables and counts
+ * are this library's own (the pages it follows keep a contiguous cache).
+ *   pool_dev    device, 16-byte aligned, layers * n_pages * KV * record bytes.
+ *   page        16, 32, 64 or 128 rows.     bits  4 or 8.
+ *   group_size  32, 64 or 128, D % group_size == 0.
+ *   D           64, 128, 256 or 512.
+ * The struct itself is host memory, read during the call.
+ */
+typedef struct aq_cache {
+    void *pool_dev;
+    int64_t layers, n_pages;
+    int64_t KV, D;
+    int page, bits, group_size;
+} aq_cache;
+
+/* Largest number of table rows an operation on a page table takes. */
+#define AQ_CACHE_MAX_ROWS 4096
+
+/* Bytes of one page's record of one KV head; 0 for sizes outside the above. */
+size_t aq_cache_record_bytes(int64_t D, int page, int bits, int group_size);
+
+/*
+ * aq_cache_append — quantise the K and V rows of T new tokens into their
+ * pages of one layer, by the rule of aq_quantize_ex per group.
+ *   dtype       AQ_F16 or AQ_BF16: the type of k and v.
+ *   k_dev       [T][KV][D], a token's heads dense, tokens k_stride elements
+ *               apart (a slice of a fused projection's output will do);
+ *               16-byte aligned, k_stride a multiple of 8.  v_dev, v_stride
+ *               the same.
+ *   cu_dev      int32 [B + 1], ascending: tokens cu[b] .. cu[b + 1] - 1 belong
+ *               to row b.  Tokens outside every row are skipped.
+ *   start_dev   int32 [B]: the position of row b's first new token.
+ *   table_dev   int32 [B][max_pages].
+ * A page that other rows hold too is written all the same: aq_cache_grow
+ * gives a row pages of its own first.  A position outside the table or a
+ * page outside the pool is skipped and sets the error word
+ * (aq_device_error).  Values must be finite and within fp16 range.
+ * Errors: AQ_ERR_INVALID_ARG for a bad cache, layer, dtype, size or NULL
+ * pointer; AQ_ERR_MISALIGNED; AQ_ERR_CUDA.  T == 0 queues nothing.
+ */
+aq_status aq_cache_append(const aq_cache *cache, int64_t layer, int dtype, const void *k_dev,
+                          int64_t k_stride, const void *v_dev, int64_t v_stride, int64_t T,
+                          const int32_t *cu_dev, const int32_t *start_dev,
+                          const int32_t *table_dev, int64_t B, int64_t max_pages, void *stream);
+
+/*
+ * aq_cache_read — the reverse: the cached rows of the same T tokens as dense
+ * k_out, v_out [T][KV][D] of `dtype` (scale * code + bias, rounded once), for
+ * attention over rows as floats or for moving a sequence elsewhere.  Rows of
+ * tokens outside every sequence, or without a page, are zeros.  k_out and
+ * v_out 16-byte aligned; errors as aq_cache_append.
+ */
+aq_status aq_cache_read(const aq_cache *cache, int64_t layer, int dtype, void *k_out_dev,
+                        void *v_out_dev, int64_t T, const int32_t *cu_dev,
+                        const int32_t *start_dev, const int32_t *table_dev, int64_t B,
+                        int64_t max_pages, void *stream);
+
+/*
+ * aq_cache_copy — page src[i] onto page dst[i], in every layer, for i < n.
+ * src_dev, dst_dev int32 [n], device.  A page must not be the target of two
+ * copies, nor the source of one and the target of another.  A page outside
+ * the pool is skipped and sets the error word.
+ */
+aq_status aq_cache_copy(const aq_cache *cache, const int32_t *src_dev, const int32_t *dst_dev,
+                        int64_t n, void *stream);
+
+/*
+ * The operations on page tables.  Each reads refs, table and lens and writes
+ * refs_out, table_out and lens_out, which are the same arrays (in place) or
+ * others (then every element is written), never parts of each other.  One
+ * launch each, no host synchronisation: a graph may capture them.  The result
+ * is reported in status_dev, int32 [4]:
+ *   [0] 0 done; 1 too few free pages; 2 bad rows; 3 done, but some table
+ *       entry named a page outside the pool (such entries change no count);
+ *       after 1 and 2 nothing has changed (refs_out, table_out and lens_out
+ *       hold what the inputs hold)
+ *   [1] the number of missing pages, or of bad rows
+ *   [2], [3] as each operation says.
+ * Free pages are those with refs <= 0; the lowest are taken first, in row
+ * order, so the outcome is the same on every run.
+ *
+ * aq_cache_fork — row b with parent[b] >= 0 becomes a copy of row parent[b]'s
+ * first keep[b] tokens (all of them for keep[b] < 0): the same pages, counted
+ * once more.  No page is copied.  Bad rows: a child that is not empty, a
+ * parent outside the batch or itself a child, keep[b] past the parent's
+ * length.  status[2]: entries copied.
+ *
+ * aq_cache_trim — row b with 0 <= keep[b] < lens[b] is cut to keep[b] tokens
+ * (0 frees it) and gives back the pages past them; other rows stay.  The
+ * entries become -1.  status[2]: pages that became free.
+ *
+ * aq_cache_grow — every row gets pages for add[b] >= 0 more tokens and its
+ * new length.  Where a growing row's last page is partly filled and shared,
+ * the row gets a page of its own and the rows it holds are copied there in
+ * every layer (copy on write); when all the page's holders grow in one call
+ * the last of them in row order keeps it.  Bad rows: a negative add, a length
+ * past the table's width.  status[2]: pages taken, status[3]: pages copied.
+ *
+ * aq_cache_compact — moves the live pages to the front of the pool: with n
+ * live pages, those at n and above move to the free pages below n (the last
+ * live page to the first free one, and so on), in every layer; counts and
+ * table entries follow.  lens is only read.  status[2]: n, status[3]: pages
+ * moved.  After it the pool's pages past n are free, e.g. to be unmapped.
+ *
+ * workspace_dev (grow, compact): device, 4-byte aligned, of at least
+ * aq_cache_workspace_bytes(n_pages, B) bytes, needing no initial value;
+ * calls that may overlap use distinct ones.
+ * Errors: AQ_ERR_INVALID_ARG for a bad cache (the pool itself is only needed
+ * by grow and compact), B outside 1..AQ_CACHE_MAX_ROWS, max_pages < 1, NULL
+ * pointers or a workspace that is too small; AQ_ERR_MISALIGNED; AQ_ERR_CUDA.
+ */
+size_t aq_cache_workspace_bytes(int64_t n_pages, int64_t B);
+
+aq_status aq_cache_fork(const aq_cache *cache, const int32_t *refs_dev, const int32_t *table_dev,
+                        const int32_t *lens_dev, const int32_t *parent_dev,
+                        const int32_t *keep_dev, int64_t B, int64_t max_pages, int32_t *refs_out,
+                        int32_t *table_out, int32_t *lens_out, int32_t *status_dev, void *stream);
+aq_status aq_cache_trim(const aq_cache *cache, const int32_t *refs_dev, const int32_t *table_dev,
+                        const int32_t *lens_dev, const int32_t *keep_dev, int64_t B,
+                        int64_t max_pages, int32_t *refs_out, int32_t *table_out,
+                        int32_t *lens_out, int32_t *status_dev, void *stream);
+aq_status aq_cache_grow(const aq_cache *cache, const int32_t *refs_dev, const int32_t *table_dev,
+                        const int32_t *lens_dev, const int32_t *add_dev, int64_t B,
+                        int64_t max_pages, int32_t *refs_out, int32_t *table_out,
+                        int32_t *lens_out, int32_t *status_dev, void *workspace_dev,
+                        size_t workspace_bytes, void *stream);
+aq_status aq_cache_compact(const aq_cache *cache, const int32_t *refs_dev,
+                           const int32_t *table_dev, const int32_t *lens_dev, int64_t B,
+                           int64_t max_pages, int32_t *refs_out, int32_t *table_out,
+                           int32_t *status_dev, void *workspace_dev, size_t workspace_bytes,
+                           void *stream);
+
+/*
+ * aq_attention_batch — attention of L new tokens of each of B sequences over
+ * one layer of the paged cache (their own K and V appended already):
+ *   o[b][l][h] = softmax_j(scale * q[b][l][h] . K[b][j][kv]) . V[b][j][kv],
+ * kv = h / (H / KV), over the tokens j < lens[b] - (L - 1 - l), so that lens
+ * counts the new tokens and token l sees those before it and itself.  A row
+ * that sees nothing (lens[b] == 0: an empty slot of the batch) is zeros.
+ * Sequences that share their first tokens are read once: group g is the
+ * sequences group_start[g] .. group_start[g + 1] - 1, and they all begin with
+ * the same shared[g] tokens.  Those are read through the table row of the
+ * group's first sequence that long, for all the group's rows at once; what
+ * follows is read per sequence.  (A member that has fewer than
+ * shared[g] + L - 1 tokens is read on its own.)
+ *   dtype        AQ_F16 or AQ_BF16: the type of q and o.
+ *   q_dev        [B][L][H][D], a token's heads dense, tokens q_stride elements
+ *                apart (a multiple of 8); 16-byte aligned.
+ *   table_dev    int32 [B][max_pages].   lens_dev  int32 [B].
+ *   group_start_dev int32 [G + 1], ascending within 0..B; shared_dev int32
+ *                [G].  G == 0: both NULL.
+ *   out_dev      [B][L][H][D] dense.
+ *   workspace_dev   device, 256-byte aligned, at least
+ *                aq_attention_batch_workspace_bytes(...) long, needing no
+ *                initial value; calls that may overlap use distinct ones.
+ * lens, tables and groups are read on the device only, so a captured graph
+ * follows their changes.  Served: D in {64, 128, 256, 512}, any H a multiple
+ * of KV, 1 <= L <= 64, B <= 1024, G <= 256.  Scores, maxima and sums are fp32;
+ * probabilities (times the value scales, or with values dequantised) enter the value product
+ * as fp16; o is rounded once.  Deterministic.  A page outside the pool, among
+ * the tokens that count, sets the error word, and the rows that see it are
+ * unspecified.
+ * Errors: AQ_ERR_INVALID_ARG for a bad cache, layer, dtype, size, a scale
+ * that is not finite, NULL pointers or a workspace that is too small;
+ * AQ_ERR_MISALIGNED; AQ_ERR_UNSUPPORTED for sizes outside the served set;
+ * AQ_ERR_CUDA.
+ */
+#define AQ_BATCH_MAX_ROWS 1024
+#define AQ_BATCH_MAX_TOKENS 64
+#define AQ_BATCH_MAX_GROUPS 256
+size_t aq_attention_batch_workspace_bytes(const aq_cache *cache, int64_t B, int64_t L, int64_t H,
+                                          int64_t G);
+aq_status aq_attention_batch(const aq_cache *cache, int64_t layer, int dtype, const void *q_dev,
+                             int64_t q_stride, const int32_t *table_dev, const int32_t *lens_dev,
+                             const int32_t *group_start_dev, const int32_t *shared_dev, int64_t B,
+                             int64_t L, int64_t H, int64_t G, int64_t max_pages, float scale,
+                             void *out_dev, void *workspace_dev, size_t workspace_bytes,
+                             void *stream);
+
 /* Largest number of projections aq_matmul_multi takes in one call. */
 #define AQ_MAX_PROJ 4
 

@@ -26,7 +26,10 @@ __all__ = [
     "aq_quantize_bf16", "aq_matmul", "aq_matmul_bf16", "aq_matmul_multi", "aq_matmul_gate_up",
     "aq_matmul_ex", "aq_quantize_ex", "aq_attention_decode", "aq_attention_describe",
     "aq_attention_workspace_bytes", "aq_attention_decode_ws", "aq_attention_describe_ws",
-    "aq_attention_decode_static",
+    "aq_attention_decode_static", "AqCache", "aq_cache_record_bytes", "aq_cache_append",
+    "aq_cache_read", "aq_cache_copy", "aq_cache_fork", "aq_cache_trim", "aq_cache_grow",
+    "aq_cache_compact", "aq_cache_workspace_bytes", "aq_attention_batch",
+    "aq_attention_batch_workspace_bytes",
     "aq_matmul_variant", "aq_matmul_host", "aq_select", "aq_describe", "aq_stats", "aq_stats_reset",
     "aq_device_error",
     "aq_free", "aq_status_string", "aq_variant_name", "aq_version", "lib_path", "load",
@@ -64,7 +67,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         raise ImportError(f"libaq.so not built at {path}")
     lib = ctypes.CDLL(path)
     p, i64, i32, u32p = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
-    sz = ctypes.c_size_t
+    sz, f32 = ctypes.c_size_t, ctypes.c_float
     sig = {
         "aq_pack": ([p, i64, i64, i32, p, p], i32),
         "aq_quantize": ([p, i64, i64, i32, p, p, p, p], i32),
@@ -88,6 +91,18 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "aq_attention_describe_ws": ([i64, i64, i64, i64, i32, i32, sz, p, i32], i32),
         "aq_attention_decode_static": ([i32, p, p, p, p, p, p, p, i64, i64, i64, i64, i32, i32, p,
                                         p], i32),
+        "aq_cache_record_bytes": ([i64, i32, i32, i32], sz),
+        "aq_cache_append": ([p, i64, i32, p, i64, p, i64, i64, p, p, p, i64, i64, p], i32),
+        "aq_cache_read": ([p, i64, i32, p, p, i64, p, p, p, i64, i64, p], i32),
+        "aq_cache_copy": ([p, p, p, i64, p], i32),
+        "aq_cache_workspace_bytes": ([i64, i64], sz),
+        "aq_cache_fork": ([p, p, p, p, p, p, i64, i64, p, p, p, p, p], i32),
+        "aq_cache_trim": ([p, p, p, p, p, i64, i64, p, p, p, p, p], i32),
+        "aq_cache_grow": ([p, p, p, p, p, i64, i64, p, p, p, p, p, sz, p], i32),
+        "aq_cache_compact": ([p, p, p, p, i64, i64, p, p, p, p, sz, p], i32),
+        "aq_attention_batch_workspace_bytes": ([p, i64, i64, i64, i64], sz),
+        "aq_attention_batch": ([p, i64, i32, p, i64, p, p, p, p, i64, i64, i64, i64, i64, f32, p,
+                                p, sz, p], i32),
         "aq_stats": ([p, i32], i32),
         "aq_stats_reset": ([], None),
         "aq_device_error": ([u32p, i32], i32),
@@ -106,10 +121,22 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: a Stream object costs microseconds a call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace for one call: handed back to torch's allocator on return,
+    so a call on another stream than the current one has to be known to it."""
+    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+        t.record_stream(stream)
+    return t
 
 
 def _check(status: int, what: str) -> None:
@@ -340,6 +367,248 @@ def aq_quantize_ex(w: torch.Tensor, bits: int, group_size: int, stream=None) -> 
                                  _dev(scales, "scales"), _dev(biases, "biases"), _stream(stream)),
            "aq_quantize_ex")
     return Wq, scales, biases
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("pool_dev", ctypes.c_void_p), ("layers", ctypes.c_int64),
+                ("n_pages", ctypes.c_int64), ("KV", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("page", ctypes.c_int), ("bits", ctypes.c_int), ("group_size", ctypes.c_int)]
+
+
+class AqCache:
+    """A paged KV cache (struct aq_cache): pool is a uint8 device tensor
+    [layers, n_pages, KV, record], record = aq_cache_record_bytes(head_dim,
+    page, bits, group_size).  The tensor stays the caller's; this object only
+    names its geometry and may be made anew for every call."""
+
+    __slots__ = ("pool", "page", "head_dim", "bits", "group_size", "layers", "n_pages", "kv_heads",
+                 "_struct", "_ref")
+
+    def __init__(self, pool: torch.Tensor, page: int, head_dim: int, bits: int, group_size: int):
+        if pool.dtype != torch.uint8 or pool.dim() != 4:
+            raise ValueError("pool must be uint8 [layers, n_pages, KV, record]")
+        layers, n_pages, kv, rec = pool.shape
+        want = aq_cache_record_bytes(head_dim, page, bits, group_size)
+        if want == 0:
+            raise ValueError("head_dim 64/128/256/512, page 16/32/64/128, bits 4/8 and group_size "
+                             "32/64/128 are served")
+        if rec != want:
+            raise ValueError(f"pool's records hold {rec} bytes; this geometry uses {want}")
+        self.pool, self.page, self.head_dim = pool, page, head_dim
+        self.bits, self.group_size = bits, group_size
+        self.layers, self.n_pages, self.kv_heads = layers, n_pages, kv
+        self._struct = _CacheStruct(_dev(pool, "pool"), layers, n_pages, kv, head_dim, page, bits,
+                                    group_size)
+        self._ref = ctypes.addressof(self._struct)
+
+    @staticmethod
+    def empty(layers: int, n_pages: int, kv_heads: int, head_dim: int, page: int, bits: int,
+              group_size: int, device="cuda") -> "AqCache":
+        """A cache over a pool allocated here (its pages need no initial value)."""
+        rec = aq_cache_record_bytes(head_dim, page, bits, group_size)
+        pool = torch.empty((layers, n_pages, kv_heads, rec), dtype=torch.uint8, device=device)
+        return AqCache(pool, page, head_dim, bits, group_size)
+
+
+def aq_cache_record_bytes(D: int, page: int, bits: int, group_size: int) -> int:
+    """Bytes of one page's record of one KV head (0: sizes not served)."""
+    return int(load().aq_cache_record_bytes(D, page, bits, group_size))
+
+
+def aq_cache_workspace_bytes(n_pages: int, B: int) -> int:
+    """Workspace bytes of aq_cache_grow and aq_cache_compact."""
+    return int(load().aq_cache_workspace_bytes(n_pages, B))
+
+
+def _ints(t: torch.Tensor, name: str, *shape) -> int:
+    """The address of a dense int32 device tensor of this shape."""
+    if t.dtype != torch.int32 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+    return _dev(t, name)
+
+
+def _table_shape(table: torch.Tensor) -> tuple:
+    if table.dim() != 2:
+        raise ValueError("table must be [B, max_pages]")
+    return tuple(table.shape)
+
+
+def _token_rows(t: torch.Tensor, name: str, heads: int, D: int) -> tuple:
+    """(address, elements between tokens) of [T, heads, D] with dense heads."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{name} must be [T, {heads}, {D}], got {list(t.shape)}")
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+        raise ValueError(f"{name}: a token's heads must be dense")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * D
+
+
+def aq_cache_append(cache: AqCache, layer: int, k, v, cu, start, table, stream=None) -> None:
+    """Quantise the rows k, v [T, KV, D] (fp16 or bf16; a slice of a fused
+    projection's output will do) into their pages: tokens cu[b] .. cu[b+1]-1
+    go to row b from position start[b] on.  cu int32 [B + 1], start int32 [B],
+    table int32 [B, max_pages]."""
+    if k.dtype not in _ACT or v.dtype != k.dtype:
+        raise ValueError("k and v must both be float16 or both bfloat16")
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    B, width = _table_shape(table)
+    kp, ks = _token_rows(k, "k", cache.kv_heads, cache.head_dim)
+    vp, vs = _token_rows(v, "v", cache.kv_heads, cache.head_dim)
+    _check(load().aq_cache_append(cache._ref, layer, AQ_BF16 if k.dtype == torch.bfloat16 else AQ_F16,
+                                  kp, ks, vp, vs, k.shape[0], _ints(cu, "cu", B + 1),
+                                  _ints(start, "start", B), _ints(table, "table", B, width), B,
+                                  width, _stream(stream)), "aq_cache_append")
+
+
+def aq_cache_read(cache: AqCache, layer: int, cu, start, table, total: int, dtype, out=None,
+                  stream=None) -> tuple:
+    """The cached rows of the same tokens as floats: (k, v), each
+    [total, KV, D] of dtype (zeros for tokens outside every sequence)."""
+    if dtype not in _ACT:
+        raise ValueError("dtype must be float16 or bfloat16")
+    B, width = _table_shape(table)
+    shape = (total, cache.kv_heads, cache.head_dim)
+    if out is None:
+        both = torch.empty((2, *shape), dtype=dtype, device=cache.pool.device)
+        out = (both[0], both[1])
+    for name, t in zip(("k", "v"), out):
+        if t.dtype != dtype or tuple(t.shape) != shape:
+            raise ValueError(f"out {name} must be {dtype} {list(shape)}")
+    _check(load().aq_cache_read(cache._ref, layer, AQ_BF16 if dtype == torch.bfloat16 else AQ_F16,
+                                _dev(out[0], "out k"), _dev(out[1], "out v"), total,
+                                _ints(cu, "cu", B + 1), _ints(start, "start", B),
+                                _ints(table, "table", B, width), B, width, _stream(stream)),
+           "aq_cache_read")
+    return tuple(out)
+
+
+def aq_cache_copy(cache: AqCache, src, dst, stream=None) -> None:
+    """Page src[i] onto page dst[i] in every layer; src, dst int32 [n]."""
+    n = src.numel()
+    _check(load().aq_cache_copy(cache._ref, _ints(src, "src", n), _ints(dst, "dst", n), n,
+                                _stream(stream)), "aq_cache_copy")
+
+
+def _tables(cache, refs, table, lens, in_place, out, with_lens=True):
+    """Addresses of the inputs and outputs of a page-table operation, the
+    outputs and a new status tensor."""
+    B, width = _table_shape(table)
+    ins = (_ints(refs, "refs", cache.n_pages), _ints(table, "table", B, width),
+           _ints(lens, "lens", B))
+    given = (refs, table, lens) if with_lens else (refs, table)
+    if out is None:
+        out = given if in_place else tuple(torch.empty_like(t) for t in given)
+    ptrs = tuple(_ints(o, f"out[{i}]", *t.shape) for i, (o, t) in enumerate(zip(out, given)))
+    status = torch.empty(4, dtype=torch.int32, device=refs.device)
+    return B, width, ins, ptrs, tuple(out), status
+
+
+def _cache_workspace(cache, B, workspace, stream):
+    if workspace is None:
+        workspace = _scratch(aq_cache_workspace_bytes(cache.n_pages, B), cache.pool.device, stream)
+    if workspace.dtype != torch.uint8:
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    return _dev(workspace, "workspace"), workspace.numel(), workspace
+
+
+def aq_cache_fork(cache, refs, table, lens, parent, keep, in_place=True, out=None,
+                  stream=None) -> tuple:
+    """Row b with parent[b] >= 0 becomes a copy of that row's first keep[b]
+    tokens (keep[b] < 0: all).  refs int32 [n_pages], table int32
+    [B, max_pages], lens, parent, keep int32 [B].  Returns (refs, table, lens,
+    status): the same tensors, or new ones with in_place=False (or out)."""
+    B, width, ins, outs, res, status = _tables(cache, refs, table, lens, in_place, out)
+    _check(load().aq_cache_fork(cache._ref, *ins, _ints(parent, "parent", B),
+                                _ints(keep, "keep", B), B, width, *outs, status.data_ptr(),
+                                _stream(stream)), "aq_cache_fork")
+    return (*res, status)
+
+
+def aq_cache_trim(cache, refs, table, lens, keep, in_place=True, out=None, stream=None) -> tuple:
+    """Row b with 0 <= keep[b] < lens[b] is cut to keep[b] tokens (0 frees
+    it).  Arguments and results as aq_cache_fork."""
+    B, width, ins, outs, res, status = _tables(cache, refs, table, lens, in_place, out)
+    _check(load().aq_cache_trim(cache._ref, *ins, _ints(keep, "keep", B), B, width, *outs,
+                                status.data_ptr(), _stream(stream)), "aq_cache_trim")
+    return (*res, status)
+
+
+def aq_cache_grow(cache, refs, table, lens, add, in_place=True, out=None, workspace=None,
+                  stream=None) -> tuple:
+    """Pages for add[b] more tokens of every row, with copy on write of shared
+    partial pages.  Arguments and results as aq_cache_fork."""
+    B, width, ins, outs, res, status = _tables(cache, refs, table, lens, in_place, out)
+    ws, n, keep_alive = _cache_workspace(cache, B, workspace, stream)
+    _check(load().aq_cache_grow(cache._ref, *ins, _ints(add, "add", B), B, width, *outs,
+                                status.data_ptr(), ws, n, _stream(stream)), "aq_cache_grow")
+    return (*res, status)
+
+
+def aq_cache_compact(cache, refs, table, lens, in_place=True, out=None, workspace=None,
+                     stream=None) -> tuple:
+    """Moves the live pages to the front of the pool.  Returns (refs, table,
+    status); lens is only read."""
+    B, width, ins, outs, res, status = _tables(cache, refs, table, lens, in_place, out, False)
+    ws, n, keep_alive = _cache_workspace(cache, B, workspace, stream)
+    _check(load().aq_cache_compact(cache._ref, *ins, B, width, *outs, status.data_ptr(), ws, n,
+                                   _stream(stream)), "aq_cache_compact")
+    return (*res, status)
+
+
+def aq_attention_batch_workspace_bytes(cache: AqCache, B: int, L: int, H: int, G: int = 0) -> int:
+    """Workspace bytes of aq_attention_batch (0: sizes that it refuses)."""
+    return int(load().aq_attention_batch_workspace_bytes(cache._ref, B, L, H, G))
+
+
+def aq_attention_batch(q, cache: AqCache, layer: int, table, lens, scale: float, group_start=None,
+                       shared=None, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Attention of the last L tokens of each of B sequences over one layer of
+    the paged cache, the keys that a group of sequences shares read once.
+    q [B, L, H, D] (fp16 or bf16, a token's heads dense); table int32
+    [B, max_pages]; lens int32 [B] counts the L new tokens; group_start int32
+    [G + 1] and shared int32 [G] name the groups and how many first tokens
+    each shares.  Returns o [B, L, H, D] in q's dtype."""
+    if q.dtype not in _ACT:
+        raise ValueError("q must be float16 or bfloat16")
+    if q.dim() != 4 or q.shape[3] != cache.head_dim:
+        raise ValueError(f"q must be [B, L, H, {cache.head_dim}], got {list(q.shape)}")
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    B, L, H, D = q.shape
+    stride = H * D
+    if B * L > 1:
+        stride = q.stride(1) if L > 1 else q.stride(0)
+        if L > 1 and B > 1 and q.stride(0) != L * stride:
+            raise ValueError("q: tokens must lie a fixed step apart")
+    if q.numel() and (q.stride(3) != 1 or (H > 1 and q.stride(2) != D)):
+        raise ValueError("q: a token's heads must be dense")
+    rows, width = _table_shape(table)
+    if rows != B:
+        raise ValueError(f"table has {rows} rows for {B} sequences")
+    G = 0
+    gs = sh = None
+    if (group_start is None) != (shared is None):
+        raise ValueError("group_start and shared go together")
+    if shared is not None:
+        G = shared.numel()
+        gs, sh = _ints(group_start, "group_start", G + 1), _ints(shared, "shared", G)
+    if out is None:
+        out = torch.empty((B, L, H, D), dtype=q.dtype, device=q.device)
+    _check_out(out, "out", B * L * H * D, q.dtype)
+    lib = load()
+    if workspace is None:
+        n = lib.aq_attention_batch_workspace_bytes(cache._ref, B, L, H, G)
+        workspace = _scratch(max(n, 256), q.device, stream)
+    if workspace.dtype != torch.uint8:
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    _check(lib.aq_attention_batch(cache._ref, layer, AQ_BF16 if q.dtype == torch.bfloat16 else AQ_F16,
+                                  q.data_ptr(), stride, _ints(table, "table", B, width),
+                                  _ints(lens, "lens", B), gs, sh, B, L, H, G, width, scale,
+                                  _dev(out, "out"), _dev(workspace, "workspace"),
+                                  workspace.numel(), _stream(stream)), "aq_attention_batch")
+    return out
 
 
 def aq_matmul_multi(x, weights, bits, outs=None, stream=None) -> list:

@@ -8,7 +8,9 @@
 
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <mutex>
 #include <cstdlib>
@@ -403,6 +405,215 @@ aq_status aq_attention_decode_ws(int dtype, const void *q_dev, const uint32_t *k
     return AQ_OK;
 }
 
+// ---------------------------------------------------------------------------
+// The paged cache.
+// ---------------------------------------------------------------------------
+
+size_t aq_cache_record_bytes(int64_t D, int page, int bits, int group_size) {
+    if ((D != 64 && D != 128 && D != 256 && D != 512) ||
+        (page != 16 && page != 32 && page != 64 && page != 128) || (bits != 4 && bits != 8) ||
+        (group_size != 32 && group_size != 64 && group_size != 128) || D % group_size != 0)
+        return 0;
+    return (size_t)page * (size_t)(2 * D * bits / 8 + 8 * (D / group_size));
+}
+
+static aq_status check_cache(const aq_cache *c, bool pool) {
+    if (!c || c->layers < 1 || c->n_pages < 1 || c->n_pages > (1 << 30) || c->KV < 1 ||
+        c->KV > 4096 || aq_cache_record_bytes(c->D, c->page, c->bits, c->group_size) == 0)
+        return AQ_ERR_INVALID_ARG;
+    if (pool) {
+        if (!c->pool_dev) return AQ_ERR_INVALID_ARG;
+        if (!aligned(c->pool_dev, 16)) return AQ_ERR_MISALIGNED;
+    }
+    return AQ_OK;
+}
+
+static aq_status check_rows(const aq_cache *c, int64_t layer, int dtype, const void *k,
+                            const void *v, int64_t T, const void *cu, const void *start,
+                            const void *table, int64_t B, int64_t max_pages) {
+    const aq_status st = check_cache(c, true);
+    if (st != AQ_OK) return st;
+    if (layer < 0 || layer >= c->layers || (dtype != AQ_F16 && dtype != AQ_BF16) || T < 0 ||
+        T > INT32_MAX || B < 1 || B > INT32_MAX - 1 || max_pages < 1 ||
+        max_pages > (1 << 29) / c->page)
+        return AQ_ERR_INVALID_ARG;
+    if (T * (c->KV * c->D / 8) > (int64_t)INT32_MAX * 256) return AQ_ERR_INVALID_ARG;
+    if (T == 0) return AQ_OK;
+    if (!k || !v || !cu || !start || !table) return AQ_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu, 4) || !aligned(start, 4) ||
+        !aligned(table, 4))
+        return AQ_ERR_MISALIGNED;
+    return AQ_OK;
+}
+
+aq_status aq_cache_append(const aq_cache *cache, int64_t layer, int dtype, const void *k_dev,
+                          int64_t k_stride, const void *v_dev, int64_t v_stride, int64_t T,
+                          const int32_t *cu_dev, const int32_t *start_dev,
+                          const int32_t *table_dev, int64_t B, int64_t max_pages, void *stream) {
+    const aq_status st =
+        check_rows(cache, layer, dtype, k_dev, v_dev, T, cu_dev, start_dev, table_dev, B, max_pages);
+    if (st != AQ_OK) return st;
+    if (T == 0) return AQ_OK;
+    if (T > 1 && (k_stride < cache->KV * cache->D || v_stride < cache->KV * cache->D))
+        return AQ_ERR_INVALID_ARG;
+    if (k_stride % 8 != 0 || v_stride % 8 != 0) return AQ_ERR_MISALIGNED;
+    return cache_append_launch(cache, layer, dtype, k_dev, k_stride, v_dev, v_stride, nullptr,
+                               nullptr, T, cu_dev, start_dev, table_dev, B, max_pages,
+                               static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? AQ_OK
+               : AQ_ERR_CUDA;
+}
+
+aq_status aq_cache_read(const aq_cache *cache, int64_t layer, int dtype, void *k_out_dev,
+                        void *v_out_dev, int64_t T, const int32_t *cu_dev,
+                        const int32_t *start_dev, const int32_t *table_dev, int64_t B,
+                        int64_t max_pages, void *stream) {
+    const aq_status st = check_rows(cache, layer, dtype, k_out_dev, v_out_dev, T, cu_dev, start_dev,
+                                    table_dev, B, max_pages);
+    if (st != AQ_OK) return st;
+    if (T == 0) return AQ_OK;
+    return cache_append_launch(cache, layer, dtype, nullptr, 0, nullptr, 0, k_out_dev, v_out_dev, T,
+                               cu_dev, start_dev, table_dev, B, max_pages,
+                               static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? AQ_OK
+               : AQ_ERR_CUDA;
+}
+
+aq_status aq_cache_copy(const aq_cache *cache, const int32_t *src_dev, const int32_t *dst_dev,
+                        int64_t n, void *stream) {
+    const aq_status st = check_cache(cache, true);
+    if (st != AQ_OK) return st;
+    if (n < 0 || n > INT32_MAX || (n > 0 && (!src_dev || !dst_dev))) return AQ_ERR_INVALID_ARG;
+    if (n == 0) return AQ_OK;
+    if (!aligned(src_dev, 4) || !aligned(dst_dev, 4)) return AQ_ERR_MISALIGNED;
+    return cache_copy_launch(cache, src_dev, dst_dev, n, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? AQ_OK
+               : AQ_ERR_CUDA;
+}
+
+size_t aq_cache_workspace_bytes(int64_t n_pages, int64_t B) {
+    if (n_pages < 1 || B < 1) return 0;
+    return 4 * (size_t)std::max<int64_t>(1 + 4 * B, 1 + 3 * n_pages);
+}
+
+static aq_status check_tables(const aq_cache *c, const CacheTables &t, bool lens_out, bool arg1,
+                              bool ws, size_t ws_bytes) {
+    const aq_status st = check_cache(c, ws);
+    if (st != AQ_OK) return st;
+    if (t.B < 1 || t.B > AQ_CACHE_MAX_ROWS || t.max_pages < 1 ||
+        t.max_pages > (1 << 30) / c->page)
+        return AQ_ERR_INVALID_ARG;
+    const void *need[] = {t.refs_in, t.table_in, t.lens_in, t.refs, t.table, t.status};
+    for (const void *x : need) {
+        if (!x) return AQ_ERR_INVALID_ARG;
+        if (!aligned(x, 4)) return AQ_ERR_MISALIGNED;
+    }
+    if (lens_out && (!t.lens || !t.arg0)) return AQ_ERR_INVALID_ARG;
+    if (arg1 && !t.arg1) return AQ_ERR_INVALID_ARG;
+    if (ws && (!t.ws || ws_bytes < aq_cache_workspace_bytes(c->n_pages, t.B)))
+        return AQ_ERR_INVALID_ARG;
+    if (!aligned(t.lens, 4) || !aligned(t.arg0, 4) || !aligned(t.arg1, 4) || !aligned(t.ws, 4))
+        return AQ_ERR_MISALIGNED;
+    return AQ_OK;
+}
+
+aq_status aq_cache_fork(const aq_cache *cache, const int32_t *refs_dev, const int32_t *table_dev,
+                        const int32_t *lens_dev, const int32_t *parent_dev,
+                        const int32_t *keep_dev, int64_t B, int64_t max_pages, int32_t *refs_out,
+                        int32_t *table_out, int32_t *lens_out, int32_t *status_dev, void *stream) {
+    const CacheTables t = {refs_dev, table_dev,  lens_dev, refs_out, table_out, lens_out,
+                           parent_dev, keep_dev, status_dev, nullptr, B, max_pages};
+    const aq_status st = check_tables(cache, t, true, true, false, 0);
+    if (st != AQ_OK) return st;
+    return cache_fork_launch(cache, t, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? AQ_OK
+               : AQ_ERR_CUDA;
+}
+
+aq_status aq_cache_trim(const aq_cache *cache, const int32_t *refs_dev, const int32_t *table_dev,
+                        const int32_t *lens_dev, const int32_t *keep_dev, int64_t B,
+                        int64_t max_pages, int32_t *refs_out, int32_t *table_out,
+                        int32_t *lens_out, int32_t *status_dev, void *stream) {
+    const CacheTables t = {refs_dev, table_dev, lens_dev,   refs_out, table_out, lens_out,
+                           keep_dev, nullptr,   status_dev, nullptr,  B,         max_pages};
+    const aq_status st = check_tables(cache, t, true, false, false, 0);
+    if (st != AQ_OK) return st;
+    return cache_trim_launch(cache, t, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? AQ_OK
+               : AQ_ERR_CUDA;
+}
+
+aq_status aq_cache_grow(const aq_cache *cache, const int32_t *refs_dev, const int32_t *table_dev,
+                        const int32_t *lens_dev, const int32_t *add_dev, int64_t B,
+                        int64_t max_pages, int32_t *refs_out, int32_t *table_out,
+                        int32_t *lens_out, int32_t *status_dev, void *workspace_dev,
+                        size_t workspace_bytes, void *stream) {
+    const CacheTables t = {refs_dev, table_dev, lens_dev, refs_out, table_out, lens_out, add_dev,
+                           nullptr, status_dev, static_cast<int32_t *>(workspace_dev), B,
+                           max_pages};
+    const aq_status st = check_tables(cache, t, true, false, true, workspace_bytes);
+    if (st != AQ_OK) return st;
+    return cache_grow_launch(cache, t, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? AQ_OK
+               : AQ_ERR_CUDA;
+}
+
+aq_status aq_cache_compact(const aq_cache *cache, const int32_t *refs_dev,
+                           const int32_t *table_dev, const int32_t *lens_dev, int64_t B,
+                           int64_t max_pages, int32_t *refs_out, int32_t *table_out,
+                           int32_t *status_dev, void *workspace_dev, size_t workspace_bytes,
+                           void *stream) {
+    const CacheTables t = {refs_dev, table_dev, lens_dev, refs_out, table_out, nullptr, nullptr,
+                           nullptr, status_dev, static_cast<int32_t *>(workspace_dev), B,
+                           max_pages};
+    const aq_status st = check_tables(cache, t, false, false, true, workspace_bytes);
+    if (st != AQ_OK) return st;
+    return cache_compact_launch(cache, t, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? AQ_OK
+               : AQ_ERR_CUDA;
+}
+
+static aq_status check_batch(const aq_cache *c, int64_t B, int64_t L, int64_t H, int64_t G) {
+    const aq_status st = check_cache(c, false);
+    if (st != AQ_OK) return st;
+    if (B < 1 || L < 1 || H < 1 || G < 0 || H > (1 << 16) || H % c->KV != 0)
+        return AQ_ERR_INVALID_ARG;
+    if (B > AQ_BATCH_MAX_ROWS || G > AQ_BATCH_MAX_GROUPS || !batch_supported(c, L, H))
+        return AQ_ERR_UNSUPPORTED;
+    return AQ_OK;
+}
+
+size_t aq_attention_batch_workspace_bytes(const aq_cache *cache, int64_t B, int64_t L, int64_t H,
+                                          int64_t G) {
+    return check_batch(cache, B, L, H, G) == AQ_OK ? batch_workspace_bytes(cache, B, L, H, G) : 0;
+}
+
+aq_status aq_attention_batch(const aq_cache *cache, int64_t layer, int dtype, const void *q_dev,
+                             int64_t q_stride, const int32_t *table_dev, const int32_t *lens_dev,
+                             const int32_t *group_start_dev, const int32_t *shared_dev, int64_t B,
+                             int64_t L, int64_t H, int64_t G, int64_t max_pages, float scale,
+                             void *out_dev, void *workspace_dev, size_t workspace_bytes,
+                             void *stream) {
+    aq_status st = check_cache(cache, true);
+    if (st == AQ_OK) st = check_batch(cache, B, L, H, G);
+    if (st != AQ_OK) return st;
+    if (layer < 0 || layer >= cache->layers || (dtype != AQ_F16 && dtype != AQ_BF16) ||
+        max_pages < 1 || max_pages > (1 << 29) / cache->page || !std::isfinite(scale) || !q_dev ||
+        !table_dev || !lens_dev || !out_dev || !workspace_dev ||
+        (G > 0 && (!group_start_dev || !shared_dev)) || (B * L > 1 && q_stride < H * cache->D))
+        return AQ_ERR_INVALID_ARG;
+    if (!aligned(q_dev, 16) || q_stride % 8 != 0 || !aligned(out_dev, 16) ||
+        !aligned(workspace_dev, 256) || !aligned(table_dev, 4) || !aligned(lens_dev, 4) ||
+        !aligned(group_start_dev, 4) || !aligned(shared_dev, 4))
+        return AQ_ERR_MISALIGNED;
+    if (workspace_bytes < batch_workspace_bytes(cache, B, L, H, G)) return AQ_ERR_INVALID_ARG;
+    const BatchArgs a = {dtype, q_dev, q_stride, table_dev, lens_dev, group_start_dev, shared_dev,
+                         B, L, H, G, max_pages, scale, out_dev, workspace_dev, workspace_bytes,
+                         static_cast<cudaStream_t>(stream)};
+    return batch_launch(cache, layer, a) == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
+}
+
 aq_status aq_matmul_multi(int dtype, const void *x_dev, int nproj, const uint32_t *const *Wq_dev,
                           const void *const *scales_dev, const void *const *biases_dev,
                           const int64_t *N, int64_t M, int64_t K, int bits, void *const *out_dev,
@@ -561,7 +772,10 @@ aq_status aq_device_error(uint32_t *code, int clear) {
     if (tc_read_error(&b, clear != 0) != cudaSuccess) return AQ_ERR_CUDA;
     if (gemv_read_error(&c, clear != 0) != cudaSuccess) return AQ_ERR_CUDA;
     if (attn_read_error(&d, clear != 0) != cudaSuccess) return AQ_ERR_CUDA;
-    *code = a | b | c | d;
+    uint32_t e = 0, f = 0;
+    if (cache_read_error(&e, clear != 0) != cudaSuccess) return AQ_ERR_CUDA;
+    if (batch_read_error(&f, clear != 0) != cudaSuccess) return AQ_ERR_CUDA;
+    *code = a | b | c | d | e | f;
     return AQ_OK;
 }
 

@@ -1,0 +1,79 @@
+// Host side of the batch attention's own-keys kernel: launch geometry of one
+// instantiation, included by the files that instantiate it.
+#pragma once
+
+#include "aq_batch_own.cuh"
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+namespace aq {
+
+struct BatchRun {
+    BatchParams prm;
+    bool do_shared;      // this kernel also takes the shared keys
+    int nb;              // blocks of 8 query rows a tile
+    int64_t max_items;   // pieces there can be, whatever the lengths are
+    cudaStream_t stream;
+    // planning only: CTAs the device holds at once, rows a tile
+    int *resident;
+};
+
+template <int BITS, int D, int GROUP, int NB>
+cudaError_t own_run_nb(const BatchRun &r) {
+    using S = Own<BITS, D, GROUP, NB>;
+    auto kern = own_kernel<BITS, D, GROUP, NB>;
+    const size_t smem = S::kBody + S::kTail + plan_bytes(r.prm.B, r.prm.G);
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [&] {
+        attr = cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            (int)(S::kBody + S::kTail + plan_bytes(AQ_BATCH_MAX_ROWS, kBatchMaxGroups)));
+    });
+    if (attr != cudaSuccess) return attr;
+    if (r.resident) {
+        // the query takes microseconds: the last answer is kept (by size, so
+        // that what is kept is right for any caller)
+        static std::atomic<uint64_t> last{0};
+        uint64_t k = last.load(std::memory_order_relaxed);
+        if (k >> 16 != smem) {
+            int n = 0;
+            const cudaError_t e =
+                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, S::kThreads, smem);
+            if (e != cudaSuccess) return e;
+            k = (uint64_t)smem << 16 | (uint64_t)n;
+            last.store(k, std::memory_order_relaxed);
+        }
+        *r.resident = (int)(k & 0xffff) * num_sms();
+        return cudaSuccess;
+    }
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(r.prm.own_target, r.max_items));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(S::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = r.stream;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = a;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, r.prm, (int)r.do_shared);
+}
+
+template <int BITS, int D, int GROUP>
+cudaError_t own_run(const BatchRun &r) {
+    if constexpr (D == 512)  // 128 accumulators a lane for one block of 8 rows
+        return own_run_nb<BITS, D, GROUP, 1>(r);
+    else
+        return r.nb == 1 ? own_run_nb<BITS, D, GROUP, 1>(r) : own_run_nb<BITS, D, GROUP, 2>(r);
+}
+
+cudaError_t batch_own4a(int64_t D, int group, const BatchRun &r);
+cudaError_t batch_own4b(int64_t D, int group, const BatchRun &r);
+cudaError_t batch_own8a(int64_t D, int group, const BatchRun &r);
+cudaError_t batch_own8b(int64_t D, int group, const BatchRun &r);
+
+}  // namespace aq
