@@ -1,6 +1,7 @@
 // Attention of a batch over the paged quantised cache: the kernel that adds
 // the pieces' partial results, the choice of kernels and the workspace.
 #include "aq_batch_host.cuh"
+#include "aq_batch_shared.cuh"
 
 namespace aq {
 
@@ -113,6 +114,10 @@ int resident_ctas(const aq_cache *c, int64_t B, int64_t G, int nb) {
 BatchPlan plan_for(const aq_cache *c, int64_t B, int64_t L, int64_t H, int64_t G) {
     BatchPlan pl = {};
     const int64_t R = H / c->KV;
+    // rows a KV head that read a group's shared keys, if the batch is one of
+    // even groups
+    const int64_t rows = G > 0 ? B * L * R / G : 0;
+    if (c->D <= 256 && rows > 32) pl.row_tiles = c->D <= 128 && rows > 128 ? 2 : 1;
     pl.nb = c->D < 512 && (L * R > 8 || (G > 0 && !pl.row_tiles)) ? 2 : 1;
     pl.own_rows = 8 * pl.nb;
     pl.shared_rows = pl.row_tiles ? 128 * pl.row_tiles : pl.own_rows;
@@ -185,6 +190,10 @@ cudaError_t batch_launch(const aq_cache *c, int64_t layer, const BatchArgs &a) {
     cudaError_t e = cudaGetSymbolAddress(&err, g_batch_error);
     if (e != cudaSuccess) return e;
     p.err = static_cast<uint32_t *>(err);
+    if (pl.row_tiles) {
+        e = batch_shared(p, pl.row_tiles, num_sms(), a.stream);
+        if (e != cudaSuccess) return e;
+    }
     r.do_shared = !pl.row_tiles;
     r.nb = pl.nb;
     r.stream = a.stream;

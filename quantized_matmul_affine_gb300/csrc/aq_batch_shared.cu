@@ -1,0 +1,598 @@
+// The batch attention's kernel for keys that many rows share: tcgen05.
+//
+//   S[row][key] = q'[row] . k[key],  P = 2^(scale S - m),  O[row] += P v
+//
+// One CTA a SM takes pieces (a range of shared keys, one KV head, a tile of
+// 128 or 256 query rows).  Unlike a decode step over own keys, this is bound
+// by the tensor core and by what feeds it, since each key meets hundreds of
+// rows: 4 D flops a (row, key) against 2 D bits/8 bytes a key.
+//
+//   warps 0-7    softmax: a thread a row of its row tile (warps 0-3 the first
+//                tile, 4-7 the second).  Scores come from tensor memory in
+//                two halves, P goes back to tensor memory as fp16, over the
+//                scores, and is the A operand of the value product there.
+//   warps 8-15   dequantise: codes straight from global memory into
+//                registers one step ahead, fp16 k and v into shared memory in
+//                the swizzled layout the tensor core reads (k as the K-major,
+//                v as the MN-major operand: one layout, rows of keys).  The
+//                values of a 4-bit word land in the order 0 4 1 5 2 6 3 7,
+//                which q' and the output follow, so that no code is moved.
+//   warp 16      issues the MMAs.
+//
+// Scores of two steps are in flight (two row tiles of the same keys, or the
+// same row tile and two tiles of keys), so that the tensor core works on one
+// while the softmax has the other.  MMAs of one thread run in issue order,
+// which is what lets a step's scores overwrite the P two steps before it.
+// The running maximum only moves when a row's scores exceed it by 2^8 (P
+// then still fits fp16), so O is seldom rescaled; the sum uses the same
+// reference.  k and v are rounded once to fp16 (2^-11).
+#include "aq_batch_shared.cuh"
+
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <mutex>
+
+namespace aq {
+namespace {
+
+template <int BITS, int D, int GROUP>
+struct Shd {
+    static constexpr int kThreads = 17 * 32;
+    static constexpr int kKeys = D <= 128 ? 128 : 64;      // keys a tile
+    static constexpr int kBlocks = D / 64;                 // 64-value blocks of a row
+    static constexpr int kTileBytes = kKeys * D * 2;       // k or v tile
+    static constexpr int kQBytes = 128 * D * 2;            // q' of one row tile
+    static constexpr int kG = D / GROUP;
+    static constexpr int kRB = D * BITS / 8;
+    static constexpr int kVals = kKeys * D / 256;          // values a thread dequantises a tile
+    static constexpr int kParts = D / kVals;               // threads a key
+    static constexpr int kWords = kVals * BITS / 32;
+    static constexpr int kGV = kVals / GROUP > 0 ? kVals / GROUP : 1;  // groups of them
+    static constexpr int kRT = D <= 128 ? 2 : 1;           // row tiles a CTA can hold
+    static constexpr int kTmemO = 2 * kKeys;               // first column of O
+    static_assert(kTmemO + kRT * D <= 512, "tensor memory");
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+          "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Waits for the loads so far; naming the registers keeps their uses behind it.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t *v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                   "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                   "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                   "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(v[30]), "+r"(v[31])::"memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15])
+        : "memory");
+}
+
+// Descriptor of the v tile as the MN-major operand: 64-value blocks (128
+// bytes a key, swizzled) block_bytes apart, groups of 8 keys 1024 bytes.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t smem_addr, uint32_t block_bytes) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(block_bytes >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// Byte offset of 16-byte chunk c (8 values) of row r in an operand of
+// `rows` rows: 64-value blocks, each row 128 bytes with its chunks swizzled.
+__device__ __forceinline__ uint32_t operand_at(int rows, int r, int c) {
+    return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// Eight codes (a 4-bit word; two 8-bit words) to fp16 scale * code + bias,
+// each rounded once; 4-bit codes in the order 0 4 1 5 2 6 3 7.
+template <int BITS>
+__device__ __forceinline__ uint4 values8(const uint32_t *w, __half2 s, __half2 b) {
+    uint32_t o[4];
+    auto put = [&](int i, uint32_t u, __half2 mul, __half2 add) {
+        const __half2 q = __hfma2(*reinterpret_cast<const __half2 *>(&u), mul, add);
+        const __half2 v = __hfma2(q, s, b);
+        o[i] = *reinterpret_cast<const uint32_t *>(&v);
+    };
+    const __half2 one = __float2half2_rn(1.f), m1024 = __float2half2_rn(-1024.f);
+    if constexpr (BITS == 4) {
+        const __half2 sixteenth = __float2half2_rn(0.0625f), m64 = __float2half2_rn(-64.f);
+        const uint32_t h = w[0] >> 8;
+        put(0, (w[0] & 0x000F000Fu) | 0x64006400u, one, m1024);
+        put(1, (w[0] & 0x00F000F0u) | 0x64006400u, sixteenth, m64);
+        put(2, (h & 0x000F000Fu) | 0x64006400u, one, m1024);
+        put(3, (h & 0x00F000F0u) | 0x64006400u, sixteenth, m64);
+    } else {
+        put(0, prmt(w[0], 0x64646464u, 0x4140u), one, m1024);
+        put(1, prmt(w[0], 0x64646464u, 0x4342u), one, m1024);
+        put(2, prmt(w[1], 0x64646464u, 0x4140u), one, m1024);
+        put(3, prmt(w[1], 0x64646464u, 0x4342u), one, m1024);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// A bounded wait that records where it gave up.
+__device__ __forceinline__ bool shd_wait(uint64_t *bar, uint32_t parity, volatile int *flag,
+                                         uint32_t *err, uint32_t code) {
+    if (mbar_wait(bar, parity)) return true;
+    *flag = 1;
+    atomicOr(err, code);
+    return false;
+}
+
+template <int BITS, int D, int GROUP>
+__global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
+    shared_kernel(const __grid_constant__ BatchParams p, int row_tiles) {
+    using S = Shd<BITS, D, GROUP>;
+    constexpr int KT = S::kKeys;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *qs = smem;                                  // [row tiles][blocks][128][128 B]
+    uint8_t *ks = qs + S::kRT * S::kQBytes;              // [2] k tiles
+    uint8_t *vs = ks + 2 * S::kTileBytes;                // [2] v tiles
+    float *qsc = reinterpret_cast<float *>(vs + 2 * S::kTileBytes);  // [row tiles][128]
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(qsc + S::kRT * 128);
+    uint64_t *k_empty = k_full + 2, *v_full = k_empty + 2, *v_empty = v_full + 2;
+    uint64_t *s_full = v_empty + 2, *p_ready = s_full + 2, *pv_done = p_ready + 2;
+    uint64_t *drain = pv_done + 2;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+    int *flag_s = reinterpret_cast<int *>(tmem_holder + 1);
+    volatile int *flag = flag_s;
+    long long *tmp = reinterpret_cast<long long *>(drain + 2);
+    int *plan_mem = reinterpret_cast<int *>(tmp + 33);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], 8);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 8);
+            mbar_init(&v_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_ready[i], 4);
+            mbar_init(&pv_done[i], 1);
+        }
+        mbar_init(drain, 1);
+        *flag_s = 0;
+        fence_mbar_init();
+    }
+    if (warp == 16) {
+        tmem_alloc(tmem_holder, 512);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    launch_dependents();
+    grid_dependency_wait();
+    const PlanView v = batch_plan(p, plan_mem, tmp);
+    const int n_items = v.shared_items * p.c.KV;
+    const int tile_rows = 128 * row_tiles;
+    // running counts: tiles of keys, steps, value products a row tile
+    uint32_t kt = 0, step = 0, pv[2] = {0u, 0u};
+    bool issued = false;
+
+    for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+        const Piece w = shared_piece(p, v, item, tile_rows);
+        const int tiles = (w.k1 - w.k0 + KT - 1) / KT;
+        const int steps = tiles * row_tiles;
+        // ------------------------------------------------- q', by warps 0-15
+        if (warp < 16) {
+            constexpr int LPR = D / 8;           // lanes a row, 8 values each
+            constexpr int RPW = 32 / LPR;        // rows a warp at a time
+            const int c = lane % LPR;
+            for (int r = warp * RPW + lane / LPR; r < tile_rows; r += 16 * RPW) {
+                uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                if (r < w.rows) raw = *reinterpret_cast<const uint4 *>(q_row(p, w, r) + 8 * c);
+                const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+                float f[8], mx = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    f[i] = q_float(p, (uint16_t)(u[i / 2] >> (16 * (i & 1))));
+                    mx = fmaxf(mx, fabsf(f[i]));
+                }
+#pragma unroll
+                for (int o = LPR / 2; o >= 1; o >>= 1)
+                    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+                const int e = batch_exp(mx);
+                // a negative scale goes into q', so that the largest score is
+                // the largest of the products
+                const float sc = p.scale2 < 0.f ? -batch_pow2(e) : batch_pow2(e);
+                uint32_t h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int a = BITS == 4 ? i : 2 * i, b = BITS == 4 ? i + 4 : 2 * i + 1;
+                    h[i] = pack_half2(f[a] * sc, f[b] * sc);
+                }
+                *reinterpret_cast<uint4 *>(qs + (r >> 7) * S::kQBytes +
+                                           operand_at(128, r & 127, c)) =
+                    make_uint4(h[0], h[1], h[2], h[3]);
+                if (c == 0) qsc[r] = batch_pow2(-e) * fabsf(p.scale2);
+            }
+            fence_proxy_async_smem();
+        }
+        __syncthreads();
+
+        if (warp < 8) {
+            // ------------------------------------------------------- softmax
+            const int wg = warp >> 2;
+            if (wg < row_tiles) {
+                const int r = wg * 128 + (warp & 3) * 32 + lane;
+                const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+                const uint32_t o_at = tmem + lanes + S::kTmemO + wg * D;
+                const float c = qsc[r];
+                float m = -INFINITY;            // reference of this row's weights
+                float2 sum = make_float2(0.f, 0.f);
+                bool ok = true;
+                for (int j = 0; j < tiles; ++j) {
+                    const uint32_t st = step + (row_tiles == 2 ? 2 * j + wg : j);
+                    const uint32_t slot = st & 1, s_at = tmem + lanes + slot * KT;
+                    ok = shd_wait(&s_full[slot], (st >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
+                    if (!__all_sync(~0u, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int valid = w.k1 - w.k0 - j * KT;   // keys of the tile that count
+                    // scores in chunks of 32 keys, the next one in flight while one
+                    // is worked on: once for the maximum, once for P
+                    uint32_t xa[32], xb[32];
+                    auto mask = [&](uint32_t (&x)[32], int chunk) {
+                        if (32 * chunk + 32 > valid) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * chunk + i >= valid) x[i] = 0xff800000u;  // -inf
+                        }
+                    };
+                    float mx = -INFINITY;
+                    auto largest = [&](uint32_t (&x)[32], int chunk) {
+                        mask(x, chunk);
+                        float a = mx, b = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            a = fmaxf(a, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+                            b = fmaxf(b, fmaxf(__uint_as_float(x[i + 2]),
+                                               __uint_as_float(x[i + 3])));
+                        }
+                        mx = fmaxf(a, b);
+                    };
+                    tmem_ld32(s_at, xa);
+#pragma unroll
+                    for (int k = 0; k < KT / 32; k += 2) {
+                        tmem_wait_ld32(xa);
+                        tmem_ld32(s_at + 32 * (k + 1), xb);
+                        largest(xa, k);
+                        tmem_wait_ld32(xb);
+                        tmem_ld32(s_at + 32 * ((k + 2) % (KT / 32)), xa);  // at the end: chunk 0 again
+                        largest(xb, k + 1);
+                    }
+                    mx *= c;
+                    // the reference moves when a weight could pass 2^8
+                    float f = 1.f;
+                    if (mx > m + 8.f || (m == -INFINITY && mx > m)) {
+                        f = m == -INFINITY ? 0.f : batch_ex2(m - mx);
+                        m = mx;
+                    }
+                    tmem_wait_ld32(xa);
+                    if (j > 0 && __any_sync(~0u, f != 1.f)) {
+                        // O of the tiles so far, once their products are done
+                        ok = shd_wait(&pv_done[wg], (pv[wg] + j - 1) & 1, flag, p.err,
+                                      ERR_BATCH_BASE);
+                        if (!__all_sync(~0u, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 32) {
+                            tmem_ld32(o_at + k, xb);
+                            tmem_wait_ld32(xb);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                xb[i] = __float_as_uint(__uint_as_float(xb[i]) * f);
+                            tmem_st32(o_at + k, xb);
+                        }
+                        sum.x *= f;
+                        sum.y *= f;
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    const float2 c2 = make_float2(c, c), m2 = make_float2(-ref, -ref);
+                    // P of chunk k takes 16 columns at 16 k: over scores that have
+                    // been read (chunk k + 1, in flight, starts at 32 k + 32)
+                    auto weigh = [&](uint32_t (&x)[32], int chunk) {
+                        mask(x, chunk);
+                        uint32_t h[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float2 t = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]),
+                                                              __uint_as_float(x[2 * i + 1])),
+                                                  c2, m2);
+                            t.x = batch_ex2(t.x);
+                            t.y = batch_ex2(t.y);
+                            sum = __fadd2_rn(sum, t);
+                            h[i] = pack_half2(t.x, t.y);
+                        }
+                        tmem_st16(s_at + 16 * chunk, h);
+                    };
+#pragma unroll
+                    for (int k = 0; k < KT / 32; k += 2) {
+                        if (k > 0) tmem_wait_ld32(xa);
+                        tmem_ld32(s_at + 32 * (k + 1), xb);
+                        weigh(xa, k);
+                        tmem_wait_ld32(xb);
+                        if (k + 2 < KT / 32) tmem_ld32(s_at + 32 * (k + 2), xa);
+                        weigh(xb, k + 1);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_ready[slot]);
+                }
+                // ------------------------------------------------- partial out
+                if (ok) ok = shd_wait(&pv_done[wg], (pv[wg] + tiles - 1) & 1, flag, p.err,
+                                      ERR_BATCH_BASE);
+                if (__all_sync(~0u, ok)) {
+                    tc_fence_after();
+                    const bool mine = r < w.rows;
+                    const int64_t at = mine ? part_row(p, w, r) : 0;
+                    if (mine) p.part_ml[at] = make_float2(m, sum.x + sum.y);
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * D);
+#pragma unroll 1
+                    for (int k = 0; k < D; k += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_at + k, o);
+                        tmem_wait_ld32(o);
+                        if (!mine) continue;
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const uint32_t *u = o + 8 * g;
+                            float4 a, b;
+                            if constexpr (BITS == 4) {
+                                a = make_float4(__uint_as_float(u[0]), __uint_as_float(u[2]),
+                                                __uint_as_float(u[4]), __uint_as_float(u[6]));
+                                b = make_float4(__uint_as_float(u[1]), __uint_as_float(u[3]),
+                                                __uint_as_float(u[5]), __uint_as_float(u[7]));
+                            } else {
+                                a = make_float4(__uint_as_float(u[0]), __uint_as_float(u[1]),
+                                                __uint_as_float(u[2]), __uint_as_float(u[3]));
+                                b = make_float4(__uint_as_float(u[4]), __uint_as_float(u[5]),
+                                                __uint_as_float(u[6]), __uint_as_float(u[7]));
+                            }
+                            dst[k / 4 + 2 * g] = a;
+                            dst[k / 4 + 2 * g + 1] = b;
+                        }
+                    }
+                }
+                tc_fence_before();
+            }
+        } else if (warp < 16) {
+            // ---------------------------------------------------- dequantise
+            const int u = threadIdx.x - 256;
+            const int key = u % KT, part = u / KT;       // kVals values of one key
+            const int d0 = part * S::kVals;
+            const int32_t *trow = p.table + (int64_t)w.row * p.max_pages;
+            struct Raw {
+                uint32_t w[S::kWords];
+                __half2 sb[S::kGV];
+            };
+            auto fetch = [&](Raw &x, const uint8_t *rec, int slot, int which) {
+                if (rec) {
+                    const uint4 *c = reinterpret_cast<const uint4 *>(
+                        rec + which * p.c.side_codes + slot * S::kRB + d0 * BITS / 8);
+#pragma unroll
+                    for (int i = 0; i < S::kWords / 4; ++i) {
+                        const uint4 t = __ldg(c + i);
+                        x.w[4 * i] = t.x;
+                        x.w[4 * i + 1] = t.y;
+                        x.w[4 * i + 2] = t.z;
+                        x.w[4 * i + 3] = t.w;
+                    }
+                    const __half2 *sb = reinterpret_cast<const __half2 *>(
+                                            rec + 2 * (int64_t)p.c.side_codes + which * p.c.side_sb) +
+                                        slot * S::kG + d0 / GROUP;
+#pragma unroll
+                    for (int g = 0; g < S::kGV; ++g) x.sb[g] = __ldg(sb + g);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < S::kWords; ++i) x.w[i] = 0u;
+#pragma unroll
+                    for (int g = 0; g < S::kGV; ++g) x.sb[g] = __float2half2_rn(0.f);
+                }
+            };
+            auto store = [&](const Raw &x, uint8_t *tile) {
+#pragma unroll
+                for (int i = 0; i < S::kVals / 8; ++i) {
+                    const __half2 sb = x.sb[i * 8 / GROUP];
+                    *reinterpret_cast<uint4 *>(tile + operand_at(KT, key, d0 / 8 + i)) =
+                        values8<BITS>(x.w + i * BITS / 4, __low2half2(sb), __high2half2(sb));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            };
+            // the record and slot of this thread's key of tile j; nullptr past the
+            // end, or where the table names no page of the pool
+            auto place = [&](int j, int &slot) -> const uint8_t * {
+                const int at = w.k0 + j * KT + key;
+                slot = at & (p.c.page - 1);
+                if (j >= tiles || at >= w.k1) return nullptr;
+                const int id = __ldg(trow + (at >> p.c.page_log2));
+                if (id < 0 || id >= p.c.n_pages) {
+                    atomicOr(p.err, ERR_BATCH_TABLE);
+                    return nullptr;
+                }
+                return p.layer + id * p.c.page_bytes + w.kv * p.c.rec;
+            };
+            Raw a, b;
+            int slot, slot_next;
+            const uint8_t *rec = place(0, slot), *rec_next;
+            fetch(a, rec, slot, 0);
+            for (int j = 0; j < tiles; ++j) {
+                const uint32_t n = kt + j, s = n & 1, lap = n >> 1;
+                fetch(b, rec, slot, 1);
+                rec_next = place(j + 1, slot_next);
+                bool ok = lap == 0 || shd_wait(&k_empty[s], (lap - 1) & 1, flag, p.err,
+                                               ERR_BATCH_BASE);
+                if (!__all_sync(~0u, ok)) break;
+                store(a, ks + s * S::kTileBytes);
+                if (lane == 0) mbar_arrive(&k_full[s]);
+                fetch(a, rec_next, slot_next, 0);
+                ok = lap == 0 || shd_wait(&v_empty[s], (lap - 1) & 1, flag, p.err, ERR_BATCH_BASE);
+                if (!__all_sync(~0u, ok)) break;
+                store(b, vs + s * S::kTileBytes);
+                if (lane == 0) mbar_arrive(&v_full[s]);
+                rec = rec_next;
+                slot = slot_next;
+            }
+        } else {
+            // ----------------------------------------------------------- MMA
+            const uint32_t id_s = (1u << 4) | ((uint32_t)(KT >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+            const uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+                                  ((uint32_t)(128 >> 4) << 24);
+            const uint64_t qd0 = sw128_desc(smem_u32(qs)), kd0 = sw128_desc(smem_u32(ks));
+            const uint64_t vd0 = mn_desc(smem_u32(vs), KT * 128);
+            bool ok = true;
+            // scores of step i (of this piece)
+            auto scores = [&](int i) {
+                const int j = row_tiles == 2 ? i >> 1 : i, t = row_tiles == 2 ? i & 1 : 0;
+                const uint32_t n = kt + j, s = n & 1, slot = (step + i) & 1;
+                ok = shd_wait(&k_full[s], (n >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
+                ok = __all_sync(~0u, ok);
+                if (!ok) return;
+                tc_fence_after();
+                issued = true;
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        tc_mma_f16(tmem + slot * KT,
+                                   qd0 + (uint64_t)((t * S::kQBytes + (k >> 2) * 16384 +
+                                                     (k & 3) * 32) >> 4),
+                                   kd0 + (uint64_t)((s * S::kTileBytes + (k >> 2) * (KT * 128) +
+                                                     (k & 3) * 32) >> 4),
+                                   id_s, k != 0);
+                    tc_commit(&s_full[slot]);
+                    if (t == row_tiles - 1) tc_commit(&k_empty[s]);
+                }
+                __syncwarp();
+            };
+            for (int i = 0; i < 2 && i < steps && ok; ++i) scores(i);
+            for (int i = 0; i < steps && ok; ++i) {
+                const int j = row_tiles == 2 ? i >> 1 : i, t = row_tiles == 2 ? i & 1 : 0;
+                const uint32_t n = kt + j, s = n & 1, st = step + i, slot = st & 1;
+                ok = shd_wait(&v_full[s], (n >> 1) & 1, flag, p.err, ERR_BATCH_BASE) &&
+                     shd_wait(&p_ready[slot], (st >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < KT / 16; ++k)
+                        tc_mma_f16_ta(tmem + S::kTmemO + t * D,
+                                      tmem + slot * KT + k * 8,
+                                      vd0 + (uint64_t)((s * S::kTileBytes + k * 2048) >> 4), id_o,
+                                      j != 0 || k != 0);
+                    tc_commit(&pv_done[t]);
+                    if (t == row_tiles - 1) tc_commit(&v_empty[s]);
+                }
+                __syncwarp();
+                if (i + 2 < steps) scores(i + 2);
+            }
+        }
+        kt += tiles;
+        step += steps;
+        pv[0] += tiles;
+        pv[1] += tiles;
+        __syncthreads();  // the piece is done: q', O and the rings' ends
+        tc_fence_after();
+        if (*flag) break;
+    }
+    // every MMA that was issued has completed before tensor memory is freed
+    if (warp == 16 && issued) {
+        if (lane == 0) tc_commit(drain);
+        __syncwarp();
+        if (!mbar_wait(drain, 0) && lane == 0) atomicOr(p.err, ERR_BATCH_BASE);
+        __syncwarp();
+    }
+    __syncthreads();
+    if (warp == 16) tmem_dealloc(tmem, 512);
+}
+
+template <int BITS, int D, int GROUP>
+cudaError_t shared_run(const BatchParams &p, int row_tiles, int grid, cudaStream_t stream) {
+    using S = Shd<BITS, D, GROUP>;
+    auto kern = shared_kernel<BITS, D, GROUP>;
+    constexpr size_t body = 1024 + (size_t)S::kRT * S::kQBytes + 4 * (size_t)S::kTileBytes +
+                            S::kRT * 512 + 16 * 8 + 33 * 8 + 64;
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [&] {
+        attr = cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            (int)std::min<size_t>(227 * 1024,
+                                  body + plan_bytes(AQ_BATCH_MAX_ROWS, kBatchMaxGroups)));
+    });
+    if (attr != cudaSuccess) return attr;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(S::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = body + plan_bytes(p.B, p.G);
+    cfg.stream = stream;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = a;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, row_tiles);
+}
+
+template <int BITS, int D>
+cudaError_t shared_group(const BatchParams &p, int row_tiles, int grid, cudaStream_t stream) {
+    if (p.c.group == 32) return shared_run<BITS, D, 32>(p, row_tiles, grid, stream);
+    if (p.c.group == 64) return shared_run<BITS, D, 64>(p, row_tiles, grid, stream);
+    if constexpr (D >= 128) return shared_run<BITS, D, 128>(p, row_tiles, grid, stream);
+    return cudaErrorInvalidValue;
+}
+
+template <int BITS>
+cudaError_t shared_dim(const BatchParams &p, int row_tiles, int grid, cudaStream_t stream) {
+    switch (p.c.D) {
+        case 64: return shared_group<BITS, 64>(p, row_tiles, grid, stream);
+        case 128: return shared_group<BITS, 128>(p, row_tiles, grid, stream);
+        case 256: return shared_group<BITS, 256>(p, row_tiles, grid, stream);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t batch_shared(const BatchParams &p, int row_tiles, int grid, cudaStream_t stream) {
+    return p.c.bits == 4 ? shared_dim<4>(p, row_tiles, grid, stream)
+                         : shared_dim<8>(p, row_tiles, grid, stream);
+}
+
+}  // namespace aq
