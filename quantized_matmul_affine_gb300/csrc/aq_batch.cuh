@@ -69,11 +69,11 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, long long *tmp) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-    __syncthreads();
     if (lane == 0) tmp[warp] = v;
     __syncthreads();
     int64_t s = 0;
     for (int w = 0; w < nw; ++w) s += tmp[w];
+    __syncthreads();  // tmp may be written again
     return s;
 }
 

@@ -45,10 +45,13 @@ struct Shd {
     static constexpr int kQBytes = 128 * D * 2;            // q' of one row tile
     static constexpr int kG = D / GROUP;
     static constexpr int kRB = D * BITS / 8;
-    static constexpr int kVals = kKeys * D / 256;          // values a thread dequantises a tile
-    static constexpr int kParts = D / kVals;               // threads a key
-    static constexpr int kWords = kVals * BITS / 32;
-    static constexpr int kGV = kVals / GROUP > 0 ? kVals / GROUP : 1;  // groups of them
+    static constexpr int kWKeys = kKeys / 8;               // keys a dequantising warp takes of a tile
+    static constexpr int kLane = 128 / BITS;               // values of a lane's 16 bytes
+    static constexpr int kChunks = kLane / 8;              // 16-byte chunks of k or v of them
+    static constexpr int kLpr = kRB / 16;                  // lanes a row
+    static constexpr int kLRows = 32 / kLpr;               // rows a load
+    static constexpr int kLoads = kWKeys / kLRows;
+    static_assert(kLane <= GROUP && kWKeys <= 16 && kLoads >= 1, "a lane's values are of one group");
     static constexpr int kRT = D <= 128 ? 2 : 1;           // row tiles a CTA can hold
     static constexpr int kTmemO = 2 * kKeys;               // first column of O
     static_assert(kTmemO + kRT * D <= 512, "tensor memory");
@@ -194,8 +197,12 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
     const PlanView v = batch_plan(p, plan_mem, tmp);
     const int n_items = v.shared_items * p.c.KV;
     const int tile_rows = 128 * row_tiles;
-    // running counts: tiles of keys, steps, value products a row tile
-    uint32_t kt = 0, step = 0, pv[2] = {0u, 0u};
+    // running counts: tiles of keys, and steps (row tiles x tiles of keys).  A
+    // step's scores, its P and its value product have the barriers of its
+    // parity.  Scores of step i follow the product of step i - 2, so whoever
+    // has seen them may wait for the product of step i - 1 or i: no barrier is
+    // ever two phases ahead of a waiter.
+    uint32_t kt = 0, step = 0;
     bool issued = false;
 
     for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
@@ -302,7 +309,8 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     tmem_wait_ld32(xa);
                     if (j > 0 && __any_sync(~0u, f != 1.f)) {
                         // O of the tiles so far, once their products are done
-                        ok = shd_wait(&pv_done[wg], (pv[wg] + j - 1) & 1, flag, p.err,
+                        const uint32_t before = st - row_tiles;
+                        ok = shd_wait(&pv_done[before & 1], (before >> 1) & 1, flag, p.err,
                                       ERR_BATCH_BASE);
                         if (!__all_sync(~0u, ok)) {
                             ok = false;
@@ -355,7 +363,8 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     if (lane == 0) mbar_arrive(&p_ready[slot]);
                 }
                 // ------------------------------------------------- partial out
-                if (ok) ok = shd_wait(&pv_done[wg], (pv[wg] + tiles - 1) & 1, flag, p.err,
+                const uint32_t last = step + (row_tiles == 2 ? 2 * tiles - 2 + wg : tiles - 1);
+                if (ok) ok = shd_wait(&pv_done[last & 1], (last >> 1) & 1, flag, p.err,
                                       ERR_BATCH_BASE);
                 if (__all_sync(~0u, ok)) {
                     tc_fence_after();
@@ -393,81 +402,109 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
             }
         } else if (warp < 16) {
             // ---------------------------------------------------- dequantise
-            const int u = threadIdx.x - 256;
-            const int key = u % KT, part = u / KT;       // kVals values of one key
-            const int d0 = part * S::kVals;
+            // A warp takes KT / 8 consecutive keys (within one page) of every
+            // tile: 16 bytes of codes a lane, kLpr lanes a row, so that a
+            // load covers 512 bytes in a row.
+            const int dw = warp - 8;
+            const int key0 = dw * S::kWKeys, row = lane / S::kLpr, l = lane % S::kLpr;
             const int32_t *trow = p.table + (int64_t)w.row * p.max_pages;
             struct Raw {
-                uint32_t w[S::kWords];
-                __half2 sb[S::kGV];
+                uint4 c[S::kLoads];
+                __half2 sb[S::kLoads];
             };
-            auto fetch = [&](Raw &x, const uint8_t *rec, int slot, int which) {
-                if (rec) {
-                    const uint4 *c = reinterpret_cast<const uint4 *>(
-                        rec + which * p.c.side_codes + slot * S::kRB + d0 * BITS / 8);
-#pragma unroll
-                    for (int i = 0; i < S::kWords / 4; ++i) {
-                        const uint4 t = __ldg(c + i);
-                        x.w[4 * i] = t.x;
-                        x.w[4 * i + 1] = t.y;
-                        x.w[4 * i + 2] = t.z;
-                        x.w[4 * i + 3] = t.w;
-                    }
-                    const __half2 *sb = reinterpret_cast<const __half2 *>(
-                                            rec + 2 * (int64_t)p.c.side_codes + which * p.c.side_sb) +
-                                        slot * S::kG + d0 / GROUP;
-#pragma unroll
-                    for (int g = 0; g < S::kGV; ++g) x.sb[g] = __ldg(sb + g);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < S::kWords; ++i) x.w[i] = 0u;
-#pragma unroll
-                    for (int g = 0; g < S::kGV; ++g) x.sb[g] = __float2half2_rn(0.f);
-                }
-            };
-            auto store = [&](const Raw &x, uint8_t *tile) {
-#pragma unroll
-                for (int i = 0; i < S::kVals / 8; ++i) {
-                    const __half2 sb = x.sb[i * 8 / GROUP];
-                    *reinterpret_cast<uint4 *>(tile + operand_at(KT, key, d0 / 8 + i)) =
-                        values8<BITS>(x.w + i * BITS / 4, __low2half2(sb), __high2half2(sb));
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-            };
-            // the record and slot of this thread's key of tile j; nullptr past the
-            // end, or where the table names no page of the pool
-            auto place = [&](int j, int &slot) -> const uint8_t * {
-                const int at = w.k0 + j * KT + key;
-                slot = at & (p.c.page - 1);
+            // the record of this warp's keys of tile j; nullptr past the end,
+            // or where the table names no page of the pool
+            auto place = [&](int j) -> const uint8_t * {
+                const int at = w.k0 + j * KT + key0;
                 if (j >= tiles || at >= w.k1) return nullptr;
                 const int id = __ldg(trow + (at >> p.c.page_log2));
                 if (id < 0 || id >= p.c.n_pages) {
-                    atomicOr(p.err, ERR_BATCH_TABLE);
+                    if (lane == 0) atomicOr(p.err, ERR_BATCH_TABLE);
                     return nullptr;
                 }
                 return p.layer + id * p.c.page_bytes + w.kv * p.c.rec;
             };
+            auto fetch = [&](Raw &x, const uint8_t *rec, int j, int which) {
+                const int at = w.k0 + j * KT + key0, slot = at & (p.c.page - 1);
+                const uint4 *c = reinterpret_cast<const uint4 *>(
+                                     rec + which * p.c.side_codes + slot * S::kRB) + lane;
+                const __half2 *sb = reinterpret_cast<const __half2 *>(
+                                        rec + 2 * (int64_t)p.c.side_codes + which * p.c.side_sb) +
+                                    (slot + row) * S::kG + l * S::kLane / GROUP;
+#pragma unroll
+                for (int i = 0; i < S::kLoads; ++i) {
+                    const bool in = rec && at + row + i * S::kLRows < w.k1;
+                    x.c[i] = in ? __ldg(c + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+                    x.sb[i] = in ? __ldg(sb + i * S::kLRows * S::kG) : __float2half2_rn(0.f);
+                }
+            };
+            // the lines of the tile after the next into L2
+            auto prefetch = [&](const uint8_t *rec, int j) {
+                if (!rec) return;
+                const int slot = (w.k0 + j * KT + key0) & (p.c.page - 1);
+                constexpr int kLines = (S::kWKeys * S::kRB + 127) / 128;  // of K codes, of V codes
+                for (int i = lane; i < 2 * kLines; i += 32)
+                    prefetch_l2(rec + (i < kLines ? 0 : p.c.side_codes) + slot * S::kRB +
+                                128 * (i < kLines ? i : i - kLines));
+                if (lane < 2)
+                    prefetch_l2(rec + 2 * (int64_t)p.c.side_codes + lane * p.c.side_sb +
+                                slot * S::kG * 4);
+            };
+            const int turn = BITS == 4 ? (l >> 1) * (D == 128 ? 2 : 1) & 3 : (l >> 2) & 1;
+            auto store = [&](const Raw &x, uint8_t *tile) {
+#pragma unroll
+                for (int i = 0; i < S::kLoads; ++i) {
+                    const __half2 s = __low2half2(x.sb[i]), b = __high2half2(x.sb[i]);
+                    // the lane's 16-byte chunks are stored in an order turned by
+                    // lane, so that 8 lanes store to 8 distinct bank groups;
+                    // swaps bring the words of chunk k ^ turn to place k
+                    uint32_t cw[4] = {x.c[i].x, x.c[i].y, x.c[i].z, x.c[i].w};
+                    auto swap = [&](bool on, int u, int v) {
+                        const uint32_t t = on ? cw[v] : cw[u];
+                        cw[v] = on ? cw[u] : cw[v];
+                        cw[u] = t;
+                    };
+                    if constexpr (BITS == 4) {
+                        swap(turn & 1, 0, 1);
+                        swap(turn & 1, 2, 3);
+                        swap(turn & 2, 0, 2);
+                        swap(turn & 2, 1, 3);
+                    } else {
+                        swap(turn & 1, 0, 2);
+                        swap(turn & 1, 1, 3);
+                    }
+                    const uint32_t at =
+                        operand_at(KT, key0 + row + i * S::kLRows, l * S::kChunks) ^
+                        ((uint32_t)turn << 4);
+#pragma unroll
+                    for (int k = 0; k < S::kChunks; ++k)
+                        *reinterpret_cast<uint4 *>(tile + (at ^ ((uint32_t)k << 4))) =
+                            values8<BITS>(cw + k * BITS / 4, s, b);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            };
             Raw a, b;
-            int slot, slot_next;
-            const uint8_t *rec = place(0, slot), *rec_next;
-            fetch(a, rec, slot, 0);
+            const uint8_t *rec = place(0), *rec1 = place(1), *rec2;
+            fetch(a, rec, 0, 0);
+            prefetch(rec1, 1);
             for (int j = 0; j < tiles; ++j) {
                 const uint32_t n = kt + j, s = n & 1, lap = n >> 1;
-                fetch(b, rec, slot, 1);
-                rec_next = place(j + 1, slot_next);
+                fetch(b, rec, j, 1);
+                rec2 = place(j + 2);
                 bool ok = lap == 0 || shd_wait(&k_empty[s], (lap - 1) & 1, flag, p.err,
                                                ERR_BATCH_BASE);
                 if (!__all_sync(~0u, ok)) break;
                 store(a, ks + s * S::kTileBytes);
                 if (lane == 0) mbar_arrive(&k_full[s]);
-                fetch(a, rec_next, slot_next, 0);
+                prefetch(rec2, j + 2);
+                fetch(a, rec1, j + 1, 0);
                 ok = lap == 0 || shd_wait(&v_empty[s], (lap - 1) & 1, flag, p.err, ERR_BATCH_BASE);
                 if (!__all_sync(~0u, ok)) break;
                 store(b, vs + s * S::kTileBytes);
                 if (lane == 0) mbar_arrive(&v_full[s]);
-                rec = rec_next;
-                slot = slot_next;
+                rec = rec1;
+                rec1 = rec2;
             }
         } else {
             // ----------------------------------------------------------- MMA
@@ -516,7 +553,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                                       tmem + slot * KT + k * 8,
                                       vd0 + (uint64_t)((s * S::kTileBytes + k * 2048) >> 4), id_o,
                                       j != 0 || k != 0);
-                    tc_commit(&pv_done[t]);
+                    tc_commit(&pv_done[slot]);
                     if (t == row_tiles - 1) tc_commit(&v_empty[s]);
                 }
                 __syncwarp();
@@ -525,8 +562,6 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
         }
         kt += tiles;
         step += steps;
-        pv[0] += tiles;
-        pv[1] += tiles;
         __syncthreads();  // the piece is done: q', O and the rings' ends
         tc_fence_after();
         if (*flag) break;
