@@ -138,6 +138,19 @@ __device__ __forceinline__ uint4 values8(const uint32_t *w, __half2 s, __half2 b
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// True in one lane of a converged warp, the same one every time.  Unlike a
+// test of the lane number it tells the compiler that a single thread goes on,
+// which is what issuing MMAs from uniform registers wants.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t on;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(on));
+    return on != 0;
+}
+
 // A bounded wait that records where it gave up.
 __device__ __forceinline__ bool shd_wait(uint64_t *bar, uint32_t parity, volatile int *flag,
                                          uint32_t *err, uint32_t code) {
@@ -161,8 +174,8 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
     float *qsc = reinterpret_cast<float *>(vs + 2 * S::kTileBytes);  // [row tiles][128]
     uint64_t *k_full = reinterpret_cast<uint64_t *>(qsc + S::kRT * 128);
     uint64_t *k_empty = k_full + 2, *v_full = k_empty + 2, *v_empty = v_full + 2;
-    uint64_t *s_full = v_empty + 2, *p_ready = s_full + 2, *pv_done = p_ready + 2;
-    uint64_t *drain = pv_done + 2;
+    uint64_t *s_full = v_empty + 2, *p_ready = s_full + 2, *o_done = p_ready + 2;
+    uint64_t *drain = o_done + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     int *flag_s = reinterpret_cast<int *>(tmem_holder + 1);
     volatile int *flag = flag_s;
@@ -178,8 +191,8 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
             mbar_init(&v_empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 4);
-            mbar_init(&pv_done[i], 1);
         }
+        mbar_init(o_done, 1);
         mbar_init(drain, 1);
         *flag_s = 0;
         fence_mbar_init();
@@ -197,12 +210,12 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
     const PlanView v = batch_plan(p, plan_mem, tmp);
     const int n_items = v.shared_items * p.c.KV;
     const int tile_rows = 128 * row_tiles;
-    // running counts: tiles of keys, and steps (row tiles x tiles of keys).  A
-    // step's scores, its P and its value product have the barriers of its
-    // parity.  Scores of step i follow the product of step i - 2, so whoever
-    // has seen them may wait for the product of step i - 1 or i: no barrier is
-    // ever two phases ahead of a waiter.
-    uint32_t kt = 0, step = 0;
+    // Running counts: tiles of keys, steps (row tiles x tiles of keys), pieces.
+    // A step's scores and P have the barriers of its parity, a k or v tile
+    // those of its slot.  MMAs complete in issue order, so that scores of step
+    // i are behind the product of step i - 2.  No barrier is ever two phases
+    // ahead of a waiter: a slot's next phase needs what the waiter does next.
+    uint32_t kt = 0, step = 0, piece = 0;
     bool issued = false;
 
     for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
@@ -309,9 +322,11 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     tmem_wait_ld32(xa);
                     if (j > 0 && __any_sync(~0u, f != 1.f)) {
                         // O of the tiles so far, once their products are done
-                        const uint32_t before = st - row_tiles;
-                        ok = shd_wait(&pv_done[before & 1], (before >> 1) & 1, flag, p.err,
-                                      ERR_BATCH_BASE);
+                        // (with two row tiles these scores follow the last one)
+                        const uint32_t n = kt + j - 1;
+                        if (row_tiles == 1)
+                            ok = shd_wait(&v_empty[n & 1], (n >> 1) & 1, flag, p.err,
+                                          ERR_BATCH_BASE);
                         if (!__all_sync(~0u, ok)) {
                             ok = false;
                             break;
@@ -363,9 +378,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     if (lane == 0) mbar_arrive(&p_ready[slot]);
                 }
                 // ------------------------------------------------- partial out
-                const uint32_t last = step + (row_tiles == 2 ? 2 * tiles - 2 + wg : tiles - 1);
-                if (ok) ok = shd_wait(&pv_done[last & 1], (last >> 1) & 1, flag, p.err,
-                                      ERR_BATCH_BASE);
+                if (ok) ok = shd_wait(o_done, piece & 1, flag, p.err, ERR_BATCH_BASE);
                 if (__all_sync(~0u, ok)) {
                     tc_fence_after();
                     const bool mine = r < w.rows;
@@ -492,8 +505,8 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                 const uint32_t n = kt + j, s = n & 1, lap = n >> 1;
                 fetch(b, rec, j, 1);
                 rec2 = place(j + 2);
-                bool ok = lap == 0 || shd_wait(&k_empty[s], (lap - 1) & 1, flag, p.err,
-                                               ERR_BATCH_BASE);
+                bool ok = lap == 0 || shd_wait(row_tiles == 1 ? &s_full[s] : &k_empty[s],
+                                               (lap - 1) & 1, flag, p.err, ERR_BATCH_BASE);
                 if (!__all_sync(~0u, ok)) break;
                 store(a, ks + s * S::kTileBytes);
                 if (lane == 0) mbar_arrive(&k_full[s]);
@@ -508,69 +521,89 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
             }
         } else {
             // ----------------------------------------------------------- MMA
-            const uint32_t id_s = (1u << 4) | ((uint32_t)(KT >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-            const uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
-                                  ((uint32_t)(128 >> 4) << 24);
-            const uint64_t qd0 = sw128_desc(smem_u32(qs)), kd0 = sw128_desc(smem_u32(ks));
-            const uint64_t vd0 = mn_desc(smem_u32(vs), KT * 128);
-            bool ok = true;
-            // scores of step i (of this piece)
-            auto scores = [&](int i) {
-                const int j = row_tiles == 2 ? i >> 1 : i, t = row_tiles == 2 ? i & 1 : 0;
-                const uint32_t n = kt + j, s = n & 1, slot = (step + i) & 1;
-                ok = shd_wait(&k_full[s], (n >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
-                ok = __all_sync(~0u, ok);
-                if (!ok) return;
-                tc_fence_after();
-                issued = true;
-                if (lane == 0) {
+            // One thread waits and issues.  A step's value product and the
+            // scores two steps on go out together, then the commits: each
+            // wait and commit costs 100 cycles or more in which a queue of
+            // eight MMAs (64 cycles each) would run dry.
+            if (elect_lane()) {
+                const uint32_t id_s =
+                    (1u << 4) | ((uint32_t)(KT >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+                const uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+                                      ((uint32_t)(128 >> 4) << 24);
+                const uint64_t qd0 = sw128_desc(smem_u32(qs)), kd0 = sw128_desc(smem_u32(ks));
+                const uint64_t vd0 = mn_desc(smem_u32(vs), KT * 128);
+                auto tile_of = [&](int i) { return row_tiles == 2 ? i >> 1 : i; };
+                auto row_of = [&](int i) { return row_tiles == 2 ? i & 1 : 0; };
+                auto wait_k = [&](int i) {
+                    const uint32_t n = kt + tile_of(i);
+                    return shd_wait(&k_full[n & 1], (n >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
+                };
+                auto scores = [&](int i) {
+                    const uint32_t s = (kt + tile_of(i)) & 1;
+                    const uint32_t d = tmem + ((step + i) & 1) * KT;
+                    const uint64_t qd = qd0 + (uint64_t)((row_of(i) * S::kQBytes) >> 4);
+                    const uint64_t kd = kd0 + (uint64_t)((s * S::kTileBytes) >> 4);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        tc_mma_f16(tmem + slot * KT,
-                                   qd0 + (uint64_t)((t * S::kQBytes + (k >> 2) * 16384 +
-                                                     (k & 3) * 32) >> 4),
-                                   kd0 + (uint64_t)((s * S::kTileBytes + (k >> 2) * (KT * 128) +
-                                                     (k & 3) * 32) >> 4),
+                        tc_mma_f16(d, qd + (uint64_t)(((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                                   kd + (uint64_t)(((k >> 2) * (KT * 128) + (k & 3) * 32) >> 4),
                                    id_s, k != 0);
-                    tc_commit(&s_full[slot]);
-                    if (t == row_tiles - 1) tc_commit(&k_empty[s]);
-                }
-                __syncwarp();
-            };
-            for (int i = 0; i < 2 && i < steps && ok; ++i) scores(i);
-            for (int i = 0; i < steps && ok; ++i) {
-                const int j = row_tiles == 2 ? i >> 1 : i, t = row_tiles == 2 ? i & 1 : 0;
-                const uint32_t n = kt + j, s = n & 1, st = step + i, slot = st & 1;
-                ok = shd_wait(&v_full[s], (n >> 1) & 1, flag, p.err, ERR_BATCH_BASE) &&
-                     shd_wait(&p_ready[slot], (st >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
-                ok = __all_sync(~0u, ok);
-                if (!ok) break;
-                tc_fence_after();
-                if (lane == 0) {
+                };
+                auto values = [&](int i) {
+                    const uint32_t s = (kt + tile_of(i)) & 1;
+                    const uint32_t d = tmem + S::kTmemO + row_of(i) * D;
+                    const uint32_t a = tmem + ((step + i) & 1) * KT;
+                    const uint64_t vd = vd0 + (uint64_t)((s * S::kTileBytes) >> 4);
 #pragma unroll
                     for (int k = 0; k < KT / 16; ++k)
-                        tc_mma_f16_ta(tmem + S::kTmemO + t * D,
-                                      tmem + slot * KT + k * 8,
-                                      vd0 + (uint64_t)((s * S::kTileBytes + k * 2048) >> 4), id_o,
-                                      j != 0 || k != 0);
-                    tc_commit(&pv_done[slot]);
-                    if (t == row_tiles - 1) tc_commit(&v_empty[s]);
+                        tc_mma_f16_ta(d, a + k * 8, vd + (uint64_t)((k * 2048) >> 4), id_o,
+                                      tile_of(i) != 0 || k != 0);
+                };
+                auto scores_done = [&](int i) {
+                    tc_commit(&s_full[(step + i) & 1]);
+                    // with one row tile the scores are also the k tile's last use
+                    if (row_tiles == 2 && (i & 1)) tc_commit(&k_empty[(kt + tile_of(i)) & 1]);
+                };
+                bool ok = true;
+                for (int i = 0; i < 2 && i < steps && ok; ++i) {
+                    ok = wait_k(i);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issued = true;
+                    scores(i);
+                    scores_done(i);
                 }
-                __syncwarp();
-                if (i + 2 < steps) scores(i + 2);
+                for (int i = 0; i < steps && ok; ++i) {
+                    const uint32_t n = kt + tile_of(i), s = n & 1, st = step + i, slot = st & 1;
+                    ok = shd_wait(&v_full[s], (n >> 1) & 1, flag, p.err, ERR_BATCH_BASE) &&
+                         (i + 2 >= steps || wait_k(i + 2)) &&
+                         shd_wait(&p_ready[slot], (st >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
+                    if (!ok) break;
+                    tc_fence_after();
+                    values(i);
+                    if (i + 2 < steps) {
+                        scores(i + 2);
+                        scores_done(i + 2);
+                    }
+                    if (row_of(i) == row_tiles - 1) tc_commit(&v_empty[s]);
+                }
+                if (issued) tc_commit(o_done);
             }
+            __syncwarp();
         }
         kt += tiles;
         step += steps;
+        ++piece;
         __syncthreads();  // the piece is done: q', O and the rings' ends
         tc_fence_after();
         if (*flag) break;
     }
     // every MMA that was issued has completed before tensor memory is freed
-    if (warp == 16 && issued) {
-        if (lane == 0) tc_commit(drain);
-        __syncwarp();
-        if (!mbar_wait(drain, 0) && lane == 0) atomicOr(p.err, ERR_BATCH_BASE);
+    if (warp == 16) {
+        if (issued) {  // the issuing lane
+            tc_commit(drain);
+            if (!mbar_wait(drain, 0)) atomicOr(p.err, ERR_BATCH_BASE);
+        }
         __syncwarp();
     }
     __syncthreads();
