@@ -9,24 +9,45 @@ __device__ uint32_t g_batch_error;
 
 namespace {
 
-constexpr int kJoinThreads = 128;
-
-// One warp a row (sequence, token, head): its slots in plan order - the
-// shared pieces, then its own - weighted by 2^(max - largest max).  Reads
-// 4 (D + 2) bytes a slot; a row without slots, or whose keys were all past
-// its limit, is zeros.
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ BatchParams p) {
+// A row's output (sequence, token, head): its slots in plan order - the
+// shared pieces, then its own - weighted by 2^(max - largest max), 4 (D + 2)
+// bytes each.  WPR warps a row: one where there are rows for every warp of the
+// device; eight, which take every eighth slot and add up in warp order, where
+// a few rows have hundreds of slots each (one row of a 32k-token sequence:
+// 200).  A row without slots, or whose keys were all past its limit, is zeros.
+template <int D, int WPR>
+__global__ void __launch_bounds__(WPR == 1 ? 128 : 32 * WPR)
+    join_kernel(const __grid_constant__ BatchParams p) {
+    constexpr int kRows = WPR == 1 ? 4 : 1;        // rows a CTA
+    constexpr int V = D / 128 > 0 ? D / 128 : 1;   // float4 a lane (half the lanes at D = 64)
+    constexpr int kPart = WPR > 1 ? WPR : 1;
+    __shared__ float4 part[kPart][D / 4];
+    __shared__ float psum[kPart];
     launch_dependents();
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * (kJoinThreads / 32) + warp;
+    const int sub = WPR == 1 ? 0 : warp;
+    const int64_t row = WPR == 1 ? (int64_t)blockIdx.x * kRows + warp : (int64_t)blockIdx.x;
     const int64_t LH = (int64_t)p.L * p.H;
-    if (row >= p.B * LH) return;
+    if (row >= p.B * LH) return;  // whole warps, and only with one warp a row
     const int b = (int)(row / LH);
-    const int64_t lh = row - b * LH;
-    const int32_t *d = p.desc + 5 * b;
-    const int own0 = d[0], own_n = d[1], sh0 = d[2], sh_step = d[3], sh_n = d[4];
+    const int lh = (int)(row - b * LH), l = lh / p.H, h = lh - l * p.H;
+    const int kv = h / p.R, lr = l * p.R + (h - kv * p.R), LR = p.L * p.R;
+    const int64_t per = *reinterpret_cast<const int64_t *>(p.desc);
+    const int32_t *d = p.desc + 2 + kDesc * (int64_t)b;
+    // pieces of a segment of `tiles` tiles from tile u0 on
+    auto pieces = [&](int64_t u0, int tiles) {
+        return tiles > 0 ? (int)((u0 + tiles - 1) / per - u0 / per) + 1 : 0;
+    };
+    const int own0 = d[0], tiles = d[1], sh0 = d[4], sh_step = d[5];
+    const int own_n = pieces(*reinterpret_cast<const int64_t *>(d + 2) +
+                                 (int64_t)(kv * ceil_div(LR, p.own_rows) + lr / p.own_rows) * tiles,
+                             tiles);
+    int sh_n = d[8];
+    if (d[9] > 0) {
+        const int rt = (d[10] * LR + lr) / p.own_rows;
+        sh_n = pieces(*reinterpret_cast<const int64_t *>(d + 6) + (int64_t)(kv * d[9] + rt) * d[8], d[8]);
+    }
     const int n = sh_n + own_n;
     auto slot_row = [&](int i) -> int64_t {
         const int64_t s = i < sh_n ? sh0 + (int64_t)i * sh_step : own0 + (i - sh_n);
@@ -37,26 +58,45 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
     const float ref = M == -INFINITY ? 0.f : M;
-    constexpr int V = D / 128 > 0 ? D / 128 : 1;  // float4 a lane (half the lanes at D = 64)
     float4 acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     float L = 0.f;
     const bool on = D >= 128 || lane < D / 4;
-    for (int i = 0; i < n; ++i) {
+#pragma unroll 4
+    for (int i = sub; i < n; i += WPR) {
         const int64_t at = slot_row(i);
         const float2 ml = p.part_ml[at];
         const float g = batch_ex2(ml.x - ref);
         L = fmaf(ml.y, g, L);
-        if (!on) continue;
         const float4 *o = reinterpret_cast<const float4 *>(p.part_o + at * D);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const float4 v = o[lane + 32 * k];
+            const float4 v = on ? o[lane + 32 * k] : make_float4(0.f, 0.f, 0.f, 0.f);
             acc[k].x = fmaf(v.x, g, acc[k].x);
             acc[k].y = fmaf(v.y, g, acc[k].y);
             acc[k].z = fmaf(v.z, g, acc[k].z);
             acc[k].w = fmaf(v.w, g, acc[k].w);
+        }
+    }
+    if constexpr (WPR > 1) {
+        if (on)
+#pragma unroll
+            for (int k = 0; k < V; ++k) part[warp][lane + 32 * k] = acc[k];
+        if (lane == 0) psum[warp] = L;
+        __syncthreads();
+        if (warp > 0) return;
+        for (int w = 1; w < WPR; ++w) {
+            L += psum[w];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                if (!on) break;
+                const float4 v = part[w][lane + 32 * k];
+                acc[k].x += v.x;
+                acc[k].y += v.y;
+                acc[k].z += v.z;
+                acc[k].w += v.w;
+            }
         }
     }
     if (!on) return;
@@ -78,68 +118,75 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     }
 }
 
-// Workspace: the slots' (max, sum), the slots' outputs, the rows' slots.
-struct BatchWs {
+template <int D>
+cudaError_t join_run(const BatchParams &p, cudaStream_t stream) {
+    const int64_t rows = (int64_t)p.B * p.L * p.H;
+    const bool wide = rows <= 4 * (int64_t)num_sms();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 3) / 4), 1, 1);
+    cfg.blockDim = dim3(wide ? 256 : 128, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return wide ? cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, p)
+                : cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, p);
+}
+
+struct BatchPlan {
+    int nb, own_rows;      // own_kernel: blocks of 8 query rows, rows a tile
+    int own_ctas, unit_keys;
+    int row_tiles;         // shared_kernel: tiles of 128 rows a CTA (0: not taken)
+    int shared_rows, shared_target;
+    // the workspace: the slots' (max, sum), the slots' outputs, the rows' slots
     int64_t slots;
     size_t off_o, off_desc, bytes;
 };
 
-struct BatchPlan {
-    int nb, own_rows;      // own-keys kernel: blocks of 8 query rows, rows a tile
-    int row_tiles;         // shared keys on the tensor core: tiles a CTA (0: not)
-    int shared_rows;       // rows a tile of the kernel that takes shared keys
-    int own_target, shared_target;
-    BatchWs ws;
-};
-
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
-
-cudaError_t own_dispatch(const aq_cache *c, const BatchRun &r);
-
-// CTAs of the own-keys kernel the device holds at once (2 a SM without one).
-int resident_ctas(const aq_cache *c, int64_t B, int64_t G, int nb) {
-    int n = 0;
-    BatchRun r = {};
-    r.prm.B = (int)B;
-    r.prm.G = (int)G;
-    r.nb = nb;
-    r.resident = &n;
-    if (own_dispatch(c, r) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        return 2 * num_sms();
-    }
-    return n;
-}
-
-BatchPlan plan_for(const aq_cache *c, int64_t B, int64_t L, int64_t H, int64_t G) {
-    BatchPlan pl = {};
-    const int64_t R = H / c->KV;
-    // rows a KV head that read a group's shared keys, if the batch is one of
-    // even groups
-    const int64_t rows = G > 0 ? B * L * R / G : 0;
-    if (c->D <= 256 && rows > 32) pl.row_tiles = c->D <= 128 && rows > 128 ? 2 : 1;
-    pl.nb = c->D < 512 && (L * R > 8 || (G > 0 && !pl.row_tiles)) ? 2 : 1;
-    pl.own_rows = 8 * pl.nb;
-    pl.shared_rows = pl.row_tiles ? 128 * pl.row_tiles : pl.own_rows;
-    pl.own_target = resident_ctas(c, B, G, pl.nb);
-    pl.shared_target = pl.row_tiles ? num_sms() : pl.own_target;
-    // Slots.  With T pieces x row tiles x heads wanted, own keys make at most
-    // T / heads + B pieces; a group's shared keys make at most T / (heads *
-    // its row tiles) + 1 pieces, one slot a sequence of the group each.
-    const int64_t T = pl.own_target / c->KV + 1, Ts = pl.shared_target / c->KV + 1;
-    const int64_t per_tile = pl.shared_rows / (L * R) + 1;  // sequences a tile
-    pl.ws.slots = 3 * B + T + (G > 0 ? std::min(B, per_tile * G) * Ts : 0);
-    const size_t each = (size_t)(pl.ws.slots * L * H);
-    pl.ws.off_o = up256(each * sizeof(float2));
-    pl.ws.off_desc = pl.ws.off_o + up256(each * (size_t)c->D * sizeof(float));
-    pl.ws.bytes = pl.ws.off_desc + up256((size_t)B * 5 * sizeof(int32_t));
-    return pl;
-}
 
 cudaError_t own_dispatch(const aq_cache *c, const BatchRun &r) {
     if (c->bits == 4)
         return c->D <= 128 ? batch_own4a(c->D, c->group_size, r) : batch_own4b(c->D, c->group_size, r);
     return c->D <= 128 ? batch_own8a(c->D, c->group_size, r) : batch_own8b(c->D, c->group_size, r);
+}
+
+BatchPlan plan_for(const aq_cache *c, int64_t B, int64_t L, int64_t H, int64_t G) {
+    BatchPlan pl = {};
+    const int64_t R = H / c->KV;
+    // rows a KV head that read a group's shared keys, if the groups are even
+    const int64_t rows = G > 0 ? B * L * R / G : 0;
+    if (c->D <= 256 && rows > 32) pl.row_tiles = c->D <= 128 && rows > 128 ? 2 : 1;
+    pl.nb = c->D < 512 && (L * R > 8 || (G > 0 && !pl.row_tiles)) ? 2 : 1;
+    pl.own_rows = 8 * pl.nb;
+    BatchRun r = {};
+    r.prm.B = (int)B;
+    r.prm.G = (int)G;
+    r.nb = pl.nb;
+    r.resident = &pl.own_ctas;
+    r.unit_keys = &pl.unit_keys;
+    if (own_dispatch(c, r) != cudaSuccess || pl.own_ctas < 1) {  // no device: sizes only
+        cudaGetLastError();
+        pl.own_ctas = 2 * num_sms();
+        pl.unit_keys = 16;
+    }
+    pl.shared_rows = 128 * std::max(1, pl.row_tiles);
+    pl.shared_target = num_sms();
+    // Slots.  With T runs of own_kernel, a segment of t tiles needs 2 + t / per
+    // of them; the segments of all heads and row tiles together make t / per
+    // at most T / (heads x row tiles).  A group has a slot a sequence for each
+    // piece; shared_kernel makes at most T / (heads x row tiles) + 1.
+    const int64_t T = 4 * (int64_t)pl.own_ctas / c->KV + 1;
+    const int64_t Ts = (pl.row_tiles ? pl.shared_target : 4 * (int64_t)pl.own_ctas) / c->KV + 2;
+    const int64_t per_tile = (pl.row_tiles ? pl.shared_rows : pl.own_rows) / (L * R) + 1;
+    pl.slots = 5 * B + T + (G > 0 ? std::min(B, per_tile * G) * Ts : 0);
+    const size_t each = (size_t)(pl.slots * L * H);
+    pl.off_o = up256(each * sizeof(float2));
+    pl.off_desc = pl.off_o + up256(each * (size_t)c->D * sizeof(float));
+    pl.bytes = pl.off_desc + up256(desc_bytes(B));
+    return pl;
 }
 
 }  // namespace
@@ -149,7 +196,7 @@ bool batch_supported(const aq_cache *c, int64_t L, int64_t H) {
 }
 
 size_t batch_workspace_bytes(const aq_cache *c, int64_t B, int64_t L, int64_t H, int64_t G) {
-    return plan_for(c, B, L, H, G).ws.bytes;
+    return plan_for(c, B, L, H, G).bytes;
 }
 
 cudaError_t batch_launch(const aq_cache *c, int64_t layer, const BatchArgs &a) {
@@ -176,16 +223,24 @@ cudaError_t batch_launch(const aq_cache *c, int64_t layer, const BatchArgs &a) {
     p.scale2 = a.scale * 1.4426950408889634f;
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     p.part_ml = reinterpret_cast<float2 *>(ws);
-    p.part_o = reinterpret_cast<float *>(ws + pl.ws.off_o);
-    p.desc = reinterpret_cast<int32_t *>(ws + pl.ws.off_desc);
-    p.slots = pl.ws.slots;
+    p.part_o = reinterpret_cast<float *>(ws + pl.off_o);
+    p.desc = reinterpret_cast<int32_t *>(ws + pl.off_desc);
+    p.slots = pl.slots;
     p.key_cap = a.max_pages * c->page;
-    p.own_target = pl.own_target;
     p.own_rows = pl.own_rows;
-    p.own_unit = 128;
+    p.unit_keys = pl.unit_keys;
+    p.own_min = 64 / pl.unit_keys;
+    p.shared_tc = pl.row_tiles > 0;
     p.shared_target = pl.shared_target;
     p.shared_rows = pl.shared_rows;
     p.shared_unit = 128;
+    // no more CTAs than the longest sequences there can be give work to
+    const int64_t most = p.key_cap / pl.unit_keys + 1, LR = a.L * R;
+    const int64_t tiles =
+        (a.B * ((LR + pl.own_rows - 1) / pl.own_rows) +
+         (a.G > 0 && !pl.row_tiles ? a.B * LR / pl.own_rows + a.G : 0)) * c->KV * most;
+    p.own_warps = 4 * (int)std::max<int64_t>(
+                          1, std::min<int64_t>(pl.own_ctas, (tiles / p.own_min + 3) / 4));
     void *err = nullptr;
     cudaError_t e = cudaGetSymbolAddress(&err, g_batch_error);
     if (e != cudaSuccess) return e;
@@ -194,31 +249,15 @@ cudaError_t batch_launch(const aq_cache *c, int64_t layer, const BatchArgs &a) {
         e = batch_shared(p, pl.row_tiles, num_sms(), a.stream);
         if (e != cudaSuccess) return e;
     }
-    r.do_shared = !pl.row_tiles;
     r.nb = pl.nb;
     r.stream = a.stream;
-    const int64_t pieces = (p.key_cap + p.own_unit - 1) / p.own_unit;
-    const int64_t tiles = (a.L * R + pl.own_rows - 1) / pl.own_rows;
-    r.max_items = (a.B * pieces * tiles +
-                   (r.do_shared && a.G > 0 ? (a.B * a.L * R / pl.own_rows + a.G) * pieces : 0)) *
-                  c->KV;
     e = own_dispatch(c, r);
     if (e != cudaSuccess) return e;
-    const int64_t rows = a.B * a.L * a.H;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)), 1, 1);
-    cfg.blockDim = dim3(kJoinThreads, 1, 1);
-    cfg.stream = a.stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
     switch (c->D) {
-        case 64: return cudaLaunchKernelEx(&cfg, join_kernel<64>, p);
-        case 128: return cudaLaunchKernelEx(&cfg, join_kernel<128>, p);
-        case 256: return cudaLaunchKernelEx(&cfg, join_kernel<256>, p);
-        default: return cudaLaunchKernelEx(&cfg, join_kernel<512>, p);
+        case 64: return join_run<64>(p, a.stream);
+        case 128: return join_run<128>(p, a.stream);
+        case 256: return join_run<256>(p, a.stream);
+        default: return join_run<512>(p, a.stream);
     }
 }
 

@@ -8,6 +8,13 @@
 // the unnormalised output, fp32.  The slots of a row are added in a fixed
 // order afterwards.  All lengths are known to the device only, so every CTA
 // works out the same plan from lens, group_start and shared by itself.
+//
+// Two kernels take pieces.  shared_kernel (tensor core, many rows) takes
+// ranges of shared_chunk keys of a group.  own_kernel takes own keys, and
+// shared keys of groups of few rows: its tiles of unit_keys keys, in order of
+// (group or sequence, KV head, row tile, key), are dealt to its warps in even
+// runs of `per` tiles, so that all warps have the same work however uneven
+// the sequences are.
 #pragma once
 
 #include "aq_cache.cuh"
@@ -30,41 +37,46 @@ struct BatchParams {
     float scale2;            // scale * log2(e)
     float *part_o;           // [slots][L][H][D]
     float2 *part_ml;         // [slots][L][H]
-    int32_t *desc;           // [B][5], see PlanView
+    int32_t *desc;           // see write_desc
     int64_t slots;           // slots of the workspace
     int64_t key_cap;         // max_pages * page, at most 2^29
-    int own_target;          // pieces x KV heads x row tiles wanted of own keys
-    int own_rows;            // rows a tile of the kernel for own keys
-    int shared_target;       // the same of shared keys
-    int shared_rows;
-    int shared_unit;         // piece lengths are multiples of these
-    int own_unit;
+    int own_rows;            // query rows a tile of own_kernel
+    int own_warps;           // its warps
+    int own_min;             // tiles a warp takes at least
+    int unit_keys;           // keys a tile
+    int shared_tc;           // shared_kernel takes the shared keys (else own_kernel)
+    int shared_target;       // its CTAs
+    int shared_rows;         // query rows a tile of it
+    int shared_unit;         // its chunks are multiples of this
     uint32_t *err;
 };
 
 // What a CTA knows after batch_plan, in shared memory.
 struct PlanView {
-    int *start;    // [B] first own key
-    int *sbase;    // [B + 1] own pieces before row b
-    int *gidx;     // [B] group that row b shares with, or -1
-    int *g_len;    // [G] shared keys (0: nobody shares)
-    int *g_lead;   // [G] row whose table entries serve them
-    int *g_items;  // [G + 1] (piece, row tile) pairs before group g
-    int *g_slot;   // [G] first slot
-    int *g_first;  // [G] first row
-    int *g_rows;   // [G] rows of the group
-    int own_chunk, shared_chunk;
-    int own_items, shared_items;  // pieces (x row tiles for shared), per KV head
-    int shared_slots;
+    int64_t *ubase;    // [B + 1] tiles of own_kernel before row b's own keys
+    int64_t *g_ubase;  // [G + 1] the same before group g's (groups come first)
+    int *start;        // [B] first own key
+    int *sbase;        // [B] first slot of the own keys
+    int *gidx;         // [B] group that row b shares with, or -1
+    int *g_len;        // [G] shared keys (0: nobody shares)
+    int *g_lead;       // [G] row whose table entries serve them
+    int *g_items;      // [G + 1] shared_kernel's (chunk, row tile) pairs before group g
+    int *g_slot;       // [G] first slot
+    int *g_first;      // [G] first row
+    int *g_rows;       // [G] rows of the group
+    int64_t per;       // tiles a warp of own_kernel takes
+    int shared_chunk;  // keys a chunk of shared_kernel
+    int shared_items;  // g_items[G]
 };
 
 __host__ __device__ inline size_t plan_bytes(int B, int G) {
-    return sizeof(int) * ((size_t)3 * B + 1 + (size_t)6 * G + 1 + 64);
+    return sizeof(int64_t) * ((size_t)B + G + 3) +
+           sizeof(int) * ((size_t)3 * B + 6 * (size_t)G + 2);
 }
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((int64_t)a + b - 1) / b); }
 
-// Sum over the CTA, returned to every thread; tmp: 33 ints.
+// Sum over the CTA, returned to every thread; tmp: 32 values.
 __device__ __forceinline__ int64_t block_sum(int64_t v, long long *tmp) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
 #pragma unroll
@@ -77,20 +89,46 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, long long *tmp) {
     return s;
 }
 
-// Own pieces of row b for pieces of `chunk` keys.
-__device__ __forceinline__ int own_pieces(const BatchParams &p, const PlanView &v, int b,
-                                          int chunk) {
-    const int n = min((int)p.key_cap, max(0, __ldg(p.lens + b))) - v.start[b];
-    return n > 0 ? ceil_div(n, chunk) : 0;
+// Sum over the CTA's threads before this one, and over all; tmp as above.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *total, long long *tmp) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    int64_t upto = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) tmp[warp] = upto;
+    __syncthreads();
+    int64_t skip = 0, all = 0;
+    for (int w = 0; w < nw; ++w) {
+        if (w < warp) skip += tmp[w];
+        all += tmp[w];
+    }
+    __syncthreads();
+    *total = all;
+    return skip + upto - v;
+}
+
+// Tiles of own_kernel that row b's own keys take.
+__device__ __forceinline__ int own_tiles(const BatchParams &p, const PlanView &v, int b) {
+    const int len = min((int)p.key_cap, __ldg(p.lens + b));
+    return len > v.start[b] ? ceil_div(len, p.unit_keys) - v.start[b] / p.unit_keys : 0;
+}
+// Slots that a segment of so many tiles may need: the runs it can touch.
+__device__ __forceinline__ int64_t seg_slots(int64_t tiles, int64_t per) {
+    return tiles > 0 ? (tiles - 1) / per + 2 : 0;
 }
 
 // The plan, by all threads of a CTA (a multiple of 32, at most 1024).  mem:
-// plan_bytes(B, G); tmp: 33 long longs.
+// plan_bytes(B, G); tmp: 32 values.
 __device__ inline PlanView batch_plan(const BatchParams &p, int *mem, long long *tmp) {
     PlanView v;
-    v.start = mem;
+    v.ubase = reinterpret_cast<int64_t *>((reinterpret_cast<uintptr_t>(mem) + 7) & ~(uintptr_t)7);
+    v.g_ubase = v.ubase + p.B + 1;
+    v.start = reinterpret_cast<int *>(v.g_ubase + p.G + 1);
     v.sbase = v.start + p.B;
-    v.gidx = v.sbase + p.B + 1;
+    v.gidx = v.sbase + p.B;
     v.g_len = v.gidx + p.B;
     v.g_lead = v.g_len + p.G;
     v.g_items = v.g_lead + p.G;
@@ -99,25 +137,25 @@ __device__ inline PlanView batch_plan(const BatchParams &p, int *mem, long long 
     v.g_rows = v.g_first + p.G;
     int *g_count = v.g_items;  // until the items are counted
     const int nt = blockDim.x, cap = (int)p.key_cap;
-    int disorder = 0;
-    for (int g = threadIdx.x; g < p.G; g += nt) {
-        const int b0 = __ldg(p.gstart + g), b1 = __ldg(p.gstart + g + 1);
-        disorder |= b0 < 0 || b1 < b0 || b1 > p.B;
-        v.g_first[g] = b0;
-        v.g_rows[g] = b1 - b0;
-        v.g_len[g] = min(cap, max(0, __ldg(p.shared + g)));
-        v.g_lead[g] = p.B;
-        g_count[g] = 0;
-    }
-    // groups that do not ascend within the batch share nothing
-    if (p.G > 0 && __syncthreads_or(disorder)) {
-        for (int g = threadIdx.x; g < p.G; g += nt) v.g_first[g] = v.g_rows[g] = v.g_len[g] = 0;
-        if (threadIdx.x == 0) atomicOr(p.err, ERR_BATCH_TABLE);
-    }
-    __syncthreads();
-    for (int b = threadIdx.x; b < p.B; b += nt) {
-        int g = -1;
-        if (p.G > 0) {
+    if (p.G > 0) {
+        int disorder = 0;
+        for (int g = threadIdx.x; g < p.G; g += nt) {
+            const int b0 = __ldg(p.gstart + g), b1 = __ldg(p.gstart + g + 1);
+            disorder |= b0 < 0 || b1 < b0 || b1 > p.B;
+            v.g_first[g] = b0;
+            v.g_rows[g] = b1 - b0;
+            v.g_len[g] = min(cap, max(0, __ldg(p.shared + g)));
+            v.g_lead[g] = p.B;
+            g_count[g] = 0;
+        }
+        // groups that do not ascend within the batch share nothing
+        if (__syncthreads_or(disorder)) {
+            for (int g = threadIdx.x; g < p.G; g += nt)
+                v.g_first[g] = v.g_rows[g] = v.g_len[g] = 0;
+            if (threadIdx.x == 0) atomicOr(p.err, ERR_BATCH_TABLE);
+        }
+        __syncthreads();
+        for (int b = threadIdx.x; b < p.B; b += nt) {
             int lo = 0, hi = p.G;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
@@ -127,139 +165,141 @@ __device__ inline PlanView batch_plan(const BatchParams &p, int *mem, long long 
                     hi = mid;
             }
             const int len = min(cap, __ldg(p.lens + b));
+            int g = -1;
             if (b >= v.g_first[lo] && b < v.g_first[lo] + v.g_rows[lo] && v.g_len[lo] > 0 &&
                 len - (p.L - 1) >= v.g_len[lo]) {
                 g = lo;
                 atomicMin(&v.g_lead[lo], b);
                 atomicAdd(&g_count[lo], 1);
             }
+            v.gidx[b] = g;
         }
-        v.gidx[b] = g;
+        __syncthreads();
+        // a group of one shares with nobody
+        for (int g = threadIdx.x; g < p.G; g += nt)
+            if (g_count[g] < 2) v.g_len[g] = 0;
+        __syncthreads();
     }
-    __syncthreads();
-    // a group of one shares with nobody
-    for (int g = threadIdx.x; g < p.G; g += nt)
-        if (g_count[g] < 2) v.g_len[g] = 0;
-    __syncthreads();
-    int64_t own = 0;
+    int64_t units = 0;
     for (int b = threadIdx.x; b < p.B; b += nt) {
-        int g = v.gidx[b];
-        if (g >= 0 && v.g_len[g] == 0) v.gidx[b] = g = -1;
+        int g = p.G > 0 ? v.gidx[b] : -1;
+        if (g >= 0 && v.g_len[g] == 0) g = -1;
+        v.gidx[b] = g;
         v.start[b] = g >= 0 ? v.g_len[g] : 0;
-        own += max(0, min(cap, __ldg(p.lens + b)) - v.start[b]);
+        units += own_tiles(p, v, b);
     }
-    // units of work: keys x row tiles x KV heads
-    const int own_tiles = ceil_div(p.L * p.R, p.own_rows);
-    own = block_sum(own, tmp) * own_tiles * p.c.KV;
-    int64_t sh = 0;
-    for (int g = threadIdx.x; g < p.G; g += nt)
-        sh += (int64_t)v.g_len[g] * ceil_div(v.g_rows[g] * p.L * p.R, p.shared_rows) * p.c.KV;
-    sh = block_sum(sh, tmp);
-    auto piece = [](int64_t units, int target, int unit) {
-        const int64_t each = (units + target - 1) / target;
-        return (int)min((int64_t)(1 << 29), max((int64_t)unit, (each + unit - 1) / unit * unit));
+    const int LR = p.L * p.R, own_rt = ceil_div(LR, p.own_rows), KV = p.c.KV;
+    units = block_sum(units, tmp) * own_rt * KV;
+    // a group's work: tiles of own_kernel, or items of shared_kernel
+    auto group_tiles = [&](int g) -> int64_t {
+        return p.shared_tc ? 0
+                           : (int64_t)ceil_div(v.g_len[g], p.unit_keys) *
+                                 ceil_div(v.g_rows[g] * LR, p.own_rows) * KV;
     };
-    v.own_chunk = piece(own, p.own_target, p.own_unit);
-    v.shared_chunk = piece(sh, p.shared_target, p.shared_unit);
-    // one piece more than the device holds at once would cost a whole round:
-    // shared pieces grow until they fit (each group has at least one)
-    for (int k = 0; k < 8 && p.G > 0; ++k) {
+    auto group_items = [&](int g) -> int64_t {
+        return p.shared_tc ? (int64_t)ceil_div(v.g_len[g], v.shared_chunk) *
+                                 ceil_div(v.g_rows[g] * LR, p.shared_rows)
+                           : 0;
+    };
+    v.shared_chunk = p.shared_unit;
+    if (p.G > 0 && p.shared_tc) {
         int64_t n = 0;
         for (int g = threadIdx.x; g < p.G; g += nt)
-            n += (int64_t)ceil_div(v.g_len[g], v.shared_chunk) *
-                 ceil_div(v.g_rows[g] * p.L * p.R, p.shared_rows) * p.c.KV;
-        n = block_sum(n, tmp);
-        if (n <= p.shared_target || v.shared_chunk >= cap) break;
-        const int64_t want = ((int64_t)v.shared_chunk * n / p.shared_target + p.shared_unit - 1) /
-                             p.shared_unit * p.shared_unit;
-        v.shared_chunk = (int)min((int64_t)(1 << 29), max(want, (int64_t)v.shared_chunk + p.shared_unit));
+            n += (int64_t)v.g_len[g] * ceil_div(v.g_rows[g] * LR, p.shared_rows) * KV;
+        int64_t want = block_sum(n, tmp) / p.shared_target;
+        // one item more than the device holds at once would cost a whole
+        // round: chunks grow until all fit (each group has at least one)
+        for (int k = 0; k < 8; ++k) {
+            want = max((want + p.shared_unit - 1) / p.shared_unit * p.shared_unit,
+                       (int64_t)v.shared_chunk + (k > 0 ? p.shared_unit : 0));
+            v.shared_chunk = (int)min((int64_t)(1 << 29), want);
+            n = 0;
+            for (int g = threadIdx.x; g < p.G; g += nt) n += group_items(g) * KV;
+            n = block_sum(n, tmp);
+            if (n <= p.shared_target || v.shared_chunk >= cap) break;
+            want = (int64_t)v.shared_chunk * n / p.shared_target;
+        }
+    } else if (p.G > 0) {
+        int64_t n = 0;
+        for (int g = threadIdx.x; g < p.G; g += nt) n += group_tiles(g);
+        units += block_sum(n, tmp);
     }
+    v.per = max((int64_t)p.own_min, (units + p.own_warps - 1) / p.own_warps);
     // pieces grow until their slots fit the workspace
+    auto group_slots = [&](int g) -> int64_t {
+        return v.g_rows[g] * (p.shared_tc ? (int64_t)ceil_div(v.g_len[g], v.shared_chunk)
+                                          : seg_slots(ceil_div(v.g_len[g], p.unit_keys), v.per));
+    };
     for (;;) {
         int64_t n = 0;
-        for (int b = threadIdx.x; b < p.B; b += nt) n += own_pieces(p, v, b, v.own_chunk);
-        for (int g = threadIdx.x; g < p.G; g += nt)
-            n += (int64_t)ceil_div(v.g_len[g], v.shared_chunk) * v.g_rows[g];
-        if (block_sum(n, tmp) <= p.slots || (v.own_chunk >= cap && v.shared_chunk >= cap)) break;
-        if (v.own_chunk < cap) v.own_chunk *= 2;
+        for (int b = threadIdx.x; b < p.B; b += nt) n += seg_slots(own_tiles(p, v, b), v.per);
+        for (int g = threadIdx.x; g < p.G; g += nt) n += group_slots(g);
+        if (block_sum(n, tmp) <= p.slots || (v.per >= cap && v.shared_chunk >= cap)) break;
+        if (v.per < cap) v.per *= 2;
         if (v.shared_chunk < cap) v.shared_chunk *= 2;
     }
-    // groups' items and slots (warp 0), then the rows' pieces
-    if (threadIdx.x < 32) {
-        int items = 0, slots = 0;
-        for (int g0 = 0; g0 < p.G; g0 += 32) {
-            const int g = g0 + threadIdx.x;
-            int it = 0, sl = 0;
-            if (g < p.G) {
-                const int n = ceil_div(v.g_len[g], v.shared_chunk);
-                it = n * ceil_div(v.g_rows[g] * p.L * p.R, p.shared_rows);
-                sl = n * v.g_rows[g];
-            }
-            int bi = it, bs = sl;
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(~0u, bi, o), y = __shfl_up_sync(~0u, bs, o);
-                if ((int)threadIdx.x >= o) bi += x, bs += y;
-            }
-            if (g < p.G) {
-                v.g_items[g] = items + bi - it;
-                v.g_slot[g] = slots + bs - sl;
-            }
-            items += __shfl_sync(~0u, bi, 31);
-            slots += __shfl_sync(~0u, bs, 31);
-        }
-        if (threadIdx.x == 0) {
-            v.g_items[p.G] = items;
-            tmp[0] = items;
-            tmp[1] = slots;
-        }
+    // groups first, then the rows: tiles, slots and items before each
+    int64_t tiles_at = 0, slots_at = 0, items_at = 0, all;
+    for (int g0 = 0; g0 < p.G; g0 += nt) {
+        const int g = g0 + threadIdx.x;
+        const bool in = g < p.G;
+        const int64_t t = block_scan(in ? group_tiles(g) : 0, &all, tmp);
+        if (in) v.g_ubase[g] = tiles_at + t;
+        tiles_at += all;
+        const int64_t sl = block_scan(in ? group_slots(g) : 0, &all, tmp);
+        if (in) v.g_slot[g] = (int)(slots_at + sl);
+        slots_at += all;
+        const int64_t it = block_scan(in ? group_items(g) : 0, &all, tmp);
+        if (in) v.g_items[g] = (int)(items_at + it);
+        items_at += all;
     }
-    __syncthreads();
-    v.shared_items = (int)tmp[0];
-    v.shared_slots = (int)tmp[1];
-    __syncthreads();
-    int carry = 0;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        v.g_ubase[p.G] = tiles_at;
+        v.g_items[p.G] = (int)items_at;
+    }
+    v.shared_items = (int)items_at;
     for (int b0 = 0; b0 < p.B; b0 += nt) {
         const int b = b0 + threadIdx.x;
-        const int n = b < p.B ? own_pieces(p, v, b, v.own_chunk) : 0;
-        int before = n;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(~0u, before, o);
-            if (lane >= o) before += x;
-        }
-        if (lane == 31) tmp[warp] = before;
-        __syncthreads();
-        int skip = carry, all = carry;
-        for (int w = 0; w < nt >> 5; ++w) {
-            if (w < warp) skip += (int)tmp[w];
-            all += (int)tmp[w];
-        }
-        carry = all;
-        if (b < p.B) v.sbase[b] = skip + before - n;
-        __syncthreads();
+        const int64_t n = b < p.B ? own_tiles(p, v, b) : 0;
+        const int64_t t = block_scan(n * own_rt * KV, &all, tmp);
+        if (b < p.B) v.ubase[b] = tiles_at + t;
+        tiles_at += all;
+        const int64_t sl = block_scan(seg_slots(n, v.per), &all, tmp);
+        if (b < p.B) v.sbase[b] = (int)(slots_at + sl);
+        slots_at += all;
     }
-    if (threadIdx.x == 0) v.sbase[p.B] = carry;
-    v.own_items = carry;
+    if (threadIdx.x == 0) v.ubase[p.B] = tiles_at;
     __syncthreads();
     return v;
 }
 
-// For the kernel that adds the slots: per row b its first own slot, own
-// pieces, first shared slot, step from one shared piece to the next, pieces.
+// For the kernel that adds the slots: `per`, then of each row its own keys'
+// first slot, tiles and tiles before, and its group's: first slot, step from
+// one piece to the next, chunks (shared_kernel) or tiles, tiles before, row
+// tiles a KV head (0: chunks), and the row's place in the group.
+constexpr int kDesc = 12;
+__host__ __device__ inline size_t desc_bytes(int64_t B) { return 4 * (2 + kDesc * (size_t)B); }
+
 __device__ inline void write_desc(const BatchParams &p, const PlanView &v) {
+    if (threadIdx.x == 0) *reinterpret_cast<int64_t *>(p.desc) = v.per;
     for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
         const int g = v.gidx[b];
-        int32_t *d = p.desc + 5 * b;
-        d[0] = v.shared_slots + v.sbase[b];
-        d[1] = v.sbase[b + 1] - v.sbase[b];
-        d[2] = g >= 0 ? v.g_slot[g] + (b - v.g_first[g]) : 0;
-        d[3] = g >= 0 ? v.g_rows[g] : 0;
-        d[4] = g >= 0 ? ceil_div(v.g_len[g], v.shared_chunk) : 0;
+        int32_t *d = p.desc + 2 + kDesc * b;
+        d[0] = v.sbase[b];
+        d[1] = own_tiles(p, v, b);
+        *reinterpret_cast<int64_t *>(d + 2) = v.ubase[b];
+        d[4] = g >= 0 ? v.g_slot[g] + (b - v.g_first[g]) : 0;
+        d[5] = g >= 0 ? v.g_rows[g] : 0;
+        *reinterpret_cast<int64_t *>(d + 6) = g >= 0 ? v.g_ubase[g] : 0;
+        d[8] = g < 0 ? 0 : p.shared_tc ? ceil_div(v.g_len[g], v.shared_chunk)
+                                       : ceil_div(v.g_len[g], p.unit_keys);
+        d[9] = g >= 0 && !p.shared_tc ? ceil_div(v.g_rows[g] * p.L * p.R, p.own_rows) : 0;
+        d[10] = g >= 0 ? b - v.g_first[g] : 0;
     }
 }
 
 // The last index i in [0, n) with base[i] <= x (base ascends, base[0] <= x).
-__device__ __forceinline__ int last_at_most(const int *base, int n, int x) {
+__device__ __forceinline__ int last_at_most(const int64_t *base, int n, int64_t x) {
     int lo = 0, hi = n;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -271,20 +311,20 @@ __device__ __forceinline__ int last_at_most(const int *base, int n, int x) {
     return lo;
 }
 
-// A piece of work of one CTA: keys [k0, k1) of table row `row`, for the rows
-// [r0, r0 + n) of sequences from b0 on (row r: sequence b0 + r / (L * R),
+// A piece of work: keys [k0, k1) of table row `row`, for the rows
+// [r0, r0 + rows) of sequences from b0 on (row r: sequence b0 + r / (L * R),
 // token r / R % L, query head r % R of KV head kv), partial results to slot
 // slot0 + r / (L * R).
 struct Piece {
     int row, k0, k1, b0, r0, rows, kv, slot0;
 };
 
-// The i-th piece of the shared keys, i < shared_items * KV: row tiles
-// fastest, so that the tiles that read the same keys run together.
-__device__ __forceinline__ Piece shared_piece(const BatchParams &p, const PlanView &v, int i,
-                                              int tile_rows) {
+// shared_kernel's i-th item, i < shared_items * KV: row tiles fastest, so
+// that the tiles that read the same keys run together.
+__device__ __forceinline__ Piece shared_piece(const BatchParams &p, const PlanView &v, int i) {
     Piece w;
-    // item = ((piece * KV) + kv) * tiles + tile within the group
+    // item = ((chunk * KV) + kv) * tiles + tile within the group; groups
+    // without items have their successor's base: lo ends at the last
     const int KV = p.c.KV;
     int lo = 0, hi = p.G;
     while (hi - lo > 1) {
@@ -294,35 +334,62 @@ __device__ __forceinline__ Piece shared_piece(const BatchParams &p, const PlanVi
         else
             hi = mid;
     }
-    // groups without items have their successor's base: lo is the last
-    const int g = lo, rows = v.g_rows[g] * p.L * p.R, tiles = ceil_div(rows, tile_rows);
+    const int g = lo, rows = v.g_rows[g] * p.L * p.R, tiles = ceil_div(rows, p.shared_rows);
     const int rem = i - v.g_items[g] * KV;
     const int tile = rem % tiles, kc = rem / tiles, kv = kc % KV, chunk = kc / KV;
     w.row = v.g_lead[g];
     w.k0 = chunk * v.shared_chunk;
     w.k1 = min(v.g_len[g], w.k0 + v.shared_chunk);
     w.b0 = v.g_first[g];
-    w.r0 = tile * tile_rows;
-    w.rows = min(tile_rows, rows - w.r0);
+    w.r0 = tile * p.shared_rows;
+    w.rows = min(p.shared_rows, rows - w.r0);
     w.kv = kv;
     w.slot0 = v.g_slot[g] + chunk * v.g_rows[g];
     return w;
 }
 
-__device__ __forceinline__ Piece own_piece(const BatchParams &p, const PlanView &v, int i,
-                                           int tile_rows) {
+// own_kernel: the piece at tile u of the run that ends before tile `end`, run
+// `me`, and the tile after the piece.
+__device__ __forceinline__ Piece own_piece(const BatchParams &p, const PlanView &v, int64_t u,
+                                           int64_t end, int64_t me, bool *is_shared,
+                                           int64_t *next) {
     Piece w;
-    const int tiles = ceil_div(p.L * p.R, tile_rows);
-    const int tile = i % tiles, kc = i / tiles, kv = kc % p.c.KV, q = kc / p.c.KV;
-    const int b = last_at_most(v.sbase, p.B, q);
-    const int chunk = q - v.sbase[b];
-    w.row = w.b0 = b;
-    w.k0 = v.start[b] + chunk * v.own_chunk;
-    w.k1 = min(min((int)p.key_cap, __ldg(p.lens + b)), w.k0 + v.own_chunk);
-    w.r0 = tile * tile_rows;
-    w.rows = min(tile_rows, p.L * p.R - w.r0);
-    w.kv = kv;
-    w.slot0 = v.shared_slots + q;
+    int rows, tiles, first = 0, step = 1;
+    int64_t base;
+    *is_shared = u < v.g_ubase[p.G];
+    if (*is_shared) {
+        const int g = last_at_most(v.g_ubase, p.G, u);
+        rows = v.g_rows[g] * p.L * p.R;
+        base = v.g_ubase[g];
+        step = v.g_rows[g];
+        w.row = v.g_lead[g];
+        w.b0 = v.g_first[g];
+        w.k0 = 0;
+        w.k1 = v.g_len[g];
+        w.slot0 = v.g_slot[g];
+    } else {
+        const int b = last_at_most(v.ubase, p.B, u);
+        rows = p.L * p.R;
+        base = v.ubase[b];
+        w.row = w.b0 = b;
+        w.k0 = v.start[b];
+        w.k1 = min((int)p.key_cap, __ldg(p.lens + b));
+        first = w.k0 / p.unit_keys;
+        w.slot0 = v.sbase[b];
+    }
+    tiles = ceil_div(w.k1, p.unit_keys) - first;
+    const int rt = ceil_div(rows, p.own_rows);
+    const int64_t rem = u - base;
+    const int seg = (int)(rem / tiles), at = (int)(rem - (int64_t)seg * tiles);
+    const int n = (int)min((int64_t)(tiles - at), end - u);
+    w.kv = seg / rt;
+    w.r0 = (seg - w.kv * rt) * p.own_rows;
+    w.rows = min(p.own_rows, rows - w.r0);
+    // a slot (a sequence) for each run that touches the segment
+    w.slot0 += (int)(me - (base + (int64_t)seg * tiles) / v.per) * step;
+    w.k0 = max(w.k0, (first + at) * p.unit_keys);
+    w.k1 = min(w.k1, (first + at + n) * p.unit_keys);
+    *next = u + n;
     return w;
 }
 

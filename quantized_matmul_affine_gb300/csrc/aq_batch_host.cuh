@@ -12,25 +12,23 @@ namespace aq {
 
 struct BatchRun {
     BatchParams prm;
-    bool do_shared;      // this kernel also takes the shared keys
     int nb;              // blocks of 8 query rows a tile
-    int64_t max_items;   // pieces there can be, whatever the lengths are
     cudaStream_t stream;
-    // planning only: CTAs the device holds at once, rows a tile
-    int *resident;
+    // planning only: CTAs the device holds at once, keys a tile
+    int *resident, *unit_keys;
 };
 
 template <int BITS, int D, int GROUP, int NB>
 cudaError_t own_run_nb(const BatchRun &r) {
     using S = Own<BITS, D, GROUP, NB>;
     auto kern = own_kernel<BITS, D, GROUP, NB>;
-    const size_t smem = S::kBody + S::kTail + plan_bytes(r.prm.B, r.prm.G);
+    const size_t smem = S::kSmem + plan_bytes(r.prm.B, r.prm.G);
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [&] {
         attr = cudaFuncSetAttribute(
             kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-            (int)(S::kBody + S::kTail + plan_bytes(AQ_BATCH_MAX_ROWS, kBatchMaxGroups)));
+            (int)(S::kSmem + plan_bytes(AQ_BATCH_MAX_ROWS, kBatchMaxGroups)));
     });
     if (attr != cudaSuccess) return attr;
     if (r.resident) {
@@ -47,11 +45,11 @@ cudaError_t own_run_nb(const BatchRun &r) {
             last.store(k, std::memory_order_relaxed);
         }
         *r.resident = (int)(k & 0xffff) * num_sms();
+        *r.unit_keys = S::kKeys;
         return cudaSuccess;
     }
-    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(r.prm.own_target, r.max_items));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.gridDim = dim3((unsigned)(r.prm.own_warps / S::kWarps), 1, 1);
     cfg.blockDim = dim3(S::kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = r.stream;
@@ -60,7 +58,7 @@ cudaError_t own_run_nb(const BatchRun &r) {
     a[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = a;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, r.prm, (int)r.do_shared);
+    return cudaLaunchKernelEx(&cfg, kern, r.prm);
 }
 
 template <int BITS, int D, int GROUP>

@@ -16,11 +16,12 @@
 // p * scale_v * 2^ev enters as fp16 (2^-11 relative; ev a power of two a warp
 // lowers as larger scales appear).
 //
-// A CTA of four warps takes one piece of keys at a time; each warp streams
-// its tiles of 16 or 32 keys through a ring of its own in shared memory with
-// 16-byte cp.async (no CTA barrier in the loop), the page numbers one tile
-// ahead.  Rows in the ring are padded so that the fragment reads fall in
-// distinct banks.  The warps' results merge in warp order at the piece's end.
+// Every warp works alone: it takes an even run of the call's tiles (16 or 32
+// keys of one KV head, see aq_batch.cuh), streams them through a ring of its
+// own in shared memory with 16-byte cp.async, the page numbers one tile ahead,
+// and writes its own partial results - no CTA barrier after the plan, and no
+// piece so short that others wait for it.  Rows in the ring are padded so that
+// the fragment reads fall in distinct banks.
 #pragma once
 
 #include "aq_batch.cuh"
@@ -38,22 +39,20 @@ struct Own {
     static constexpr int kRB = D * BITS / 8;           // bytes of a row's codes
     static constexpr int kG = D / GROUP;
     static constexpr int kGB = GROUP * BITS / 8;       // bytes of a group's codes
-    static constexpr int kBlk = kRB <= 128 ? 2 : 1;    // 16-key blocks a tile
+    static constexpr int kBlk = kRB <= 64 ? 2 : 1;     // 16-key blocks a tile
     static constexpr int kKeys = 16 * kBlk;            // keys a tile
     static constexpr int kKS = kRB + (kRB >= 64 ? 32 : 0);  // K row stride in the ring
     static constexpr int kVS = kRB + 16;               // V row stride
     static constexpr int kSB = kKeys * kG * 4;         // bytes of a tile's K (or V) pairs
     static constexpr int kStage = kKeys * (kKS + kVS) + 2 * kSB;
-    static constexpr int kStages = kStage <= 10240 ? 3 : 2;
-    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kStages = kStage <= 4096 ? 3 : 2;
     static constexpr int kSteps = GROUP / 16;
-    // merge area, over the ring: (max, sum) [warps][rows], o [warps][rows][D]
-    static constexpr int kMerge = 4 * kWarps * kRows * (D + 2);
-    static constexpr int kBody = ((kRing > kMerge ? kRing : kMerge) + 127) / 128 * 128;
-    // q' fragments, q' rows (while they are made), sums of q, factors
-    static constexpr int kFrag = NB * (D / 16) * 32 * 8;
-    static constexpr int kTail = kFrag + 4 * kRows * (kG + 2);
-    static_assert(4 * kRows * D <= kBody, "q' rows are staged in the ring");
+    // the q' fragments stay in registers unless they are 64 or more of them
+    static constexpr bool kQRegs = NB * D <= 256;
+    static constexpr int kFrag = kQRegs ? 0 : NB * (D / 16) * 32 * 8;
+    static constexpr int kSums = 4 * kRows * kG;       // sums of q
+    static constexpr int kWarpBytes = (kStages * kStage + kFrag + kSums + 15) / 16 * 16;
+    static constexpr int kSmem = kWarps * kWarpBytes;
 };
 
 template <int N>
@@ -100,120 +99,31 @@ __device__ __forceinline__ uint32_t centred(uint32_t codes, float middle) {
 }
 
 template <int BITS, int D, int GROUP, int NB>
-__global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchParams p,
-                                                  int do_shared) {
+__global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchParams p) {
     using S = Own<BITS, D, GROUP, NB>;
-    constexpr int G = S::kG, BLK = S::kBlk, ROWS = S::kRows;
+    constexpr int G = S::kG, BLK = S::kBlk;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long tmp[33];
-    uint8_t *ring = smem;
-    uint2 *qfrag = reinterpret_cast<uint2 *>(smem + S::kBody);
-    float *qs2 = reinterpret_cast<float *>(smem + S::kBody + S::kFrag);  // [rows][G]
-    float *qsc = qs2 + ROWS * G;                                        // [rows]
-    int *limit = reinterpret_cast<int *>(qsc + ROWS);                   // [rows]
-    int *plan_mem = limit + ROWS;
+    __shared__ long long tmp[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int gid = lane >> 2, t = lane & 3;
+    uint8_t *my = smem + warp * S::kWarpBytes;
+    uint2 *qfrag = reinterpret_cast<uint2 *>(my + S::kStages * S::kStage);
+    float *qs2 = reinterpret_cast<float *>(my + S::kStages * S::kStage + S::kFrag);  // [rows][G]
 
     launch_dependents();
     grid_dependency_wait();
-    const PlanView v = batch_plan(p, plan_mem, tmp);
+    const PlanView v = batch_plan(p, reinterpret_cast<int *>(smem + S::kSmem), tmp);
     if (blockIdx.x == 0) write_desc(p, v);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int gid = lane >> 2, t = lane & 3;
-    const int tiles_own = ceil_div(p.L * p.R, ROWS);
-    const int n_shared = do_shared ? v.shared_items * p.c.KV : 0;
-    const int n_items = n_shared + v.own_items * p.c.KV * tiles_own;
-    uint8_t *my = ring + warp * S::kStages * S::kStage;
+    const int64_t me = (int64_t)blockIdx.x * S::kWarps + warp;
+    int64_t u = me * v.per;
+    const int64_t end = min(v.ubase[p.B], u + v.per);
     uint32_t outside = 0;
 
-    for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-        const bool is_shared = item < n_shared;
-        const Piece w = is_shared ? shared_piece(p, v, item, ROWS)
-                                  : own_piece(p, v, item - n_shared, ROWS);
-        // ---------------------------------------------------------------- q
-        __syncthreads();  // the ring and q' of the last piece are done with
-        float *qf = reinterpret_cast<float *>(ring);  // [rows][D]
-        for (int r = warp; r < ROWS; r += S::kWarps) {
-            float qv[D / 32];
-            float mx = 0.f;
-            if (r < w.rows) {
-                const uint16_t *src = q_row(p, w, r);
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) qv[i] = q_float(p, src[lane + 32 * i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) qv[i] = 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) mx = fmaxf(mx, fabsf(qv[i]));
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-            const int e = batch_exp(mx);
-            const float sc = batch_pow2(e);
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) qf[r * D + lane + 32 * i] = qv[i] * sc;
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                float sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < GROUP / 32; ++i) sum += qv[g * (GROUP / 32) + i];
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-                if (lane == 0) qs2[r * G + g] = sum * p.scale2;
-            }
-            if (lane == 0) {
-                qsc[r] = batch_pow2(24 - e) * p.scale2;
-                // keys at and past the limit are not seen by the row
-                const int l = (w.r0 + r) % (p.L * p.R) / p.R;
-                limit[r] = r >= w.rows ? 0
-                           : is_shared ? w.k1
-                                       : min(w.k1, min((int)p.key_cap, __ldg(p.lens + w.b0)) -
-                                                       (p.L - 1 - l));
-            }
-        }
-        __syncthreads();
-        for (int e = threadIdx.x; e < NB * (D / 16) * 32; e += S::kThreads) {
-            const int nb = e / ((D / 16) * 32), rem = e - nb * (D / 16) * 32;
-            const int k = rem >> 5, hg = nb * 8 + ((rem >> 2) & 7), tt = rem & 3;
-            const int g = k / S::kSteps, s2 = k % S::kSteps;
-            uint32_t r[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int i = 2 * s2 + j;
-                float x[2];
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    int d;
-                    float f = 1.f;
-                    if constexpr (BITS == 4) {
-                        d = g * GROUP + tt * (GROUP / 4) + 8 * (i / 4) + (i % 4) + 4 * hf;
-                        if (i & 1) f = 0.0625f;
-                    } else {
-                        d = g * GROUP + tt * (GROUP / 4) + 4 * (i / 2) + (i % 2) + 2 * hf;
-                    }
-                    x[hf] = qf[hg * D + d] * f;
-                }
-                r[j] = pack_half2(x[0], x[1]);
-            }
-            qfrag[e] = make_uint2(r[0], r[1]);
-        }
-        int lim[2 * NB], lim_min = w.k1;
-        float qc[2 * NB];
-#pragma unroll
-        for (int c = 0; c < 2 * NB; ++c) {
-            const int r = (c >> 1) * 8 + 2 * t + (c & 1);
-            lim[c] = limit[r];
-            qc[c] = qsc[r];
-            if (r < w.rows) lim_min = min(lim_min, lim[c]);
-        }
-        lim_min = __reduce_min_sync(~0u, lim_min);
-        __syncthreads();
-
-        // --------------------------------------------------------- the keys
-        // tiles of the piece, from the one that holds k0; this warp's are
-        // first, first + kWarps, ...
+    while (u < end) {
+        bool is_shared;
+        const Piece w = own_piece(p, v, u, end, me, &is_shared, &u);
         const int tile0 = w.k0 / S::kKeys, tile1 = (w.k1 + S::kKeys - 1) / S::kKeys;
-        const int first = tile0 + warp;
         const int32_t *trow = p.table + (int64_t)w.row * p.max_pages;
         // the page of each 16-key block of a tile, in lane = block
         auto page_of = [&](int tile) -> int {
@@ -258,6 +168,104 @@ __global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchP
             }
         };
 
+
+        // the first tiles are under way while q' is made
+        int ids = page_of(tile0);
+#pragma unroll
+        for (int s = 0; s < S::kStages - 1; ++s) {
+            const int nxt = page_of(tile0 + s + 1);
+            if (tile0 + s < tile1) load(tile0 + s, s, ids);
+            cp_async_commit();
+            ids = nxt;
+        }
+
+        // ---------------------------------------------------------------- q'
+        // Lane (gid, t) holds D / 4 values of row gid: those that meet the
+        // codes it reads.  q' = q * 2^e a row, in fp16; at 4 bits the values
+        // of codes at bit 4 carry another 2^-4.
+        uint2 qr[S::kQRegs ? NB * (D / 16) : 1];
+        int lim[2 * NB], lim_min = w.k1;
+        float qc[2 * NB];
+        __syncwarp();
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int r = nb * 8 + gid;
+            uint4 raw[D / 32];
+            const uint4 *src = nullptr;
+            if (r < w.rows) src = reinterpret_cast<const uint4 *>(q_row(p, w, r));
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < GROUP / 32; ++i)
+                    raw[g * (GROUP / 32) + i] =
+                        src ? src[g * (GROUP / 8) + t * (GROUP / 32) + i]
+                            : make_uint4(0u, 0u, 0u, 0u);
+            float mx = 0.f;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < GROUP / 32; ++i) {
+                    const uint4 x = raw[g * (GROUP / 32) + i];
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float f = q_float(p, (uint16_t)(xs[k / 2] >> (16 * (k & 1))));
+                        mx = fmaxf(mx, fabsf(f));
+                        sum += f;
+                    }
+                }
+                sum += __shfl_xor_sync(~0u, sum, 1);
+                sum += __shfl_xor_sync(~0u, sum, 2);
+                if (t == 0) qs2[r * G + g] = sum * p.scale2;
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+            const int e = batch_exp(mx);
+            const float sc = batch_pow2(e);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint32_t xs[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                float f[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    f[k] = q_float(p, (uint16_t)(xs[k / 2] >> (16 * (k & 1)))) * sc;
+                uint2 fr[2];
+                if constexpr (BITS == 4) {
+                    fr[0] = make_uint2(pack_half2(f[0], f[4]),
+                                       pack_half2(f[1] * 0.0625f, f[5] * 0.0625f));
+                    fr[1] = make_uint2(pack_half2(f[2], f[6]),
+                                       pack_half2(f[3] * 0.0625f, f[7] * 0.0625f));
+                } else {
+                    fr[0] = make_uint2(pack_half2(f[0], f[2]), pack_half2(f[1], f[3]));
+                    fr[1] = make_uint2(pack_half2(f[4], f[6]), pack_half2(f[5], f[7]));
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if constexpr (S::kQRegs)
+                        qr[nb * (D / 16) + 2 * i + k] = fr[k];
+                    else
+                        qfrag[(nb * (D / 16) + 2 * i + k) * 32 + lane] = fr[k];
+                }
+            }
+            // factors and limits of the columns this lane has: rows 2t, 2t + 1
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = 2 * nb + i, rc = nb * 8 + 2 * t + i;
+                qc[c] = batch_pow2(24 - __shfl_sync(~0u, e, (2 * t + i) * 4)) * p.scale2;
+                // keys at and past the limit are not seen by the row
+                const int l = (w.r0 + rc) % (p.L * p.R) / p.R;
+                lim[c] = rc >= w.rows ? 0
+                         : is_shared  ? w.k1
+                                      : min(w.k1, min((int)p.key_cap, __ldg(p.lens + w.b0)) -
+                                                      (p.L - 1 - l));
+                if (rc < w.rows) lim_min = min(lim_min, lim[c]);
+            }
+        }
+        lim_min = __reduce_min_sync(~0u, lim_min);
+        __syncwarp();
+
+        // --------------------------------------------------------- the keys
         float m2[2 * NB], l[2 * NB], bt[2 * NB][G], O[D / 16][NB][4];
         int ev = 127;
 #pragma unroll
@@ -272,21 +280,12 @@ __global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchP
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
                 O[i][nb][0] = O[i][nb][1] = O[i][nb][2] = O[i][nb][3] = 0.f;
-
-        int ids = page_of(first);
-#pragma unroll
-        for (int s = 0; s < S::kStages - 1; ++s) {
-            const int tile = first + s * S::kWarps;
-            const int nxt = page_of(tile + S::kWarps);
-            if (tile < tile1) load(tile, s, ids);
-            cp_async_commit();
-            ids = nxt;
-        }
         int stage = 0;
-        for (int tile = first; tile < tile1; tile += S::kWarps) {
+#pragma unroll 1
+        for (int tile = tile0; tile < tile1; ++tile) {
             {
-                const int ahead = tile + (S::kStages - 1) * S::kWarps;
-                const int nxt = page_of(ahead + S::kWarps);
+                const int ahead = tile + S::kStages - 1;
+                const int nxt = page_of(ahead + 1);
                 const int into = stage == 0 ? S::kStages - 1 : stage - 1;
                 if (ahead < tile1) load(ahead, into, ids);
                 cp_async_commit();
@@ -351,8 +350,8 @@ __global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchP
                                                        Rb[2 * k + 1]};
 #pragma unroll
                                 for (int nb = 0; nb < NB; ++nb) {
-                                    const uint2 bq =
-                                        qfrag[(nb * (D / 16) + g * S::kSteps + step) * 32 + lane];
+                                    const int at = nb * (D / 16) + g * S::kSteps + step;
+                                    const uint2 bq = S::kQRegs ? qr[at] : qfrag[at * 32 + lane];
                                     own_mma(acc[nb], a, bq.x, bq.y);
                                 }
                             }
@@ -542,66 +541,36 @@ __global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchP
         }
         cp_async_wait<0>();
 
-        // ---------------------------------------- the warps' results together
+        // ------------------------------------------------------ partial out
+        const int evf = ev == 127 ? 0 : ev;
+        const float fa = batch_pow2(-evf), fb = BITS == 4 ? batch_pow2(-4 - evf) : fa;
 #pragma unroll
-        for (int c = 0; c < 2 * NB; ++c)
+        for (int c = 0; c < 2 * NB; ++c) {
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) {
                 l[c] += __shfl_xor_sync(~0u, l[c], o);
 #pragma unroll
                 for (int g = 0; g < G; ++g) bt[c][g] += __shfl_xor_sync(~0u, bt[c][g], o);
             }
-        __syncthreads();  // every warp is done with its ring
-        float *wm = reinterpret_cast<float *>(ring);   // [warps][rows]
-        float *wl = wm + S::kWarps * ROWS;
-        float *wo = wl + S::kWarps * ROWS;             // [warps][rows][D]
-        const int evf = ev == 127 ? 0 : ev;            // a warp without keys holds zeros
-        const float fa = batch_pow2(-evf), fb = BITS == 4 ? batch_pow2(-4 - evf) : fa;
-#pragma unroll
-        for (int c = 0; c < 2 * NB; ++c) {
             const int r = (c >> 1) * 8 + 2 * t + (c & 1);
             if (r >= w.rows) continue;
-            if (gid == 0) {
-                wm[warp * ROWS + r] = m2[c];
-                wl[warp * ROWS + r] = l[c];
-            }
-            float *o = wo + (warp * ROWS + r) * D;
+            const int64_t at = part_row(p, w, r);
+            if (gid == 0) p.part_ml[at] = make_float2(m2[c], l[c]);
+            float *o = p.part_o + at * D;
+            // M-tile m of a group: values 2m, 2m + 1 of the lane's GROUP / 8
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
-                for (int m = 0; m < S::kSteps; ++m) {
-                    const int u = g * S::kSteps + m;
-                    const int d = g * GROUP + gid * (GROUP / 8) + 2 * m;
-                    *reinterpret_cast<float2 *>(o + d) =
-                        make_float2(fmaf(O[u][c >> 1][c & 1], fa, bt[c][g]),
-                                    fmaf(O[u][c >> 1][2 + (c & 1)], fb, bt[c][g]));
+                for (int m = 0; m < S::kSteps; m += 2) {
+                    const int x = g * S::kSteps + m, nb = c >> 1, i = c & 1;
+                    *reinterpret_cast<float4 *>(o + g * GROUP + gid * (GROUP / 8) + 2 * m) =
+                        make_float4(fmaf(O[x][nb][i], fa, bt[c][g]),
+                                    fmaf(O[x][nb][2 + i], fb, bt[c][g]),
+                                    fmaf(O[x + 1][nb][i], fa, bt[c][g]),
+                                    fmaf(O[x + 1][nb][2 + i], fb, bt[c][g]));
                 }
         }
-        __syncthreads();
-        for (int x = threadIdx.x; x < w.rows * (D / 4); x += S::kThreads) {
-            const int r = x / (D / 4), d4 = x - r * (D / 4);
-            float M = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < S::kWarps; ++k) M = fmaxf(M, wm[k * ROWS + r]);
-            // a warp that saw nothing adds 0 of 0; one that saw only NaN has
-            // no maximum either, but its sum is NaN and stays so
-            const float ref = M == -INFINITY ? 0.f : M;
-            float L = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < S::kWarps; ++k) {
-                const float g = batch_ex2(wm[k * ROWS + r] - ref);
-                L = fmaf(wl[k * ROWS + r], g, L);
-                const float4 o = reinterpret_cast<const float4 *>(wo + (k * ROWS + r) * D)[d4];
-                acc.x = fmaf(o.x, g, acc.x);
-                acc.y = fmaf(o.y, g, acc.y);
-                acc.z = fmaf(o.z, g, acc.z);
-                acc.w = fmaf(o.w, g, acc.w);
-            }
-            const int64_t at = part_row(p, w, r);
-            reinterpret_cast<float4 *>(p.part_o + at * D)[d4] = acc;
-            if (d4 == 0) p.part_ml[at] = make_float2(M, L);
-        }
+        __syncwarp();
     }
     if (outside) atomicOr(p.err, ERR_BATCH_TABLE);
 }

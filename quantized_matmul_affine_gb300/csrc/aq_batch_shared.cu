@@ -40,7 +40,6 @@ template <int BITS, int D, int GROUP>
 struct Shd {
     static constexpr int kThreads = 17 * 32;
     static constexpr int kKeys = D <= 128 ? 128 : 64;      // keys a tile
-    static constexpr int kBlocks = D / 64;                 // 64-value blocks of a row
     static constexpr int kTileBytes = kKeys * D * 2;       // k or v tile
     static constexpr int kQBytes = 128 * D * 2;            // q' of one row tile
     static constexpr int kG = D / GROUP;
@@ -81,6 +80,23 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t *v) {
                  :
                  : "memory");
     asm volatile("" : "+r"(v[30]), "+r"(v[31])::"memory");
+}
+
+// Eight columns: a load that waits, and a store.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+        : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -175,7 +191,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
     uint64_t *k_full = reinterpret_cast<uint64_t *>(qsc + S::kRT * 128);
     uint64_t *k_empty = k_full + 2, *v_full = k_empty + 2, *v_empty = v_full + 2;
     uint64_t *s_full = v_empty + 2, *p_ready = s_full + 2, *o_done = p_ready + 2;
-    uint64_t *drain = o_done + 1;
+    uint64_t *q_ready = o_done + 1, *drain = q_ready + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     int *flag_s = reinterpret_cast<int *>(tmem_holder + 1);
     volatile int *flag = flag_s;
@@ -193,6 +209,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
             mbar_init(&p_ready[i], 4);
         }
         mbar_init(o_done, 1);
+        mbar_init(q_ready, 4 * row_tiles);
         mbar_init(drain, 1);
         *flag_s = 0;
         fence_mbar_init();
@@ -209,212 +226,200 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
     grid_dependency_wait();
     const PlanView v = batch_plan(p, plan_mem, tmp);
     const int n_items = v.shared_items * p.c.KV;
-    const int tile_rows = 128 * row_tiles;
-    // Running counts: tiles of keys, steps (row tiles x tiles of keys), pieces.
-    // A step's scores and P have the barriers of its parity, a k or v tile
-    // those of its slot.  MMAs complete in issue order, so that scores of step
-    // i are behind the product of step i - 2.  No barrier is ever two phases
-    // ahead of a waiter: a slot's next phase needs what the waiter does next.
+    __syncthreads();
+    // Each role walks the pieces by itself, with running counts of pieces,
+    // tiles of keys and steps (row tiles x tiles of keys).  A step's scores
+    // and P have the barriers of its parity, a k or v tile those of its slot.
+    // MMAs complete in issue order, so that scores of step i are behind the
+    // product of step i - 2.  No barrier is ever two phases ahead of a waiter:
+    // a slot's next phase needs what the waiter does next.
     uint32_t kt = 0, step = 0, piece = 0;
     bool issued = false;
 
-    for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-        const Piece w = shared_piece(p, v, item, tile_rows);
-        const int tiles = (w.k1 - w.k0 + KT - 1) / KT;
-        const int steps = tiles * row_tiles;
-        // ------------------------------------------------- q', by warps 0-15
-        if (warp < 16) {
-            constexpr int LPR = D / 8;           // lanes a row, 8 values each
-            constexpr int RPW = 32 / LPR;        // rows a warp at a time
-            const int c = lane % LPR;
-            for (int r = warp * RPW + lane / LPR; r < tile_rows; r += 16 * RPW) {
-                uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-                if (r < w.rows) raw = *reinterpret_cast<const uint4 *>(q_row(p, w, r) + 8 * c);
-                const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-                float f[8], mx = 0.f;
+    if (warp < 8) {
+        // ----------------------------------------------------------- softmax
+        const int wg = warp >> 2;
+        bool ok = wg < row_tiles;
+        for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x, ++piece) {
+            const Piece w = shared_piece(p, v, item);
+            const int tiles = (w.k1 - w.k0 + KT - 1) / KT;
+            // q' of this row tile.  The last piece's MMAs are done (o_done), and
+            // its O has been read: the MMAs of this piece wait for q_ready.
+            {
+                constexpr int LPR = D / 8;           // lanes a row, 8 values each
+                constexpr int RPW = 32 / LPR;        // rows a warp at a time
+                const int c = lane % LPR;
+#pragma unroll 2
+                for (int r = (warp & 3) * RPW + lane / LPR; r < 128; r += 4 * RPW) {
+                    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                    if (wg * 128 + r < w.rows)
+                        raw = *reinterpret_cast<const uint4 *>(q_row(p, w, wg * 128 + r) + 8 * c);
+                    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+                    float f[8], mx = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    f[i] = q_float(p, (uint16_t)(u[i / 2] >> (16 * (i & 1))));
-                    mx = fmaxf(mx, fabsf(f[i]));
+                    for (int i = 0; i < 8; ++i) {
+                        f[i] = q_float(p, (uint16_t)(u[i / 2] >> (16 * (i & 1))));
+                        mx = fmaxf(mx, fabsf(f[i]));
+                    }
+#pragma unroll
+                    for (int o = LPR / 2; o >= 1; o >>= 1)
+                        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+                    const int e = batch_exp(mx);
+                    // a negative scale goes into q', so that the largest score
+                    // is the largest of the products
+                    const float sc = p.scale2 < 0.f ? -batch_pow2(e) : batch_pow2(e);
+                    uint32_t h[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int a = BITS == 4 ? i : 2 * i, b = BITS == 4 ? i + 4 : 2 * i + 1;
+                        h[i] = pack_half2(f[a] * sc, f[b] * sc);
+                    }
+                    *reinterpret_cast<uint4 *>(qs + wg * S::kQBytes + operand_at(128, r, c)) =
+                        make_uint4(h[0], h[1], h[2], h[3]);
+                    if (c == 0) qsc[wg * 128 + r] = batch_pow2(-e) * fabsf(p.scale2);
                 }
-#pragma unroll
-                for (int o = LPR / 2; o >= 1; o >>= 1)
-                    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-                const int e = batch_exp(mx);
-                // a negative scale goes into q', so that the largest score is
-                // the largest of the products
-                const float sc = p.scale2 < 0.f ? -batch_pow2(e) : batch_pow2(e);
-                uint32_t h[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int a = BITS == 4 ? i : 2 * i, b = BITS == 4 ? i + 4 : 2 * i + 1;
-                    h[i] = pack_half2(f[a] * sc, f[b] * sc);
-                }
-                *reinterpret_cast<uint4 *>(qs + (r >> 7) * S::kQBytes +
-                                           operand_at(128, r & 127, c)) =
-                    make_uint4(h[0], h[1], h[2], h[3]);
-                if (c == 0) qsc[r] = batch_pow2(-e) * fabsf(p.scale2);
-            }
-            fence_proxy_async_smem();
-        }
-        __syncthreads();
-
-        if (warp < 8) {
-            // ------------------------------------------------------- softmax
-            const int wg = warp >> 2;
-            if (wg < row_tiles) {
-                const int r = wg * 128 + (warp & 3) * 32 + lane;
-                const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-                const uint32_t o_at = tmem + lanes + S::kTmemO + wg * D;
-                const float c = qsc[r];
-                float m = -INFINITY;            // reference of this row's weights
-                float2 sum = make_float2(0.f, 0.f);
-                bool ok = true;
-                for (int j = 0; j < tiles; ++j) {
-                    const uint32_t st = step + (row_tiles == 2 ? 2 * j + wg : j);
-                    const uint32_t slot = st & 1, s_at = tmem + lanes + slot * KT;
-                    ok = shd_wait(&s_full[slot], (st >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
-                    if (!__all_sync(~0u, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const int valid = w.k1 - w.k0 - j * KT;   // keys of the tile that count
-                    // scores in chunks of 32 keys, the next one in flight while one
-                    // is worked on: once for the maximum, once for P
-                    uint32_t xa[32], xb[32];
-                    auto mask = [&](uint32_t (&x)[32], int chunk) {
-                        if (32 * chunk + 32 > valid) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (32 * chunk + i >= valid) x[i] = 0xff800000u;  // -inf
-                        }
-                    };
-                    float mx = -INFINITY;
-                    auto largest = [&](uint32_t (&x)[32], int chunk) {
-                        mask(x, chunk);
-                        float a = mx, b = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            a = fmaxf(a, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
-                            b = fmaxf(b, fmaxf(__uint_as_float(x[i + 2]),
-                                               __uint_as_float(x[i + 3])));
-                        }
-                        mx = fmaxf(a, b);
-                    };
-                    tmem_ld32(s_at, xa);
-#pragma unroll
-                    for (int k = 0; k < KT / 32; k += 2) {
-                        tmem_wait_ld32(xa);
-                        tmem_ld32(s_at + 32 * (k + 1), xb);
-                        largest(xa, k);
-                        tmem_wait_ld32(xb);
-                        tmem_ld32(s_at + 32 * ((k + 2) % (KT / 32)), xa);  // at the end: chunk 0 again
-                        largest(xb, k + 1);
-                    }
-                    mx *= c;
-                    // the reference moves when a weight could pass 2^8
-                    float f = 1.f;
-                    if (mx > m + 8.f || (m == -INFINITY && mx > m)) {
-                        f = m == -INFINITY ? 0.f : batch_ex2(m - mx);
-                        m = mx;
-                    }
-                    tmem_wait_ld32(xa);
-                    if (j > 0 && __any_sync(~0u, f != 1.f)) {
-                        // O of the tiles so far, once their products are done
-                        // (with two row tiles these scores follow the last one)
-                        const uint32_t n = kt + j - 1;
-                        if (row_tiles == 1)
-                            ok = shd_wait(&v_empty[n & 1], (n >> 1) & 1, flag, p.err,
-                                          ERR_BATCH_BASE);
-                        if (!__all_sync(~0u, ok)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int k = 0; k < D; k += 32) {
-                            tmem_ld32(o_at + k, xb);
-                            tmem_wait_ld32(xb);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                xb[i] = __float_as_uint(__uint_as_float(xb[i]) * f);
-                            tmem_st32(o_at + k, xb);
-                        }
-                        sum.x *= f;
-                        sum.y *= f;
-                    }
-                    const float ref = m == -INFINITY ? 0.f : m;
-                    const float2 c2 = make_float2(c, c), m2 = make_float2(-ref, -ref);
-                    // P of chunk k takes 16 columns at 16 k: over scores that have
-                    // been read (chunk k + 1, in flight, starts at 32 k + 32)
-                    auto weigh = [&](uint32_t (&x)[32], int chunk) {
-                        mask(x, chunk);
-                        uint32_t h[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float2 t = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]),
-                                                              __uint_as_float(x[2 * i + 1])),
-                                                  c2, m2);
-                            t.x = batch_ex2(t.x);
-                            t.y = batch_ex2(t.y);
-                            sum = __fadd2_rn(sum, t);
-                            h[i] = pack_half2(t.x, t.y);
-                        }
-                        tmem_st16(s_at + 16 * chunk, h);
-                    };
-#pragma unroll
-                    for (int k = 0; k < KT / 32; k += 2) {
-                        if (k > 0) tmem_wait_ld32(xa);
-                        tmem_ld32(s_at + 32 * (k + 1), xb);
-                        weigh(xa, k);
-                        tmem_wait_ld32(xb);
-                        if (k + 2 < KT / 32) tmem_ld32(s_at + 32 * (k + 2), xa);
-                        weigh(xb, k + 1);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_ready[slot]);
-                }
-                // ------------------------------------------------- partial out
-                if (ok) ok = shd_wait(o_done, piece & 1, flag, p.err, ERR_BATCH_BASE);
-                if (__all_sync(~0u, ok)) {
-                    tc_fence_after();
-                    const bool mine = r < w.rows;
-                    const int64_t at = mine ? part_row(p, w, r) : 0;
-                    if (mine) p.part_ml[at] = make_float2(m, sum.x + sum.y);
-                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * D);
-#pragma unroll 1
-                    for (int k = 0; k < D; k += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(o_at + k, o);
-                        tmem_wait_ld32(o);
-                        if (!mine) continue;
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const uint32_t *u = o + 8 * g;
-                            float4 a, b;
-                            if constexpr (BITS == 4) {
-                                a = make_float4(__uint_as_float(u[0]), __uint_as_float(u[2]),
-                                                __uint_as_float(u[4]), __uint_as_float(u[6]));
-                                b = make_float4(__uint_as_float(u[1]), __uint_as_float(u[3]),
-                                                __uint_as_float(u[5]), __uint_as_float(u[7]));
-                            } else {
-                                a = make_float4(__uint_as_float(u[0]), __uint_as_float(u[1]),
-                                                __uint_as_float(u[2]), __uint_as_float(u[3]));
-                                b = make_float4(__uint_as_float(u[4]), __uint_as_float(u[5]),
-                                                __uint_as_float(u[6]), __uint_as_float(u[7]));
-                            }
-                            dst[k / 4 + 2 * g] = a;
-                            dst[k / 4 + 2 * g + 1] = b;
-                        }
-                    }
-                }
+                fence_proxy_async_smem();
                 tc_fence_before();
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");  // qsc of the row tile
+                if (lane == 0) mbar_arrive(q_ready);
             }
-        } else if (warp < 16) {
-            // ---------------------------------------------------- dequantise
+            const int r = wg * 128 + (warp & 3) * 32 + lane;
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t o_at = tmem + lanes + S::kTmemO + wg * D;
+            const float c = qsc[r];
+            float m = -INFINITY;            // reference of this row's weights
+            float2 sum = make_float2(0.f, 0.f);
+            for (int j = 0; j < tiles; ++j) {
+                const uint32_t st = step + (row_tiles == 2 ? 2 * j + wg : j);
+                const uint32_t slot = st & 1, s_at = tmem + lanes + slot * KT;
+                ok = shd_wait(&s_full[slot], (st >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const int valid = w.k1 - w.k0 - j * KT;   // keys of the tile that count
+                // scores 32 at a time, in loops that stay short: the roles' code
+                // shares the instruction caches
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int k = 0; k < KT; k += 32) {
+                    uint32_t x[32];
+                    tmem_ld32(s_at + k, x);
+                    tmem_wait_ld32(x);
+                    if (k + 32 > valid) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (k + i >= valid) x[i] = 0xff800000u;  // -inf
+                    }
+                    float a = mx, b = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        a = fmaxf(a, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+                        b = fmaxf(b, fmaxf(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])));
+                    }
+                    mx = fmaxf(a, b);
+                }
+                mx *= c;
+                // the reference moves when a weight could pass 2^8
+                float f = 1.f;
+                if (mx > m + 8.f || (m == -INFINITY && mx > m)) {
+                    f = m == -INFINITY ? 0.f : batch_ex2(m - mx);
+                    m = mx;
+                }
+                if (j > 0 && __any_sync(~0u, f != 1.f)) {
+                    // O of the tiles so far, once their products are done
+                    // (with two row tiles these scores follow the last one)
+                    const uint32_t n = kt + j - 1;
+                    if (row_tiles == 1)
+                        ok = shd_wait(&v_empty[n & 1], (n >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < D; k += 8) {
+                        uint32_t o[8];
+                        tmem_ld8(o_at + k, o);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st8(o_at + k, o);
+                    }
+                    sum.x *= f;
+                    sum.y *= f;
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+                const float2 c2 = make_float2(c, c), m2 = make_float2(-ref, -ref);
+                // P of scores k .. k + 31 takes 16 columns at k / 2, over scores that
+                // have been read
+#pragma unroll 1
+                for (int k = 0; k < KT; k += 32) {
+                    uint32_t x[32], h[16];
+                    tmem_ld32(s_at + k, x);
+                    tmem_wait_ld32(x);
+                    if (k + 32 > valid) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (k + i >= valid) x[i] = 0xff800000u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float2 t = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]),
+                                                          __uint_as_float(x[2 * i + 1])),
+                                              c2, m2);
+                        t.x = batch_ex2(t.x);
+                        t.y = batch_ex2(t.y);
+                        sum = __fadd2_rn(sum, t);
+                        h[i] = pack_half2(t.x, t.y);
+                    }
+                    tmem_st16(s_at + k / 2, h);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[slot]);
+            }
+            // ----------------------------------------------------- partial out
+            if (ok) ok = shd_wait(o_done, piece & 1, flag, p.err, ERR_BATCH_BASE);
+            ok = __all_sync(~0u, ok);
+            if (ok) {
+                tc_fence_after();
+                const bool mine = r < w.rows;
+                const int64_t at = mine ? part_row(p, w, r) : 0;
+                if (mine) p.part_ml[at] = make_float2(m, sum.x + sum.y);
+                float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * D);
+#pragma unroll 1
+                for (int k = 0; k < D; k += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o_at + k, o);
+                    tmem_wait_ld32(o);
+                    if (!mine) continue;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const uint32_t *u = o + 8 * g;
+                        float4 a, b;
+                        if constexpr (BITS == 4) {
+                            a = make_float4(__uint_as_float(u[0]), __uint_as_float(u[2]),
+                                            __uint_as_float(u[4]), __uint_as_float(u[6]));
+                            b = make_float4(__uint_as_float(u[1]), __uint_as_float(u[3]),
+                                            __uint_as_float(u[5]), __uint_as_float(u[7]));
+                        } else {
+                            a = make_float4(__uint_as_float(u[0]), __uint_as_float(u[1]),
+                                            __uint_as_float(u[2]), __uint_as_float(u[3]));
+                            b = make_float4(__uint_as_float(u[4]), __uint_as_float(u[5]),
+                                            __uint_as_float(u[6]), __uint_as_float(u[7]));
+                        }
+                        dst[k / 4 + 2 * g] = a;
+                        dst[k / 4 + 2 * g + 1] = b;
+                    }
+                }
+            }
+            kt += tiles;
+            step += tiles * row_tiles;
+        }
+    } else if (warp < 16) {
+        // -------------------------------------------------------- dequantise
+        for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+            const Piece w = shared_piece(p, v, item);
+            const int tiles = (w.k1 - w.k0 + KT - 1) / KT;
             // A warp takes KT / 8 consecutive keys (within one page) of every
             // tile: 16 bytes of codes a lane, kLpr lanes a row, so that a
             // load covers 512 bytes in a row.
@@ -507,25 +512,34 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                 rec2 = place(j + 2);
                 bool ok = lap == 0 || shd_wait(row_tiles == 1 ? &s_full[s] : &k_empty[s],
                                                (lap - 1) & 1, flag, p.err, ERR_BATCH_BASE);
-                if (!__all_sync(~0u, ok)) break;
+                if (!__all_sync(~0u, ok)) goto wound_down;
                 store(a, ks + s * S::kTileBytes);
                 if (lane == 0) mbar_arrive(&k_full[s]);
                 prefetch(rec2, j + 2);
                 fetch(a, rec1, j + 1, 0);
                 ok = lap == 0 || shd_wait(&v_empty[s], (lap - 1) & 1, flag, p.err, ERR_BATCH_BASE);
-                if (!__all_sync(~0u, ok)) break;
+                if (!__all_sync(~0u, ok)) goto wound_down;
                 store(b, vs + s * S::kTileBytes);
                 if (lane == 0) mbar_arrive(&v_full[s]);
                 rec = rec1;
                 rec1 = rec2;
             }
-        } else {
-            // ----------------------------------------------------------- MMA
-            // One thread waits and issues.  A step's value product and the
-            // scores two steps on go out together, then the commits: each
-            // wait and commit costs 100 cycles or more in which a queue of
-            // eight MMAs (64 cycles each) would run dry.
-            if (elect_lane()) {
+            kt += tiles;
+        }
+    } else {
+        // --------------------------------------------------------------- MMA
+        // One thread waits and issues.  A step's value product and the
+        // scores two steps on go out together, then the commits: each wait
+        // and commit costs 100 cycles or more in which a queue of eight MMAs
+        // (64 cycles each) would run dry.
+        if (warp == 16 && elect_lane()) {
+            bool ok = true;
+            for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x, ++piece) {
+                const Piece w = shared_piece(p, v, item);
+                const int tiles = (w.k1 - w.k0 + KT - 1) / KT;
+                const int steps = tiles * row_tiles;
+                ok = shd_wait(q_ready, piece & 1, flag, p.err, ERR_BATCH_BASE);
+                if (!ok) break;
                 const uint32_t id_s =
                     (1u << 4) | ((uint32_t)(KT >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
                 const uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
@@ -543,7 +557,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     const uint32_t d = tmem + ((step + i) & 1) * KT;
                     const uint64_t qd = qd0 + (uint64_t)((row_of(i) * S::kQBytes) >> 4);
                     const uint64_t kd = kd0 + (uint64_t)((s * S::kTileBytes) >> 4);
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < D / 16; ++k)
                         tc_mma_f16(d, qd + (uint64_t)(((k >> 2) * 16384 + (k & 3) * 32) >> 4),
                                    kd + (uint64_t)(((k >> 2) * (KT * 128) + (k & 3) * 32) >> 4),
@@ -554,7 +568,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     const uint32_t d = tmem + S::kTmemO + row_of(i) * D;
                     const uint32_t a = tmem + ((step + i) & 1) * KT;
                     const uint64_t vd = vd0 + (uint64_t)((s * S::kTileBytes) >> 4);
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < KT / 16; ++k)
                         tc_mma_f16_ta(d, a + k * 8, vd + (uint64_t)((k * 2048) >> 4), id_o,
                                       tile_of(i) != 0 || k != 0);
@@ -564,7 +578,6 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     // with one row tile the scores are also the k tile's last use
                     if (row_tiles == 2 && (i & 1)) tc_commit(&k_empty[(kt + tile_of(i)) & 1]);
                 };
-                bool ok = true;
                 for (int i = 0; i < 2 && i < steps && ok; ++i) {
                     ok = wait_k(i);
                     if (!ok) break;
@@ -587,24 +600,18 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     }
                     if (row_of(i) == row_tiles - 1) tc_commit(&v_empty[s]);
                 }
-                if (issued) tc_commit(o_done);
+                tc_commit(o_done);
+                kt += tiles;
+                step += steps;
             }
-            __syncwarp();
-        }
-        kt += tiles;
-        step += steps;
-        ++piece;
-        __syncthreads();  // the piece is done: q', O and the rings' ends
-        tc_fence_after();
-        if (*flag) break;
-    }
-    // every MMA that was issued has completed before tensor memory is freed
-    if (warp == 16) {
-        if (issued) {  // the issuing lane
-            tc_commit(drain);
-            if (!mbar_wait(drain, 0)) atomicOr(p.err, ERR_BATCH_BASE);
         }
         __syncwarp();
+    }
+wound_down:
+    // every MMA that was issued has completed before tensor memory is freed
+    if (issued) {  // the issuing thread
+        tc_commit(drain);
+        if (!mbar_wait(drain, 0)) atomicOr(p.err, ERR_BATCH_BASE);
     }
     __syncthreads();
     if (warp == 16) tmem_dealloc(tmem, 512);
@@ -615,7 +622,7 @@ cudaError_t shared_run(const BatchParams &p, int row_tiles, int grid, cudaStream
     using S = Shd<BITS, D, GROUP>;
     auto kern = shared_kernel<BITS, D, GROUP>;
     constexpr size_t body = 1024 + (size_t)S::kRT * S::kQBytes + 4 * (size_t)S::kTileBytes +
-                            S::kRT * 512 + 16 * 8 + 33 * 8 + 64;
+                            S::kRT * 512 + 18 * 8 + 33 * 8 + 64;
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [&] {
