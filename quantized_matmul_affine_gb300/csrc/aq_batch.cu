@@ -9,6 +9,245 @@ __device__ uint32_t g_batch_error;
 
 namespace {
 
+// Sum over the CTA, and over the threads before this one, of two counts in
+// one 64-bit value (neither half overflows: see kMostTiles); tmp: 32 values.
+struct Scan {
+    uint64_t before, all;
+};
+__device__ __noinline__ Scan block_scan(uint64_t v, uint64_t *tmp) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    uint64_t upto = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t x = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) tmp[warp] = upto;
+    __syncthreads();
+    uint64_t t = lane < nw ? tmp[lane] : 0;
+    uint64_t skip = lane < warp ? t : 0;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        t += __shfl_xor_sync(~0u, t, o);
+        skip += __shfl_xor_sync(~0u, skip, o);
+    }
+    __syncthreads();  // tmp may be written again
+    return {skip + upto - v, t};
+}
+
+// More tiles than a pool of pages could hold: lens that say so are not real.
+constexpr uint64_t kMostTiles = 1u << 30;
+
+// The tables of aq_batch.cuh, by one CTA.  A thread a sequence; a few scans
+// over the batch, whose latency is what the kernel costs (3 us for a batch of
+// 64).
+__global__ void plan_kernel(const __grid_constant__ BatchParams p) {
+    extern __shared__ PlanGroup s_g[];                       // [G]
+    int *s_n = reinterpret_cast<int *>(s_g + p.G);           // [G] rows that share
+    int *s_grp = s_n + p.G;                                  // [B] the row's group, or -1
+    int *s_at = s_grp + p.B;                                 // [B] its tiles, then those before it
+    __shared__ uint64_t tmp[32];
+    const int nt = blockDim.x, cap = (int)p.key_cap, LR = p.L * p.R, KV = p.c.KV;
+    launch_dependents();
+    grid_dependency_wait();
+
+    // groups: who shares.  Rows that are long enough for all their tokens to
+    // see all shared keys do; the first of them lends its table entries.
+    if (p.G > 0) {
+        int disorder = 0;
+#pragma unroll 1
+        for (int g = threadIdx.x; g < p.G; g += nt) {
+            const int b0 = p.gstart[g], b1 = p.gstart[g + 1];
+            disorder |= b0 < 0 || b1 < b0 || b1 > p.B;
+            s_g[g].first = b0;
+            s_g[g].rows = b1 - b0;
+            s_g[g].len = min(cap, max(0, p.shared[g]));
+            s_g[g].lead = p.B;
+            s_n[g] = 0;
+        }
+        // groups that do not ascend within the batch share nothing
+        if (__syncthreads_or(disorder)) {
+#pragma unroll 1
+            for (int g = threadIdx.x; g < p.G; g += nt) s_g[g].first = s_g[g].rows = s_g[g].len = 0;
+            if (threadIdx.x == 0) atomicOr(p.err, ERR_BATCH_TABLE);
+        }
+        __syncthreads();
+    }
+    auto group_of = [&](int b, int len) {
+        if (p.G == 0) return -1;
+        int lo = 0, hi = p.G;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_g[mid].first <= b)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const PlanGroup &g = s_g[lo];
+        return b >= g.first && b < g.first + g.rows && g.len > 0 && len - (p.L - 1) >= g.len ? lo
+                                                                                             : -1;
+    };
+#pragma unroll 1
+    for (int b = threadIdx.x; b < p.B; b += nt) {
+        const int g = group_of(b, min(cap, p.lens[b]));
+        s_grp[b] = g;
+        if (g >= 0) {
+            atomicMin(&s_g[g].lead, b);
+            atomicAdd(&s_n[g], 1);
+        }
+    }
+    if (p.G > 0) {
+        __syncthreads();
+        // a group of one shares with nobody
+#pragma unroll 1
+        for (int g = threadIdx.x; g < p.G; g += nt)
+            if (s_n[g] < 2) s_g[g].len = 0;
+        __syncthreads();
+    }
+    const int own_rt = ceil_div(LR, p.own_rows);
+    auto row_of = [&](int b) {
+        PlanRow r;
+        const int len = min(cap, p.lens[b]);
+        r.group = s_grp[b];
+        r.k0 = r.group >= 0 ? s_g[r.group].len : 0;
+        if (r.k0 == 0) r.group = -1;
+        r.k1 = max(len, r.k0);
+        r.tiles = r.k1 > r.k0 ? ceil_div(r.k1, p.unit_keys) - r.k0 / p.unit_keys : 0;
+        return r;
+    };
+    auto group_rt = [&](const PlanGroup &g) {
+        return ceil_div(g.rows * LR, p.shared_tc ? p.shared_rows : p.own_rows);
+    };
+    uint64_t n = 0;
+#pragma unroll 1
+    for (int b = threadIdx.x; b < p.B; b += nt) n += s_at[b] = row_of(b).tiles;
+    uint64_t units = block_scan(n, tmp).all * own_rt * KV;
+    int chunk = p.shared_unit;
+    if (p.G > 0 && p.shared_tc) {
+        n = 0;
+#pragma unroll 1
+        for (int g = threadIdx.x; g < p.G; g += nt)
+            n += (uint64_t)s_g[g].len * group_rt(s_g[g]) * KV;
+        uint64_t want = block_scan(n, tmp).all / p.shared_target;
+        // one item more than the device holds at once would cost a whole
+        // round: chunks grow until all fit (each group has at least one)
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            want = (want + p.shared_unit - 1) / p.shared_unit * p.shared_unit;
+            chunk = (int)min((uint64_t)(1 << 29), max(want, (uint64_t)(chunk + (k ? p.shared_unit : 0))));
+            n = 0;
+#pragma unroll 1
+            for (int g = threadIdx.x; g < p.G; g += nt)
+                n += (uint64_t)ceil_div(s_g[g].len, chunk) * group_rt(s_g[g]) * KV;
+            n = block_scan(n, tmp).all;
+            if (n <= (uint64_t)p.shared_target || chunk >= cap) break;
+            want = chunk * n / p.shared_target;
+        }
+    } else if (p.G > 0) {
+        n = 0;
+#pragma unroll 1
+        for (int g = threadIdx.x; g < p.G; g += nt)
+            n += (uint64_t)ceil_div(s_g[g].len, p.unit_keys) * group_rt(s_g[g]) * KV;
+        units += block_scan(n, tmp).all;
+    }
+    const bool real = units <= kMostTiles;
+    if (!real && threadIdx.x == 0) atomicOr(p.err, ERR_BATCH_TABLE);
+    if (!real) units = 0;
+    int per = max(p.own_min, (int)((units + p.own_warps - 1) / p.own_warps));
+    // slots that a segment of so many tiles may need: the runs it can touch
+    auto seg_slots = [&](int tiles) { return tiles > 0 ? (unsigned)(tiles - 1) / (unsigned)per + 2u : 0u; };
+    auto group_slots = [&](const PlanGroup &g) -> uint64_t {
+        return (uint64_t)g.rows *
+               (p.shared_tc ? ceil_div(g.len, chunk) : seg_slots(ceil_div(g.len, p.unit_keys)));
+    };
+    // pieces grow until their slots fit the workspace
+#pragma unroll 1
+    for (;;) {
+        n = 0;
+#pragma unroll 1
+        for (int b = threadIdx.x; b < p.B; b += nt) n += seg_slots(s_at[b]);
+#pragma unroll 1
+        for (int g = threadIdx.x; g < p.G; g += nt) n += group_slots(s_g[g]);
+        if (block_scan(n, tmp).all <= (uint64_t)p.slots || (per >= cap && chunk >= cap)) break;
+        if (per < cap) per *= 2;
+        if (chunk < cap) chunk *= 2;
+    }
+    // groups first, then the rows: tiles (or items) and slots before each
+    uint64_t at = 0;
+    int items = 0;
+#pragma unroll 1
+    for (int g0 = 0; g0 < p.G; g0 += nt) {
+        const int g = g0 + threadIdx.x;
+        uint64_t v = 0;
+        int pieces = 0;
+        if (g < p.G) {
+            pieces = real ? ceil_div(s_g[g].len, p.shared_tc ? chunk : p.unit_keys) : 0;
+            v = (uint64_t)(pieces * group_rt(s_g[g]) * (p.shared_tc ? 1 : KV)) << 32 |
+                (real ? group_slots(s_g[g]) : 0);
+        }
+        const Scan sc = block_scan(v, tmp);
+        if (g < p.G) {
+            PlanGroup x = s_g[g];
+            x.at = (int)((at + sc.before) >> 32);
+            x.slot = (int)(uint32_t)(at + sc.before);
+            x.pieces = pieces;
+            p.groups[g] = x;
+            s_g[g] = x;
+        }
+        at += sc.all;
+    }
+    if (p.shared_tc) {
+        items = (int)(at >> 32);
+        at = (uint32_t)at;  // the rows' tiles start at 0
+    }
+    const int group_tiles = (int)(at >> 32);
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.B; b0 += nt) {
+        const int b = b0 + threadIdx.x;
+        PlanRow r;
+        uint64_t v = 0;
+        if (b < p.B) {
+            r = row_of(b);
+            if (!real) r.tiles = 0;
+            v = (uint64_t)(r.tiles * own_rt * KV) << 32 | seg_slots(r.tiles);
+        }
+        const Scan sc = block_scan(v, tmp);
+        if (b < p.B) {
+            r.at = (int)((at + sc.before) >> 32);
+            r.slot = (int)(uint32_t)(at + sc.before);
+            p.rows[b] = r;
+            s_at[b] = r.at;
+        }
+        at += sc.all;
+    }
+    const int tiles = (int)(at >> 32);
+    if (threadIdx.x == 0) {
+        PlanHead h = {};
+        h.per = per;
+        h.tiles = tiles;
+        h.group_tiles = group_tiles;
+        h.shared_items = items;
+        h.shared_chunk = chunk;
+        *p.head = h;
+    }
+    __syncthreads();
+    // where each run starts: the last group or row with `at` <= its first tile
+#pragma unroll 1
+    for (int w = threadIdx.x; w < p.own_warps && (int64_t)w * per < tiles; w += nt) {
+        const int u = w * per;
+        const bool in_groups = u < group_tiles;
+        int lo = 0, hi = in_groups ? p.G : p.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if ((in_groups ? s_g[mid].at : s_at[mid]) <= u)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        p.runs[w] = in_groups ? -1 - lo : lo;
+    }
+}
+
 // A row's output (sequence, token, head): its slots in plan order - the
 // shared pieces, then its own - weighted by 2^(max - largest max), 4 (D + 2)
 // bytes each.  WPR warps a row: one where there are rows for every warp of the
@@ -33,20 +272,26 @@ __global__ void __launch_bounds__(WPR == 1 ? 128 : 32 * WPR)
     const int b = (int)(row / LH);
     const int lh = (int)(row - b * LH), l = lh / p.H, h = lh - l * p.H;
     const int kv = h / p.R, lr = l * p.R + (h - kv * p.R), LR = p.L * p.R;
-    const int64_t per = *reinterpret_cast<const int64_t *>(p.desc);
-    const int32_t *d = p.desc + 2 + kDesc * (int64_t)b;
+    const int per = p.head->per;
+    const PlanRow d = p.rows[b];
     // pieces of a segment of `tiles` tiles from tile u0 on
-    auto pieces = [&](int64_t u0, int tiles) {
-        return tiles > 0 ? (int)((u0 + tiles - 1) / per - u0 / per) + 1 : 0;
+    auto pieces = [&](int u0, int tiles) {
+        return tiles > 0 ? (u0 + tiles - 1) / per - u0 / per + 1 : 0;
     };
-    const int own0 = d[0], tiles = d[1], sh0 = d[4], sh_step = d[5];
-    const int own_n = pieces(*reinterpret_cast<const int64_t *>(d + 2) +
-                                 (int64_t)(kv * ceil_div(LR, p.own_rows) + lr / p.own_rows) * tiles,
-                             tiles);
-    int sh_n = d[8];
-    if (d[9] > 0) {
-        const int rt = (d[10] * LR + lr) / p.own_rows;
-        sh_n = pieces(*reinterpret_cast<const int64_t *>(d + 6) + (int64_t)(kv * d[9] + rt) * d[8], d[8]);
+    const int own0 = d.slot;
+    const int own_n =
+        pieces(d.at + (kv * ceil_div(LR, p.own_rows) + lr / p.own_rows) * d.tiles, d.tiles);
+    int sh_n = 0, sh0 = 0, sh_step = 0;
+    if (d.group >= 0) {
+        const PlanGroup g = p.groups[d.group];
+        const int place = b - g.first;
+        sh0 = g.slot + place;
+        sh_step = g.rows;
+        sh_n = p.shared_tc
+                   ? g.pieces
+                   : pieces(g.at + (kv * ceil_div(g.rows * LR, p.own_rows) +
+                                    (place * LR + lr) / p.own_rows) * g.pieces,
+                            g.pieces);
     }
     const int n = sh_n + own_n;
     auto slot_row = [&](int i) -> int64_t {
@@ -118,6 +363,21 @@ __global__ void __launch_bounds__(WPR == 1 ? 128 : 32 * WPR)
     }
 }
 
+cudaError_t plan_run(const BatchParams &p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, 1, 1);
+    // a thread a sequence; runs' starts want some more
+    cfg.blockDim = dim3((unsigned)std::min(1024, std::max(256, (p.B + 31) / 32 * 32)), 1, 1);
+    cfg.dynamicSmemBytes = 8 * (size_t)p.B + (sizeof(PlanGroup) + 4) * (size_t)p.G;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, plan_kernel, p);
+}
+
 template <int D>
 cudaError_t join_run(const BatchParams &p, cudaStream_t stream) {
     const int64_t rows = (int64_t)p.B * p.L * p.H;
@@ -142,7 +402,7 @@ struct BatchPlan {
     int shared_rows, shared_target;
     // the workspace: the slots' (max, sum), the slots' outputs, the rows' slots
     int64_t slots;
-    size_t off_o, off_desc, bytes;
+    size_t off_o, off_plan, bytes;
 };
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
@@ -162,8 +422,6 @@ BatchPlan plan_for(const aq_cache *c, int64_t B, int64_t L, int64_t H, int64_t G
     pl.nb = c->D < 512 && (L * R > 8 || (G > 0 && !pl.row_tiles)) ? 2 : 1;
     pl.own_rows = 8 * pl.nb;
     BatchRun r = {};
-    r.prm.B = (int)B;
-    r.prm.G = (int)G;
     r.nb = pl.nb;
     r.resident = &pl.own_ctas;
     r.unit_keys = &pl.unit_keys;
@@ -184,8 +442,9 @@ BatchPlan plan_for(const aq_cache *c, int64_t B, int64_t L, int64_t H, int64_t G
     pl.slots = 5 * B + T + (G > 0 ? std::min(B, per_tile * G) * Ts : 0);
     const size_t each = (size_t)(pl.slots * L * H);
     pl.off_o = up256(each * sizeof(float2));
-    pl.off_desc = pl.off_o + up256(each * (size_t)c->D * sizeof(float));
-    pl.bytes = pl.off_desc + up256(desc_bytes(B));
+    pl.off_plan = pl.off_o + up256(each * (size_t)c->D * sizeof(float));
+    pl.bytes = pl.off_plan + sizeof(PlanHead) + (size_t)B * sizeof(PlanRow) +
+               (size_t)G * sizeof(PlanGroup) + 16 * (size_t)pl.own_ctas;
     return pl;
 }
 
@@ -224,7 +483,10 @@ cudaError_t batch_launch(const aq_cache *c, int64_t layer, const BatchArgs &a) {
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     p.part_ml = reinterpret_cast<float2 *>(ws);
     p.part_o = reinterpret_cast<float *>(ws + pl.off_o);
-    p.desc = reinterpret_cast<int32_t *>(ws + pl.off_desc);
+    p.head = reinterpret_cast<PlanHead *>(ws + pl.off_plan);
+    p.rows = reinterpret_cast<PlanRow *>(p.head + 1);
+    p.groups = reinterpret_cast<PlanGroup *>(p.rows + a.B);
+    p.runs = reinterpret_cast<int *>(p.groups + a.G);
     p.slots = pl.slots;
     p.key_cap = a.max_pages * c->page;
     p.own_rows = pl.own_rows;
@@ -245,6 +507,8 @@ cudaError_t batch_launch(const aq_cache *c, int64_t layer, const BatchArgs &a) {
     cudaError_t e = cudaGetSymbolAddress(&err, g_batch_error);
     if (e != cudaSuccess) return e;
     p.err = static_cast<uint32_t *>(err);
+    e = plan_run(p, a.stream);
+    if (e != cudaSuccess) return e;
     if (pl.row_tiles) {
         e = batch_shared(p, pl.row_tiles, num_sms(), a.stream);
         if (e != cudaSuccess) return e;

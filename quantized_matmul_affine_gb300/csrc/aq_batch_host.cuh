@@ -5,7 +5,6 @@
 #include "aq_batch_own.cuh"
 
 #include <algorithm>
-#include <atomic>
 #include <mutex>
 
 namespace aq {
@@ -22,29 +21,18 @@ template <int BITS, int D, int GROUP, int NB>
 cudaError_t own_run_nb(const BatchRun &r) {
     using S = Own<BITS, D, GROUP, NB>;
     auto kern = own_kernel<BITS, D, GROUP, NB>;
-    const size_t smem = S::kSmem + plan_bytes(r.prm.B, r.prm.G);
+    constexpr int smem = S::kSmem;
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
+    static int per_sm = 0;
     std::call_once(once, [&] {
-        attr = cudaFuncSetAttribute(
-            kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-            (int)(S::kSmem + plan_bytes(AQ_BATCH_MAX_ROWS, kBatchMaxGroups)));
+        attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (attr == cudaSuccess)
+            attr = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, S::kThreads, smem);
     });
     if (attr != cudaSuccess) return attr;
     if (r.resident) {
-        // the query takes microseconds: the last answer is kept (by size, so
-        // that what is kept is right for any caller)
-        static std::atomic<uint64_t> last{0};
-        uint64_t k = last.load(std::memory_order_relaxed);
-        if (k >> 16 != smem) {
-            int n = 0;
-            const cudaError_t e =
-                cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, S::kThreads, smem);
-            if (e != cudaSuccess) return e;
-            k = (uint64_t)smem << 16 | (uint64_t)n;
-            last.store(k, std::memory_order_relaxed);
-        }
-        *r.resident = (int)(k & 0xffff) * num_sms();
+        *r.resident = per_sm * num_sms();
         *r.unit_keys = S::kKeys;
         return cudaSuccess;
     }

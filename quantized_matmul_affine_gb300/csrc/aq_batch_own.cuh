@@ -103,7 +103,6 @@ __global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchP
     using S = Own<BITS, D, GROUP, NB>;
     constexpr int G = S::kG, BLK = S::kBlk;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long tmp[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, t = lane & 3;
     uint8_t *my = smem + warp * S::kWarpBytes;
@@ -112,18 +111,60 @@ __global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchP
 
     launch_dependents();
     grid_dependency_wait();
-    const PlanView v = batch_plan(p, reinterpret_cast<int *>(smem + S::kSmem), tmp);
-    if (blockIdx.x == 0) write_desc(p, v);
-
-    const int64_t me = (int64_t)blockIdx.x * S::kWarps + warp;
-    int64_t u = me * v.per;
-    const int64_t end = min(v.ubase[p.B], u + v.per);
+    const int me = (int)blockIdx.x * S::kWarps + warp;
+    const int per = p.head->per, LR = p.L * p.R;
+    // (long long: runs past the last tile are empty, wherever they start)
+    long long u64 = (long long)me * per;
+    const int end = (int)min((long long)p.head->tiles, u64 + per);
+    int u = (int)min(u64, (long long)end), at = u < end ? p.runs[me] : 0;
     uint32_t outside = 0;
 
     while (u < end) {
-        bool is_shared;
-        const Piece w = own_piece(p, v, u, end, me, &is_shared, &u);
-        const int tile0 = w.k0 / S::kKeys, tile1 = (w.k1 + S::kKeys - 1) / S::kKeys;
+        // the segment (one KV head and row tile of a group's or row's keys) of
+        // tile u, and this run's part of it
+        Piece w;
+        const bool is_shared = at < 0;
+        int base, tiles, rows, first, step;
+        if (is_shared) {
+            const PlanGroup g = p.groups[-1 - at];
+            base = g.at;
+            tiles = g.pieces;
+            rows = g.rows * LR;
+            step = g.rows;
+            w.row = g.lead;
+            w.b0 = g.first;
+            w.k0 = 0;
+            w.k1 = g.len;
+            w.slot0 = g.slot;
+        } else {
+            const PlanRow b = p.rows[at];
+            base = b.at;
+            tiles = b.tiles;
+            rows = LR;
+            step = 1;
+            w.row = w.b0 = at;
+            w.k0 = b.k0;
+            w.k1 = b.k1;
+            w.slot0 = b.slot;
+        }
+        const int rt = ceil_div(rows, S::kRows);
+        if (u - base >= tiles * p.c.KV * rt) {  // the next one (empty ones are passed over)
+            at = is_shared && at > -p.G ? at - 1 : is_shared ? 0 : at + 1;
+            continue;
+        }
+        const int seg = (u - base) / tiles, off = u - base - seg * tiles;
+        const int n = min(tiles - off, end - u);
+        first = w.k0 / S::kKeys + off;
+        w.kv = seg / rt;
+        w.r0 = (seg - w.kv * rt) * S::kRows;
+        w.rows = min(S::kRows, rows - w.r0);
+        // a slot (a sequence) for each run that touches the segment
+        w.slot0 += (me - (base + seg * tiles) / per) * step;
+        const int row_len = w.k1;
+        w.k0 = max(w.k0, first * S::kKeys);
+        w.k1 = min(w.k1, (first + n) * S::kKeys);
+        u += n;
+        const int tile0 = first, tile1 = first + n;
         const int32_t *trow = p.table + (int64_t)w.row * p.max_pages;
         // the page of each 16-key block of a tile, in lane = block
         auto page_of = [&](int tile) -> int {
@@ -257,8 +298,7 @@ __global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchP
                 const int l = (w.r0 + rc) % (p.L * p.R) / p.R;
                 lim[c] = rc >= w.rows ? 0
                          : is_shared  ? w.k1
-                                      : min(w.k1, min((int)p.key_cap, __ldg(p.lens + w.b0)) -
-                                                      (p.L - 1 - l));
+                                      : min(w.k1, row_len - (p.L - 1 - l));
                 if (rc < w.rows) lim_min = min(lim_min, lim[c]);
             }
         }

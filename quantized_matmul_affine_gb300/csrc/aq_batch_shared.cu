@@ -195,9 +195,6 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     int *flag_s = reinterpret_cast<int *>(tmem_holder + 1);
     volatile int *flag = flag_s;
-    long long *tmp = reinterpret_cast<long long *>(drain + 2);
-    int *plan_mem = reinterpret_cast<int *>(tmp + 33);
-
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -224,9 +221,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
     const uint32_t tmem = *tmem_holder;
     launch_dependents();
     grid_dependency_wait();
-    const PlanView v = batch_plan(p, plan_mem, tmp);
-    const int n_items = v.shared_items * p.c.KV;
-    __syncthreads();
+    const int n_items = p.head->shared_items * p.c.KV;
     // Each role walks the pieces by itself, with running counts of pieces,
     // tiles of keys and steps (row tiles x tiles of keys).  A step's scores
     // and P have the barriers of its parity, a k or v tile those of its slot.
@@ -241,7 +236,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
         const int wg = warp >> 2;
         bool ok = wg < row_tiles;
         for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x, ++piece) {
-            const Piece w = shared_piece(p, v, item);
+            const Piece w = shared_piece(p, item);
             const int tiles = (w.k1 - w.k0 + KT - 1) / KT;
             // q' of this row tile.  The last piece's MMAs are done (o_done), and
             // its O has been read: the MMAs of this piece wait for q_ready.
@@ -418,7 +413,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
     } else if (warp < 16) {
         // -------------------------------------------------------- dequantise
         for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-            const Piece w = shared_piece(p, v, item);
+            const Piece w = shared_piece(p, item);
             const int tiles = (w.k1 - w.k0 + KT - 1) / KT;
             // A warp takes KT / 8 consecutive keys (within one page) of every
             // tile: 16 bytes of codes a lane, kLpr lanes a row, so that a
@@ -535,7 +530,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
         if (warp == 16 && elect_lane()) {
             bool ok = true;
             for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x, ++piece) {
-                const Piece w = shared_piece(p, v, item);
+                const Piece w = shared_piece(p, item);
                 const int tiles = (w.k1 - w.k0 + KT - 1) / KT;
                 const int steps = tiles * row_tiles;
                 ok = shd_wait(q_ready, piece & 1, flag, p.err, ERR_BATCH_BASE);
@@ -622,20 +617,18 @@ cudaError_t shared_run(const BatchParams &p, int row_tiles, int grid, cudaStream
     using S = Shd<BITS, D, GROUP>;
     auto kern = shared_kernel<BITS, D, GROUP>;
     constexpr size_t body = 1024 + (size_t)S::kRT * S::kQBytes + 4 * (size_t)S::kTileBytes +
-                            S::kRT * 512 + 18 * 8 + 33 * 8 + 64;
+                            S::kRT * 512 + 18 * 8;
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [&] {
         attr = cudaFuncSetAttribute(
-            kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-            (int)std::min<size_t>(227 * 1024,
-                                  body + plan_bytes(AQ_BATCH_MAX_ROWS, kBatchMaxGroups)));
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)body);
     });
     if (attr != cudaSuccess) return attr;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3(S::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = body + plan_bytes(p.B, p.G);
+    cfg.dynamicSmemBytes = body;
     cfg.stream = stream;
     cudaLaunchAttribute a[1];
     a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
