@@ -466,7 +466,8 @@ aq_status aq_cache_compact(const aq_cache *cache, const int32_t *refs_dev,
  *   dtype        AQ_F16 or AQ_BF16: the type of q and o.
  *   q_dev        [B][L][H][D], a token's heads dense, tokens q_stride elements
  *                apart (a multiple of 8); 16-byte aligned.
- *   table_dev    int32 [B][max_pages].   lens_dev  int32 [B].
+ *   table_dev    int32 [B][max_pages], max_pages * page at most 2^24.
+ *   lens_dev     int32 [B].
  *   group_start_dev int32 [G + 1], ascending within 0..B; shared_dev int32
  *                [G].  G == 0: both NULL.
  *   out_dev      [B][L][H][D] dense.

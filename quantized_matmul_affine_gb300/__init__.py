@@ -13,6 +13,7 @@ this package fails if libaq.so cannot be loaded.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import List, Optional
 
@@ -385,20 +386,20 @@ class AqCache:
                  "_struct", "_ref")
 
     def __init__(self, pool: torch.Tensor, page: int, head_dim: int, bits: int, group_size: int):
-        if pool.dtype != torch.uint8 or pool.dim() != 4:
+        shape = pool.shape
+        if pool.dtype != torch.uint8 or len(shape) != 4:
             raise ValueError("pool must be uint8 [layers, n_pages, KV, record]")
-        layers, n_pages, kv, rec = pool.shape
         want = aq_cache_record_bytes(head_dim, page, bits, group_size)
         if want == 0:
             raise ValueError("head_dim 64/128/256/512, page 16/32/64/128, bits 4/8 and group_size "
                              "32/64/128 are served")
-        if rec != want:
-            raise ValueError(f"pool's records hold {rec} bytes; this geometry uses {want}")
+        if shape[3] != want:
+            raise ValueError(f"pool's records hold {shape[3]} bytes; this geometry uses {want}")
         self.pool, self.page, self.head_dim = pool, page, head_dim
         self.bits, self.group_size = bits, group_size
-        self.layers, self.n_pages, self.kv_heads = layers, n_pages, kv
-        self._struct = _CacheStruct(_dev(pool, "pool"), layers, n_pages, kv, head_dim, page, bits,
-                                    group_size)
+        self.layers, self.n_pages, self.kv_heads = shape[0], shape[1], shape[2]
+        self._struct = _CacheStruct(_dev(pool, "pool"), shape[0], shape[1], shape[2], head_dim, page,
+                                    bits, group_size)
         self._ref = ctypes.addressof(self._struct)
 
     @staticmethod
@@ -410,6 +411,7 @@ class AqCache:
         return AqCache(pool, page, head_dim, bits, group_size)
 
 
+@functools.lru_cache(maxsize=256)
 def aq_cache_record_bytes(D: int, page: int, bits: int, group_size: int) -> int:
     """Bytes of one page's record of one KV head (0: sizes not served)."""
     return int(load().aq_cache_record_bytes(D, page, bits, group_size))
@@ -422,9 +424,11 @@ def aq_cache_workspace_bytes(n_pages: int, B: int) -> int:
 
 def _ints(t: torch.Tensor, name: str, *shape) -> int:
     """The address of a dense int32 device tensor of this shape."""
-    if t.dtype != torch.int32 or tuple(t.shape) != shape:
+    if t.dtype != torch.int32 or t.shape != shape:
         raise ValueError(f"{name} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
-    return _dev(t, name)
+    if not t.is_cuda or not t.is_contiguous():
+        return _dev(t, name)  # says which
+    return t.data_ptr()
 
 
 def _table_shape(table: torch.Tensor) -> tuple:
@@ -498,11 +502,14 @@ def _tables(cache, refs, table, lens, in_place, out, with_lens=True):
     ins = (_ints(refs, "refs", cache.n_pages), _ints(table, "table", B, width),
            _ints(lens, "lens", B))
     given = (refs, table, lens) if with_lens else (refs, table)
-    if out is None:
-        out = given if in_place else tuple(torch.empty_like(t) for t in given)
-    ptrs = tuple(_ints(o, f"out[{i}]", *t.shape) for i, (o, t) in enumerate(zip(out, given)))
     status = torch.empty(4, dtype=torch.int32, device=refs.device)
-    return B, width, ins, ptrs, tuple(out), status
+    if out is None and in_place:
+        return B, width, ins, ins[:len(given)], given, status
+    if out is None:
+        out = [torch.empty_like(t) for t in given]
+        return B, width, ins, [o.data_ptr() for o in out], out, status
+    ptrs = [_ints(o, f"out[{i}]", *t.shape) for i, (o, t) in enumerate(zip(out, given))]
+    return B, width, ins, ptrs, out, status
 
 
 def _cache_workspace(cache, B, workspace, stream):
@@ -557,9 +564,18 @@ def aq_cache_compact(cache, refs, table, lens, in_place=True, out=None, workspac
     return (*res, status)
 
 
+@functools.lru_cache(maxsize=1024)
+def _batch_workspace(device: int, n_pages: int, KV: int, D: int, page: int, bits: int, group_size: int,
+                     B: int, L: int, H: int, G: int) -> int:
+    # a function of sizes and of the device's SMs only; the pool is not read
+    c = _CacheStruct(256, 1, n_pages, KV, D, page, bits, group_size)
+    return int(load().aq_attention_batch_workspace_bytes(ctypes.addressof(c), B, L, H, G))
+
+
 def aq_attention_batch_workspace_bytes(cache: AqCache, B: int, L: int, H: int, G: int = 0) -> int:
     """Workspace bytes of aq_attention_batch (0: sizes that it refuses)."""
-    return int(load().aq_attention_batch_workspace_bytes(cache._ref, B, L, H, G))
+    return _batch_workspace(cache.pool.get_device(), cache.n_pages, cache.kv_heads, cache.head_dim,
+                            cache.page, cache.bits, cache.group_size, B, L, H, G)
 
 
 def aq_attention_batch(q, cache: AqCache, layer: int, table, lens, scale: float, group_start=None,
@@ -597,13 +613,12 @@ def aq_attention_batch(q, cache: AqCache, layer: int, table, lens, scale: float,
     if out is None:
         out = torch.empty((B, L, H, D), dtype=q.dtype, device=q.device)
     _check_out(out, "out", B * L * H * D, q.dtype)
-    lib = load()
     if workspace is None:
-        n = lib.aq_attention_batch_workspace_bytes(cache._ref, B, L, H, G)
+        n = aq_attention_batch_workspace_bytes(cache, B, L, H, G)
         workspace = _scratch(max(n, 256), q.device, stream)
     if workspace.dtype != torch.uint8:
         raise ValueError("workspace must be a contiguous uint8 tensor")
-    _check(lib.aq_attention_batch(cache._ref, layer, AQ_BF16 if q.dtype == torch.bfloat16 else AQ_F16,
+    _check(load().aq_attention_batch(cache._ref, layer, AQ_BF16 if q.dtype == torch.bfloat16 else AQ_F16,
                                   q.data_ptr(), stride, _ints(table, "table", B, width),
                                   _ints(lens, "lens", B), gs, sh, B, L, H, G, width, scale,
                                   _dev(out, "out"), _dev(workspace, "workspace"),

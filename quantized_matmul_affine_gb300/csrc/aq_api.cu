@@ -599,7 +599,7 @@ aq_status aq_attention_batch(const aq_cache *cache, int64_t layer, int dtype, co
     if (st == AQ_OK) st = check_batch(cache, B, L, H, G);
     if (st != AQ_OK) return st;
     if (layer < 0 || layer >= cache->layers || (dtype != AQ_F16 && dtype != AQ_BF16) ||
-        max_pages < 1 || max_pages > (1 << 29) / cache->page || !std::isfinite(scale) || !q_dev ||
+        max_pages < 1 || max_pages > (1 << 24) / cache->page || !std::isfinite(scale) || !q_dev ||
         !table_dev || !lens_dev || !out_dev || !workspace_dev ||
         (G > 0 && (!group_start_dev || !shared_dev)) || (B * L > 1 && q_stride < H * cache->D))
         return AQ_ERR_INVALID_ARG;

@@ -9,73 +9,52 @@ __device__ uint32_t g_batch_error;
 
 namespace {
 
-// Sum over the CTA, and over the threads before this one, of two counts in
-// one 64-bit value (neither half overflows: see kMostTiles); tmp: 32 values.
-struct Scan {
-    uint64_t before, all;
-};
-__device__ __noinline__ Scan block_scan(uint64_t v, uint64_t *tmp) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    uint64_t upto = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t x = __shfl_up_sync(~0u, upto, o);
-        if (lane >= o) upto += x;
-    }
-    if (lane == 31) tmp[warp] = upto;
-    __syncthreads();
-    uint64_t t = lane < nw ? tmp[lane] : 0;
-    uint64_t skip = lane < warp ? t : 0;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        t += __shfl_xor_sync(~0u, t, o);
-        skip += __shfl_xor_sync(~0u, skip, o);
-    }
-    __syncthreads();  // tmp may be written again
-    return {skip + upto - v, t};
-}
-
-// More tiles than a pool of pages could hold: lens that say so are not real.
+// More tiles than a call could have: lens that say so are not real.
 constexpr uint64_t kMostTiles = 1u << 30;
 
-// The tables of aq_batch.cuh, by one CTA.  A thread a sequence; a few scans
-// over the batch, whose latency is what the kernel costs (3 us for a batch of
-// 64).
-__global__ void plan_kernel(const __grid_constant__ BatchParams p) {
+constexpr int kPlanThreads = 256;
+
+// The tables of aq_batch.cuh, by one CTA.  What it costs is latency - of its
+// loads, barriers and, cold as it is in every call, its own instructions - so
+// sums are a warp reduction and a shared-memory add, and what concerns groups
+// every warp works out for itself.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ BatchParams p) {
     extern __shared__ PlanGroup s_g[];                       // [G]
     int *s_n = reinterpret_cast<int *>(s_g + p.G);           // [G] rows that share
     int *s_grp = s_n + p.G;                                  // [B] the row's group, or -1
     int *s_at = s_grp + p.B;                                 // [B] its tiles, then those before it
-    __shared__ uint64_t tmp[32];
-    const int nt = blockDim.x, cap = (int)p.key_cap, LR = p.L * p.R, KV = p.c.KV;
+    __shared__ unsigned s_total, s_warp[2][kPlanThreads / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cap = (int)p.key_cap, LR = p.L * p.R, KV = p.c.KV;
+    if (threadIdx.x == 0) s_total = 0;
     launch_dependents();
     grid_dependency_wait();
 
-    // groups: who shares.  Rows that are long enough for all their tokens to
-    // see all shared keys do; the first of them lends its table entries.
-    if (p.G > 0) {
-        int disorder = 0;
+    // Groups: rows that are long enough for all their tokens to see all
+    // shared keys share them; the first of them lends its table entries.
+    int disorder = 0;
 #pragma unroll 1
-        for (int g = threadIdx.x; g < p.G; g += nt) {
-            const int b0 = p.gstart[g], b1 = p.gstart[g + 1];
-            disorder |= b0 < 0 || b1 < b0 || b1 > p.B;
-            s_g[g].first = b0;
-            s_g[g].rows = b1 - b0;
-            s_g[g].len = min(cap, max(0, p.shared[g]));
-            s_g[g].lead = p.B;
-            s_n[g] = 0;
-        }
-        // groups that do not ascend within the batch share nothing
-        if (__syncthreads_or(disorder)) {
-#pragma unroll 1
-            for (int g = threadIdx.x; g < p.G; g += nt) s_g[g].first = s_g[g].rows = s_g[g].len = 0;
-            if (threadIdx.x == 0) atomicOr(p.err, ERR_BATCH_TABLE);
-        }
+    for (int g = threadIdx.x; g < p.G; g += kPlanThreads) {
+        const int b0 = p.gstart[g], b1 = p.gstart[g + 1];
+        disorder |= b0 < 0 || b1 < b0 || b1 > p.B;
+        s_g[g].first = b0;
+        s_g[g].rows = b1 - b0;
+        s_g[g].len = min(cap, max(0, p.shared[g]));
+        s_g[g].lead = p.B;
+        s_n[g] = 0;
+    }
+    disorder = __syncthreads_or(disorder);
+    if (disorder) {  // groups that do not ascend within the batch share nothing
+        for (int g = threadIdx.x; g < p.G; g += kPlanThreads)
+            s_g[g].first = s_g[g].rows = s_g[g].len = 0;
+        if (threadIdx.x == 0) atomicOr(p.err, ERR_BATCH_TABLE);
         __syncthreads();
     }
-    auto group_of = [&](int b, int len) {
-        if (p.G == 0) return -1;
+#pragma unroll 1
+    for (int b = threadIdx.x; b < p.B; b += kPlanThreads) {
+        const int len = min(cap, p.lens[b]);
         int lo = 0, hi = p.G;
+#pragma unroll 1
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (s_g[mid].first <= b)
@@ -83,169 +62,176 @@ __global__ void plan_kernel(const __grid_constant__ BatchParams p) {
             else
                 hi = mid;
         }
-        const PlanGroup &g = s_g[lo];
-        return b >= g.first && b < g.first + g.rows && g.len > 0 && len - (p.L - 1) >= g.len ? lo
-                                                                                             : -1;
-    };
-#pragma unroll 1
-    for (int b = threadIdx.x; b < p.B; b += nt) {
-        const int g = group_of(b, min(cap, p.lens[b]));
-        s_grp[b] = g;
-        if (g >= 0) {
+        int g = -1;
+        if (p.G > 0 && b >= s_g[lo].first && b < s_g[lo].first + s_g[lo].rows && s_g[lo].len > 0 &&
+            len - (p.L - 1) >= s_g[lo].len) {
+            g = lo;
             atomicMin(&s_g[g].lead, b);
             atomicAdd(&s_n[g], 1);
         }
+        s_grp[b] = g;
+        s_at[b] = len;
     }
-    if (p.G > 0) {
-        __syncthreads();
-        // a group of one shares with nobody
-#pragma unroll 1
-        for (int g = threadIdx.x; g < p.G; g += nt)
-            if (s_n[g] < 2) s_g[g].len = 0;
-        __syncthreads();
-    }
-    const int own_rt = ceil_div(LR, p.own_rows);
-    auto row_of = [&](int b) {
+    __syncthreads();
+    // rows: their own keys, and tiles of them
+    auto row_of = [&](int b, int len) {
         PlanRow r;
-        const int len = min(cap, p.lens[b]);
         r.group = s_grp[b];
+        if (r.group >= 0 && s_n[r.group] < 2) r.group = -1;  // a group of one shares with nobody
         r.k0 = r.group >= 0 ? s_g[r.group].len : 0;
-        if (r.k0 == 0) r.group = -1;
         r.k1 = max(len, r.k0);
         r.tiles = r.k1 > r.k0 ? ceil_div(r.k1, p.unit_keys) - r.k0 / p.unit_keys : 0;
         return r;
     };
-    auto group_rt = [&](const PlanGroup &g) {
-        return ceil_div(g.rows * LR, p.shared_tc ? p.shared_rows : p.own_rows);
-    };
-    uint64_t n = 0;
+    unsigned n = 0;
 #pragma unroll 1
-    for (int b = threadIdx.x; b < p.B; b += nt) n += s_at[b] = row_of(b).tiles;
-    uint64_t units = block_scan(n, tmp).all * own_rt * KV;
+    for (int b = threadIdx.x; b < p.B; b += kPlanThreads) n += row_of(b, s_at[b]).tiles;
+    n = __reduce_add_sync(~0u, n);
+    if (lane == 0) atomicAdd(&s_total, n);
+    __syncthreads();
+    const int own_rt = ceil_div(LR, p.own_rows);
+    uint64_t units = (uint64_t)s_total * (unsigned)(own_rt * KV);
+
+    // groups: (len x row tiles) summed over them, in units of `each` keys
+    const int row_tile = p.shared_tc ? p.shared_rows : p.own_rows;
+    auto group_len = [&](int g) { return s_n[g] < 2 ? 0 : s_g[g].len; };
+    auto group_units = [&](int each) {
+        float sum = 0.f;  // (24 bits are plenty for a choice of size)
+#pragma unroll 1
+        for (int g = lane; g < p.G; g += 32)
+            sum += (float)ceil_div(group_len(g), each) * (float)(ceil_div(s_g[g].rows * LR, row_tile) * KV);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        return sum;
+    };
     int chunk = p.shared_unit;
     if (p.G > 0 && p.shared_tc) {
-        n = 0;
-#pragma unroll 1
-        for (int g = threadIdx.x; g < p.G; g += nt)
-            n += (uint64_t)s_g[g].len * group_rt(s_g[g]) * KV;
-        uint64_t want = block_scan(n, tmp).all / p.shared_target;
-        // one item more than the device holds at once would cost a whole
-        // round: chunks grow until all fit (each group has at least one)
+        // Chunks such that all items run at once: one more than the device
+        // holds would cost a whole round (each group has at least one).
+        float want = group_units(1) / (float)p.shared_target;
 #pragma unroll 1
         for (int k = 0; k < 8; ++k) {
-            want = (want + p.shared_unit - 1) / p.shared_unit * p.shared_unit;
-            chunk = (int)min((uint64_t)(1 << 29), max(want, (uint64_t)(chunk + (k ? p.shared_unit : 0))));
-            n = 0;
-#pragma unroll 1
-            for (int g = threadIdx.x; g < p.G; g += nt)
-                n += (uint64_t)ceil_div(s_g[g].len, chunk) * group_rt(s_g[g]) * KV;
-            n = block_scan(n, tmp).all;
-            if (n <= (uint64_t)p.shared_target || chunk >= cap) break;
-            want = chunk * n / p.shared_target;
+            chunk = max(chunk + (k ? p.shared_unit : 0),
+                        ceil_div((int)fminf(want, 1e9f), p.shared_unit) * p.shared_unit);
+            const float items = group_units(chunk);
+            if (items <= (float)p.shared_target || chunk >= cap) break;
+            want = (float)chunk * items / (float)p.shared_target;
         }
-    } else if (p.G > 0) {
-        n = 0;
-#pragma unroll 1
-        for (int g = threadIdx.x; g < p.G; g += nt)
-            n += (uint64_t)ceil_div(s_g[g].len, p.unit_keys) * group_rt(s_g[g]) * KV;
-        units += block_scan(n, tmp).all;
     }
-    const bool real = units <= kMostTiles;
-    if (!real && threadIdx.x == 0) atomicOr(p.err, ERR_BATCH_TABLE);
-    if (!real) units = 0;
-    int per = max(p.own_min, (int)((units + p.own_warps - 1) / p.own_warps));
+    bool real = units <= kMostTiles;
+    if (p.G > 0 && !p.shared_tc) {
+        real = real && group_units(p.unit_keys) <= (float)kMostTiles;
+        unsigned t = 0;
+#pragma unroll 1
+        for (int g = lane; g < p.G; g += 32)
+            t += ceil_div(group_len(g), p.unit_keys) * ceil_div(s_g[g].rows * LR, row_tile) * KV;
+        units += __reduce_add_sync(~0u, t);
+    }
+    const int per = max(p.own_min, real ? ceil_div((int)units, p.own_warps) : 1);
     // slots that a segment of so many tiles may need: the runs it can touch
-    auto seg_slots = [&](int tiles) { return tiles > 0 ? (unsigned)(tiles - 1) / (unsigned)per + 2u : 0u; };
-    auto group_slots = [&](const PlanGroup &g) -> uint64_t {
-        return (uint64_t)g.rows *
-               (p.shared_tc ? ceil_div(g.len, chunk) : seg_slots(ceil_div(g.len, p.unit_keys)));
+    auto seg_slots = [&](int tiles) {
+        return tiles > 0 ? (unsigned)(tiles - 1) / (unsigned)per + 2u : 0u;
     };
-    // pieces grow until their slots fit the workspace
+    // groups first: tiles (or items) and slots before each, by every warp
+    unsigned tiles_at = 0, slots_at = 0;
 #pragma unroll 1
-    for (;;) {
-        n = 0;
-#pragma unroll 1
-        for (int b = threadIdx.x; b < p.B; b += nt) n += seg_slots(s_at[b]);
-#pragma unroll 1
-        for (int g = threadIdx.x; g < p.G; g += nt) n += group_slots(s_g[g]);
-        if (block_scan(n, tmp).all <= (uint64_t)p.slots || (per >= cap && chunk >= cap)) break;
-        if (per < cap) per *= 2;
-        if (chunk < cap) chunk *= 2;
-    }
-    // groups first, then the rows: tiles (or items) and slots before each
-    uint64_t at = 0;
-    int items = 0;
-#pragma unroll 1
-    for (int g0 = 0; g0 < p.G; g0 += nt) {
-        const int g = g0 + threadIdx.x;
-        uint64_t v = 0;
-        int pieces = 0;
+    for (int g0 = 0; g0 < p.G; g0 += 32) {
+        const int g = g0 + lane;
+        PlanGroup x = {};
+        unsigned t = 0, sl = 0;
         if (g < p.G) {
-            pieces = real ? ceil_div(s_g[g].len, p.shared_tc ? chunk : p.unit_keys) : 0;
-            v = (uint64_t)(pieces * group_rt(s_g[g]) * (p.shared_tc ? 1 : KV)) << 32 |
-                (real ? group_slots(s_g[g]) : 0);
+            x = s_g[g];
+            x.len = group_len(g);
+            x.pieces = ceil_div(x.len, p.shared_tc ? chunk : p.unit_keys);
+            t = x.pieces * ceil_div(x.rows * LR, row_tile) * (p.shared_tc ? 1 : KV);
+            sl = x.rows * (p.shared_tc ? x.pieces : seg_slots(x.pieces));
         }
-        const Scan sc = block_scan(v, tmp);
-        if (g < p.G) {
-            PlanGroup x = s_g[g];
-            x.at = (int)((at + sc.before) >> 32);
-            x.slot = (int)(uint32_t)(at + sc.before);
-            x.pieces = pieces;
-            p.groups[g] = x;
-            s_g[g] = x;
+        unsigned bt = t, bs = sl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned u = __shfl_up_sync(~0u, bt, o), w = __shfl_up_sync(~0u, bs, o);
+            if (lane >= o) bt += u, bs += w;
         }
-        at += sc.all;
+        x.at = (int)(tiles_at + bt - t);
+        x.slot = (int)(slots_at + bs - sl);
+        if (warp == 0 && g < p.G) p.groups[g] = x;
+        tiles_at += __shfl_sync(~0u, bt, 31);
+        slots_at += __shfl_sync(~0u, bs, 31);
     }
-    if (p.shared_tc) {
-        items = (int)(at >> 32);
-        at = (uint32_t)at;  // the rows' tiles start at 0
-    }
-    const int group_tiles = (int)(at >> 32);
+    const int items = p.shared_tc ? (int)tiles_at : 0, group_tiles = p.shared_tc ? 0 : (int)tiles_at;
+    tiles_at = group_tiles;
+    // then the rows
 #pragma unroll 1
-    for (int b0 = 0; b0 < p.B; b0 += nt) {
+    for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
         const int b = b0 + threadIdx.x;
-        PlanRow r;
-        uint64_t v = 0;
+        PlanRow r = {};
+        unsigned t = 0, sl = 0;
         if (b < p.B) {
-            r = row_of(b);
+            r = row_of(b, s_at[b]);
             if (!real) r.tiles = 0;
-            v = (uint64_t)(r.tiles * own_rt * KV) << 32 | seg_slots(r.tiles);
+            t = r.tiles * own_rt * KV;
+            sl = seg_slots(r.tiles);
         }
-        const Scan sc = block_scan(v, tmp);
+        unsigned bt = t, bs = sl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned u = __shfl_up_sync(~0u, bt, o), w = __shfl_up_sync(~0u, bs, o);
+            if (lane >= o) bt += u, bs += w;
+        }
+        if (lane == 31) {
+            s_warp[0][warp] = bt;
+            s_warp[1][warp] = bs;
+        }
+        __syncthreads();
+        unsigned at = tiles_at + bt - t, slot = slots_at + bs - sl;
+#pragma unroll 1
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            const unsigned x = s_warp[0][w], y = s_warp[1][w];
+            if (w < warp) at += x, slot += y;
+            tiles_at += x;
+            slots_at += y;
+        }
         if (b < p.B) {
-            r.at = (int)((at + sc.before) >> 32);
-            r.slot = (int)(uint32_t)(at + sc.before);
+            r.at = (int)at;
+            r.slot = (int)slot;
             p.rows[b] = r;
             s_at[b] = r.at;
         }
-        at += sc.all;
+        __syncthreads();
     }
-    const int tiles = (int)(at >> 32);
+    // the workspace's formula covers every plan; a plan past it does nothing
+    real = real && slots_at <= (uint64_t)p.slots;
+    if (!real && threadIdx.x == 0) atomicOr(p.err, ERR_BATCH_TABLE);
+    if (!real)
+        for (int b = threadIdx.x; b < p.B; b += kPlanThreads) {
+            p.rows[b].tiles = 0;
+            p.rows[b].group = -1;
+        }
+    const int tiles = real ? (int)tiles_at : 0;
     if (threadIdx.x == 0) {
         PlanHead h = {};
         h.per = per;
         h.tiles = tiles;
         h.group_tiles = group_tiles;
-        h.shared_items = items;
+        h.shared_items = real ? items : 0;
         h.shared_chunk = chunk;
         *p.head = h;
     }
-    __syncthreads();
-    // where each run starts: the last group or row with `at` <= its first tile
+    // where each run starts: a warp a group or row writes the runs that start in it
+    auto starts = [&](int at, int count, int name) {
 #pragma unroll 1
-    for (int w = threadIdx.x; w < p.own_warps && (int64_t)w * per < tiles; w += nt) {
-        const int u = w * per;
-        const bool in_groups = u < group_tiles;
-        int lo = 0, hi = in_groups ? p.G : p.B;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if ((in_groups ? s_g[mid].at : s_at[mid]) <= u)
-                lo = mid;
-            else
-                hi = mid;
+        for (int w = ceil_div(at, per) + lane; (int64_t)w * per < at + count; w += 32) p.runs[w] = name;
+    };
+    if (!real) return;
+    if (!p.shared_tc)
+#pragma unroll 1
+        for (int g = warp; g < p.G; g += kPlanThreads / 32) {
+            const int to = g + 1 < p.G ? p.groups[g + 1].at : group_tiles;
+            starts(p.groups[g].at, to - p.groups[g].at, -1 - g);
         }
-        p.runs[w] = in_groups ? -1 - lo : lo;
-    }
+#pragma unroll 1
+    for (int b = warp; b < p.B; b += kPlanThreads / 32)
+        starts(s_at[b], (b + 1 < p.B ? s_at[b + 1] : tiles) - s_at[b], b);
 }
 
 // A row's output (sequence, token, head): its slots in plan order - the
@@ -366,8 +352,7 @@ __global__ void __launch_bounds__(WPR == 1 ? 128 : 32 * WPR)
 cudaError_t plan_run(const BatchParams &p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, 1, 1);
-    // a thread a sequence; runs' starts want some more
-    cfg.blockDim = dim3((unsigned)std::min(1024, std::max(256, (p.B + 31) / 32 * 32)), 1, 1);
+    cfg.blockDim = dim3(kPlanThreads, 1, 1);
     cfg.dynamicSmemBytes = 8 * (size_t)p.B + (sizeof(PlanGroup) + 4) * (size_t)p.G;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
@@ -503,10 +488,8 @@ cudaError_t batch_launch(const aq_cache *c, int64_t layer, const BatchArgs &a) {
          (a.G > 0 && !pl.row_tiles ? a.B * LR / pl.own_rows + a.G : 0)) * c->KV * most;
     p.own_warps = 4 * (int)std::max<int64_t>(
                           1, std::min<int64_t>(pl.own_ctas, (tiles / p.own_min + 3) / 4));
-    void *err = nullptr;
-    cudaError_t e = cudaGetSymbolAddress(&err, g_batch_error);
+    cudaError_t e = device_symbol(g_batch_error, &p.err);
     if (e != cudaSuccess) return e;
-    p.err = static_cast<uint32_t *>(err);
     e = plan_run(p, a.stream);
     if (e != cudaSuccess) return e;
     if (pl.row_tiles) {

@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                 constexpr int LPR = D / 8;           // lanes a row, 8 values each
                 constexpr int RPW = 32 / LPR;        // rows a warp at a time
                 const int c = lane % LPR;
-#pragma unroll 2
+#pragma unroll 8  // eight loads under way
                 for (int r = (warp & 3) * RPW + lane / LPR; r < 128; r += 4 * RPW) {
                     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
                     if (wg * 128 + r < w.rows)

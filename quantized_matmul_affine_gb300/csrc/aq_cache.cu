@@ -35,12 +35,13 @@ struct RowParams {
     const int32_t *cu, *start, *table;
     int64_t T;
     int B;
+    int span;                 // lanes a token
     int64_t max_pages;
     uint32_t *err;
 };
 
 // The sequence b with cu[b] <= t < cu[b + 1] (cu ascends), or -1.
-__device__ __forceinline__ int find_row(const int32_t *cu, int B, int64_t t) {
+__device__ __forceinline__ int find_row(const int32_t *cu, int B, int t) {
     int lo = 0, hi = B;  // the answer, if any, is in [lo, hi)
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -55,7 +56,7 @@ __device__ __forceinline__ int find_row(const int32_t *cu, int B, int64_t t) {
 // The record of token t's page and KV head 0, its slot in the page; nullptr
 // where the token has no place (padding, or a table that names none: the
 // latter sets the error word).
-__device__ __forceinline__ uint8_t *token_record(const RowParams &p, int64_t t, int *slot) {
+__device__ __forceinline__ uint8_t *token_record(const RowParams &p, int t, int *slot) {
     const int b = find_row(p.cu, p.B, t);
     if (b < 0) return nullptr;
     const int64_t pos = (int64_t)p.start[b] + (t - p.cu[b]);
@@ -89,121 +90,150 @@ __device__ __forceinline__ void widen(const uint4 &u, float (&f)[8]) {
     }
 }
 
-// One lane takes 8 values (a 16-byte load) and the GROUP / 8 lanes of a
-// group reduce min and max by shuffles; the quantiser's rule is
-// aq_quantize_ex's (codes of the IEEE quotient, see aq_quant.cu, whose
-// reciprocal-and-check form of the quotient this uses too).
+constexpr int kRowThreads = 256;
+constexpr int kRowLoads = 4;  // 16-byte loads a lane has under way
+
+// One lane takes 8 values (a 16-byte load), `p.span` lanes (8, 16 or 32: the
+// most that divide a token's lanes) take a token and look up its page once;
+// the GROUP / 8 lanes of a group reduce min and max by shuffles.  The
+// quantiser's rule is aq_quantize_ex's (codes of the IEEE quotient, by the
+// reciprocal-and-check form of aq_quant.cu).  blockIdx.y: K or V.
 template <int BITS, bool BF16>
-__global__ void __launch_bounds__(256) append_kernel(const RowParams p) {
+__global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_constant__ RowParams p) {
     constexpr int kQmax = (1 << BITS) - 1;
-    const int which = blockIdx.y;  // 0: K, 1: V
-    const int per_token = p.c.KV * p.c.D / 8;
-    const int64_t total = p.T * per_token;
-    const int lanes = p.c.group / 8;
-    const uint16_t *in = static_cast<const uint16_t *>(p.in[which]);
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const bool live = i < total;
-    const int64_t t = live ? i / per_token : 0;
-    const int e = live ? (int)(i - t * per_token) : 0;
-    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (live) raw = *reinterpret_cast<const uint4 *>(in + t * p.in_stride[which] + 8 * (int64_t)e);
-    float f[8];
-    widen<BF16>(raw, f);
-    float lo = f[0], hi = f[0];
+    const int which = blockIdx.y;
+    const int per_token = p.c.KV * p.c.D / 8, lanes = p.c.group / 8;
+    const int at = (int)(threadIdx.x % p.span);
+    const int t = (int)(blockIdx.x * (kRowThreads / p.span) + threadIdx.x / p.span);
+    const bool live = t < p.T;
+    int slot = 0;
+    uint8_t *rec = live ? token_record(p, t, &slot) : nullptr;
+    const uint4 *in = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.in[which]) +
+                                                      (int64_t)t * p.in_stride[which]);
+    uint8_t *codes = rec + which * p.c.side_codes + slot * p.c.rb;
+    __half2 *pairs = reinterpret_cast<__half2 *>(rec + 2 * p.c.side_codes + which * p.c.side_sb) +
+                     slot * p.c.groups;
+    const int per_head = p.c.D / 8;
+    for (int e0 = 0; e0 < per_token; e0 += kRowLoads * p.span) {
+        uint4 raw[kRowLoads];
 #pragma unroll
-    for (int j = 1; j < 8; ++j) {
-        lo = fminf(lo, f[j]);
-        hi = fmaxf(hi, f[j]);
-    }
-    for (int o = 1; o < lanes; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
-    }
-    if (!live) return;
-    int slot;
-    uint8_t *rec = token_record(p, t, &slot);
-    if (!rec) return;
-    const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), (float)kQmax));
-    const __half b16 = __float2half_rn(lo);
-    const float s = __half2float(s16), b = __half2float(b16);
-    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
-    constexpr float kEdge = BITS == 4 ? 3.0517578125e-05f : 4.8828125e-04f;
-    const float r = __frcp_rn(s);
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float a = __fsub_rn(f[j], b);
-        float q = fminf(fmaxf(__fmul_rn(a, r), 0.f), (float)kQmax);
-        float m = __fadd_rn(q, kMagic);
-        if (fabsf(__fsub_rn(q, __fsub_rn(m, kMagic))) > 0.5f - kEdge) {  // near a tie
-            q = fminf(fmaxf(__fdiv_rn(a, s), 0.f), (float)kQmax);
-            m = __fadd_rn(q, kMagic);
+        for (int k = 0; k < kRowLoads; ++k) {
+            const int e = e0 + k * p.span + at;
+            raw[k] = rec && e < per_token ? in[e] : make_uint4(0u, 0u, 0u, 0u);
         }
-        const uint32_t code = s == 0.f ? 0u : (__float_as_uint(m) & (uint32_t)kQmax);
-        w[j * BITS / 32] |= code << (j * BITS % 32);
+#pragma unroll
+        for (int k = 0; k < kRowLoads; ++k) {
+            const int e = e0 + k * p.span + at;
+            if (e0 + k * p.span >= per_token) break;  // alike for all lanes
+            float f[8];
+            widen<BF16>(raw[k], f);
+            float lo = f[0], hi = f[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) {
+                lo = fminf(lo, f[j]);
+                hi = fmaxf(hi, f[j]);
+            }
+            for (int o = 1; o < lanes; o <<= 1) {
+                lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
+                hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
+            }
+            const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), (float)kQmax));
+            const __half b16 = __float2half_rn(lo);
+            const float s = __half2float(s16), b = __half2float(b16);
+            constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
+            // the product with the rounded reciprocal is within 1.5 * 2^-23
+            // relative of the IEEE quotient: this much of an integer and a half
+            constexpr float kEdge = BITS == 4 ? 3.0517578125e-05f : 4.8828125e-04f;
+            const float r = __frcp_rn(s);
+            uint32_t w[2] = {0u, 0u};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float a = __fsub_rn(f[j], b);
+                float q = fminf(fmaxf(__fmul_rn(a, r), 0.f), (float)kQmax);
+                float m = __fadd_rn(q, kMagic);
+                if (fabsf(__fsub_rn(q, __fsub_rn(m, kMagic))) > 0.5f - kEdge) {  // near a tie
+                    q = fminf(fmaxf(__fdiv_rn(a, s), 0.f), (float)kQmax);
+                    m = __fadd_rn(q, kMagic);
+                }
+                w[j * BITS / 32] |= (__float_as_uint(m) & (uint32_t)kQmax) << (j * BITS % 32);
+            }
+            if (s == 0.f) w[0] = w[1] = 0u;
+            if (!rec) continue;
+            const int kv = e / per_head, d8 = e - kv * per_head;
+            uint32_t *dst = reinterpret_cast<uint32_t *>(codes + kv * p.c.rec) + d8 * (BITS / 4);
+            if constexpr (BITS == 4)
+                *dst = w[0];
+            else
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+            if (d8 % lanes == 0)
+                reinterpret_cast<__half2 *>(reinterpret_cast<uint8_t *>(pairs) +
+                                            kv * p.c.rec)[d8 / lanes] = __halves2half2(s16, b16);
+        }
     }
-    const int kv = e / (p.c.D / 8), d8 = e - kv * (p.c.D / 8);
-    rec += kv * p.c.rec;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(rec + which * p.c.side_codes + slot * p.c.rb) +
-                    d8 * (BITS / 4);
-    if constexpr (BITS == 4)
-        *dst = w[0];
-    else
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-    if (d8 % lanes == 0)
-        reinterpret_cast<__half2 *>(rec + 2 * p.c.side_codes + which * p.c.side_sb)
-            [slot * p.c.groups + d8 / lanes] = __halves2half2(s16, b16);
 }
 
-// The reverse: one lane turns 8 codes into 8 values of the output type, each
-// scale * code + bias in one fp32 fma (the product is exact) and one rounding.
+// The reverse, shared out alike: one lane turns 8 codes into 8 values of the
+// output type, each scale * code + bias in one fp32 fma (the product is exact)
+// and one rounding.
 template <int BITS, bool BF16>
-__global__ void __launch_bounds__(256) read_kernel(const RowParams p) {
+__global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant__ RowParams p) {
     const int which = blockIdx.y;
     const int per_token = p.c.KV * p.c.D / 8;
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= p.T * per_token) return;
-    const int64_t t = i / per_token;
-    const int e = (int)(i - t * per_token);
-    uint32_t o[4] = {0u, 0u, 0u, 0u};
-    int slot;
+    const int at = (int)(threadIdx.x % p.span);
+    const int t = (int)(blockIdx.x * (kRowThreads / p.span) + threadIdx.x / p.span);
+    if (t >= p.T) return;
+    int slot = 0;
     const uint8_t *rec = token_record(p, t, &slot);
-    if (rec) {
-        const int kv = e / (p.c.D / 8), d8 = e - kv * (p.c.D / 8);
-        rec += kv * p.c.rec;
-        const uint32_t *src =
-            reinterpret_cast<const uint32_t *>(rec + which * p.c.side_codes + slot * p.c.rb) +
-            d8 * (BITS / 4);
-        uint32_t w[2];
-        if constexpr (BITS == 4) {
-            w[0] = *src;
-            w[1] = 0u;
-        } else {
-            const uint2 v = *reinterpret_cast<const uint2 *>(src);
-            w[0] = v.x;
-            w[1] = v.y;
-        }
-        const float2 sb = __half22float2(
-            reinterpret_cast<const __half2 *>(rec + 2 * p.c.side_codes + which * p.c.side_sb)
-                [slot * p.c.groups + d8 * 8 / p.c.group]);
+    const uint8_t *codes = rec + which * p.c.side_codes + slot * p.c.rb;
+    const uint8_t *pairs = rec + 2 * p.c.side_codes + which * p.c.side_sb + slot * p.c.groups * 4;
+    const int per_head = p.c.D / 8, lanes = p.c.group / 8;
+    uint4 *out = static_cast<uint4 *>(p.out[which]) + (int64_t)t * per_token;
+    for (int e0 = at; e0 < per_token; e0 += kRowLoads * p.span) {
+        uint32_t w[kRowLoads][2];
+        __half2 sb[kRowLoads];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float v[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int bit = (2 * j + h) * BITS;
-                const uint32_t code = (w[bit / 32] >> (bit % 32)) & ((1u << BITS) - 1u);
-                v[h] = fmaf((float)code, sb.x, sb.y);
-            }
-            if constexpr (BF16) {
-                const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]);
-                o[j] = *reinterpret_cast<const uint32_t *>(&x);
+        for (int k = 0; k < kRowLoads; ++k) {
+            const int e = e0 + k * p.span;
+            w[k][0] = w[k][1] = 0u;
+            sb[k] = __float2half2_rn(0.f);
+            if (!rec || e >= per_token) continue;
+            const int kv = e / per_head, d8 = e - kv * per_head;
+            const uint32_t *src =
+                reinterpret_cast<const uint32_t *>(codes + kv * p.c.rec) + d8 * (BITS / 4);
+            if constexpr (BITS == 4) {
+                w[k][0] = *src;
             } else {
-                o[j] = pack_half2(v[0], v[1]);
+                const uint2 v = *reinterpret_cast<const uint2 *>(src);
+                w[k][0] = v.x;
+                w[k][1] = v.y;
             }
+            sb[k] = reinterpret_cast<const __half2 *>(pairs + kv * p.c.rec)[d8 / lanes];
+        }
+#pragma unroll
+        for (int k = 0; k < kRowLoads; ++k) {
+            const int e = e0 + k * p.span;
+            if (e >= per_token) break;
+            const float2 f = __half22float2(sb[k]);
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float v[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int bit = (2 * j + h) * BITS;
+                    const uint32_t code = (w[k][bit / 32] >> (bit % 32)) & ((1u << BITS) - 1u);
+                    v[h] = fmaf((float)code, f.x, f.y);
+                }
+                if constexpr (BF16) {
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]);
+                    o[j] = *reinterpret_cast<const uint32_t *>(&x);
+                } else {
+                    o[j] = pack_half2(v[0], v[1]);
+                }
+            }
+            out[e] = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
-    static_cast<uint4 *>(p.out[which])[i] = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // ---------------------------------------------------------------------------
@@ -748,11 +778,9 @@ cudaError_t launch_pdl(void (*kern)(P), dim3 grid, int threads, size_t smem, cud
     return cudaLaunchKernelEx(&cfg, kern, prm);
 }
 
+// The error word of the current device, looked up once a device.
 cudaError_t error_word(uint32_t **err) {
-    void *a = nullptr;
-    const cudaError_t e = cudaGetSymbolAddress(&a, g_cache_error);
-    *err = static_cast<uint32_t *>(a);
-    return e;
+    return device_symbol(g_cache_error, err);
 }
 
 TableParams table_params(const CacheTables &t, const aq_cache *c) {
@@ -808,8 +836,11 @@ cudaError_t cache_append_launch(const aq_cache *c, int64_t layer, int dtype, con
     p.max_pages = max_pages;
     const cudaError_t e = error_word(&p.err);
     if (e != cudaSuccess) return e;
-    const int64_t lanes = T * (p.c.KV * p.c.D / 8);
-    const dim3 grid((unsigned)((lanes + 255) / 256), 2, 1);
+    const int per_token = p.c.KV * p.c.D / 8;
+    p.span = 32;
+    while (per_token % p.span != 0) p.span /= 2;
+    const int64_t tokens = kRowThreads / p.span;  // a CTA
+    const dim3 grid((unsigned)((T + tokens - 1) / tokens), 2, 1);
     void (*kern)(RowParams);
     const bool bf = dtype == AQ_BF16;
     if (k)
@@ -818,7 +849,7 @@ cudaError_t cache_append_launch(const aq_cache *c, int64_t layer, int dtype, con
     else
         kern = c->bits == 4 ? (bf ? read_kernel<4, true> : read_kernel<4, false>)
                             : (bf ? read_kernel<8, true> : read_kernel<8, false>);
-    kern<<<grid, 256, 0, stream>>>(p);
+    kern<<<grid, kRowThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -3,6 +3,8 @@
 
 #include "aq_internal.h"
 
+#include <atomic>
+
 namespace aq {
 
 // One page holds, for each KV head, a record of `rec` bytes: K codes, V
@@ -36,6 +38,27 @@ inline CacheGeom cache_geom(const aq_cache *c) {
     g.rec = 2 * ((int64_t)g.side_codes + g.side_sb);
     g.page_bytes = g.KV * g.rec;
     return g;
+}
+
+// The address of a device variable on the current device, looked up once a
+// device (a translation unit's one error word: the lookup takes longer than
+// a launch).
+static inline cudaError_t device_symbol(const uint32_t &symbol, uint32_t **address) {
+    static std::atomic<uint32_t *> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    uint32_t *a = known[dev].load(std::memory_order_relaxed);
+    if (!a) {
+        void *v = nullptr;
+        e = cudaGetSymbolAddress(&v, symbol);
+        if (e != cudaSuccess) return e;
+        a = static_cast<uint32_t *>(v);
+        known[dev].store(a, std::memory_order_relaxed);
+    }
+    *address = a;
+    return cudaSuccess;
 }
 
 }  // namespace aq
