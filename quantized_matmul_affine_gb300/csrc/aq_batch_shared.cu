@@ -7,17 +7,17 @@
 // by the tensor core and by what feeds it, since each key meets hundreds of
 // rows: 4 D flops a (row, key) against 2 D bits/8 bytes a key.
 //
-//   warps 0-7    softmax: a thread a row of its row tile (warps 0-3 the first
-//                tile, 4-7 the second).  Scores come from tensor memory in
-//                two halves, P goes back to tensor memory as fp16, over the
-//                scores, and is the A operand of the value product there.
-//   warps 8-15   dequantise: codes straight from global memory into
+//   warps 0-15   softmax: eight warps a row tile, two threads a row (half of a
+//                tile's keys each).  Scores come from tensor memory, P goes
+//                back there as fp16, over the scores, and is the A operand of
+//                the value product.
+//   warps 16-23  dequantise: codes straight from global memory into
 //                registers one step ahead, fp16 k and v into shared memory in
 //                the swizzled layout the tensor core reads (k as the K-major,
 //                v as the MN-major operand: one layout, rows of keys).  The
 //                values of a 4-bit word land in the order 0 4 1 5 2 6 3 7,
 //                which q' and the output follow, so that no code is moved.
-//   warp 16      issues the MMAs.
+//   warp 24      issues the MMAs.
 //
 // Scores of two steps are in flight (two row tiles of the same keys, or the
 // same row tile and two tiles of keys), so that the tensor core works on one
@@ -38,7 +38,7 @@ namespace {
 
 template <int BITS, int D, int GROUP>
 struct Shd {
-    static constexpr int kThreads = 17 * 32;
+    static constexpr int kThreads = 25 * 32;
     static constexpr int kKeys = D <= 128 ? 128 : 64;      // keys a tile
     static constexpr int kTileBytes = kKeys * D * 2;       // k or v tile
     static constexpr int kQBytes = 128 * D * 2;            // q' of one row tile
@@ -167,6 +167,11 @@ __device__ __forceinline__ bool elect_lane() {
     return on != 0;
 }
 
+// A barrier of the 256 threads of a row tile's softmax.
+__device__ __forceinline__ void row_tile_sync(int wg) {
+    asm volatile("bar.sync %0, 256;" ::"r"(1 + wg) : "memory");
+}
+
 // A bounded wait that records where it gave up.
 __device__ __forceinline__ bool shd_wait(uint64_t *bar, uint32_t parity, volatile int *flag,
                                          uint32_t *err, uint32_t code) {
@@ -188,7 +193,8 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
     uint8_t *ks = qs + S::kRT * S::kQBytes;              // [2] k tiles
     uint8_t *vs = ks + 2 * S::kTileBytes;                // [2] v tiles
     float *qsc = reinterpret_cast<float *>(vs + 2 * S::kTileBytes);  // [row tiles][128]
-    uint64_t *k_full = reinterpret_cast<uint64_t *>(qsc + S::kRT * 128);
+    float *xch = qsc + S::kRT * 128;                     // [2][row tiles][halves][128]
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(xch + 2 * S::kRT * 256);
     uint64_t *k_empty = k_full + 2, *v_full = k_empty + 2, *v_empty = v_full + 2;
     uint64_t *s_full = v_empty + 2, *p_ready = s_full + 2, *o_done = p_ready + 2;
     uint64_t *q_ready = o_done + 1, *drain = q_ready + 1;
@@ -203,15 +209,15 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
             mbar_init(&v_full[i], 8);
             mbar_init(&v_empty[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_ready[i], 4);
+            mbar_init(&p_ready[i], 8);
         }
         mbar_init(o_done, 1);
-        mbar_init(q_ready, 4 * row_tiles);
+        mbar_init(q_ready, 8 * row_tiles);
         mbar_init(drain, 1);
         *flag_s = 0;
         fence_mbar_init();
     }
-    if (warp == 16) {
+    if (warp == 24) {
         tmem_alloc(tmem_holder, 512);
         tmem_relinquish();
         tc_fence_before();
@@ -231,9 +237,13 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
     uint32_t kt = 0, step = 0, piece = 0;
     bool issued = false;
 
-    if (warp < 8) {
+    if (warp < 16) {
         // ----------------------------------------------------------- softmax
-        const int wg = warp >> 2;
+        // Two warpgroups a row tile, each half of the keys of a tile: a step's
+        // scores wait for nothing longer than this, so it is the latency that
+        // counts.
+        const int wg = warp >> 3, half = (warp >> 2) & 1;
+        constexpr int KH = KT / 2;
         bool ok = wg < row_tiles;
         for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x, ++piece) {
             const Piece w = shared_piece(p, item);
@@ -244,8 +254,8 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                 constexpr int LPR = D / 8;           // lanes a row, 8 values each
                 constexpr int RPW = 32 / LPR;        // rows a warp at a time
                 const int c = lane % LPR;
-#pragma unroll 8  // eight loads under way
-                for (int r = (warp & 3) * RPW + lane / LPR; r < 128; r += 4 * RPW) {
+#pragma unroll 4  // loads under way together
+                for (int r = (warp & 7) * RPW + lane / LPR; r < 128; r += 8 * RPW) {
                     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
                     if (wg * 128 + r < w.rows)
                         raw = *reinterpret_cast<const uint4 *>(q_row(p, w, wg * 128 + r) + 8 * c);
@@ -275,29 +285,27 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + wg) : "memory");  // qsc of the row tile
+                row_tile_sync(wg);  // qsc of the row tile
                 if (lane == 0) mbar_arrive(q_ready);
             }
-            const int r = wg * 128 + (warp & 3) * 32 + lane;
+            const int rl = (warp & 3) * 32 + lane, r = wg * 128 + rl;
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-            const uint32_t o_at = tmem + lanes + S::kTmemO + wg * D;
+            const uint32_t o_at = tmem + lanes + S::kTmemO + wg * D + half * (D / 2);
+            float *other = xch + (wg * 2 + (half ^ 1)) * 128 + rl;   // of the row's other half
+            float *mine = xch + (wg * 2 + half) * 128 + rl;
             const float c = qsc[r];
-            float m = -INFINITY;            // reference of this row's weights
+            float m = 0.f;                  // reference of this row's weights
             float2 sum = make_float2(0.f, 0.f);
             for (int j = 0; j < tiles; ++j) {
                 const uint32_t st = step + (row_tiles == 2 ? 2 * j + wg : j);
-                const uint32_t slot = st & 1, s_at = tmem + lanes + slot * KT;
+                const uint32_t slot = st & 1, s_at = tmem + lanes + slot * KT + half * KH;
                 ok = shd_wait(&s_full[slot], (st >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
                 ok = __all_sync(~0u, ok);
-                if (!ok) break;
+                // a warp whose wait gave up still meets the others' barriers
                 tc_fence_after();
-                const int valid = w.k1 - w.k0 - j * KT;   // keys of the tile that count
-                // scores 32 at a time, in loops that stay short: the roles' code
-                // shares the instruction caches
-                float mx = -INFINITY;
-#pragma unroll 1
-                for (int k = 0; k < KT; k += 32) {
-                    uint32_t x[32];
+                // keys of this half that count
+                const int valid = w.k1 - w.k0 - j * KT - half * KH;
+                auto scores = [&](int k, uint32_t (&x)[32]) {
                     tmem_ld32(s_at + k, x);
                     tmem_wait_ld32(x);
                     if (k + 32 > valid) {
@@ -305,6 +313,14 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                         for (int i = 0; i < 32; ++i)
                             if (k + i >= valid) x[i] = 0xff800000u;  // -inf
                     }
+                };
+                // the row's largest score: of this half, then of both (two places
+                // in turn, so that one barrier a tile is enough)
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int k = 0; k < KH; k += 32) {
+                    uint32_t x[32];
+                    scores(k, x);
                     float a = mx, b = -INFINITY;
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
@@ -313,24 +329,29 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     }
                     mx = fmaxf(a, b);
                 }
-                mx *= c;
+                const int turn = (j & 1) * S::kRT * 256;
+                mine[turn] = mx;
+                row_tile_sync(wg);
+                mx = fmaxf(mx, other[turn]) * c;
                 // the reference moves when a weight could pass 2^8
                 float f = 1.f;
-                if (mx > m + 8.f || (m == -INFINITY && mx > m)) {
-                    f = m == -INFINITY ? 0.f : batch_ex2(m - mx);
+                if (j == 0) {
+                    m = mx == -INFINITY ? 0.f : mx;
+                } else if (mx > m + 8.f) {
+                    f = batch_ex2(m - mx);
                     m = mx;
                 }
-                if (j > 0 && __any_sync(~0u, f != 1.f)) {
+                if (__any_sync(~0u, f != 1.f)) {
                     // O of the tiles so far, once their products are done
                     // (with two row tiles these scores follow the last one)
                     const uint32_t n = kt + j - 1;
-                    if (row_tiles == 1)
+                    if (row_tiles == 1 && ok) {
                         ok = shd_wait(&v_empty[n & 1], (n >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
-                    ok = __all_sync(~0u, ok);
-                    if (!ok) break;
+                        ok = __all_sync(~0u, ok);
+                    }
                     tc_fence_after();
 #pragma unroll 1
-                    for (int k = 0; k < D; k += 8) {
+                    for (int k = 0; k < D / 2; k += 8) {
                         uint32_t o[8];
                         tmem_ld8(o_at + k, o);
 #pragma unroll
@@ -341,20 +362,14 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     sum.x *= f;
                     sum.y *= f;
                 }
-                const float ref = m == -INFINITY ? 0.f : m;
-                const float2 c2 = make_float2(c, c), m2 = make_float2(-ref, -ref);
-                // P of scores k .. k + 31 takes 16 columns at k / 2, over scores that
-                // have been read
+                const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
+                // P of scores k .. k + 31 takes 16 columns at k / 2 of this half's,
+                // over scores that have been read
+                float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll 1
-                for (int k = 0; k < KT; k += 32) {
+                for (int k = 0; k < KH; k += 32) {
                     uint32_t x[32], h[16];
-                    tmem_ld32(s_at + k, x);
-                    tmem_wait_ld32(x);
-                    if (k + 32 > valid) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (k + i >= valid) x[i] = 0xff800000u;
-                    }
+                    scores(k, x);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float2 t = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]),
@@ -362,55 +377,58 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                                               c2, m2);
                         t.x = batch_ex2(t.x);
                         t.y = batch_ex2(t.y);
-                        sum = __fadd2_rn(sum, t);
+                        if (i & 1)
+                            sum = __fadd2_rn(sum, t);
+                        else
+                            sum2 = __fadd2_rn(sum2, t);
                         h[i] = pack_half2(t.x, t.y);
                     }
                     tmem_st16(s_at + k / 2, h);
                 }
+                sum = __fadd2_rn(sum, sum2);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
+                if (!ok) break;
                 if (lane == 0) mbar_arrive(&p_ready[slot]);
             }
             // ----------------------------------------------------- partial out
             if (ok) ok = shd_wait(o_done, piece & 1, flag, p.err, ERR_BATCH_BASE);
             ok = __all_sync(~0u, ok);
+            row_tile_sync(wg);  // (the last tile's exchange has been read)
+            *mine = sum.x + sum.y;
+            row_tile_sync(wg);
             if (ok) {
                 tc_fence_after();
-                const bool mine = r < w.rows;
-                const int64_t at = mine ? part_row(p, w, r) : 0;
-                if (mine) p.part_ml[at] = make_float2(m, sum.x + sum.y);
-                float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * D);
+                const bool in = r < w.rows;
+                const int64_t at = in ? part_row(p, w, r) : 0;
+                if (in && half == 0) p.part_ml[at] = make_float2(m, *mine + *other);
+                float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * D + half * (D / 2));
 #pragma unroll 1
-                for (int k = 0; k < D; k += 32) {
+                for (int k = 0; k < D / 2; k += 32) {
                     uint32_t o[32];
                     tmem_ld32(o_at + k, o);
                     tmem_wait_ld32(o);
-                    if (!mine) continue;
+                    if (!in) continue;
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const uint32_t *u = o + 8 * g;
-                        float4 a, b;
-                        if constexpr (BITS == 4) {
-                            a = make_float4(__uint_as_float(u[0]), __uint_as_float(u[2]),
-                                            __uint_as_float(u[4]), __uint_as_float(u[6]));
-                            b = make_float4(__uint_as_float(u[1]), __uint_as_float(u[3]),
-                                            __uint_as_float(u[5]), __uint_as_float(u[7]));
-                        } else {
-                            a = make_float4(__uint_as_float(u[0]), __uint_as_float(u[1]),
-                                            __uint_as_float(u[2]), __uint_as_float(u[3]));
-                            b = make_float4(__uint_as_float(u[4]), __uint_as_float(u[5]),
-                                            __uint_as_float(u[6]), __uint_as_float(u[7]));
-                        }
-                        dst[k / 4 + 2 * g] = a;
-                        dst[k / 4 + 2 * g + 1] = b;
+                        constexpr int i1 = BITS == 4 ? 2 : 1, i4 = BITS == 4 ? 1 : 4;
+                        dst[k / 4 + 2 * g] = make_float4(
+                            __uint_as_float(u[0]), __uint_as_float(u[i1]),
+                            __uint_as_float(u[2 * i1]), __uint_as_float(u[3 * i1]));
+                        dst[k / 4 + 2 * g + 1] = make_float4(
+                            __uint_as_float(u[i4]), __uint_as_float(u[i4 + i1]),
+                            __uint_as_float(u[i4 + 2 * i1]), __uint_as_float(u[i4 + 3 * i1]));
                     }
                 }
             }
+            row_tile_sync(wg);  // the exchange is read before the next piece's
+            tc_fence_before();
             kt += tiles;
             step += tiles * row_tiles;
         }
-    } else if (warp < 16) {
+    } else if (warp < 24) {
         // -------------------------------------------------------- dequantise
         for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
             const Piece w = shared_piece(p, item);
@@ -418,7 +436,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
             // A warp takes KT / 8 consecutive keys (within one page) of every
             // tile: 16 bytes of codes a lane, kLpr lanes a row, so that a
             // load covers 512 bytes in a row.
-            const int dw = warp - 8;
+            const int dw = warp - 16;
             const int key0 = dw * S::kWKeys, row = lane / S::kLpr, l = lane % S::kLpr;
             const int32_t *trow = p.table + (int64_t)w.row * p.max_pages;
             struct Raw {
@@ -497,107 +515,136 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
             };
-            Raw a, b;
-            const uint8_t *rec = place(0), *rec1 = place(1), *rec2;
-            fetch(a, rec, 0, 0);
+            // k and v of a tile in turn, by the same code; the next codes are
+            // under way while these are turned into values
+            Raw x, y;
+            const uint8_t *rec = place(0), *rec1 = place(1);
+            fetch(x, rec, 0, 0);
             prefetch(rec1, 1);
-            for (int j = 0; j < tiles; ++j) {
+#pragma unroll 1
+            for (int h = 0; h < 2 * tiles; ++h) {
+                const int j = h >> 1, which = h & 1;
                 const uint32_t n = kt + j, s = n & 1, lap = n >> 1;
-                fetch(b, rec, j, 1);
-                rec2 = place(j + 2);
-                bool ok = lap == 0 || shd_wait(row_tiles == 1 ? &s_full[s] : &k_empty[s],
-                                               (lap - 1) & 1, flag, p.err, ERR_BATCH_BASE);
+                fetch(y, which ? rec1 : rec, j + which, which ^ 1);
+                if (which) {
+                    rec = rec1;
+                    rec1 = place(j + 2);
+                    prefetch(rec1, j + 2);
+                }
+                uint64_t *empty = which ? &v_empty[s] : row_tiles == 1 ? &s_full[s] : &k_empty[s];
+                const bool ok =
+                    lap == 0 || shd_wait(empty, (lap - 1) & 1, flag, p.err, ERR_BATCH_BASE);
                 if (!__all_sync(~0u, ok)) goto wound_down;
-                store(a, ks + s * S::kTileBytes);
-                if (lane == 0) mbar_arrive(&k_full[s]);
-                prefetch(rec2, j + 2);
-                fetch(a, rec1, j + 1, 0);
-                ok = lap == 0 || shd_wait(&v_empty[s], (lap - 1) & 1, flag, p.err, ERR_BATCH_BASE);
-                if (!__all_sync(~0u, ok)) goto wound_down;
-                store(b, vs + s * S::kTileBytes);
-                if (lane == 0) mbar_arrive(&v_full[s]);
-                rec = rec1;
-                rec1 = rec2;
+                store(x, (which ? vs : ks) + s * S::kTileBytes);
+                if (lane == 0) mbar_arrive(which ? &v_full[s] : &k_full[s]);
+                x = y;
             }
             kt += tiles;
         }
     } else {
         // --------------------------------------------------------------- MMA
-        // One thread waits and issues.  A step's value product and the
-        // scores two steps on go out together, then the commits: each wait
-        // and commit costs 100 cycles or more in which a queue of eight MMAs
-        // (64 cycles each) would run dry.
-        if (warp == 16 && elect_lane()) {
+        // One thread waits and issues.  A step's value product and the scores
+        // two steps on go out together, then the commits.  Its time is its own
+        // instructions (the roles' code crowds the instruction caches, and a
+        // wait costs 150 cycles even when it is over): no wait twice, offsets
+        // known when compiled.
+        if (elect_lane()) {
+            const uint32_t id_s =
+                (1u << 4) | ((uint32_t)(KT >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+            const uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+                                  ((uint32_t)(128 >> 4) << 24);
+            const uint64_t qd = sw128_desc(smem_u32(qs)), kd0 = sw128_desc(smem_u32(ks));
+            const uint64_t vd0 = mn_desc(smem_u32(vs), KT * 128);
+            // scores of row tile t with the k tile in slot s, to score slot `to`
+            auto scores = [&](int t, uint32_t s, uint32_t to) {
+                const uint64_t a = qd + (uint64_t)((t * S::kQBytes) >> 4);
+                const uint64_t b = kd0 + (s ? (uint64_t)(S::kTileBytes >> 4) : 0);
+                const uint32_t d = tmem + to * KT;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    tc_mma_f16(d, a + (uint64_t)(((k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                               b + (uint64_t)(((k >> 2) * (KT * 128) + (k & 3) * 32) >> 4), id_s,
+                               k != 0);
+            };
+            // O of row tile t (+)= P in score slot `from` x the v tile in slot s
+            auto values = [&](int t, uint32_t s, uint32_t from, uint32_t more) {
+                const uint32_t a = tmem + from * KT, d = tmem + S::kTmemO + t * D;
+                const uint64_t b = vd0 + (s ? (uint64_t)(S::kTileBytes >> 4) : 0);
+#pragma unroll
+                for (int k = 0; k < KT / 16; ++k)
+                    tc_mma_f16_ta(d, a + (k / (KT / 32)) * (KT / 2) + (k % (KT / 32)) * 8,
+                                  b + (uint64_t)((k * 2048) >> 4), id_o, k != 0 ? 1u : more);
+            };
+            auto wait = [&](uint64_t *bar, uint32_t n) {
+                return shd_wait(bar, n & 1, flag, p.err, ERR_BATCH_BASE);
+            };
             bool ok = true;
             for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x, ++piece) {
                 const Piece w = shared_piece(p, item);
                 const int tiles = (w.k1 - w.k0 + KT - 1) / KT;
-                const int steps = tiles * row_tiles;
-                ok = shd_wait(q_ready, piece & 1, flag, p.err, ERR_BATCH_BASE);
+                ok = wait(q_ready, piece) && wait(&k_full[kt & 1], kt >> 1);
                 if (!ok) break;
-                const uint32_t id_s =
-                    (1u << 4) | ((uint32_t)(KT >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-                const uint32_t id_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
-                                      ((uint32_t)(128 >> 4) << 24);
-                const uint64_t qd0 = sw128_desc(smem_u32(qs)), kd0 = sw128_desc(smem_u32(ks));
-                const uint64_t vd0 = mn_desc(smem_u32(vs), KT * 128);
-                auto tile_of = [&](int i) { return row_tiles == 2 ? i >> 1 : i; };
-                auto row_of = [&](int i) { return row_tiles == 2 ? i & 1 : 0; };
-                auto wait_k = [&](int i) {
-                    const uint32_t n = kt + tile_of(i);
-                    return shd_wait(&k_full[n & 1], (n >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
-                };
-                auto scores = [&](int i) {
-                    const uint32_t s = (kt + tile_of(i)) & 1;
-                    const uint32_t d = tmem + ((step + i) & 1) * KT;
-                    const uint64_t qd = qd0 + (uint64_t)((row_of(i) * S::kQBytes) >> 4);
-                    const uint64_t kd = kd0 + (uint64_t)((s * S::kTileBytes) >> 4);
+                tc_fence_after();
+                issued = true;
+                if (row_tiles == 2) {
+                    // score slot = row tile; both row tiles use each k and v tile
+                    scores(0, kt & 1, 0);
+                    tc_commit(&s_full[0]);
+                    scores(1, kt & 1, 1);
+                    tc_commit(&s_full[1]);
+                    tc_commit(&k_empty[kt & 1]);
 #pragma unroll 1
-                    for (int k = 0; k < D / 16; ++k)
-                        tc_mma_f16(d, qd + (uint64_t)(((k >> 2) * 16384 + (k & 3) * 32) >> 4),
-                                   kd + (uint64_t)(((k >> 2) * (KT * 128) + (k & 3) * 32) >> 4),
-                                   id_s, k != 0);
-                };
-                auto values = [&](int i) {
-                    const uint32_t s = (kt + tile_of(i)) & 1;
-                    const uint32_t d = tmem + S::kTmemO + row_of(i) * D;
-                    const uint32_t a = tmem + ((step + i) & 1) * KT;
-                    const uint64_t vd = vd0 + (uint64_t)((s * S::kTileBytes) >> 4);
-#pragma unroll 1
-                    for (int k = 0; k < KT / 16; ++k)
-                        tc_mma_f16_ta(d, a + k * 8, vd + (uint64_t)((k * 2048) >> 4), id_o,
-                                      tile_of(i) != 0 || k != 0);
-                };
-                auto scores_done = [&](int i) {
-                    tc_commit(&s_full[(step + i) & 1]);
-                    // with one row tile the scores are also the k tile's last use
-                    if (row_tiles == 2 && (i & 1)) tc_commit(&k_empty[(kt + tile_of(i)) & 1]);
-                };
-                for (int i = 0; i < 2 && i < steps && ok; ++i) {
-                    ok = wait_k(i);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issued = true;
-                    scores(i);
-                    scores_done(i);
-                }
-                for (int i = 0; i < steps && ok; ++i) {
-                    const uint32_t n = kt + tile_of(i), s = n & 1, st = step + i, slot = st & 1;
-                    ok = shd_wait(&v_full[s], (n >> 1) & 1, flag, p.err, ERR_BATCH_BASE) &&
-                         (i + 2 >= steps || wait_k(i + 2)) &&
-                         shd_wait(&p_ready[slot], (st >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
-                    if (!ok) break;
-                    tc_fence_after();
-                    values(i);
-                    if (i + 2 < steps) {
-                        scores(i + 2);
-                        scores_done(i + 2);
+                    for (int j = 0; j < tiles; ++j, ++kt) {
+                        const uint32_t s = kt & 1, n = kt + 1;
+                        const bool next = j + 1 < tiles;
+                        ok = wait(&v_full[s], kt >> 1) && (!next || wait(&k_full[n & 1], n >> 1)) &&
+                             wait(&p_ready[0], kt);
+                        if (!ok) break;
+                        tc_fence_after();
+                        values(0, s, 0, j != 0);
+                        if (next) {
+                            scores(0, n & 1, 0);
+                            tc_commit(&s_full[0]);
+                        }
+                        ok = wait(&p_ready[1], kt);
+                        if (!ok) break;
+                        tc_fence_after();
+                        values(1, s, 1, j != 0);
+                        if (next) {
+                            scores(1, n & 1, 1);
+                            tc_commit(&s_full[1]);
+                            tc_commit(&k_empty[n & 1]);
+                        }
+                        tc_commit(&v_empty[s]);
                     }
-                    if (row_of(i) == row_tiles - 1) tc_commit(&v_empty[s]);
+                } else {
+                    // score slot = k and v slot; s_full also says that k is free
+                    scores(0, kt & 1, kt & 1);
+                    tc_commit(&s_full[kt & 1]);
+                    if (tiles > 1) {
+                        ok = wait(&k_full[(kt + 1) & 1], (kt + 1) >> 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(0, (kt + 1) & 1, (kt + 1) & 1);
+                        tc_commit(&s_full[(kt + 1) & 1]);
+                    }
+#pragma unroll 1
+                    for (int j = 0; j < tiles; ++j, ++kt) {
+                        const uint32_t s = kt & 1;
+                        const bool next = j + 2 < tiles;
+                        ok = wait(&v_full[s], kt >> 1) && (!next || wait(&k_full[s], (kt + 2) >> 1)) &&
+                             wait(&p_ready[s], kt >> 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        values(0, s, s, j != 0);
+                        if (next) {
+                            scores(0, s, s);
+                            tc_commit(&s_full[s]);
+                        }
+                        tc_commit(&v_empty[s]);
+                    }
                 }
                 tc_commit(o_done);
-                kt += tiles;
-                step += steps;
             }
         }
         __syncwarp();
@@ -609,7 +656,7 @@ wound_down:
         if (!mbar_wait(drain, 0)) atomicOr(p.err, ERR_BATCH_BASE);
     }
     __syncthreads();
-    if (warp == 16) tmem_dealloc(tmem, 512);
+    if (warp == 24) tmem_dealloc(tmem, 512);
 }
 
 template <int BITS, int D, int GROUP>
@@ -617,7 +664,7 @@ cudaError_t shared_run(const BatchParams &p, int row_tiles, int grid, cudaStream
     using S = Shd<BITS, D, GROUP>;
     auto kern = shared_kernel<BITS, D, GROUP>;
     constexpr size_t body = 1024 + (size_t)S::kRT * S::kQBytes + 4 * (size_t)S::kTileBytes +
-                            S::kRT * 512 + 18 * 8;
+                            S::kRT * 2560 + 18 * 8;
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [&] {
