@@ -82,6 +82,19 @@ struct BatchParams {
     uint32_t *err;
 };
 
+// A row or group of the plan, past L1.
+template <class T>
+__device__ __forceinline__ T plan_load(const T *p) {
+    static_assert(sizeof(T) == 32, "two 16-byte loads");
+    union {
+        T t;
+        int4 v[2];
+    } u;
+    u.v[0] = __ldcg(reinterpret_cast<const int4 *>(p));
+    u.v[1] = __ldcg(reinterpret_cast<const int4 *>(p) + 1);
+    return u.t;
+}
+
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) {
     return (int)(((unsigned)a + (unsigned)b - 1u) / (unsigned)b);
 }

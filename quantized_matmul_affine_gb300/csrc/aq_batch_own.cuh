@@ -112,14 +112,18 @@ __global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchP
     uint2 *qfrag = reinterpret_cast<uint2 *>(my + S::kStages * S::kStage);
     float *qs2 = reinterpret_cast<float *>(my + S::kStages * S::kStage + S::kFrag);  // [rows][G]
 
+    // After shared_kernel, which has seen the plan complete before it let this
+    // kernel start, there is nothing to wait for: its pieces are other slots.
+    // (What earlier kernels wrote is then read past L1, which may be older.)
+    if (!p.shared_tc) grid_dependency_wait();
     launch_dependents();
-    grid_dependency_wait();
     const int me = (int)blockIdx.x * S::kWarps + warp;
-    const int per = p.head->per, LR = p.L * p.R;
+    const int4 head = __ldcg(reinterpret_cast<const int4 *>(p.head));  // per, tiles, ..
+    const int per = head.x, LR = p.L * p.R;
     // (long long: runs past the last tile are empty, wherever they start)
     long long u64 = (long long)me * per;
-    const int end = (int)min((long long)p.head->tiles, u64 + per);
-    int u = (int)min(u64, (long long)end), at = u < end ? p.runs[me] : 0;
+    const int end = (int)min((long long)head.y, u64 + per);
+    int u = (int)min(u64, (long long)end), at = u < end ? __ldcg(p.runs + me) : 0;
     uint32_t outside = 0;
 
     while (u < end) {
@@ -129,7 +133,7 @@ __global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchP
         const bool is_shared = at < 0;
         int base, tiles, rows, first, step;
         if (is_shared) {
-            const PlanGroup g = p.groups[-1 - at];
+            const PlanGroup g = plan_load(p.groups - 1 - at);
             base = g.at;
             tiles = g.pieces;
             rows = g.rows * LR;
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchP
             w.k1 = g.len;
             w.slot0 = g.slot;
         } else {
-            const PlanRow b = p.rows[at];
+            const PlanRow b = plan_load(p.rows + at);
             base = b.at;
             tiles = b.tiles;
             rows = LR;
@@ -174,7 +178,7 @@ __global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchP
             int id = -1;
             const int key = tile * S::kKeys + 16 * (lane & (BLK - 1));
             if (tile < tile1 && key < w.k1) {
-                id = __ldg(trow + (key >> p.c.page_log2));
+                id = __ldcg(trow + (key >> p.c.page_log2));
                 if (id < 0 || id >= p.c.n_pages) {
                     id = -1;
                     outside = 1;
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchP
 #pragma unroll
                 for (int i = 0; i < GROUP / 32; ++i)
                     raw[g * (GROUP / 32) + i] =
-                        src ? src[g * (GROUP / 8) + t * (GROUP / 32) + i]
+                        src ? __ldcg(src + g * (GROUP / 8) + t * (GROUP / 32) + i)
                             : make_uint4(0u, 0u, 0u, 0u);
             float mx = 0.f;
 #pragma unroll
@@ -616,6 +620,8 @@ __global__ void __launch_bounds__(128) own_kernel(const __grid_constant__ BatchP
         __syncwarp();
     }
     if (outside) atomicOr(p.err, ERR_BATCH_TABLE);
+    // this grid's end is the end of both kernels for the one that follows
+    if (p.shared_tc) grid_dependency_wait();
 }
 
 }  // namespace aq

@@ -225,8 +225,8 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    launch_dependents();
     grid_dependency_wait();
+    launch_dependents();  // own_kernel needs the plan, but nothing of this kernel
     const int n_items = p.head->shared_items * p.c.KV;
     // Each role walks the pieces by itself, with running counts of pieces,
     // tiles of keys and steps (row tiles x tiles of keys).  A step's scores
@@ -593,20 +593,22 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     scores(1, kt & 1, 1);
                     tc_commit(&s_full[1]);
                     tc_commit(&k_empty[kt & 1]);
+                    ok = wait(&v_full[kt & 1], kt >> 1);
 #pragma unroll 1
-                    for (int j = 0; j < tiles; ++j, ++kt) {
+                    for (int j = 0; ok && j < tiles; ++j, ++kt) {
                         const uint32_t s = kt & 1, n = kt + 1;
                         const bool next = j + 1 < tiles;
-                        ok = wait(&v_full[s], kt >> 1) && (!next || wait(&k_full[n & 1], n >> 1)) &&
-                             wait(&p_ready[0], kt);
+                        ok = (!next || wait(&k_full[n & 1], n >> 1)) && wait(&p_ready[0], kt);
                         if (!ok) break;
                         tc_fence_after();
                         values(0, s, 0, j != 0);
                         if (next) {
                             scores(0, n & 1, 0);
                             tc_commit(&s_full[0]);
+                            // in the time until P of the other row tile
+                            ok = wait(&v_full[n & 1], n >> 1);
                         }
-                        ok = wait(&p_ready[1], kt);
+                        ok = ok && wait(&p_ready[1], kt);
                         if (!ok) break;
                         tc_fence_after();
                         values(1, s, 1, j != 0);
@@ -617,6 +619,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                         }
                         tc_commit(&v_empty[s]);
                     }
+                    if (!ok) break;
                 } else {
                     // score slot = k and v slot; s_full also says that k is free
                     scores(0, kt & 1, kt & 1);

@@ -36,6 +36,7 @@ struct RowParams {
     int64_t T;
     int B;
     int span;                 // lanes a token
+    int each;                 // tokens they take one after another
     int64_t max_pages;
     uint32_t *err;
 };
@@ -104,10 +105,18 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
     const int which = blockIdx.y;
     const int per_token = p.c.KV * p.c.D / 8, lanes = p.c.group / 8;
     const int at = (int)(threadIdx.x % p.span);
-    const int t = (int)(blockIdx.x * (kRowThreads / p.span) + threadIdx.x / p.span);
-    const bool live = t < p.T;
-    int slot = 0;
-    uint8_t *rec = live ? token_record(p, t, &slot) : nullptr;
+    const int t0 = (int)(blockIdx.x * (kRowThreads / p.span) + threadIdx.x / p.span) * p.each;
+    // lane i looks up the page of the i-th of these tokens, for all of them
+    int my_slot = 0;
+    uint8_t *my_rec = nullptr;
+    if (at < p.each && t0 + at < p.T) my_rec = token_record(p, t0 + at, &my_slot);
+    const int lead = (int)(threadIdx.x & 31) - at;
+#pragma unroll 1
+    for (int i = 0; i < p.each; ++i) {
+    const int t = t0 + i;
+    const int slot = __shfl_sync(~0u, my_slot, lead + i);
+    uint8_t *rec = reinterpret_cast<uint8_t *>(
+        __shfl_sync(~0u, reinterpret_cast<unsigned long long>(my_rec), lead + i));
     const uint4 *in = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.in[which]) +
                                                       (int64_t)t * p.in_stride[which]);
     uint8_t *codes = rec + which * p.c.side_codes + slot * p.c.rb;
@@ -170,6 +179,7 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
                                             kv * p.c.rec)[d8 / lanes] = __halves2half2(s16, b16);
         }
     }
+    }
 }
 
 // The reverse, shared out alike: one lane turns 8 codes into 8 values of the
@@ -180,10 +190,18 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
     const int which = blockIdx.y;
     const int per_token = p.c.KV * p.c.D / 8;
     const int at = (int)(threadIdx.x % p.span);
-    const int t = (int)(blockIdx.x * (kRowThreads / p.span) + threadIdx.x / p.span);
-    if (t >= p.T) return;
-    int slot = 0;
-    const uint8_t *rec = token_record(p, t, &slot);
+    const int t0 = (int)(blockIdx.x * (kRowThreads / p.span) + threadIdx.x / p.span) * p.each;
+    int my_slot = 0;
+    const uint8_t *my_rec = nullptr;
+    if (at < p.each && t0 + at < p.T) my_rec = token_record(p, t0 + at, &my_slot);
+    const int lead = (int)(threadIdx.x & 31) - at;
+#pragma unroll 1
+    for (int i = 0; i < p.each; ++i) {
+    const int t = t0 + i;
+    const int slot = __shfl_sync(~0u, my_slot, lead + i);
+    const uint8_t *rec = reinterpret_cast<const uint8_t *>(
+        __shfl_sync(~0u, reinterpret_cast<unsigned long long>(my_rec), lead + i));
+    if (t >= p.T) continue;
     const uint8_t *codes = rec + which * p.c.side_codes + slot * p.c.rb;
     const uint8_t *pairs = rec + 2 * p.c.side_codes + which * p.c.side_sb + slot * p.c.groups * 4;
     const int per_head = p.c.D / 8, lanes = p.c.group / 8;
@@ -233,6 +251,7 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
             }
             out[e] = make_uint4(o[0], o[1], o[2], o[3]);
         }
+    }
     }
 }
 
@@ -839,7 +858,11 @@ cudaError_t cache_append_launch(const aq_cache *c, int64_t layer, int dtype, con
     const int per_token = p.c.KV * p.c.D / 8;
     p.span = 32;
     while (per_token % p.span != 0) p.span /= 2;
-    const int64_t tokens = kRowThreads / p.span;  // a CTA
+    // The chain of loads that finds a page takes longer than a token's data:
+    // where there are tokens enough to fill the device, four share it (16k
+    // tokens: 48 -> 40 us and 28 -> 24 us to append and to read)
+    p.each = T >= 4096 ? 4 : 1;
+    const int64_t tokens = (int64_t)(kRowThreads / p.span) * p.each;  // a CTA
     const dim3 grid((unsigned)((T + tokens - 1) / tokens), 2, 1);
     void (*kern)(RowParams);
     const bool bf = dtype == AQ_BF16;
