@@ -37,6 +37,7 @@ struct RowParams {
     int B;
     int span;                 // lanes a token
     int each;                 // tokens they take one after another
+    int head_log2, lane_log2;  // lanes a head (D / 8) and a group (group / 8)
     int64_t max_pages;
     uint32_t *err;
 };
@@ -91,7 +92,7 @@ __device__ __forceinline__ void widen(const uint4 &u, float (&f)[8]) {
     }
 }
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 constexpr int kRowLoads = 4;  // 16-byte loads a lane has under way
 
 // One lane takes 8 values (a 16-byte load), `p.span` lanes (8, 16 or 32: the
@@ -122,7 +123,6 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
     uint8_t *codes = rec + which * p.c.side_codes + slot * p.c.rb;
     __half2 *pairs = reinterpret_cast<__half2 *>(rec + 2 * p.c.side_codes + which * p.c.side_sb) +
                      slot * p.c.groups;
-    const int per_head = p.c.D / 8;
     for (int e0 = 0; e0 < per_token; e0 += kRowLoads * p.span) {
         uint4 raw[kRowLoads];
 #pragma unroll
@@ -142,41 +142,72 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
                 lo = fminf(lo, f[j]);
                 hi = fmaxf(hi, f[j]);
             }
-            for (int o = 1; o < lanes; o <<= 1) {
-                lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
-                hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
-            }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1)
+                if (o < lanes) {
+                    lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
+                    hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
+                }
             const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), (float)kQmax));
             const __half b16 = __float2half_rn(lo);
             const float s = __half2float(s16), b = __half2float(b16);
-            constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
+            // Adding 1.5 * 2^23 rounds to an integer, which is then the low bits
+            // of the sum: codes are gathered by shifted adds of the sums' bits,
+            // less what the magic number's own bits add up to.
+            constexpr float kMagic = 12582912.0f;
+            constexpr int kWords = BITS / 4, kCodes = 32 / BITS;
+            constexpr uint32_t kOnes = BITS == 4 ? 0x11111111u : 0x01010101u;
             // the product with the rounded reciprocal is within 1.5 * 2^-23
             // relative of the IEEE quotient: this much of an integer and a half
             constexpr float kEdge = BITS == 4 ? 3.0517578125e-05f : 4.8828125e-04f;
             const float r = __frcp_rn(s);
-            uint32_t w[2] = {0u, 0u};
+            const float2 r2 = make_float2(r, r), b2 = make_float2(-b, -b);
+            const float2 m2 = make_float2(kMagic, kMagic), n2 = make_float2(-kMagic, -kMagic);
+            uint32_t w[kWords];
+            float far = 0.f;  // from the nearest integer
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float a = __fsub_rn(f[j], b);
-                float q = fminf(fmaxf(__fmul_rn(a, r), 0.f), (float)kQmax);
-                float m = __fadd_rn(q, kMagic);
-                if (fabsf(__fsub_rn(q, __fsub_rn(m, kMagic))) > 0.5f - kEdge) {  // near a tie
-                    q = fminf(fmaxf(__fdiv_rn(a, s), 0.f), (float)kQmax);
-                    m = __fadd_rn(q, kMagic);
-                }
-                w[j * BITS / 32] |= (__float_as_uint(m) & (uint32_t)kQmax) << (j * BITS % 32);
+            for (int u = 0; u < kWords; ++u) w[u] = 0u - (kOnes * __float_as_uint(kMagic));
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                float2 q = __fmul2_rn(__fadd2_rn(make_float2(f[j], f[j + 1]), b2), r2);
+                q.x = fminf(fmaxf(q.x, 0.f), (float)kQmax);
+                q.y = fminf(fmaxf(q.y, 0.f), (float)kQmax);
+                const float2 m = __fadd2_rn(q, m2);
+                const float2 d = __ffma2_rn(__fadd2_rn(m, n2), make_float2(-1.f, -1.f), q);
+                far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
+                w[j / kCodes] += __float_as_uint(m.x) << (j % kCodes * BITS);
+                w[j / kCodes] += __float_as_uint(m.y) << ((j + 1) % kCodes * BITS);
             }
-            if (s == 0.f) w[0] = w[1] = 0u;
+            if (far > 0.5f - kEdge) {  // near a tie: by the quotient itself
+#pragma unroll
+                for (int u = 0; u < kWords; ++u) w[u] = 0u;
+#pragma unroll 1
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t h = reinterpret_cast<const uint32_t *>(&raw[k])[j / 2];
+                    const float v = BF16 ? __uint_as_float(j & 1 ? h & 0xFFFF0000u : h << 16)
+                                         : __half2float(__ushort_as_half((uint16_t)(h >> (16 * (j & 1)))));
+                    const float q =
+                        fminf(fmaxf(__fdiv_rn(__fsub_rn(v, b), s), 0.f), (float)kQmax);
+                    const uint32_t code = __float_as_uint(__fadd_rn(q, kMagic)) & (uint32_t)kQmax;
+                    if (kWords == 1 || j < kCodes)
+                        w[0] |= code << (j % kCodes * BITS);
+                    else
+                        w[kWords - 1] |= code << (j % kCodes * BITS);
+                }
+            }
+            if (s == 0.f)
+#pragma unroll
+                for (int u = 0; u < kWords; ++u) w[u] = 0u;
             if (!rec) continue;
-            const int kv = e / per_head, d8 = e - kv * per_head;
+            const int kv = e >> p.head_log2, d8 = e & ((1 << p.head_log2) - 1);
             uint32_t *dst = reinterpret_cast<uint32_t *>(codes + kv * p.c.rec) + d8 * (BITS / 4);
             if constexpr (BITS == 4)
                 *dst = w[0];
             else
-                *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-            if (d8 % lanes == 0)
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[kWords - 1]);
+            if ((d8 & (lanes - 1)) == 0)
                 reinterpret_cast<__half2 *>(reinterpret_cast<uint8_t *>(pairs) +
-                                            kv * p.c.rec)[d8 / lanes] = __halves2half2(s16, b16);
+                                            kv * p.c.rec)[d8 >> p.lane_log2] = __halves2half2(s16, b16);
         }
     }
     }
@@ -204,7 +235,6 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
     if (t >= p.T) continue;
     const uint8_t *codes = rec + which * p.c.side_codes + slot * p.c.rb;
     const uint8_t *pairs = rec + 2 * p.c.side_codes + which * p.c.side_sb + slot * p.c.groups * 4;
-    const int per_head = p.c.D / 8, lanes = p.c.group / 8;
     uint4 *out = static_cast<uint4 *>(p.out[which]) + (int64_t)t * per_token;
     for (int e0 = at; e0 < per_token; e0 += kRowLoads * p.span) {
         uint32_t w[kRowLoads][2];
@@ -215,7 +245,7 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
             w[k][0] = w[k][1] = 0u;
             sb[k] = __float2half2_rn(0.f);
             if (!rec || e >= per_token) continue;
-            const int kv = e / per_head, d8 = e - kv * per_head;
+            const int kv = e >> p.head_log2, d8 = e & ((1 << p.head_log2) - 1);
             const uint32_t *src =
                 reinterpret_cast<const uint32_t *>(codes + kv * p.c.rec) + d8 * (BITS / 4);
             if constexpr (BITS == 4) {
@@ -225,7 +255,7 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
                 w[k][0] = v.x;
                 w[k][1] = v.y;
             }
-            sb[k] = reinterpret_cast<const __half2 *>(pairs + kv * p.c.rec)[d8 / lanes];
+            sb[k] = reinterpret_cast<const __half2 *>(pairs + kv * p.c.rec)[d8 >> p.lane_log2];
         }
 #pragma unroll
         for (int k = 0; k < kRowLoads; ++k) {
@@ -240,7 +270,8 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
                 for (int h = 0; h < 2; ++h) {
                     const int bit = (2 * j + h) * BITS;
                     const uint32_t code = (w[k][bit / 32] >> (bit % 32)) & ((1u << BITS) - 1u);
-                    v[h] = fmaf((float)code, f.x, f.y);
+                    // 2^23 + code, less 2^23: the code as a float
+                    v[h] = fmaf(__uint_as_float(0x4B000000u | code) - 8388608.f, f.x, f.y);
                 }
                 if constexpr (BF16) {
                     const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]);
@@ -856,12 +887,14 @@ cudaError_t cache_append_launch(const aq_cache *c, int64_t layer, int dtype, con
     const cudaError_t e = error_word(&p.err);
     if (e != cudaSuccess) return e;
     const int per_token = p.c.KV * p.c.D / 8;
+    while (8 << p.head_log2 < p.c.D) ++p.head_log2;
+    while (8 << p.lane_log2 < p.c.group) ++p.lane_log2;
     p.span = 32;
     while (per_token % p.span != 0) p.span /= 2;
     // The chain of loads that finds a page takes longer than a token's data:
     // where there are tokens enough to fill the device, four share it (16k
     // tokens: 48 -> 40 us and 28 -> 24 us to append and to read)
-    p.each = T >= 4096 ? 4 : 1;
+    p.each = T >= 4096 ? 2 : 1;
     const int64_t tokens = (int64_t)(kRowThreads / p.span) * p.each;  // a CTA
     const dim3 grid((unsigned)((T + tokens - 1) / tokens), 2, 1);
     void (*kern)(RowParams);
