@@ -492,6 +492,9 @@ cudaError_t batch_launch(const aq_cache *c, int64_t layer, const BatchArgs &a) {
     if (e != cudaSuccess) return e;
     e = plan_run(p, a.stream);
     if (e != cudaSuccess) return e;
+#ifdef AQ_TEST_HOOKS
+    p.withhold = g_test_withhold == 3;
+#endif
     if (pl.row_tiles) {
         e = batch_shared(p, pl.row_tiles, num_sms(), a.stream);
         if (e != cudaSuccess) return e;

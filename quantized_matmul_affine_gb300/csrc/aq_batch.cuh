@@ -80,6 +80,7 @@ struct BatchParams {
     int shared_rows;         // query rows a tile of it
     int shared_unit;         // its chunks are multiples of this
     uint32_t *err;
+    int withhold;            // test builds only: shared_kernel's first k tile is not announced
 };
 
 // A row or group of the plan, past L1.

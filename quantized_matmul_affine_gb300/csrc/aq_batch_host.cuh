@@ -17,6 +17,10 @@ struct BatchRun {
     int *resident, *unit_keys;
 };
 
+// (Without a name for the linker: what is kept once a kernel must not be
+// shared with another copy of the library in the process.)
+namespace {
+
 template <int BITS, int D, int GROUP, int NB>
 cudaError_t own_run_nb(const BatchRun &r) {
     using S = Own<BITS, D, GROUP, NB>;
@@ -56,6 +60,8 @@ cudaError_t own_run(const BatchRun &r) {
     else
         return r.nb == 1 ? own_run_nb<BITS, D, GROUP, 1>(r) : own_run_nb<BITS, D, GROUP, 2>(r);
 }
+
+}  // namespace
 
 cudaError_t batch_own4a(int64_t D, int group, const BatchRun &r);
 cudaError_t batch_own4b(int64_t D, int group, const BatchRun &r);

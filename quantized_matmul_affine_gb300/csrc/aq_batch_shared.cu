@@ -167,9 +167,25 @@ __device__ __forceinline__ bool elect_lane() {
     return on != 0;
 }
 
-// A barrier of the 256 threads of a row tile's softmax.
+// A barrier of the 256 threads of a row tile's softmax, and one that tells
+// them all whether all of them say so (a wait that gave up in one warp ends
+// the tile loop of all of them together, so that none misses a barrier).
 __device__ __forceinline__ void row_tile_sync(int wg) {
+    __syncwarp();
     asm volatile("bar.sync %0, 256;" ::"r"(1 + wg) : "memory");
+}
+__device__ __forceinline__ bool row_tile_all(int wg, bool me) {
+    uint32_t all;
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "bar.red.and.pred q, %1, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(1 + wg), "r"((uint32_t)me)
+        : "memory");
+    return all != 0;
 }
 
 // A bounded wait that records where it gave up.
@@ -299,9 +315,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
             for (int j = 0; j < tiles; ++j) {
                 const uint32_t st = step + (row_tiles == 2 ? 2 * j + wg : j);
                 const uint32_t slot = st & 1, s_at = tmem + lanes + slot * KT + half * KH;
-                ok = shd_wait(&s_full[slot], (st >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
-                ok = __all_sync(~0u, ok);
-                // a warp whose wait gave up still meets the others' barriers
+                ok = ok && shd_wait(&s_full[slot], (st >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
                 tc_fence_after();
                 // keys of this half that count
                 const int valid = w.k1 - w.k0 - j * KT - half * KH;
@@ -331,7 +345,8 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                 }
                 const int turn = (j & 1) * S::kRT * 256;
                 mine[turn] = mx;
-                row_tile_sync(wg);
+                ok = row_tile_all(wg, ok);
+                if (!ok) break;
                 mx = fmaxf(mx, other[turn]) * c;
                 // the reference moves when a weight could pass 2^8
                 float f = 1.f;
@@ -345,10 +360,8 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     // O of the tiles so far, once their products are done
                     // (with two row tiles these scores follow the last one)
                     const uint32_t n = kt + j - 1;
-                    if (row_tiles == 1 && ok) {
+                    if (row_tiles == 1)  // (one that gives up is told of at the next barrier)
                         ok = shd_wait(&v_empty[n & 1], (n >> 1) & 1, flag, p.err, ERR_BATCH_BASE);
-                        ok = __all_sync(~0u, ok);
-                    }
                     tc_fence_after();
 #pragma unroll 1
                     for (int k = 0; k < D / 2; k += 8) {
@@ -388,14 +401,12 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                 sum = __fadd2_rn(sum, sum2);
                 tmem_wait_st();
                 tc_fence_before();
-                __syncwarp();
-                if (!ok) break;
-                if (lane == 0) mbar_arrive(&p_ready[slot]);
+                ok = __all_sync(~0u, ok);
+                if (lane == 0 && ok) mbar_arrive(&p_ready[slot]);
             }
             // ----------------------------------------------------- partial out
             if (ok) ok = shd_wait(o_done, piece & 1, flag, p.err, ERR_BATCH_BASE);
-            ok = __all_sync(~0u, ok);
-            row_tile_sync(wg);  // (the last tile's exchange has been read)
+            ok = row_tile_all(wg, ok);  // (and the last tile's exchange has been read)
             *mine = sum.x + sum.y;
             row_tile_sync(wg);
             if (ok) {
@@ -536,7 +547,8 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     lap == 0 || shd_wait(empty, (lap - 1) & 1, flag, p.err, ERR_BATCH_BASE);
                 if (!__all_sync(~0u, ok)) goto wound_down;
                 store(x, (which ? vs : ks) + s * S::kTileBytes);
-                if (lane == 0) mbar_arrive(which ? &v_full[s] : &k_full[s]);
+                const bool withheld = p.withhold && n == 0 && !which;  // tests: nothing completes k_full[0]
+                if (lane == 0 && !withheld) mbar_arrive(which ? &v_full[s] : &k_full[s]);
                 x = y;
             }
             kt += tiles;

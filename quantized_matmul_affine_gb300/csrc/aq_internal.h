@@ -151,7 +151,8 @@ cudaError_t batch_launch(const aq_cache *c, int64_t layer, const BatchArgs &a);
 #ifdef AQ_TEST_HOOKS
 // Test builds only (never in libaq.so): which producer withholds the copies
 // of its first stage, so that the waits on them run out (1 = the resident
-// small-M kernel, 2 = the large-M tensor-core kernel, 0 = none).
+// small-M kernel, 2 = the large-M tensor-core kernel, 3 = the batch
+// attention's kernel for shared keys, 0 = none).
 extern int g_test_withhold;
 // Test builds only: the tensor-core kernel's clustered K split, forced to
 // (CTAs << 8) | tiles a cluster where that plan is valid (-1: never; 0: the

@@ -321,6 +321,48 @@ def test_strided_queries_streams_and_repeats():
         assert torch.equal(o, want)
 
 
+@pytest.mark.parametrize("D,members", [(128, 30), (128, 10), (256, 30)])   # two row tiles, one
+def test_wait_runs_out_then_next_call_is_correct(D, members):
+    # The test build of the library (1 ms waits) keeps the first k tile from
+    # being announced: every wait on it gives up, the call returns and reports
+    # it, and the next call is right.
+    import ctypes
+    from quantized_matmul_affine_gb300 import build
+    if not build.up_to_date(build.TEST_LIB):
+        build.build()
+    prod, lib = aq.load(), ctypes.CDLL(build.TEST_LIB)
+    for name in ("aq_attention_batch", "aq_attention_batch_workspace_bytes", "aq_device_error"):
+        getattr(lib, name).argtypes = getattr(prod, name).argtypes
+        getattr(lib, name).restype = getattr(prod, name).restype
+    c = Case(10, 2, D, 32, 4, 64, "fp16", 1, [9] * members, [(members, 700)])
+    geo = c.geo
+    cache = aq.AqCache(torch.from_numpy(c.pool).cuda(), geo.page, geo.D, geo.bits, geo.group)
+    q, table, lens = c.q.cuda(), _ints(c.table), _ints(c.lens)
+    starts, shared = _ints(c.starts), _ints(c.shared)
+    n = lib.aq_attention_batch_workspace_bytes(cache._ref, c.B, 1, 10, 1)
+    ws, out = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty_like(q)
+    code = ctypes.c_uint32(0)
+
+    def call():
+        st = lib.aq_attention_batch(cache._ref, 0, aq.AQ_F16, q.data_ptr(), 10 * D, table.data_ptr(),
+                                    lens.data_ptr(), starts.data_ptr(), shared.data_ptr(), c.B, 1, 10, 1,
+                                    table.shape[1], c.scale, out.data_ptr(), ws.data_ptr(), n,
+                                    torch.cuda.current_stream().cuda_stream)
+        assert st == 0
+        torch.cuda.synchronize()
+        assert lib.aq_device_error(ctypes.addressof(code), 1) == 0
+        return code.value
+
+    try:
+        lib.aq_test_withhold(3)
+        assert call() & 0xff == 0x06
+    finally:
+        lib.aq_test_withhold(0)
+    for _ in range(3):
+        assert call() == 0
+        c.check(o=out)
+
+
 def test_graph_follows_lengths():
     c = Case(8, 2, 64, 16, 4, 64, "fp16", 1, [300, 250, 200], [(2, 128)])
     geo = c.geo
