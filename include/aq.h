@@ -2,8 +2,9 @@
  * aq.h — C ABI of libaq: y = x . W^T over MLX-style affine group-64 weights
  * at 3 or 4 bits, on one NVIDIA GB300 (sm_103a).  Around it: packing and the
  * float -> affine quantiser, several projections of one x per call (q/k/v,
- * gate/up with SiLU), other code widths and group sizes, and decode
- * attention over a KV cache stored in the same format.
+ * gate/up with SiLU), other code widths and group sizes, decode attention
+ * over a KV cache stored in the same format, and for batches a paged cache
+ * with the operations on its page tables and the attention that reads it.
  *
  * Weight format (mlx-bun pages, @mlx-bun/inference 1.0.0,
  * kernels/quantization/affine-split-mma.ts helper affine_unit and
@@ -34,7 +35,8 @@
  *   - Entry points are thread-safe when different threads use different
  *     streams; results do not depend on the thread or stream.
  *   - Results are deterministic: the same inputs give bit-identical outputs,
- *     call after call (fixed-order reductions, no atomics on data).
+ *     call after call (fixed-order reductions, no atomics on data; the
+ *     reference counts of pages are integers, whose sums have no order).
  *   - Consecutive matmul calls on one stream overlap (programmatic dependent
  *     launch): a call may start reading its Wq, scales and biases while the
  *     previous call on the stream is still running, and reads x and writes
@@ -477,7 +479,8 @@ aq_status aq_cache_compact(const aq_cache *cache, const int32_t *refs_dev,
  * lens, tables and groups are read on the device only, so a captured graph
  * follows their changes.  Served: D in {64, 128, 256, 512}, any H a multiple
  * of KV, 1 <= L <= 64, B <= 1024, G <= 256.  Scores, maxima and sums are fp32;
- * probabilities (times the value scales, or with values dequantised) enter the value product
+ * the probabilities (times the value scales where the codes themselves enter
+ * the product, else against values rounded to fp16) enter the value product
  * as fp16; o is rounded once.  Deterministic.  A page outside the pool, among
  * the tokens that count, sets the error word, and the rows that see it are
  * unspecified.
@@ -485,6 +488,9 @@ aq_status aq_cache_compact(const aq_cache *cache, const int32_t *refs_dev,
  * that is not finite, NULL pointers or a workspace that is too small;
  * AQ_ERR_MISALIGNED; AQ_ERR_UNSUPPORTED for sizes outside the served set;
  * AQ_ERR_CUDA.
+ * Launches: a kernel of one CTA that plans the call from lens and groups; one
+ * on tcgen05 for shared keys where 33 rows or more (B * L * H / KV / G) read
+ * them and D <= 256; one on warp MMA for the rest; one that adds the pieces.
  */
 #define AQ_BATCH_MAX_ROWS 1024
 #define AQ_BATCH_MAX_TOKENS 64
