@@ -5,6 +5,7 @@
 // times W^T, y in x's dtype, an error for no rows; plus the pack step and the
 // explicit-variant and host-memory entry points described in aq.h.
 #include "aq_internal.h"
+#include "aq_paged.h"
 
 #include <cudaTypedefs.h>
 
@@ -811,7 +812,8 @@ const char *aq_version(void) { return "aq 0.1.0 (sm_103a)"; }
 
 #ifdef AQ_TEST_HOOKS
 // Test builds only: make a producer withhold the copies of its first stage
-// (see g_test_withhold), so that a test can watch a bounded wait run out.
+// (see g_test_withhold; 3: the batch attention's kernel for shared keys), so
+// that a test can watch a bounded wait run out.
 void aq_test_withhold(int what) { aq::g_test_withhold = what; }
 // Test builds only: force the tensor-core kernel's clustered K split to
 // `ctas` CTAs sharing `tiles` tiles where that plan is valid (ctas = -1:

@@ -1,7 +1,7 @@
 // Geometry of the paged quantised KV cache, shared by its translation units.
 #pragma once
 
-#include "aq_internal.h"
+#include "aq_paged.h"
 
 #include <atomic>
 
