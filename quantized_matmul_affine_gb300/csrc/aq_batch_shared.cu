@@ -99,6 +99,19 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
         : "memory");
 }
 
+// Sixteen columns: a load that waits.
+__device__ __forceinline__ void tmem_ld16w(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -188,6 +201,8 @@ __device__ __forceinline__ bool row_tile_all(int wg, bool me) {
     return all != 0;
 }
 
+constexpr uint32_t kNoRow = 0xffffffffu;  // of a row tile: past the piece's rows
+
 // A bounded wait that records where it gave up.
 __device__ __forceinline__ bool shd_wait(uint64_t *bar, uint32_t parity, volatile int *flag,
                                          uint32_t *err, uint32_t code) {
@@ -210,7 +225,8 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
     uint8_t *vs = ks + 2 * S::kTileBytes;                // [2] v tiles
     float *qsc = reinterpret_cast<float *>(vs + 2 * S::kTileBytes);  // [row tiles][128]
     float *xch = qsc + S::kRT * 128;                     // [2][row tiles][halves][128]
-    uint64_t *k_full = reinterpret_cast<uint64_t *>(xch + 2 * S::kRT * 256);
+    uint32_t *row_ids = reinterpret_cast<uint32_t *>(xch + 2 * S::kRT * 256);  // [row tiles][128]
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(row_ids + S::kRT * 128);
     uint64_t *k_empty = k_full + 2, *v_full = k_empty + 2, *v_empty = v_full + 2;
     uint64_t *s_full = v_empty + 2, *p_ready = s_full + 2, *o_done = p_ready + 2;
     uint64_t *q_ready = o_done + 1, *drain = q_ready + 1;
@@ -260,10 +276,20 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
         // counts.
         const int wg = warp >> 3, half = (warp >> 2) & 1;
         constexpr int KH = KT / 2;
+        uint32_t *rows = row_ids + wg * 128;
         bool ok = wg < row_tiles;
         for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x, ++piece) {
             const Piece w = shared_piece(p, item);
             const int tiles = (w.k1 - w.k0 + KT - 1) / KT;
+            const int rl = (warp & 3) * 32 + lane, r = wg * 128 + rl;
+            // where the row tile's rows lie: (sequence x L + token) and head of each
+            if (half == 0) {
+                const int LR = p.L * p.R, at = w.r0 + r, i = at / LR, lr = at - i * LR, l = lr / p.R;
+                rows[rl] = r < w.rows ? (uint32_t)(i * p.L + l) << 16 |
+                                            (uint32_t)(w.kv * p.R + lr - l * p.R)
+                                      : kNoRow;
+            }
+            row_tile_sync(wg);
             // q' of this row tile.  The last piece's MMAs are done (o_done), and
             // its O has been read: the MMAs of this piece wait for q_ready.
             {
@@ -273,8 +299,12 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
 #pragma unroll 4  // loads under way together
                 for (int r = (warp & 7) * RPW + lane / LPR; r < 128; r += 8 * RPW) {
                     uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-                    if (wg * 128 + r < w.rows)
-                        raw = *reinterpret_cast<const uint4 *>(q_row(p, w, wg * 128 + r) + 8 * c);
+                    const uint32_t id = rows[r];
+                    if (id != kNoRow)
+                        raw = *reinterpret_cast<const uint4 *>(
+                            static_cast<const uint16_t *>(p.q) +
+                            ((int64_t)w.b0 * p.L + (id >> 16)) * p.q_stride +
+                            (int)(id & 0xffffu) * D + 8 * c);
                     const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
                     float f[8], mx = 0.f;
 #pragma unroll
@@ -304,7 +334,6 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                 row_tile_sync(wg);  // qsc of the row tile
                 if (lane == 0) mbar_arrive(q_ready);
             }
-            const int rl = (warp & 3) * 32 + lane, r = wg * 128 + rl;
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
             const uint32_t o_at = tmem + lanes + S::kTmemO + wg * D + half * (D / 2);
             float *other = xch + (wg * 2 + (half ^ 1)) * 128 + rl;   // of the row's other half
@@ -411,27 +440,48 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
             row_tile_sync(wg);
             if (ok) {
                 tc_fence_after();
-                const bool in = r < w.rows;
-                const int64_t at = in ? part_row(p, w, r) : 0;
-                if (in && half == 0) p.part_ml[at] = make_float2(m, *mine + *other);
-                float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * D + half * (D / 2));
+                auto part = [&](uint32_t id) {
+                    return ((int64_t)w.slot0 * p.L + (id >> 16)) * p.H + (id & 0xffffu);
+                };
+                if (half == 0 && rows[rl] != kNoRow)
+                    p.part_ml[part(rows[rl])] = make_float2(m, *mine + *other);
+                // O through this row tile's q' (done with), a quarter of the columns
+                // at a time: a thread has a row, but memory wants a row's columns
+                // next to each other.  Chunks of 16 bytes, swizzled by row.
+                constexpr int CR = D / 4, CH = CR / 4;
+                float4 *stage = reinterpret_cast<float4 *>(qs + wg * S::kQBytes + half * (S::kQBytes / 2)) +
+                                (warp & 3) * 32 * CH;
+                auto spot = [&](int row, int chunk) {
+                    return row * CH + (chunk ^ (D == 64 ? (row >> 1) & 3 : row & 7));
+                };
 #pragma unroll 1
-                for (int k = 0; k < D / 2; k += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(o_at + k, o);
-                    tmem_wait_ld32(o);
-                    if (!in) continue;
+                for (int round = 0; round < 2; ++round) {
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const uint32_t *u = o + 8 * g;
+                    for (int k = 0; k < CR; k += 16) {
+                        uint32_t u[16];
+                        tmem_ld16w(o_at + round * CR + k, u);
                         constexpr int i1 = BITS == 4 ? 2 : 1, i4 = BITS == 4 ? 1 : 4;
-                        dst[k / 4 + 2 * g] = make_float4(
-                            __uint_as_float(u[0]), __uint_as_float(u[i1]),
-                            __uint_as_float(u[2 * i1]), __uint_as_float(u[3 * i1]));
-                        dst[k / 4 + 2 * g + 1] = make_float4(
-                            __uint_as_float(u[i4]), __uint_as_float(u[i4 + i1]),
-                            __uint_as_float(u[i4 + 2 * i1]), __uint_as_float(u[i4 + 3 * i1]));
+#pragma unroll
+                        for (int g = 0; g < 16; g += 8) {
+                            const uint32_t *x = u + g;
+                            stage[spot(lane, (k + g) / 4)] = make_float4(
+                                __uint_as_float(x[0]), __uint_as_float(x[i1]),
+                                __uint_as_float(x[2 * i1]), __uint_as_float(x[3 * i1]));
+                            stage[spot(lane, (k + g) / 4 + 1)] = make_float4(
+                                __uint_as_float(x[i4]), __uint_as_float(x[i4 + i1]),
+                                __uint_as_float(x[i4 + 2 * i1]), __uint_as_float(x[i4 + 3 * i1]));
+                        }
                     }
+                    __syncwarp();
+#pragma unroll 4
+                    for (int i = lane; i < 32 * CH; i += 32) {
+                        const int row = i / CH, chunk = i % CH;
+                        const uint32_t id = rows[(warp & 3) * 32 + row];
+                        if (id != kNoRow)
+                            reinterpret_cast<float4 *>(p.part_o + part(id) * D + half * (D / 2) +
+                                                       round * CR)[chunk] = stage[spot(row, chunk)];
+                    }
+                    __syncwarp();
                 }
             }
             row_tile_sync(wg);  // the exchange is read before the next piece's
@@ -679,7 +729,7 @@ cudaError_t shared_run(const BatchParams &p, int row_tiles, int grid, cudaStream
     using S = Shd<BITS, D, GROUP>;
     auto kern = shared_kernel<BITS, D, GROUP>;
     constexpr size_t body = 1024 + (size_t)S::kRT * S::kQBytes + 4 * (size_t)S::kTileBytes +
-                            S::kRT * 2560 + 18 * 8;
+                            S::kRT * 3072 + 18 * 8;
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [&] {
