@@ -248,18 +248,20 @@ __global__ void __launch_bounds__(WPR == 1 ? 128 : 32 * WPR)
     constexpr int kPart = WPR > 1 ? WPR : 1;
     __shared__ float4 part[kPart][D / 4];
     __shared__ float psum[kPart];
-    launch_dependents();
-    grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = WPR == 1 ? 0 : warp;
     const int64_t row = WPR == 1 ? (int64_t)blockIdx.x * kRows + warp : (int64_t)blockIdx.x;
     const int64_t LH = (int64_t)p.L * p.H;
-    if (row >= p.B * LH) return;  // whole warps, and only with one warp a row
+    if (row >= p.B * LH) {  // whole warps, and only with one warp a row
+        grid_dependency_wait();
+        return;
+    }
     const int b = (int)(row / LH);
     const int lh = (int)(row - b * LH), l = lh / p.H, h = lh - l * p.H;
     const int kv = h / p.R, lr = l * p.R + (h - kv * p.R), LR = p.L * p.R;
-    const int per = p.head->per;
-    const PlanRow d = p.rows[b];
+    // the plan was complete before the kernel before this one let it start
+    const int per = __ldcg(reinterpret_cast<const int *>(p.head));
+    const PlanRow d = plan_load(p.rows + b);
     // pieces of a segment of `tiles` tiles from tile u0 on
     auto pieces = [&](int u0, int tiles) {
         return tiles > 0 ? (u0 + tiles - 1) / per - u0 / per + 1 : 0;
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(WPR == 1 ? 128 : 32 * WPR)
         pieces(d.at + (kv * ceil_div(LR, p.own_rows) + lr / p.own_rows) * d.tiles, d.tiles);
     int sh_n = 0, sh0 = 0, sh_step = 0;
     if (d.group >= 0) {
-        const PlanGroup g = p.groups[d.group];
+        const PlanGroup g = plan_load(p.groups + d.group);
         const int place = b - g.first;
         sh0 = g.slot + place;
         sh_step = g.rows;
@@ -280,6 +282,8 @@ __global__ void __launch_bounds__(WPR == 1 ? 128 : 32 * WPR)
                             g.pieces);
     }
     const int n = sh_n + own_n;
+    launch_dependents();
+    grid_dependency_wait();
     auto slot_row = [&](int i) -> int64_t {
         const int64_t s = i < sh_n ? sh0 + (int64_t)i * sh_step : own0 + (i - sh_n);
         return s * LH + lh;
