@@ -417,14 +417,18 @@ def aq_cache_record_bytes(D: int, page: int, bits: int, group_size: int) -> int:
     return int(load().aq_cache_record_bytes(D, page, bits, group_size))
 
 
+@functools.lru_cache(maxsize=256)
 def aq_cache_workspace_bytes(n_pages: int, B: int) -> int:
     """Workspace bytes of aq_cache_grow and aq_cache_compact."""
     return int(load().aq_cache_workspace_bytes(n_pages, B))
 
 
+_I32 = torch.int32
+
+
 def _ints(t: torch.Tensor, name: str, *shape) -> int:
     """The address of a dense int32 device tensor of this shape."""
-    if t.dtype != torch.int32 or t.shape != shape:
+    if t.dtype is not _I32 or t.shape != shape:
         raise ValueError(f"{name} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
     if not t.is_cuda or not t.is_contiguous():
         return _dev(t, name)  # says which
@@ -495,29 +499,44 @@ def aq_cache_copy(cache: AqCache, src, dst, stream=None) -> None:
                                 _stream(stream)), "aq_cache_copy")
 
 
-def _tables(cache, refs, table, lens, in_place, out, with_lens=True):
-    """Addresses of the inputs and outputs of a page-table operation, the
-    outputs and a new status tensor."""
+def _tables(f, cache, refs, table, lens, args, in_place, out, workspace, stream, with_lens=True):
+    """Calls a page-table operation f: the checks and the outputs that they
+    share.  args: (name, tensor) of its other inputs; workspace: None where it
+    takes none, else a list with the caller's tensor or None."""
     B, width = _table_shape(table)
-    ins = (_ints(refs, "refs", cache.n_pages), _ints(table, "table", B, width),
-           _ints(lens, "lens", B))
-    given = (refs, table, lens) if with_lens else (refs, table)
-    status = torch.empty(4, dtype=torch.int32, device=refs.device)
+    r, t, n = (_ints(refs, "refs", cache.n_pages), _ints(table, "table", B, width),
+               _ints(lens, "lens", B))
+    more = [_ints(x, name, B) for name, x in args]
+    status = torch.empty(4, dtype=_I32, device=refs.device)
     if out is None and in_place:
-        return B, width, ins, ins[:len(given)], given, status
-    if out is None:
-        out = [torch.empty_like(t) for t in given]
-        return B, width, ins, [o.data_ptr() for o in out], out, status
-    ptrs = [_ints(o, f"out[{i}]", *t.shape) for i, (o, t) in enumerate(zip(out, given))]
-    return B, width, ins, ptrs, out, status
-
-
-def _cache_workspace(cache, B, workspace, stream):
+        res, outs = [refs, table, lens], [r, t, n]
+    elif out is None:
+        res = [torch.empty_like(refs), torch.empty_like(table)]
+        if with_lens:
+            res.append(torch.empty_like(lens))
+        outs = [o.data_ptr() for o in res]
+    else:
+        res = list(out)
+        given = (refs, table, lens) if with_lens else (refs, table)
+        if len(res) != len(given):
+            raise ValueError(f"out must be {len(given)} tensors")
+        outs = [_ints(o, f"out[{i}]", *g.shape) for i, (o, g) in enumerate(zip(res, given))]
+    if not with_lens:
+        del res[2:], outs[2:]
     if workspace is None:
-        workspace = _scratch(aq_cache_workspace_bytes(cache.n_pages, B), cache.pool.device, stream)
-    if workspace.dtype != torch.uint8:
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    return _dev(workspace, "workspace"), workspace.numel(), workspace
+        st = f(cache._ref, r, t, n, *more, B, width, *outs, status.data_ptr(), _stream(stream))
+    else:
+        ws = workspace[0]
+        if ws is None:
+            ws = _scratch(aq_cache_workspace_bytes(cache.n_pages, B), cache.pool.device, stream)
+        if ws.dtype != torch.uint8:
+            raise ValueError("workspace must be a contiguous uint8 tensor")
+        st = f(cache._ref, r, t, n, *more, B, width, *outs, status.data_ptr(),
+               _dev(ws, "workspace"), ws.numel(), _stream(stream))
+    if st:
+        _check(st, f.__name__)
+    res.append(status)
+    return tuple(res)
 
 
 def aq_cache_fork(cache, refs, table, lens, parent, keep, in_place=True, out=None,
@@ -526,42 +545,31 @@ def aq_cache_fork(cache, refs, table, lens, parent, keep, in_place=True, out=Non
     tokens (keep[b] < 0: all).  refs int32 [n_pages], table int32
     [B, max_pages], lens, parent, keep int32 [B].  Returns (refs, table, lens,
     status): the same tensors, or new ones with in_place=False (or out)."""
-    B, width, ins, outs, res, status = _tables(cache, refs, table, lens, in_place, out)
-    _check(load().aq_cache_fork(cache._ref, *ins, _ints(parent, "parent", B),
-                                _ints(keep, "keep", B), B, width, *outs, status.data_ptr(),
-                                _stream(stream)), "aq_cache_fork")
-    return (*res, status)
+    return _tables(load().aq_cache_fork, cache, refs, table, lens,
+                   (("parent", parent), ("keep", keep)), in_place, out, None, stream)
 
 
 def aq_cache_trim(cache, refs, table, lens, keep, in_place=True, out=None, stream=None) -> tuple:
     """Row b with 0 <= keep[b] < lens[b] is cut to keep[b] tokens (0 frees
     it).  Arguments and results as aq_cache_fork."""
-    B, width, ins, outs, res, status = _tables(cache, refs, table, lens, in_place, out)
-    _check(load().aq_cache_trim(cache._ref, *ins, _ints(keep, "keep", B), B, width, *outs,
-                                status.data_ptr(), _stream(stream)), "aq_cache_trim")
-    return (*res, status)
+    return _tables(load().aq_cache_trim, cache, refs, table, lens, (("keep", keep),), in_place, out,
+                   None, stream)
 
 
 def aq_cache_grow(cache, refs, table, lens, add, in_place=True, out=None, workspace=None,
                   stream=None) -> tuple:
     """Pages for add[b] more tokens of every row, with copy on write of shared
     partial pages.  Arguments and results as aq_cache_fork."""
-    B, width, ins, outs, res, status = _tables(cache, refs, table, lens, in_place, out)
-    ws, n, keep_alive = _cache_workspace(cache, B, workspace, stream)
-    _check(load().aq_cache_grow(cache._ref, *ins, _ints(add, "add", B), B, width, *outs,
-                                status.data_ptr(), ws, n, _stream(stream)), "aq_cache_grow")
-    return (*res, status)
+    return _tables(load().aq_cache_grow, cache, refs, table, lens, (("add", add),), in_place, out,
+                   [workspace], stream)
 
 
 def aq_cache_compact(cache, refs, table, lens, in_place=True, out=None, workspace=None,
                      stream=None) -> tuple:
     """Moves the live pages to the front of the pool.  Returns (refs, table,
     status); lens is only read."""
-    B, width, ins, outs, res, status = _tables(cache, refs, table, lens, in_place, out, False)
-    ws, n, keep_alive = _cache_workspace(cache, B, workspace, stream)
-    _check(load().aq_cache_compact(cache._ref, *ins, B, width, *outs, status.data_ptr(), ws, n,
-                                   _stream(stream)), "aq_cache_compact")
-    return (*res, status)
+    return _tables(load().aq_cache_compact, cache, refs, table, lens, (), in_place, out, [workspace],
+                   stream, False)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -593,36 +601,45 @@ def aq_attention_batch(q, cache: AqCache, layer: int, table, lens, scale: float,
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
     B, L, H, D = q.shape
-    stride = H * D
-    if B * L > 1:
-        stride = q.stride(1) if L > 1 else q.stride(0)
-        if L > 1 and B > 1 and q.stride(0) != L * stride:
-            raise ValueError("q: tokens must lie a fixed step apart")
-    if q.numel() and (q.stride(3) != 1 or (H > 1 and q.stride(2) != D)):
-        raise ValueError("q: a token's heads must be dense")
+    step = H * D
+    stride = step
+    if not q.is_contiguous():
+        sb, sl, sh, sd = q.stride()
+        if B * L > 1:
+            stride = sl if L > 1 else sb
+        if (L > 1 and B > 1 and sb != L * stride) or sd != 1 or (H > 1 and sh != D):
+            raise ValueError("q: a token's heads must be dense, and tokens a fixed step apart")
     rows, width = _table_shape(table)
     if rows != B:
         raise ValueError(f"table has {rows} rows for {B} sequences")
     G = 0
     gs = sh = None
-    if (group_start is None) != (shared is None):
-        raise ValueError("group_start and shared go together")
-    if shared is not None:
+    if shared is not None and group_start is not None:
         G = shared.numel()
         gs, sh = _ints(group_start, "group_start", G + 1), _ints(shared, "shared", G)
+    elif shared is not None or group_start is not None:
+        raise ValueError("group_start and shared go together")
     if out is None:
-        out = torch.empty((B, L, H, D), dtype=q.dtype, device=q.device)
-    _check_out(out, "out", B * L * H * D, q.dtype)
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        to = out.data_ptr()
+    else:
+        _check_out(out, "out", B * L * step, q.dtype)
+        to = _dev(out, "out")
     if workspace is None:
         n = aq_attention_batch_workspace_bytes(cache, B, L, H, G)
-        workspace = _scratch(max(n, 256), q.device, stream)
-    if workspace.dtype != torch.uint8:
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    _check(load().aq_attention_batch(cache._ref, layer, AQ_BF16 if q.dtype == torch.bfloat16 else AQ_F16,
-                                  q.data_ptr(), stride, _ints(table, "table", B, width),
-                                  _ints(lens, "lens", B), gs, sh, B, L, H, G, width, scale,
-                                  _dev(out, "out"), _dev(workspace, "workspace"),
-                                  workspace.numel(), _stream(stream)), "aq_attention_batch")
+        n = n or 256  # so that refused sizes reach the library's checks
+        workspace = _scratch(n, q.device, stream)
+        ws = workspace.data_ptr()
+    else:
+        if workspace.dtype != torch.uint8:
+            raise ValueError("workspace must be a contiguous uint8 tensor")
+        n, ws = workspace.numel(), _dev(workspace, "workspace")
+    st = load().aq_attention_batch(cache._ref, layer, AQ_F16 if q.dtype is torch.float16 else AQ_BF16,
+                                   q.data_ptr(), stride, _ints(table, "table", B, width),
+                                   _ints(lens, "lens", B), gs, sh, B, L, H, G, width, scale, to, ws,
+                                   n, _stream(stream))
+    if st:
+        _check(st, "aq_attention_batch")
     return out
 
 
