@@ -489,7 +489,7 @@ aq_status aq_cache_compact(const aq_cache *cache, const int32_t *refs_dev,
  * AQ_ERR_MISALIGNED; AQ_ERR_UNSUPPORTED for sizes outside the served set;
  * AQ_ERR_CUDA.
  * Launches: a kernel of one CTA that plans the call from lens and groups; one
- * on tcgen05 for shared keys where 33 rows or more (B * L * H / KV / G) read
+ * on tcgen05 for shared keys where 17 rows or more (B * L * H / KV / G) read
  * them and D <= 256; one on warp MMA for the rest; one that adds the pieces.
  */
 #define AQ_BATCH_MAX_ROWS 1024

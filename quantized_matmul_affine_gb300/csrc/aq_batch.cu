@@ -17,7 +17,8 @@ constexpr int kPlanThreads = 256;
 // The tables of aq_batch.cuh, by one CTA.  What it costs is latency - of its
 // loads, barriers and, cold as it is in every call, its own instructions - so
 // sums are a warp reduction and a shared-memory add, and what concerns groups
-// every warp works out for itself.
+// every warp works out for itself.  10 us by itself with cold caches; a whole
+// call over one sequence of 37 tokens takes 9.7 when replayed.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ BatchParams p) {
     extern __shared__ PlanGroup s_g[];                       // [G]
     int *s_n = reinterpret_cast<int *>(s_g + p.G);           // [G] rows that share
@@ -240,6 +241,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 // device; eight, which take every eighth slot and add up in warp order, where
 // a few rows have hundreds of slots each (one row of a 32k-token sequence:
 // 200).  A row without slots, or whose keys were all past its limit, is zeros.
+// Bound by the latency of its dependent loads: 5120 rows of 128, 24 MB of
+// partial results, take 15 us with cold caches, DRAM at 20 %.
 template <int D, int WPR>
 __global__ void __launch_bounds__(WPR == 1 ? 128 : 32 * WPR)
     join_kernel(const __grid_constant__ BatchParams p) {
@@ -370,7 +373,10 @@ cudaError_t plan_run(const BatchParams &p, cudaStream_t stream) {
 template <int D>
 cudaError_t join_run(const BatchParams &p, cudaStream_t stream) {
     const int64_t rows = (int64_t)p.B * p.L * p.H;
-    const bool wide = rows <= 4 * (int64_t)num_sms();
+    // eight warps a row while all rows then run at once (16 sequences of 4k
+    // tokens, 640 rows: 24.5 us, 29.2 with one; 64 sequences over 8k shared
+    // tokens, 2560 rows: 63.8 and 60.4)
+    const bool wide = rows <= 8 * (int64_t)num_sms();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 3) / 4), 1, 1);
     cfg.blockDim = dim3(wide ? 256 : 128, 1, 1);
@@ -405,9 +411,16 @@ cudaError_t own_dispatch(const aq_cache *c, const BatchRun &r) {
 BatchPlan plan_for(const aq_cache *c, int64_t B, int64_t L, int64_t H, int64_t G) {
     BatchPlan pl = {};
     const int64_t R = H / c->KV;
-    // rows a KV head that read a group's shared keys, if the groups are even
+    // Rows a KV head that read a group's shared keys, if the groups are even.
+    // Up to 16 are one tile of own_kernel, which the tensor core's 128 only beats
+    // where there is a group or two (10 rows, 5 heads of 128 at 4 bits over 4k
+    // shared tokens: one group 23 us with own_kernel, 18 with shared_kernel;
+    // eight groups 44 and 58).  Above it reads the codes once more a tile (25
+    // rows in each of eight groups: 78 and 67 us; 20 in each of sixteen at 8
+    // bits: 136 and 105).  Two row tiles share the keys' dequantising (160 rows
+    // over 8k tokens: 48 us with one, 46 with two).
     const int64_t rows = G > 0 ? B * L * R / G : 0;
-    if (c->D <= 256 && rows > 32) pl.row_tiles = c->D <= 128 && rows > 128 ? 2 : 1;
+    if (c->D <= 256 && rows > 16) pl.row_tiles = c->D <= 128 && rows > 128 ? 2 : 1;
     pl.nb = c->D < 512 && (L * R > 8 || (G > 0 && !pl.row_tiles)) ? 2 : 1;
     pl.own_rows = 8 * pl.nb;
     BatchRun r = {};
