@@ -25,8 +25,8 @@
 //
 // What bounds it: the cache's bytes are 2 D bits/8 + 8 D/group a key and head
 // (30.8 us for 24 ragged sequences of up to 8k rows, 8 heads of 256 at 4 bits)
-// and it takes 57 us of the call's 73.  Issue slots are 58 % taken and DRAM is
-// at 43 %; the registers (184 a lane) leave 8 warps an SM, so that neither
+// and it takes 61 us of the call's 72.  Issue slots are 56 % taken and DRAM is
+// at 46 %; the registers (242 a lane) leave 8 warps an SM, so that neither
 // hides the other's latency: fewer query rows than the MMA's eight columns
 // make each code's unpacking dear.
 #pragma once

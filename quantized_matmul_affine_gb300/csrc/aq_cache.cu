@@ -103,8 +103,8 @@ constexpr int kRowLoads = 4;  // 16-byte loads a lane has under way
 //
 // Bytes: 2 a value in, bits / 8 and a pair a group out - 12.7 us at 16k bf16
 // tokens of 8 heads of 128 to 4 bits, where it takes 36.  The issue slots are
-// 74 % taken (a value costs a clamp, two fused steps and a shifted add, a
-// group six shuffles), DRAM 20 %: bound by instructions, and in a decode step
+// 73 % taken (a value costs a clamp, two fused steps and a shifted add, a
+// group six shuffles), DRAM 25 %: bound by instructions, and in a decode step
 // (64 tokens) by its chain of loads, 3 to 4 us.
 template <int BITS, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_constant__ RowParams p) {
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const __grid_consta
 // The reverse, shared out alike: one lane turns 8 codes into 8 values of the
 // output type, each scale * code + bias in one fp32 fma (the product is exact)
 // and one rounding.  16k tokens as above: 20 us against 12.7 of traffic, the
-// issue slots 69 % taken (a shift, a mask, an add and an fma a value).
+// issue slots 70 % taken (a shift, a mask, an add and an fma a value).
 template <int BITS, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant__ RowParams p) {
     const int which = blockIdx.y;
