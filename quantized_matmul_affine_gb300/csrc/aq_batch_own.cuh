@@ -47,8 +47,8 @@ struct Own {
     static constexpr int kG = D / GROUP;
     static constexpr int kGB = GROUP * BITS / 8;       // bytes of a group's codes
     // 16-key blocks a tile: two where a row is short or its codes cost the most
-    // work a byte (24 sequences of 8k rows of 256 at 4 bits: 76 us with one, 70
-    // with two; 128-byte rows at 8 bits: 182 and 187 us with the shared part)
+    // work a byte (24 sequences of up to 8k rows of 256 at 4 bits: 80 us with
+    // one, 72 with two, 75 with one at 168 registers and three CTAs an SM; 128-byte rows at 8 bits: 182 and 187 us with the shared part)
     static constexpr int kBlk = kRB <= 64 || (kRB == 128 && BITS == 4) ? 2 : 1;
     static constexpr int kKeys = 16 * kBlk;            // keys a tile
     static constexpr int kKS = kRB + (kRB >= 64 ? 32 : 0);  // K row stride in the ring
