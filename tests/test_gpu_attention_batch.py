@@ -212,6 +212,21 @@ def test_same_bits_every_time(H, KV, D, page, bits, group, dtype, L, members, sh
     assert all(torch.equal(o, outs[0]) for o in outs)
 
 
+@pytest.mark.parametrize("H,KV,D,page,bits,group,dtype,groups", [
+    (2, 2, 64, 16, 4, 32, "fp16", [(16, 333)]),        # 16 rows a KV head
+    (2, 2, 64, 16, 4, 32, "fp16", [(17, 333)]),        # 17
+    (10, 2, 128, 64, 8, 64, "bf16", [(3, 1000)]),      # 15
+    (10, 2, 128, 64, 8, 64, "bf16", [(4, 1000)]),      # 20
+    (2, 1, 256, 32, 4, 128, "bf16", [(9, 700)]),       # 18 of 256
+    (4, 1, 128, 32, 4, 64, "fp16", [(1, 90), (2, 400), (12, 257), (0, 5)]),   # 15 on average, one group of 48
+    (4, 1, 128, 32, 4, 64, "fp16", [(2, 400), (16, 257), (1, 70)]),           # 25 on average, one group of 8
+])
+def test_rows_around_the_choice_of_kernel(H, KV, D, page, bits, group, dtype, groups):
+    rng = np.random.default_rng(10)
+    own = [int(x) for x in rng.integers(1, 60, size=sum(n for n, _ in groups))]
+    Case(H, KV, D, page, bits, group, dtype, 1, own, groups).check()
+
+
 def test_several_large_groups():
     rng = np.random.default_rng(8)
     own = [int(x) for x in rng.integers(1, 100, size=75)]
