@@ -479,17 +479,23 @@ def aq_cache_read(cache: AqCache, layer: int, cu, start, table, total: int, dtyp
     B, width = _table_shape(table)
     shape = (total, cache.kv_heads, cache.head_dim)
     if out is None:
-        both = torch.empty((2, *shape), dtype=dtype, device=cache.pool.device)
-        out = (both[0], both[1])
-    for name, t in zip(("k", "v"), out):
-        if t.dtype != dtype or tuple(t.shape) != shape:
-            raise ValueError(f"out {name} must be {dtype} {list(shape)}")
-    _check(load().aq_cache_read(cache._ref, layer, AQ_BF16 if dtype == torch.bfloat16 else AQ_F16,
-                                _dev(out[0], "out k"), _dev(out[1], "out v"), total,
-                                _ints(cu, "cu", B + 1), _ints(start, "start", B),
-                                _ints(table, "table", B, width), B, width, _stream(stream)),
-           "aq_cache_read")
-    return tuple(out)
+        if total < 0:
+            raise ValueError("total must not be negative")
+        k = torch.empty(shape, dtype=dtype, device=cache.pool.device)
+        v = torch.empty_like(k)
+        kp, vp = k.data_ptr(), v.data_ptr()
+    else:
+        k, v = out
+        for name, t in (("k", k), ("v", v)):
+            if t.dtype != dtype or tuple(t.shape) != shape:
+                raise ValueError(f"out {name} must be {dtype} {list(shape)}")
+        kp, vp = _dev(k, "out k"), _dev(v, "out v")
+    st = load().aq_cache_read(cache._ref, layer, AQ_BF16 if dtype is torch.bfloat16 else AQ_F16, kp, vp,
+                              total, _ints(cu, "cu", B + 1), _ints(start, "start", B),
+                              _ints(table, "table", B, width), B, width, _stream(stream))
+    if st:
+        _check(st, "aq_cache_read")
+    return k, v
 
 
 def aq_cache_copy(cache: AqCache, src, dst, stream=None) -> None:
