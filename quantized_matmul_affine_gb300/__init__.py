@@ -129,15 +129,36 @@ def _stream(stream) -> int:
     return int(stream)
 
 
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """A workspace for one call: handed back to torch's allocator on return,
-    so a call on another stream than the current one has to be known to it."""
-    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-        t.record_stream(stream)
+def _side(stream, device):
+    """The torch stream of a call that is not on the current one, else None."""
+    if stream is None or device.type != "cuda":
+        return None
+    here = torch.cuda.current_stream(device)
+    if _stream(stream) == here.cuda_stream:
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def _empty(shape, dtype, device, stream, result=True) -> torch.Tensor:
+    """Memory that a call writes, of the call's stream: a block of the current
+    stream's may still be in use by kernels that wait there, and would return
+    there while this call's run.  A result is also known to the current
+    stream, where the caller may drop it while kernels there read it."""
+    side = _side(stream, device)
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(torch.cuda.current_stream(device))
     return t
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace for one call, handed back to its stream's memory on return."""
+    return _empty(nbytes, torch.uint8, device, stream, result=False)
 
 
 def _check(status: int, what: str) -> None:
@@ -207,7 +228,7 @@ def aq_pack(codes: torch.Tensor, bits: int, words: Optional[torch.Tensor] = None
     if codes.dtype != torch.uint8:
         raise ValueError("codes must be uint8")
     if words is None:
-        words = torch.empty((N, K * bits // 32), dtype=torch.int32, device=codes.device)
+        words = _empty((N, K * bits // 32), torch.int32, codes.device, stream)
     elif bits in (2, 3, 4, 5, 6, 8) and K % 32 == 0:
         _sized(words, "words", N * K * bits // 8)
     _check(load().aq_pack(_dev(codes, "codes"), N, K, bits, _dev(words, "words"),
@@ -220,9 +241,9 @@ def _quantize(dtype, w: torch.Tensor, bits: int, stream) -> tuple:
     if w.dtype != want:
         raise ValueError(f"w must be {want}")
     N, K = w.shape
-    Wq = torch.empty((N, K * bits // 32), dtype=torch.int32, device=w.device)
-    scales = torch.empty((N, K // 64), dtype=torch.float16, device=w.device)
-    biases = torch.empty((N, K // 64), dtype=torch.float16, device=w.device)
+    Wq = _empty((N, K * bits // 32), torch.int32, w.device, stream)
+    scales = _empty((N, K // 64), torch.float16, w.device, stream)
+    biases = _empty((N, K // 64), torch.float16, w.device, stream)
     f = load().aq_quantize if dtype == AQ_F16 else load().aq_quantize_bf16
     _check(f(_dev(w, "w"), N, K, bits, _dev(Wq, "Wq"), _dev(scales, "scales"),
              _dev(biases, "biases"), _stream(stream)), "aq_quantize")
@@ -252,7 +273,7 @@ def _mm(variant: int, dtype: int, x, Wq, scales, biases, bits, out, stream) -> t
     if bits in (3, 4):
         _check_weights(Wq, scales, biases, N, K, bits, 64)
     if out is None:
-        out = torch.empty((*x.shape[:-1], N), dtype=x.dtype, device=x.device)
+        out = _empty((*x.shape[:-1], N), x.dtype, x.device, stream)
     _check_out(out, "out", M * N, x.dtype)
     _check(load().aq_matmul_variant(variant, dtype, _dev(x, "x"), _dev(Wq, "Wq"),
                                     _dev(scales, "scales"), _dev(biases, "biases"), M, N, K,
@@ -281,7 +302,7 @@ def aq_matmul_ex(x, Wq, scales, biases, bits, group_size, out=None, stream=None)
     N = scales.shape[0]
     _check_weights(Wq, scales, biases, N, K, bits, group_size)
     if out is None:
-        out = torch.empty((*x.shape[:-1], N), dtype=x.dtype, device=x.device)
+        out = _empty((*x.shape[:-1], N), x.dtype, x.device, stream)
     _check_out(out, "out", M * N, x.dtype)
     _check(load().aq_matmul_ex(dtype, _dev(x, "x"), _dev(Wq, "Wq"), _dev(scales, "scales"),
                                _dev(biases, "biases"), M, N, K, bits, group_size,
@@ -289,7 +310,7 @@ def aq_matmul_ex(x, Wq, scales, biases, bits, group_size, out=None, stream=None)
     return out
 
 
-def _attention_args(q, k, v, bits, group_size, out):
+def _attention_args(q, k, v, bits, group_size, out, stream):
     if q.dtype not in _ACT:
         raise ValueError("q must be float16 or bfloat16")
     if q.dim() != 2 or len(k) != 3 or len(v) != 3 or any(t.dim() != 3 for t in (*k, *v)):
@@ -303,7 +324,7 @@ def _attention_args(q, k, v, bits, group_size, out):
             _sized(sc, f"{side}_scales", 2 * KV * N * (D // group_size), torch.float16)
             _sized(bi, f"{side}_biases", 2 * KV * N * (D // group_size), torch.float16)
     if out is None:
-        out = torch.empty((H, D), dtype=q.dtype, device=q.device)
+        out = _empty((H, D), q.dtype, q.device, stream)
     _check_out(out, "out", H * D, q.dtype)
     ptrs = (_dev(q, "q"), _dev(k[0], "k_words"), _dev(k[1], "k_scales"), _dev(k[2], "k_biases"),
             _dev(v[0], "v_words"), _dev(v[1], "v_scales"), _dev(v[2], "v_biases"))
@@ -314,7 +335,7 @@ def aq_attention_decode(q, k, v, bits, group_size, out=None, stream=None) -> tor
     """Decode attention over a quantised KV cache.  q [H, D] (fp16 or bf16);
     k and v are (words [KV, N, D*bits/32] int32, scales [KV, N, D/group] fp16,
     biases [KV, N, D/group] fp16).  Returns o [H, D] in q's dtype."""
-    dtype, ptrs, (H, KV, N, D), out = _attention_args(q, k, v, bits, group_size, out)
+    dtype, ptrs, (H, KV, N, D), out = _attention_args(q, k, v, bits, group_size, out, stream)
     _check(load().aq_attention_decode(dtype, *ptrs, H, KV, N, D, bits, group_size,
                                       _dev(out, "out"), _stream(stream)), "aq_attention_decode")
     return out
@@ -324,7 +345,7 @@ def aq_attention_decode_static(q, k, v, bits, group_size, out=None, stream=None)
     """aq_attention_decode_ws with the library's own fixed scratch instead of
     a workspace (nothing allocated per call); calls on one device must not
     overlap in time."""
-    dtype, ptrs, (H, KV, N, D), out = _attention_args(q, k, v, bits, group_size, out)
+    dtype, ptrs, (H, KV, N, D), out = _attention_args(q, k, v, bits, group_size, out, stream)
     _check(load().aq_attention_decode_static(dtype, *ptrs, H, KV, N, D, bits, group_size,
                                              _dev(out, "out"), _stream(stream)),
            "aq_attention_decode_static")
@@ -344,10 +365,11 @@ def aq_attention_decode_ws(q, k, v, bits, group_size, workspace=None, out=None,
     first KV 32-bit words are zero before the first call; every call leaves
     them zero).  workspace=None allocates a zeroed one of the size the plan
     needs for this call."""
-    dtype, ptrs, (H, KV, N, D), out = _attention_args(q, k, v, bits, group_size, out)
+    dtype, ptrs, (H, KV, N, D), out = _attention_args(q, k, v, bits, group_size, out, stream)
     if workspace is None:
         n = aq_attention_workspace_bytes(H, KV, N, D, bits, group_size)
-        workspace = torch.zeros(max(n, 1), dtype=torch.uint8, device=q.device)
+        with torch.cuda.stream(_side(stream, q.device)):  # zeroed in the call's order
+            workspace = torch.zeros(max(n, 1), dtype=torch.uint8, device=q.device)
     if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     _check(load().aq_attention_decode_ws(dtype, *ptrs, H, KV, N, D, bits, group_size,
@@ -361,9 +383,9 @@ def aq_quantize_ex(w: torch.Tensor, bits: int, group_size: int, stream=None) -> 
     """aq_quantize for any code width and group size; w fp16 or bf16 [N, K]."""
     dtype = AQ_BF16 if w.dtype == torch.bfloat16 else AQ_F16
     N, K = w.shape
-    Wq = torch.empty((N, K * bits // 32), dtype=torch.int32, device=w.device)
-    scales = torch.empty((N, K // group_size), dtype=torch.float16, device=w.device)
-    biases = torch.empty((N, K // group_size), dtype=torch.float16, device=w.device)
+    Wq = _empty((N, K * bits // 32), torch.int32, w.device, stream)
+    scales = _empty((N, K // group_size), torch.float16, w.device, stream)
+    biases = _empty((N, K // group_size), torch.float16, w.device, stream)
     _check(load().aq_quantize_ex(dtype, _dev(w, "w"), N, K, bits, group_size, _dev(Wq, "Wq"),
                                  _dev(scales, "scales"), _dev(biases, "biases"), _stream(stream)),
            "aq_quantize_ex")
@@ -481,8 +503,7 @@ def aq_cache_read(cache: AqCache, layer: int, cu, start, table, total: int, dtyp
     if out is None:
         if total < 0:
             raise ValueError("total must not be negative")
-        k = torch.empty(shape, dtype=dtype, device=cache.pool.device)
-        v = torch.empty_like(k)
+        k, v = (_empty(shape, dtype, cache.pool.device, stream) for _ in range(2))
         kp, vp = k.data_ptr(), v.data_ptr()
     else:
         k, v = out
@@ -513,13 +534,12 @@ def _tables(f, cache, refs, table, lens, args, in_place, out, workspace, stream,
     r, t, n = (_ints(refs, "refs", cache.n_pages), _ints(table, "table", B, width),
                _ints(lens, "lens", B))
     more = [_ints(x, name, B) for name, x in args]
-    status = torch.empty(4, dtype=_I32, device=refs.device)
+    status = _empty(4, _I32, refs.device, stream)
     if out is None and in_place:
         res, outs = [refs, table, lens], [r, t, n]
     elif out is None:
-        res = [torch.empty_like(refs), torch.empty_like(table)]
-        if with_lens:
-            res.append(torch.empty_like(lens))
+        res = [_empty(x.shape, _I32, refs.device, stream)
+               for x in ((refs, table, lens) if with_lens else (refs, table))]
         outs = [o.data_ptr() for o in res]
     else:
         res = list(out)
@@ -626,7 +646,7 @@ def aq_attention_batch(q, cache: AqCache, layer: int, table, lens, scale: float,
     elif shared is not None or group_start is not None:
         raise ValueError("group_start and shared go together")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _empty(q.shape, q.dtype, q.device, stream)
         to = out.data_ptr()
     else:
         _check_out(out, "out", B * L * step, q.dtype)
@@ -661,7 +681,7 @@ def aq_matmul_multi(x, weights, bits, outs=None, stream=None) -> list:
         for j, (w, n) in enumerate(zip(weights, Ns)):
             _check_weights(w[0], w[1], w[2], n, K, bits, 64, f"[{j}]")
     if outs is None:
-        outs = [torch.empty((*x.shape[:-1], n), dtype=x.dtype, device=x.device) for n in Ns]
+        outs = [_empty((*x.shape[:-1], n), x.dtype, x.device, stream) for n in Ns]
     if len(outs) != P:
         raise ValueError("one output per projection")
     for j, (o, n) in enumerate(zip(outs, Ns)):
@@ -691,7 +711,7 @@ def aq_matmul_gate_up(x, gate, up, bits, out=None, stream=None) -> torch.Tensor:
         _check_weights(gate[0], gate[1], gate[2], N, K, bits, 64, " (gate)")
         _check_weights(up[0], up[1], up[2], N, K, bits, 64, " (up)")
     if out is None:
-        out = torch.empty((*x.shape[:-1], N), dtype=x.dtype, device=x.device)
+        out = _empty((*x.shape[:-1], N), x.dtype, x.device, stream)
     _check_out(out, "out", M * N, x.dtype)
     _check(load().aq_matmul_gate_up(dtype, _dev(x, "x"), _dev(gate[0], "Wq"),
                                     _dev(gate[1], "scales"), _dev(gate[2], "biases"),
