@@ -42,6 +42,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <mutex>
 
 namespace aq {
@@ -338,7 +339,10 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     }
                     *reinterpret_cast<uint4 *>(qs + wg * S::kQBytes + operand_at(128, r, c)) =
                         make_uint4(h[0], h[1], h[2], h[3]);
-                    if (c == 0) qsc[wg * 128 + r] = batch_pow2(-e) * fabsf(p.scale2);
+                    // never 0, which would make NaN of a masked score's -inf: products
+                    // stay below 2^41, so the least normal factor scores 0 as well
+                    if (c == 0)
+                        qsc[wg * 128 + r] = fmaxf(batch_pow2(-e) * fabsf(p.scale2), FLT_MIN);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
