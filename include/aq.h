@@ -396,7 +396,7 @@ aq_status aq_cache_copy(const aq_cache *cache, const int32_t *src_dev, const int
  *       entry named a page outside the pool (such entries change no count);
  *       after 1 and 2 nothing has changed (refs_out, table_out and lens_out
  *       hold what the inputs hold)
- *   [1] the number of missing pages, or of bad rows
+ *   [1] the number of missing pages (2^31 - 1 where it is more), or of bad rows
  *   [2], [3] as each operation says.
  * Free pages are those with refs <= 0; the lowest are taken first, in row
  * order, so the outcome is the same on every run.

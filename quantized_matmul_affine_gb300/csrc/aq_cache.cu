@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
 constexpr int kCtas = 8;        // a portable cluster
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCopyBits = 16;   // of a packed (pages, copies)
 
 struct TableParams {
     const int32_t *refs_in, *table_in, *lens_in;
@@ -553,7 +554,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) grow_k
     }
     cluster_sync();
 
-    // pages and copies before each row: packed sums, 1024 rows at a time
+    // pages and copies before each row: packed sums, 1024 rows at a time (a
+    // row may ask for 2^26 pages, so that all of them together pass 32 bits)
+    static_assert(AQ_CACHE_MAX_ROWS < 1 << kCopyBits, "copies fit below the pages");
+    constexpr long long kCopyMask = (1 << kCopyBits) - 1;
     long long carry = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
@@ -562,7 +566,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) grow_k
             const int len = p.lens_in[b], copy = __ldcg(flag + b);
             const int need =
                 pages_of(len + p.arg0[b], p.page_log2) - pages_of(len, p.page_log2) + copy;
-            mine = ((long long)need << 32) | copy;
+            mine = ((long long)need << kCopyBits) | copy;
         }
         long long before = mine;
         for (int o = 1; o < 32; o <<= 1) {
@@ -579,14 +583,16 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) grow_k
         }
         carry = all;
         if (b < p.B) {
-            s_base[b] = (int)((skip + before - mine) >> 32);
+            // (more than an int's worth are more than the pool has: not used then)
+            s_base[b] = (int)((skip + before - mine) >> kCopyBits);
             // copies before this row, or -1 - that where it has none itself
-            const int c = (int)((skip + before - mine) & 0xffffffffll);
+            const int c = (int)((skip + before - mine) & kCopyMask);
             s_copy[b] = (mine & 1) ? c : -1 - c;
         }
         __syncthreads();
     }
-    const int need = (int)(carry >> 32), copies = (int)(carry & 0xffffffffll);
+    const long long need = carry >> kCopyBits;
+    const int copies = (int)(carry & kCopyMask);
     int total = 0, rank0 = 0;
     for (int r = 0; r < kCtas; ++r) {
         if (r < rank) rank0 += s_free[r];
@@ -633,8 +639,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) grow_k
     if (outside && !none) atomicMax(&p.status[0], 3);
     if (rank == 0 && threadIdx.x == 0) {
         if (none) atomicMax(&p.status[0], s_bad ? 2 : 1);
-        p.status[1] = s_bad ? s_bad : none ? need - total : 0;
-        p.status[2] = none ? 0 : need;
+        p.status[1] = s_bad ? s_bad : none ? (int)min(need - total, (long long)INT32_MAX) : 0;
+        p.status[2] = none ? 0 : (int)need;
         p.status[3] = none ? 0 : copies;
         p.ws[0] = none ? 0 : copies;
     }
