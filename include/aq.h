@@ -405,7 +405,7 @@ aq_status aq_cache_copy(const aq_cache *cache, const int32_t *src_dev, const int
  * first keep[b] tokens (all of them for keep[b] < 0): the same pages, counted
  * once more.  No page is copied.  Bad rows: a child that is not empty, a
  * parent outside the batch or itself a child, keep[b] past the parent's
- * length.  status[2]: entries copied.
+ * length.  status[2]: entries copied (2^31 - 1 where it is more).
  *
  * aq_cache_trim — row b with 0 <= keep[b] < lens[b] is cut to keep[b] tokens
  * (0 frees it) and gives back the pages past them; other rows stay.  The

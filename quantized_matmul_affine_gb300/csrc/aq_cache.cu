@@ -383,16 +383,18 @@ __device__ __forceinline__ int count_live(const int32_t *refs, Run r) {
 // in status[1], and then nothing changes.
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) fork_kernel(
     const TableParams p) {
-    __shared__ int s_bad, s_pages;
+    __shared__ int s_bad;
+    __shared__ unsigned long long s_pages;  // of all rows: may pass 32 bits
     const int rank = (int)cluster_ctarank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) s_bad = s_pages = 0;
+    if (threadIdx.x == 0) s_bad = 0, s_pages = 0;
     __syncthreads();
     launch_dependents();
     grid_dependency_wait();
     carry_over(p, rank);
     if (rank == 0 && threadIdx.x < 4) p.status[threadIdx.x] = 0;
-    int bad = 0, pages = 0;
+    int bad = 0;
+    unsigned long long pages = 0;
     for (int b = threadIdx.x; b < p.B; b += kThreads) {
         const int par = p.arg0[b], len = p.lens_in[b];
         if (par < 0) continue;
@@ -429,7 +431,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) fork_k
     if (rank == 0 && threadIdx.x == 0) {
         if (none) atomicMax(&p.status[0], 2);
         p.status[1] = s_bad;
-        p.status[2] = none ? 0 : s_pages;
+        p.status[2] = none ? 0 : (int)min(s_pages, (unsigned long long)INT32_MAX);
     }
 }
 

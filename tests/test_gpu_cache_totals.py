@@ -45,3 +45,20 @@ def test_grow_refuses_more_pages_than_32_bits_count(each, one_more, missing):
     assert lens.tolist() == [48] + [0] * (ROWS - 2) + [1]
     assert table[0, :4].tolist() == [0, 1, 2, -1] and table[-1, :2].tolist() == [3, -1]
     assert aq.aq_device_error(clear=True) == 0
+
+
+def test_fork_reports_more_entries_than_32_bits_count():
+    # 4095 children of 2^19 + 200 pages are 2^31 + 294,712 entries
+    width = 2 ** 19 + 200
+    cache, refs, table, lens = _world(width, width)
+    pages = torch.arange(width, dtype=torch.int32, device="cuda")
+    refs.fill_(1)
+    table[0] = pages
+    lens[0] = 16 * width
+    parent = torch.zeros_like(lens)
+    parent[0] = -1
+    status = aq.aq_cache_fork(cache, refs, table, lens, parent, torch.full_like(lens, -1))[3]
+    assert status.tolist() == [0, 0, 2 ** 31 - 1, 0]
+    assert bool((refs == ROWS).all() and (lens == 16 * width).all())
+    assert torch.equal(table[1], pages) and torch.equal(table[-1], pages)
+    assert aq.aq_device_error(clear=True) == 0
