@@ -23,9 +23,12 @@
 // same row tile and two tiles of keys), so that the tensor core works on one
 // while the softmax has the other.  MMAs of one thread run in issue order,
 // which is what lets a step's scores overwrite the P two steps before it.
-// The running maximum only moves when a row's scores exceed it by 2^8 (P
-// then still fits fp16), so O is seldom rescaled; the sum uses the same
-// reference.  k and v are rounded once to fp16 (2^-11).
+// The running maximum only moves when a row's scores exceed it by 2^8, so O
+// is seldom rescaled.  Weights are taken against 2^7 below it: P up to 2^15
+// still fits fp16, and weights down to 2^-21 of the maximum's keep all their
+// bits (many keys behind one that outweighs them are most of an output whose
+// heavy key has a small value); the sum uses the same reference.  k and v are
+// rounded once to fp16 (2^-11).
 //
 // What bounds it: 640 query rows by 8 heads over 32k shared keys of 128 at 8
 // bits are 86 GFLOP, 45 us at the measured bf16 rate, and take 111 us; the
@@ -214,6 +217,8 @@ __device__ __forceinline__ bool row_tile_all(int wg, bool me) {
 }
 
 constexpr uint32_t kNoRow = 0xffffffffu;  // of a row tile: past the piece's rows
+constexpr float kMove = 8.f;  // (log2) the reference moves when a score exceeds it by more
+constexpr float kRoom = 7.f;  // what weights at the reference are above 1: 2^(kMove + kRoom) fits fp16
 
 // A bounded wait that records where it gave up.
 __device__ __forceinline__ bool shd_wait(uint64_t *bar, uint32_t parity, volatile int *flag,
@@ -392,11 +397,11 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                 ok = row_tile_all(wg, ok);
                 if (!ok) break;
                 mx = fmaxf(mx, other[turn]) * c;
-                // the reference moves when a weight could pass 2^8
+                // the reference moves when a weight could pass 2^15
                 float f = 1.f;
                 if (j == 0) {
                     m = mx == -INFINITY ? 0.f : mx;
-                } else if (mx > m + 8.f) {
+                } else if (mx > m + kMove) {
                     f = batch_ex2(m - mx);
                     m = mx;
                 }
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     sum.x *= f;
                     sum.y *= f;
                 }
-                const float2 c2 = make_float2(c, c), m2 = make_float2(-m, -m);
+                const float2 c2 = make_float2(c, c), m2 = make_float2(kRoom - m, kRoom - m);
                 // P of scores k .. k + 31 takes 16 columns at k / 2 of this half's,
                 // over scores that have been read
                 float2 sum2 = make_float2(0.f, 0.f);
@@ -459,7 +464,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     return ((int64_t)w.slot0 * p.L + (id >> 16)) * p.H + (id & 0xffffu);
                 };
                 if (half == 0 && rows[rl] != kNoRow)
-                    p.part_ml[part(rows[rl])] = make_float2(m, *mine + *other);
+                    p.part_ml[part(rows[rl])] = make_float2(m - kRoom, *mine + *other);
                 // O through this row tile's q' (done with), a quarter of the columns
                 // at a time: a thread has a row, but memory wants a row's columns
                 // next to each other.  Chunks of 16 bytes, swizzled by row.
