@@ -481,7 +481,9 @@ aq_status aq_cache_compact(const aq_cache *cache, const int32_t *refs_dev,
  * of KV, 1 <= L <= 64, B <= 1024, G <= 256.  Scores, maxima and sums are fp32;
  * the probabilities (times the value scales where the codes themselves enter
  * the product, else against values rounded to fp16) enter the value product
- * as fp16; o is rounded once.  Deterministic.  A page outside the pool, among
+ * as fp16; o is rounded once.  Cached values are taken to be within fp16's
+ * range: what the rounded scale of an appended group puts past it (2^-10 at
+ * most) may count as its largest number.  Deterministic.  A page outside the pool, among
  * the tokens that count, sets the error word, and the rows that see it are
  * unspecified.
  * Errors: AQ_ERR_INVALID_ARG for a bad cache, layer, dtype, size, a scale

@@ -28,7 +28,8 @@
 // still fits fp16, and weights down to 2^-21 of the maximum's keep all their
 // bits (many keys behind one that outweighs them are most of an output whose
 // heavy key has a small value); the sum uses the same reference.  k and v are
-// rounded once to fp16 (2^-11).
+// rounded once to fp16 (2^-11), the few a pair of extremes puts past its
+// largest number to that number (2^-10).
 //
 // What bounds it: 640 query rows by 8 heads over 32k shared keys of 128 at 8
 // bits are 86 GFLOP, 45 us at the measured bf16 rate, and take 111 us; the
@@ -180,6 +181,42 @@ __device__ __forceinline__ uint4 values8(const uint32_t *w, __half2 s, __half2 b
         put(3, prmt(w[1], 0x64646464u, 0x4342u), one, m1024);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Whether values of (scale, bias) pairs of at most these magnitudes could pass
+// the largest fp16 number: the rounded scale of a group that holds values next
+// to it, of both signs, puts the outermost code up to 2^-10 past it.
+template <int BITS>
+__device__ __forceinline__ bool past_fp16(__half2 most) {
+    const __half top = __float2half_rn((float)((1 << BITS) - 1));
+    return __hgt(__hfma(__low2half(most), top, __high2half(most)), __float2half_rn(65504.f));
+}
+
+// A lane's chunks of a k or v tile again, infinite values as the largest fp16
+// number.  Hardly ever called, and kept out of the kernel's own code (tile: a
+// shared-memory address): inlined, it cost 128 sequences over 32k shared
+// tokens 5 us of 164 without being run, and so did generic addressing.
+template <class S>
+__device__ __noinline__ void clip_fp16(uint32_t tile, int row, int l) {
+    const __half2 top = __float2half2_rn(65504.f);
+#pragma unroll 1
+    for (int i = 0; i < S::kLoads * S::kChunks; ++i) {
+        const uint32_t at = tile + operand_at(S::kKeys, row + i / S::kChunks * S::kLRows,
+                                              l * S::kChunks + i % S::kChunks);
+        uint32_t v[4];
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(at)
+                     : "memory");
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __half2 x = __hmax2(__hmin2(*reinterpret_cast<const __half2 *>(&v[k]), top), __hneg2(top));
+            v[k] = *reinterpret_cast<const uint32_t *>(&x);
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+                     "r"(v[2]), "r"(v[3])
+                     : "memory");
+    }
 }
 
 // True in one lane of a converged warp, the same one every time.  Unlike a
@@ -563,7 +600,15 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                                 slot * S::kG * 4);
             };
             const int turn = BITS == 4 ? (l >> 1) * (D == 128 ? 2 : 1) & 3 : (l >> 2) & 1;
-            auto store = [&](const Raw &x, uint8_t *tile) {
+            // whether values of x could pass the largest fp16 number (pairs that
+            // are not finite leave theirs as they are)
+            auto past = [&](const Raw &x) {
+                __half2 most = __habs2(x.sb[0]);
+#pragma unroll
+                for (int i = 1; i < S::kLoads; ++i) most = __hmax2_nan(most, __habs2(x.sb[i]));
+                return past_fp16<BITS>(most) && __hble2(most, __float2half2_rn(65504.f));
+            };
+            auto store = [&](const Raw &x, uint8_t *tile, bool past) {
 #pragma unroll
                 for (int i = 0; i < S::kLoads; ++i) {
                     const __half2 s = __low2half2(x.sb[i]), b = __high2half2(x.sb[i]);
@@ -593,6 +638,7 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                         *reinterpret_cast<uint4 *>(tile + (at ^ ((uint32_t)k << 4))) =
                             values8<BITS>(cw + k * BITS / 4, s, b);
                 }
+                if (__builtin_expect(past, 0)) clip_fp16<S>(smem_u32(tile), key0 + row, l);
                 fence_proxy_async_smem();
                 __syncwarp();
             };
@@ -613,10 +659,11 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                     prefetch(rec1, j + 2);
                 }
                 uint64_t *empty = which ? &v_empty[s] : row_tiles == 1 ? &s_full[s] : &k_empty[s];
+                const bool top = past(x);
                 const bool ok =
                     lap == 0 || shd_wait(empty, (lap - 1) & 1, flag, p.err, ERR_BATCH_BASE);
                 if (!__all_sync(~0u, ok)) goto wound_down;
-                store(x, (which ? vs : ks) + s * S::kTileBytes);
+                store(x, (which ? vs : ks) + s * S::kTileBytes, top);
                 const bool withheld = p.withhold && n == 0 && !which;  // tests: nothing completes k_full[0]
                 if (lane == 0 && !withheld) mbar_arrive(which ? &v_full[s] : &k_full[s]);
                 x = y;

@@ -1,5 +1,6 @@
 """Batch attention where 16-bit floats run out of range: weights far below a
-row's largest.  Sizes are those of the kernel for many rows."""
+row's largest, and cached values next to the largest fp16 number.  Sizes are
+those of the kernel for many rows."""
 import numpy as np
 import pytest
 import torch
@@ -42,3 +43,23 @@ def test_one_key_outweighs_the_others(D, bits):
     c.q = torch.from_numpy(np.broadcast_to(power / 32, (c.B, 1, c.H, D)).copy()).to(torch.float16)
     c.scale = 32 * float(np.log(2)) / D
     c.check()
+
+
+@pytest.mark.parametrize("D,bits,scale", [
+    (128, 4, 8736.0),     # 15 * 8736 - 65504 = 65536
+    (256, 4, 8736.0),
+    (64, 8, 514.0),       # 255 * 514 - 65504 = 65566
+    (128, 8, 514.0),
+])
+@pytest.mark.parametrize("which", [2, 3])
+def test_values_next_to_the_largest_fp16(D, bits, scale, which):
+    # What the quantiser makes of a group that holds both -65504 and 65504: its
+    # rounded scale puts the top code past the largest fp16 number.  Taken as
+    # 65504 it is off by 2^-10 of itself: twice the rounding that the score's
+    # tolerance counts (so smag is doubled), and the value's counts 2^-10.
+    assert np.float16(131008 / (2 ** bits - 1)) == scale
+    c = Case(12, 2, D, 32, bits, 64, "bf16", 1, [20] * 9, [(9, 333)], qscale=2.0 ** -17 if which == 2 else 1.0)
+    for j in range(0, 320, 3):
+        _set(c, c.table[0, j // 32], j % 32, which, scale, -65504.0)
+    want, smag, vmag, bmax = c.reference()
+    c.check(ref=(want, 2 * smag, vmag, bmax))
