@@ -458,7 +458,7 @@ aq_status aq_cache_compact(const aq_cache *cache, const int32_t *refs_dev,
  *   o[b][l][h] = softmax_j(scale * q[b][l][h] . K[b][j][kv]) . V[b][j][kv],
  * kv = h / (H / KV), over the tokens j < lens[b] - (L - 1 - l), so that lens
  * counts the new tokens and token l sees those before it and itself.  A row
- * that sees nothing (lens[b] == 0: an empty slot of the batch) is zeros.
+ * that sees nothing (lens[b] <= 0: an empty slot of the batch) is zeros.
  * Sequences that share their first tokens are read once: group g is the
  * sequences group_start[g] .. group_start[g + 1] - 1, and they all begin with
  * the same shared[g] tokens.  Those are read through the table row of the

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
 #pragma unroll 1
     for (int b = threadIdx.x; b < p.B; b += kPlanThreads) {
-        const int len = min(cap, p.lens[b]);
+        const int len = min(cap, max(0, p.lens[b]));  // (so that len - L cannot wrap)
         int lo = 0, hi = p.G;
 #pragma unroll 1
         while (hi - lo > 1) {
