@@ -4,7 +4,6 @@ for).  A block of the current stream's memory may still be in use by kernels
 queued there, and one that is dropped returns to that stream at once: what a
 call writes on another stream has to come from that stream's memory, and what
 it hands back has to be known to the stream the caller is on."""
-import contextlib
 import types
 
 import pytest
@@ -14,8 +13,10 @@ import quantized_matmul_affine_gb300 as aq
 
 
 class _Stream:
+    device_index, device_type = 0, 1
+
     def __init__(self, handle):
-        self.cuda_stream = handle
+        self.cuda_stream = self.stream_id = handle
 
 
 class _Tensor(torch.Tensor):
@@ -51,11 +52,9 @@ def world(monkeypatch):
     """Allocations as (stream that was current, tensor), in order."""
     w = types.SimpleNamespace(now=_Stream(HERE), made=[], called=[])
 
-    @contextlib.contextmanager
-    def stream(s):
-        before, w.now = w.now, s or w.now
-        yield
-        w.now = before
+    def set_stream(stream_id, device_index, device_type):
+        assert (device_index, device_type) == (0, 1)
+        w.now = _Stream(stream_id)
 
     def made(t):
         t = _Tensor.of(t)
@@ -73,7 +72,8 @@ def world(monkeypatch):
     monkeypatch.setattr(torch, "empty_like", lambda t, **kw: empty(tuple(t.shape), dtype=t.dtype))
     monkeypatch.setattr(torch.cuda, "Stream", _Stream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: _Stream(h))
-    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentStream", lambda d: (w.now.cuda_stream, 0, 1), raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_setStream", set_stream, raising=False)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: w.now)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: w.now.cuda_stream, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)

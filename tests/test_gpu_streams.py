@@ -130,3 +130,18 @@ def test_workspace_of_decode_is_zero_on_the_calls_stream():
     side.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_the_current_stream_stays():
+    a = _batch(6, 9, 500)
+    side, mine = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (torch.cuda.default_stream(), mine):
+        with torch.cuda.stream(s):
+            aq.aq_attention_batch(*a, stream=side)
+            assert torch.cuda.current_stream() == s
+            with pytest.raises(aq.AqError):
+                aq.aq_attention_batch(*a[:2], 5, *a[3:], stream=side)   # no such layer
+            with pytest.raises((RuntimeError, MemoryError)):
+                aq.aq_cache_read(a[1], 0, _ints([0] * 10), a[4], a[3], 2 ** 55, torch.float16, stream=side)
+            assert torch.cuda.current_stream() == s
+    torch.cuda.synchronize()
