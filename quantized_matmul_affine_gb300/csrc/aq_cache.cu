@@ -384,10 +384,10 @@ __device__ __forceinline__ int count_live(const int32_t *refs, Run r) {
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) fork_kernel(
     const TableParams p) {
     __shared__ int s_bad;
-    __shared__ unsigned long long s_pages;  // of all rows: may pass 32 bits
+    __shared__ unsigned long long s_pages[kWarps];  // together they may pass 32 bits
     const int rank = (int)cluster_ctarank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) s_bad = 0, s_pages = 0;
+    if (threadIdx.x == 0) s_bad = 0;
     __syncthreads();
     launch_dependents();
     grid_dependency_wait();
@@ -407,7 +407,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) fork_k
         bad += !ok;
     }
     if (bad) atomicAdd(&s_bad, bad);
-    if (pages) atomicAdd(&s_pages, pages);
+    for (int o = 16; o >= 1; o >>= 1) pages += __shfl_xor_sync(~0u, pages, o);
+    if (lane == 0) s_pages[warp] = pages;
     // every CTA has counted the same rows; what was carried over is in place
     // cluster-wide before a count or an entry changes
     cluster_sync();
@@ -431,7 +432,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads) fork_k
     if (rank == 0 && threadIdx.x == 0) {
         if (none) atomicMax(&p.status[0], 2);
         p.status[1] = s_bad;
-        p.status[2] = none ? 0 : (int)min(s_pages, (unsigned long long)INT32_MAX);
+        unsigned long long all = 0;
+        for (int w = 0; w < kWarps; ++w) all += s_pages[w];
+        p.status[2] = none ? 0 : (int)min(all, (unsigned long long)INT32_MAX);
     }
 }
 
