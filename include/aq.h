@@ -34,6 +34,8 @@
  *     caller's next synchronisation, as with any CUDA call.  Nothing prints.
  *   - Entry points are thread-safe when different threads use different
  *     streams; results do not depend on the thread or stream.
+ *   - One device a process: what a kernel needs set on the device (its
+ *     shared-memory size) is set on that of its first call.
  *   - Results are deterministic: the same inputs give bit-identical outputs,
  *     call after call (fixed-order reductions, no atomics on data; the
  *     reference counts of pages are integers, whose sums have no order).
@@ -390,7 +392,8 @@ aq_status aq_cache_copy(const aq_cache *cache, const int32_t *src_dev, const int
  * The operations on page tables.  Each reads refs, table and lens and writes
  * refs_out, table_out and lens_out, which are the same arrays (in place) or
  * others (then every element is written), never parts of each other.  One
- * launch each, no host synchronisation: a graph may capture them.  The result
+ * launch each (grow and compact: a second one that copies pages), no host
+ * synchronisation: a graph may capture them.  The result
  * is reported in status_dev, int32 [4]:
  *   [0] 0 done; 1 too few free pages; 2 bad rows; 3 done, but some table
  *       entry named a page outside the pool (such entries change no count);
@@ -477,7 +480,9 @@ aq_status aq_cache_compact(const aq_cache *cache, const int32_t *refs_dev,
  *                aq_attention_batch_workspace_bytes(...) long, needing no
  *                initial value; calls that may overlap use distinct ones.
  * lens, tables and groups are read on the device only, so a captured graph
- * follows their changes.  Served: D in {64, 128, 256, 512}, any H a multiple
+ * follows their changes.  A call whose own (and, up to 16 rows, shared) keys
+ * are more than 2^30 tiles - 16 or 32 keys by 8 or 16 rows of a KV head - is
+ * told by the error word, and its rows are zeros.  Served: D in {64, 128, 256, 512}, any H a multiple
  * of KV, 1 <= L <= 64, B <= 1024, G <= 256.  Scores, maxima and sums are fp32;
  * the probabilities (times the value scales where the codes themselves enter
  * the product, else against values rounded to fp16) enter the value product

@@ -70,7 +70,7 @@ struct BatchParams {
     PlanGroup *groups;       // [G]
     int *runs;               // [own_warps] group (as -1 - g) or row of a run's first tile
     int64_t slots;           // slots of the workspace
-    int64_t key_cap;         // max_pages * page, at most 2^29
+    int64_t key_cap;         // max_pages * page, at most 2^24
     int own_rows;            // query rows a tile of own_kernel
     int own_warps;           // its warps
     int own_min;             // tiles a warp takes at least

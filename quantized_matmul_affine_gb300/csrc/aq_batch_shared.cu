@@ -32,7 +32,7 @@
 // largest number to that number (2^-10).
 //
 // What bounds it: 640 query rows by 8 heads over 32k shared keys of 128 at 8
-// bits are 86 GFLOP, 45 us at the measured bf16 rate, and take 111 us; the
+// bits are 86 GFLOP, 45 us at the measured bf16 rate, and take 114 us; the
 // tensor pipe is 39 % busy, the issue slots 67 %.  A slot's chain is scores ->
 // maximum -> exchange -> weights -> store (about 2200 cycles for a 128-key
 // tile, the two passes over the scores most of it) and then the MMAs' own
