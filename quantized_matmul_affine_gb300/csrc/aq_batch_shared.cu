@@ -560,12 +560,14 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
                 uint4 c[S::kLoads];
                 __half2 sb[S::kLoads];
             };
+            // (Tables and pages are read by ordinary loads: this grid may have started
+            // while an earlier one still wrote them, so they are not constant.)
             // the record of this warp's keys of tile j; nullptr past the end,
             // or where the table names no page of the pool
             auto place = [&](int j) -> const uint8_t * {
                 const int at = w.k0 + j * KT + key0;
                 if (j >= tiles || at >= w.k1) return nullptr;
-                const int id = __ldg(trow + (at >> p.c.page_log2));
+                const int id = trow[at >> p.c.page_log2];
                 if (id < 0 || id >= p.c.n_pages) {
                     if (lane == 0) atomicOr(p.err, ERR_BATCH_TABLE);
                     return nullptr;
@@ -582,8 +584,8 @@ __global__ void __launch_bounds__(Shd<BITS, D, GROUP>::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < S::kLoads; ++i) {
                     const bool in = rec && at + row + i * S::kLRows < w.k1;
-                    x.c[i] = in ? __ldg(c + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
-                    x.sb[i] = in ? __ldg(sb + i * S::kLRows * S::kG) : __float2half2_rn(0.f);
+                    x.c[i] = in ? __ldca(c + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+                    x.sb[i] = in ? __ldca(sb + i * S::kLRows * S::kG) : __float2half2_rn(0.f);
                 }
             };
             // the lines of the tile after the next into L2
