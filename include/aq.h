@@ -4,7 +4,9 @@
  * float -> affine quantiser, several projections of one x per call (q/k/v,
  * gate/up with SiLU), other code widths and group sizes, decode attention
  * over a KV cache stored in the same format, and for batches a paged cache
- * with the operations on its page tables and the attention that reads it.
+ * with the operations on its page tables and the attention that reads it; the
+ * layer of a mixture of experts for few tokens (router, experts, both in one
+ * call), and the lookup of embedding rows.
  *
  * Weight format (mlx-bun pages, @mlx-bun/inference 1.0.0,
  * kernels/quantization/affine-split-mma.ts helper affine_unit and
@@ -510,6 +512,136 @@ aq_status aq_attention_batch(const aq_cache *cache, int64_t layer, int dtype, co
                              int64_t L, int64_t H, int64_t G, int64_t max_pages, float scale,
                              void *out_dev, void *workspace_dev, size_t workspace_bytes,
                              void *stream);
+
+/*
+ * The layer of a mixture of experts for few tokens.  A router picks top_k of
+ * E experts for each token; each expert is a gated MLP whose matrices are in
+ * the weight format:
+ *   y[t] = sum over j of weights[t][j] * Wd_e . (silu(Wg_e . x[t]) * (Wu_e . x[t])),
+ * e = experts[t][j].  Only the experts that some token picked are read, each
+ * once for up to 32 of its tokens.  (The pages have no such layer; its products
+ * follow their gate/up with SiLU and their factored form.)
+ */
+/* Largest number of tokens of a call, of experts, and of experts a token. */
+#define AQ_MOE_MAX_TOKENS 256
+#define AQ_MOE_MAX_EXPERTS 512
+#define AQ_MOE_MAX_TOP 16
+
+typedef enum aq_score { AQ_SCORE_SOFTMAX = 0, AQ_SCORE_SIGMOID = 1 } aq_score;
+
+/*
+ * A router.  logits l[e] = x . weight[e]; p = softmax(l) over all experts, or
+ * p[e] = 1 / (1 + exp(-l[e])).  Chosen are the top_k largest l, or with a bias
+ * (sigmoid only) the top_k largest p + bias; of equal ones the lowest index.
+ * Weights: p of the chosen, without the bias; divided by their sum with
+ * normalize != 0; times scale.  The struct is host memory, read during the call.
+ *   weight_dev  [E][K] of dtype, device, 16-byte aligned.
+ *   bias_dev    float [E], device, or NULL.
+ *   dtype       AQ_F16 or AQ_BF16: of weight and of x.
+ *   K           a multiple of 64, up to 2^20.   E  1..AQ_MOE_MAX_EXPERTS.
+ *   top_k       1..min(E, AQ_MOE_MAX_TOP).    scale  finite.
+ */
+typedef struct aq_router {
+    const void *weight_dev;
+    const float *bias_dev;
+    int64_t E, K;
+    int dtype, top_k, score, normalize;
+    float scale;
+} aq_router;
+
+/*
+ * The experts' weights: three stacks of E matrices, gate and up [E][I][K],
+ * down [E][K][I], each as words uint32 [E][rows][cols*bits/32] and fp16 scales
+ * and biases [E][rows][cols/group_size], device.  Words 16-byte aligned.
+ *   K, I        hidden and inner size, multiples of 64 and of group_size, up to
+ *               2^20.
+ *   bits        2, 3, 4, 5, 6 or 8.   group_size  32, 64 or 128.
+ */
+typedef struct aq_experts {
+    const uint32_t *gate_words_dev;
+    const void *gate_scales_dev, *gate_biases_dev;
+    const uint32_t *up_words_dev;
+    const void *up_scales_dev, *up_biases_dev;
+    const uint32_t *down_words_dev;
+    const void *down_scales_dev, *down_biases_dev;
+    int64_t E, K, I;
+    int bits, group_size;
+} aq_experts;
+
+/*
+ * aq_moe_route — the experts and weights of T tokens.
+ *   x_dev        [T][K] of router->dtype, device, 16-byte aligned.
+ *   experts_dev  int32 [T][top_k], each row ascending, written entirely.
+ *   weights_dev  float [T][top_k], written entirely.
+ * The choice is the one that logits in 64 bits give: where fp32 sums leave it
+ * open, the logits in question are summed again with their rounding errors.
+ * Weights come from fp32 logits.  A token whose logits are not finite gets
+ * top_k distinct experts, which ones is unspecified, and weights that are not
+ * finite; other tokens are not affected.
+ * Errors: AQ_ERR_INVALID_ARG for a bad router, T outside 1..AQ_MOE_MAX_TOKENS
+ * or NULL pointers; AQ_ERR_UNSUPPORTED for a bias with softmax scores;
+ * AQ_ERR_MISALIGNED; AQ_ERR_CUDA.
+ */
+aq_status aq_moe_route(const aq_router *router, const void *x_dev, int64_t T,
+                       int32_t *experts_dev, float *weights_dev, void *stream);
+
+/*
+ * aq_moe_experts — the layer for experts and weights that are given.
+ *   dtype        AQ_F16 or AQ_BF16: of x and y.
+ *   x_dev        [T][K], 16-byte aligned.
+ *   experts_dev  int32 [T][top_k]; an entry outside 0..E-1 (-1: an empty slot
+ *                of a padded batch, an expert that lies elsewhere) adds nothing.
+ *                The same expert may stand twice in a row.
+ *   weights_dev  float [T][top_k].
+ *   out_dev      y [T][K], 16-byte aligned, written entirely (zeros where a
+ *                token has no expert).
+ *   workspace_dev  device, 256-byte aligned, at least
+ *                aq_moe_workspace_bytes(...) long, needing no initial value;
+ *                calls that may overlap use distinct ones.
+ * Products are fp32 sums; between the two products h is kept in fp32 and enters
+ * the second rounded to fp16's 11 bits (times a power of two); y is rounded
+ * once.  Deterministic.  The output must not alias weights that the next
+ * matmul call on the stream reads.
+ * Errors: AQ_ERR_INVALID_ARG for bad experts, sizes, T outside
+ * 1..AQ_MOE_MAX_TOKENS, top_k outside 1..AQ_MOE_MAX_TOP, NULL pointers or a
+ * workspace that is too small; AQ_ERR_MISALIGNED; AQ_ERR_CUDA.
+ */
+size_t aq_moe_workspace_bytes(const aq_experts *experts, int64_t T, int top_k);
+aq_status aq_moe_experts(const aq_experts *experts, int dtype, const void *x_dev, int64_t T,
+                         int top_k, const int32_t *experts_dev, const float *weights_dev,
+                         void *out_dev, void *workspace_dev, size_t workspace_bytes,
+                         void *stream);
+
+/*
+ * aq_moe — both: routes x and runs the chosen experts, without the host
+ * between them.  router and experts have the same E and K.  experts_dev and
+ * weights_dev receive the choice as aq_moe_route writes it.  Other arguments
+ * and errors as the two calls.
+ */
+aq_status aq_moe(const aq_router *router, const aq_experts *experts, const void *x_dev, int64_t T,
+                 int32_t *experts_dev, float *weights_dev, void *out_dev, void *workspace_dev,
+                 size_t workspace_bytes, void *stream);
+
+/*
+ * aq_embed — rows of a quantised table by token:
+ *   out[t] = scale * (s q + b) of row ids[t],
+ * in fp32, rounded once to `dtype`.  The table is in the weight format of
+ * aq_matmul_ex, so a table that is also the vocabulary projection is kept once.
+ *   ids_dev     [T] of index_bytes 4 (int32) or 8 (int64), device.  An id
+ *               outside 0..N-1 (-1: an empty slot) gives a row of zeros.
+ *   Wq_dev      uint32 [N][K*bits/32]; scales_dev, biases_dev fp16
+ *               [N][K/group_size].
+ *   out_dev     [T][K], 16-byte aligned, written entirely.
+ * Any N >= 1, T >= 0 (0 queues nothing) and K a multiple of 32 and of
+ * group_size, T * K / 8 up to 2^38.
+ * Errors: AQ_ERR_INVALID_ARG for bad sizes, widths, group or index sizes, a
+ * scale that is not finite or NULL pointers; AQ_ERR_UNSUPPORTED past the
+ * limits; AQ_ERR_MISALIGNED; AQ_ERR_CUDA.
+ */
+aq_status aq_embed(int dtype, const void *ids_dev, int index_bytes, int64_t T,
+                   const uint32_t *Wq_dev, const void *scales_dev, const void *biases_dev,
+                   int64_t N, int64_t K, int bits, int group_size, float scale, void *out_dev,
+                   void *stream);
 
 /* Largest number of projections aq_matmul_multi takes in one call. */
 #define AQ_MAX_PROJ 4

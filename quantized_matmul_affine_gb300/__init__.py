@@ -31,6 +31,8 @@ __all__ = [
     "aq_cache_read", "aq_cache_copy", "aq_cache_fork", "aq_cache_trim", "aq_cache_grow",
     "aq_cache_compact", "aq_cache_workspace_bytes", "aq_attention_batch",
     "aq_attention_batch_workspace_bytes",
+    "AQ_SCORE_SOFTMAX", "AQ_SCORE_SIGMOID", "AqRouter", "AqExperts", "aq_moe_route",
+    "aq_moe_experts", "aq_moe", "aq_moe_workspace_bytes", "aq_embed",
     "aq_matmul_variant", "aq_matmul_host", "aq_select", "aq_describe", "aq_stats", "aq_stats_reset",
     "aq_device_error",
     "aq_free", "aq_status_string", "aq_variant_name", "aq_version", "lib_path", "load",
@@ -42,6 +44,7 @@ AQ_VARIANT_AUTO, AQ_VARIANT_GENERIC, AQ_VARIANT_QMV, AQ_VARIANT_TC = -1, 0, 1, 2
 AQ_VARIANT_GEMV = 3
 AQ_VARIANT_TCW = 4
 AQ_NUM_VARIANTS = 5
+AQ_SCORE_SOFTMAX, AQ_SCORE_SIGMOID = 0, 1
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -104,6 +107,11 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         "aq_attention_batch_workspace_bytes": ([p, i64, i64, i64, i64], sz),
         "aq_attention_batch": ([p, i64, i32, p, i64, p, p, p, p, i64, i64, i64, i64, i64, f32, p,
                                 p, sz, p], i32),
+        "aq_moe_route": ([p, p, i64, p, p, p], i32),
+        "aq_moe_workspace_bytes": ([p, i64, i32], sz),
+        "aq_moe_experts": ([p, i32, p, i64, i32, p, p, p, p, sz, p], i32),
+        "aq_moe": ([p, p, p, i64, p, p, p, p, sz, p], i32),
+        "aq_embed": ([i32, p, i32, i64, p, p, p, i64, i64, i32, i32, f32, p, p], i32),
         "aq_stats": ([p, i32], i32),
         "aq_stats_reset": ([], None),
         "aq_device_error": ([u32p, i32], i32),
@@ -678,6 +686,215 @@ def aq_attention_batch(q, cache: AqCache, layer: int, table, lens, scale: float,
                                    n, _stream(stream))
     if st:
         _check(st, "aq_attention_batch")
+    return out
+
+
+class _RouterStruct(ctypes.Structure):
+    _fields_ = [("weight_dev", ctypes.c_void_p), ("bias_dev", ctypes.c_void_p),
+                ("E", ctypes.c_int64), ("K", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("top_k", ctypes.c_int), ("score", ctypes.c_int), ("normalize", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
+class _ExpertsStruct(ctypes.Structure):
+    _fields_ = [(f"{m}_{part}_dev", ctypes.c_void_p) for m in ("gate", "up", "down")
+                for part in ("words", "scales", "biases")] + \
+               [("E", ctypes.c_int64), ("K", ctypes.c_int64), ("I", ctypes.c_int64),
+                ("bits", ctypes.c_int), ("group_size", ctypes.c_int)]
+
+
+_SCORES = {"softmax": AQ_SCORE_SOFTMAX, "sigmoid": AQ_SCORE_SIGMOID}
+
+
+class AqRouter:
+    """A router (struct aq_router): weight [E, K] fp16 or bf16, bias float32
+    [E] or None (sigmoid scores only), score "softmax" or "sigmoid".  The
+    tensors stay the caller's; this object holds them and is kept for a layer."""
+
+    __slots__ = ("weight", "bias", "top_k", "_struct", "_ref")
+
+    def __init__(self, weight, top_k: int, bias=None, score: str = "softmax",
+                 normalize: bool = True, scale: float = 1.0):
+        if weight.dtype not in _ACT or weight.dim() != 2:
+            raise ValueError("weight must be float16 or bfloat16 [E, K]")
+        if score not in _SCORES:
+            raise ValueError(f"score must be one of {sorted(_SCORES)}")
+        E, K = weight.shape
+        if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (E,)):
+            raise ValueError(f"bias must be float32 [{E}]")
+        if bias is not None and bias.device != weight.device:
+            raise ValueError("bias must be on weight's device")
+        self.weight, self.bias, self.top_k = weight, bias, top_k
+        self._struct = _RouterStruct(_dev(weight, "weight"),
+                                     None if bias is None else _dev(bias, "bias"), E, K,
+                                     AQ_BF16 if weight.dtype == torch.bfloat16 else AQ_F16, top_k,
+                                     _SCORES[score], int(normalize), scale)
+        self._ref = ctypes.addressof(self._struct)
+
+
+class AqExperts:
+    """The experts of a layer (struct aq_experts): gate and up are (words
+    [E, I, K*bits/32] int32, scales [E, I, K/group] fp16, biases), down the
+    same with [E, K, I]; bits 2/3/4/5/6/8, groups of 32/64/128.  The tensors
+    stay the caller's; this object holds them and is kept for a layer."""
+
+    __slots__ = ("gate", "up", "down", "bits", "group_size", "count", "hidden", "inner", "_struct",
+                 "_ref", "_workspaces")
+
+    def __init__(self, gate, up, down, bits: int, group_size: int):
+        if bits not in (2, 3, 4, 5, 6, 8) or group_size not in (32, 64, 128):
+            raise ValueError("bits 2/3/4/5/6/8 and group_size 32/64/128 are served")
+        if any(t.dim() != 3 for m in (gate, up, down) for t in m):
+            raise ValueError("gate, up and down must be (words, scales, biases), each [E, rows, ...]")
+        E, inner, hidden = gate[1].shape[0], gate[1].shape[1], down[1].shape[1]
+        if hidden % group_size or inner % group_size or hidden % 64 or inner % 64:
+            raise ValueError(f"hidden and inner size must be multiples of 64 and of the group size, "
+                             f"got {hidden} and {inner}")
+        parts = []
+        for name, m, rows, cols in (("gate", gate, inner, hidden), ("up", up, inner, hidden),
+                                    ("down", down, hidden, inner)):
+            for part, t, last in (("words", m[0], cols * bits // 32),
+                                  ("scales", m[1], cols // group_size),
+                                  ("biases", m[2], cols // group_size)):
+                if tuple(t.shape) != (E, rows, last):
+                    raise ValueError(f"{name} {part} must be {[E, rows, last]}, got {list(t.shape)}")
+                if part != "words" and t.dtype != torch.float16:
+                    raise ValueError(f"{name} {part} must be {torch.float16}, got {t.dtype}")
+                if part == "words" and t.element_size() != 4:
+                    raise ValueError(f"{name} words must be of 32 bits, got {t.dtype}")
+                if t.device != gate[0].device:
+                    raise ValueError("gate, up and down must be on one device")
+                parts.append((t, f"{name} {part}"))
+        self.gate, self.up, self.down = tuple(gate), tuple(up), tuple(down)
+        self.bits, self.group_size = bits, group_size
+        self.count, self.hidden, self.inner = E, hidden, inner
+        self._struct = _ExpertsStruct(*(_dev(t, name) for t, name in parts), E, hidden, inner, bits, group_size)
+        self._ref = ctypes.addressof(self._struct)
+        self._workspaces = {}
+
+
+def _moe_tokens(x, K: int, device, dtype=None) -> int:
+    if x.dtype not in _ACT or (dtype is not None and x.dtype != dtype):
+        raise ValueError(f"x must be {dtype or 'float16 or bfloat16'}, got {x.dtype}")
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x must be [T, {K}], got {list(x.shape)}")
+    if x.device != device:
+        raise ValueError(f"x must be on the weights' device {device}")
+    return x.shape[0]
+
+
+def _moe_pair(ids, weights, T: int, top_k: int, device) -> tuple:
+    """The addresses of the experts' ids and weights, [T, top_k] each."""
+    if ids.dtype != _I32 or weights.dtype != torch.float32:
+        raise ValueError("experts must be int32 and weights float32")
+    for name, t in (("experts", ids), ("weights", weights)):
+        if tuple(t.shape) != (T, top_k):
+            raise ValueError(f"{name} must be {[T, top_k]}, got {list(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} must be on x's device")
+    return _dev(ids, "experts"), _dev(weights, "weights")
+
+
+def _moe_pair_out(routed, T: int, top_k: int, device, stream):
+    if routed is None:
+        routed = (_empty((T, top_k), _I32, device, stream),
+                  _empty((T, top_k), torch.float32, device, stream))
+    ids, weights = routed
+    return ids, weights, *_moe_pair(ids, weights, T, top_k, device)
+
+
+def _moe_out(x, out, workspace, experts: AqExperts, T: int, top_k: int, stream) -> tuple:
+    if out is None:
+        out = _empty(x.shape, x.dtype, x.device, stream)
+    elif tuple(out.shape) != tuple(x.shape) or out.device != x.device:
+        raise ValueError(f"out must be {list(x.shape)} on x's device")
+    _check_out(out, "out", x.numel(), x.dtype)
+    if workspace is None:
+        # refused sizes reach the library's checks
+        workspace = _scratch(max(aq_moe_workspace_bytes(experts, T, top_k), 256), x.device, stream)
+    if workspace.dtype != torch.uint8:
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    return out, _dev(out, "out"), _dev(workspace, "workspace"), workspace.numel(), workspace
+
+
+def aq_moe_workspace_bytes(experts: AqExperts, T: int, top_k: int) -> int:
+    """Workspace bytes of aq_moe and aq_moe_experts (0: sizes that they refuse)."""
+    n = experts._workspaces.get((T, top_k))
+    if n is None:
+        n = int(load().aq_moe_workspace_bytes(experts._ref, T, top_k))
+        experts._workspaces[(T, top_k)] = n
+    return n
+
+
+def aq_moe_route(x, router: AqRouter, out=None, stream=None) -> tuple:
+    """The experts of each token of x [T, K]: (experts int32 [T, top_k], each
+    row ascending, weights float32 [T, top_k])."""
+    T = _moe_tokens(x, router.weight.shape[1], router.weight.device, router.weight.dtype)
+    ids, weights, ip, wp = _moe_pair_out(out, T, router.top_k, x.device, stream)
+    _check(load().aq_moe_route(router._ref, _dev(x, "x"), T, ip, wp, _stream(stream)),
+           "aq_moe_route")
+    return ids, weights
+
+
+def aq_moe_experts(x, experts: AqExperts, ids, weights, out=None, workspace=None,
+                   stream=None) -> torch.Tensor:
+    """y[t] = sum_j weights[t, j] * expert ids[t, j] of x[t]; ids int32
+    [T, top_k] (outside 0..E-1: none), weights float32 [T, top_k]."""
+    T = _moe_tokens(x, experts.hidden, experts.gate[0].device)
+    if ids.dim() != 2:
+        raise ValueError("experts must be [T, top_k]")
+    top_k = ids.shape[1]
+    ip, wp = _moe_pair(ids, weights, T, top_k, x.device)
+    out, op, ws, n, hold = _moe_out(x, out, workspace, experts, T, top_k, stream)
+    _check(load().aq_moe_experts(experts._ref, AQ_BF16 if x.dtype == torch.bfloat16 else AQ_F16,
+                                 _dev(x, "x"), T, top_k, ip, wp, op, ws, n, _stream(stream)),
+           "aq_moe_experts")
+    return out
+
+
+def aq_moe(x, router: AqRouter, experts: AqExperts, out=None, routed=None, workspace=None,
+           stream=None) -> tuple:
+    """The whole layer: routes x [T, K] and runs the chosen experts.  Returns
+    (y [T, K], experts int32 [T, top_k], weights float32 [T, top_k]); routed:
+    tensors for the last two."""
+    T = _moe_tokens(x, experts.hidden, experts.gate[0].device, router.weight.dtype)
+    if router.weight.shape != (experts.count, experts.hidden):
+        raise ValueError(f"the router is {list(router.weight.shape)}, the experts "
+                         f"{[experts.count, experts.hidden]}")
+    if router.weight.device != x.device:
+        raise ValueError("router and experts must be on one device")
+    ids, weights, ip, wp = _moe_pair_out(routed, T, router.top_k, x.device, stream)
+    out, op, ws, n, hold = _moe_out(x, out, workspace, experts, T, router.top_k, stream)
+    _check(load().aq_moe(router._ref, experts._ref, _dev(x, "x"), T, ip, wp, op, ws, n,
+                         _stream(stream)), "aq_moe")
+    return out, ids, weights
+
+
+def aq_embed(ids, Wq, scales, biases, bits: int, group_size: int, dtype, scale: float = 1.0,
+             out=None, stream=None) -> torch.Tensor:
+    """Rows of a quantised table by token: scale * row ids[...] as dtype (fp16
+    or bf16) [..., K]; ids int32 or int64, outside 0..N-1 a row of zeros.  Wq
+    [N, K*bits/32], scales and biases fp16 [N, K/group_size]."""
+    if dtype not in _ACT:
+        raise ValueError("dtype must be float16 or bfloat16")
+    if ids.dtype not in (_I32, torch.int64):
+        raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
+    if scales.dim() != 2:
+        raise ValueError("scales must be [N, K/group_size]")
+    N, K = scales.shape[0], scales.shape[1] * group_size
+    _check_weights(Wq, scales, biases, N, K, bits, group_size)
+    if not Wq.device == scales.device == biases.device == ids.device:
+        raise ValueError("ids and the table must be on one device")
+    T = ids.numel()
+    if out is None:
+        out = _empty((*ids.shape, K), dtype, ids.device, stream)
+    elif out.device != ids.device:
+        raise ValueError("out must be on ids' device")
+    _check_out(out, "out", T * K, dtype)
+    _check(load().aq_embed(AQ_BF16 if dtype == torch.bfloat16 else AQ_F16, _dev(ids, "ids"),
+                           ids.element_size(), T, _dev(Wq, "Wq"), _dev(scales, "scales"),
+                           _dev(biases, "biases"), N, K, bits, group_size, scale, _dev(out, "out"),
+                           _stream(stream)), "aq_embed")
     return out
 
 

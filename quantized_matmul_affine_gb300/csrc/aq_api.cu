@@ -5,6 +5,7 @@
 // times W^T, y in x's dtype, an error for no rows; plus the pack step and the
 // explicit-variant and host-memory entry points described in aq.h.
 #include "aq_internal.h"
+#include "aq_moe.h"
 #include "aq_paged.h"
 
 #include <cudaTypedefs.h>
@@ -613,6 +614,127 @@ aq_status aq_attention_batch(const aq_cache *cache, int64_t layer, int dtype, co
                          B, L, H, G, max_pages, scale, out_dev, workspace_dev, workspace_bytes,
                          static_cast<cudaStream_t>(stream)};
     return batch_launch(cache, layer, a) == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
+}
+
+static aq_status check_router(const aq_router *r) {
+    if (!r || !r->weight_dev || r->E < 1 || r->E > AQ_MOE_MAX_EXPERTS || r->K < 64 ||
+        r->K > 1 << 20 || r->K % 64 != 0 || (r->dtype != AQ_F16 && r->dtype != AQ_BF16) ||
+        r->top_k < 1 || r->top_k > AQ_MOE_MAX_TOP || r->top_k > r->E ||
+        (r->score != AQ_SCORE_SOFTMAX && r->score != AQ_SCORE_SIGMOID) || !std::isfinite(r->scale))
+        return AQ_ERR_INVALID_ARG;
+    if (r->bias_dev && r->score != AQ_SCORE_SIGMOID) return AQ_ERR_UNSUPPORTED;
+    if (!aligned(r->weight_dev, 16) || !aligned(r->bias_dev, 4)) return AQ_ERR_MISALIGNED;
+    return AQ_OK;
+}
+
+static aq_status check_routed(const void *x_dev, int64_t T, const int32_t *experts_dev,
+                              const float *weights_dev) {
+    if (T < 1 || T > AQ_MOE_MAX_TOKENS || !x_dev || !experts_dev || !weights_dev)
+        return AQ_ERR_INVALID_ARG;
+    if (!aligned(x_dev, 16) || !aligned(experts_dev, 4) || !aligned(weights_dev, 4))
+        return AQ_ERR_MISALIGNED;
+    return AQ_OK;
+}
+
+static bool valid_experts_sizes(const aq_experts *x) {
+    return x && x->E >= 1 && x->E <= AQ_MOE_MAX_EXPERTS && x->K >= 64 && x->K <= 1 << 20 &&
+           x->I >= 64 && x->I <= 1 << 20 && valid_width(x->bits) &&
+           (x->group_size == 32 || x->group_size == 64 || x->group_size == 128) &&
+           x->K % 64 == 0 && x->I % 64 == 0 && x->K % x->group_size == 0 &&
+           x->I % x->group_size == 0;
+}
+
+static aq_status check_experts(const aq_experts *x, int64_t T, int top_k, const void *out_dev,
+                               const void *workspace_dev, size_t workspace_bytes) {
+    if (!valid_experts_sizes(x) || T < 1 || T > AQ_MOE_MAX_TOKENS || top_k < 1 ||
+        top_k > AQ_MOE_MAX_TOP)
+        return AQ_ERR_INVALID_ARG;
+    const void *words[3] = {x->gate_words_dev, x->up_words_dev, x->down_words_dev};
+    const void *halves[6] = {x->gate_scales_dev, x->gate_biases_dev, x->up_scales_dev,
+                             x->up_biases_dev, x->down_scales_dev, x->down_biases_dev};
+    for (const void *w : words)
+        if (!w) return AQ_ERR_INVALID_ARG;
+    for (const void *s : halves)
+        if (!s) return AQ_ERR_INVALID_ARG;
+    if (!out_dev || !workspace_dev || workspace_bytes < moe_workspace_bytes(x, T, top_k))
+        return AQ_ERR_INVALID_ARG;
+    for (const void *w : words)
+        if (!aligned(w, 16)) return AQ_ERR_MISALIGNED;
+    for (const void *s : halves)
+        if (!aligned(s, 2)) return AQ_ERR_MISALIGNED;
+    if (!aligned(out_dev, 16) || !aligned(workspace_dev, 256)) return AQ_ERR_MISALIGNED;
+    return AQ_OK;
+}
+
+aq_status aq_moe_route(const aq_router *router, const void *x_dev, int64_t T,
+                       int32_t *experts_dev, float *weights_dev, void *stream) {
+    aq_status st = check_router(router);
+    if (st == AQ_OK) st = check_routed(x_dev, T, experts_dev, weights_dev);
+    if (st != AQ_OK) return st;
+    const RouteArgs a = {router, x_dev, T, experts_dev, weights_dev,
+                         static_cast<cudaStream_t>(stream)};
+    return moe_route_launch(a) == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
+}
+
+size_t aq_moe_workspace_bytes(const aq_experts *experts, int64_t T, int top_k) {
+    if (!valid_experts_sizes(experts) || T < 1 || T > AQ_MOE_MAX_TOKENS || top_k < 1 ||
+        top_k > AQ_MOE_MAX_TOP)
+        return 0;
+    return moe_workspace_bytes(experts, T, top_k);
+}
+
+aq_status aq_moe_experts(const aq_experts *experts, int dtype, const void *x_dev, int64_t T,
+                         int top_k, const int32_t *experts_dev, const float *weights_dev,
+                         void *out_dev, void *workspace_dev, size_t workspace_bytes,
+                         void *stream) {
+    if (dtype != AQ_F16 && dtype != AQ_BF16) return AQ_ERR_INVALID_ARG;
+    aq_status st = check_experts(experts, T, top_k, out_dev, workspace_dev, workspace_bytes);
+    if (st == AQ_OK) st = check_routed(x_dev, T, experts_dev, weights_dev);
+    if (st != AQ_OK) return st;
+    const ExpertsArgs a = {experts, dtype, x_dev, T, top_k, experts_dev, weights_dev, out_dev,
+                           workspace_dev, static_cast<cudaStream_t>(stream)};
+    return moe_experts_launch(a) == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
+}
+
+aq_status aq_moe(const aq_router *router, const aq_experts *experts, const void *x_dev, int64_t T,
+                 int32_t *experts_dev, float *weights_dev, void *out_dev, void *workspace_dev,
+                 size_t workspace_bytes, void *stream) {
+    aq_status st = check_router(router);
+    if (st == AQ_OK)
+        st = check_experts(experts, T, router->top_k, out_dev, workspace_dev, workspace_bytes);
+    if (st == AQ_OK) st = check_routed(x_dev, T, experts_dev, weights_dev);
+    if (st == AQ_OK && (router->E != experts->E || router->K != experts->K))
+        st = AQ_ERR_INVALID_ARG;
+    if (st != AQ_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const RouteArgs r = {router, x_dev, T, experts_dev, weights_dev, s};
+    if (moe_route_launch(r) != cudaSuccess) return AQ_ERR_CUDA;
+    const ExpertsArgs a = {experts, router->dtype, x_dev, T, router->top_k, experts_dev,
+                           weights_dev, out_dev, workspace_dev, s};
+    return moe_experts_launch(a) == cudaSuccess ? AQ_OK : AQ_ERR_CUDA;
+}
+
+aq_status aq_embed(int dtype, const void *ids_dev, int index_bytes, int64_t T,
+                   const uint32_t *Wq_dev, const void *scales_dev, const void *biases_dev,
+                   int64_t N, int64_t K, int bits, int group_size, float scale, void *out_dev,
+                   void *stream) {
+    if ((dtype != AQ_F16 && dtype != AQ_BF16) || (index_bytes != 4 && index_bytes != 8) || T < 0 ||
+        N < 1 || K < 32 || !valid_width(bits) ||
+        (group_size != 32 && group_size != 64 && group_size != 128) || K % group_size != 0 ||
+        !std::isfinite(scale))
+        return AQ_ERR_INVALID_ARG;
+    if (T == 0) return AQ_OK;
+    if (!ids_dev || !Wq_dev || !scales_dev || !biases_dev || !out_dev) return AQ_ERR_INVALID_ARG;
+    if (K > (int64_t)1 << 26 || N > (int64_t)1 << 31 || T > ((int64_t)1 << 38) / (K / 8))
+        return AQ_ERR_UNSUPPORTED;
+    if (!aligned(ids_dev, (uintptr_t)index_bytes) || !aligned(Wq_dev, 4) || !aligned(scales_dev, 2) ||
+        !aligned(biases_dev, 2) || !aligned(out_dev, 16))
+        return AQ_ERR_MISALIGNED;
+    return embed_launch(dtype, ids_dev, index_bytes == 8, T, Wq_dev, scales_dev, biases_dev, N, K,
+                        bits, group_size, scale, out_dev,
+                        static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? AQ_OK
+               : AQ_ERR_CUDA;
 }
 
 aq_status aq_matmul_multi(int dtype, const void *x_dev, int nproj, const uint32_t *const *Wq_dev,

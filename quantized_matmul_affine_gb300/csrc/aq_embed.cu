@@ -1,0 +1,88 @@
+// aq_embed: rows of an affine-quantised table by token, out[t] = scale * (s q + b).
+//
+// The table is in the weight format (mlx-bun pages, @mlx-bun/inference 1.0.0,
+// kernels/quantization/affine-split-mma.ts helper affine_unit), so a table
+// that is also the vocabulary projection is kept once.  A thread takes 8
+// values: B bytes of codes, which lie in two words at most, one 16-byte store.
+// s q + b is one fp32 fma, the product with the scale one more rounding, the
+// output type the last.  HBM-bound for long prompts, a launch for short ones.
+#include "aq_moe.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace aq {
+namespace {
+
+struct EmbedParams {
+    const void *ids;
+    const uint32_t *words;
+    const __half *scales, *biases;
+    uint4 *out;
+    int64_t T, N;
+    int K, group, wide, bf16;
+    float scale;
+};
+
+template <int B>
+__global__ void __launch_bounds__(256) embed_kernel(const __grid_constant__ EmbedParams p) {
+    const int per = p.K / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t t = i / per;
+    if (t >= p.T) return;
+    const int c = (int)(i - t * per);
+    const int64_t id = p.wide ? static_cast<const int64_t *>(p.ids)[t]
+                              : (int64_t) static_cast<const int32_t *>(p.ids)[t];
+    if (id < 0 || id >= p.N) {
+        p.out[i] = make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
+    const int row_words = p.K * B / 32, first = c * B / 4, sh = (c * B * 8) & 31;
+    const uint32_t *row = p.words + id * row_words;
+    const uint32_t w0 = row[first];
+    const uint32_t w1 = sh + 8 * B > 32 ? row[first + 1] : 0u;
+    const uint64_t codes = ((uint64_t)w1 << 32 | w0) >> sh;
+    const int64_t at = id * (p.K / p.group) + c * 8 / p.group;
+    const float s = __half2float(p.scales[at]), b = __half2float(p.biases[at]);
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float lo = fmaf(s, (float)((uint32_t)(codes >> (2 * j * B)) & ((1u << B) - 1u)), b) * p.scale;
+        const float hi = fmaf(s, (float)((uint32_t)(codes >> ((2 * j + 1) * B)) & ((1u << B) - 1u)), b) * p.scale;
+        if (p.bf16) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+            o[j] = *reinterpret_cast<const uint32_t *>(&v);
+        } else {
+            const __half2 v = __floats2half2_rn(lo, hi);
+            o[j] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+    }
+    p.out[i] = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int B>
+cudaError_t run(const EmbedParams &p, cudaStream_t stream) {
+    const int64_t blocks = (p.T * (p.K / 8) + 255) / 256;
+    embed_kernel<B><<<(unsigned)blocks, 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t embed_launch(int dtype, const void *ids, bool wide, int64_t T, const uint32_t *words,
+                         const void *scales, const void *biases, int64_t N, int64_t K, int bits,
+                         int group, float scale, void *out, cudaStream_t stream) {
+    const EmbedParams p = {ids, words, static_cast<const __half *>(scales),
+                           static_cast<const __half *>(biases), static_cast<uint4 *>(out), T, N,
+                           (int)K, group, wide ? 1 : 0, dtype == AQ_BF16 ? 1 : 0, scale};
+    switch (bits) {
+        case 2: return run<2>(p, stream);
+        case 3: return run<3>(p, stream);
+        case 4: return run<4>(p, stream);
+        case 5: return run<5>(p, stream);
+        case 6: return run<6>(p, stream);
+        default: return run<8>(p, stream);
+    }
+}
+
+}  // namespace aq

@@ -1,0 +1,444 @@
+// The mixture-of-experts layer's router, its sum over a token's experts, and
+// the host side of both and of the experts' products (aq_moe.cuh).
+//
+// Router: logits l[t][e] = x[t] . Wr[e], a score p = softmax(l[t]) or
+// 1 / (1 + exp(-l)), the top_k largest l (with a bias: the largest p + bias),
+// ties to the lowest index, weights p / (sum of the chosen p) or p, times a
+// factor.  The choice is that of exact arithmetic as far as 64 bits tell:
+//   * the logits are MMA sums in fp32, beside them the sums of |x w|, which
+//     bound their error;
+//   * experts whose value is farther from the k-th largest than the bounds
+//     are in or out for certain; where others are left to choose from, their
+//     logits are summed again with the rounding errors carried along (products
+//     of two 16-bit floats are exact in fp32, two-sums keep what each addition
+//     rounds off), which is good to about 2^-46 of the sum of |x w|.
+//   * weights come from the fp32 logits.
+// A cluster of 8 CTAs takes 8 or 32 tokens: its CTAs deal the experts (16 an
+// MMA tile) and, where there are fewer tiles than CTAs, slices of K; the parts
+// are sent to the CTA that chooses for the token, one warp a token.
+#include "aq_moe.h"
+#include "aq_ptx.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace aq {
+namespace {
+
+constexpr int kCluster = 8;
+constexpr int kWarps = 8;
+constexpr int kThreads = 256;
+constexpr int kLanes = AQ_MOE_MAX_EXPERTS / 32;  // experts a lane chooses from
+
+struct RouteParams {
+    const uint16_t *x, *w;
+    const float *bias;
+    int32_t *ids;
+    float *weights;
+    int T, E, K, top, score, normalize;
+    float scale;
+    int tiles;   // CTAs of a cluster that take different expert tiles; the rest slice K
+    int slices;  // kCluster / tiles
+};
+
+template <bool BF16>
+__device__ __forceinline__ void mma_x(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                      uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+            "{%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float value(uint16_t bits) {
+    if constexpr (BF16)
+        return __uint_as_float((uint32_t)bits << 16);
+    else
+        return __half2float(__ushort_as_half(bits));
+}
+
+// s + e = s + v exactly, what the addition rounds off added to e.
+__device__ __forceinline__ void two_sum(float &s, float &e, float v) {
+    const float t = __fadd_rn(s, v);
+    const float b = __fsub_rn(t, s);
+    e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(v, b)));
+    s = t;
+}
+
+// One logit to about 2^-46 of its sum of magnitudes, in every lane.
+template <bool BF16>
+__device__ double precise_logit(const uint16_t *x, const uint16_t *w, int K) {
+    const int lane = threadIdx.x & 31;
+    float s = 0.f, e = 0.f;
+    for (int k = lane; k < K; k += 32) two_sum(s, e, __fmul_rn(value<BF16>(x[k]), value<BF16>(w[k])));
+    double d = (double)s + (double)e;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
+    return d;
+}
+
+// Floats in the order of unsigned integers; NaN below everything.
+__device__ __forceinline__ uint32_t ordered(float v) {
+    if (!(v == v)) return 0u;
+    const uint32_t b = __float_as_uint(v);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// The choice for token t by one warp.  parts: [slices][2][E], sums and sums of
+// magnitudes; keep: E doubles for values summed again.
+template <bool BF16>
+__device__ void choose(const RouteParams &p, int t, const float *parts, double *keep) {
+    const int lane = threadIdx.x & 31;
+    const int per = (p.E + 31) / 32;
+    const bool sigmoid = p.score == AQ_SCORE_SIGMOID;
+    float logit[kLanes], val[kLanes];
+    float slack = 0.f;      // the largest error bound of a value
+    uint32_t open = 0u;     // experts not yet taken, by position
+    // a slice's warp adds K / (16 * slices * 8) products of 16 and then 8 warps
+    // and the slices are added: each step rounds (the MMA: truncates) to 2^-22
+    // of the partial sum at most
+    const float ulps = (float)(p.K / (16 * kWarps * p.slices) + 2 + kWarps + p.slices) * 2.384185791015625e-07f;
+#pragma unroll
+    for (int j = 0; j < kLanes; ++j) {
+        logit[j] = val[j] = -INFINITY;
+        const int e = j * 32 + lane;
+        if (j < per && e < p.E) {
+            float s = 0.f, m = 0.f;
+            for (int k = 0; k < p.slices; ++k) {
+                s += parts[(size_t)k * 2 * p.E + e];
+                m += parts[(size_t)k * 2 * p.E + p.E + e];
+            }
+            logit[j] = s;
+            float bound = ulps * m;
+            float v = s;
+            if (p.bias) {
+                v = 1.f / (1.f + expf(-s)) + p.bias[e];
+                bound = 0.25f * bound + 4.76837158203125e-07f * (1.f + fabsf(v));
+            }
+            val[j] = v == v ? v : -INFINITY;
+            if (bound < INFINITY) slack = fmaxf(slack, bound);
+            open |= 1u << j;
+        }
+    }
+    slack = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(slack)));
+
+    // the top_k of the fp32 values: the last one taken is the border
+    uint32_t left = open, taken = 0u;
+    float border = 0.f;
+    for (int n = 0; n < p.top; ++n) {
+        uint32_t best = 0u;
+        int at = 0x7FFFFFFF;
+#pragma unroll
+        for (int j = 0; j < kLanes; ++j) {
+            const uint32_t o = ordered(val[j]);
+            if ((left >> j & 1u) && (at == 0x7FFFFFFF || o > best)) {
+                best = o;
+                at = j * 32 + lane;
+            }
+        }
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
+        const int e = __reduce_min_sync(0xFFFFFFFFu, best == top ? at : 0x7FFFFFFF);
+        if (at == e) {
+            left &= ~(1u << (e >> 5));
+            taken |= 1u << (e >> 5);
+        }
+        border = top & 0x80000000u ? __uint_as_float(top & 0x7FFFFFFFu) : __uint_as_float(~top);
+    }
+    // the k-th largest exact value lies within slack of the border
+    uint32_t sure = 0u, doubt = 0u;
+#pragma unroll
+    for (int j = 0; j < kLanes; ++j) {
+        if (!(open >> j & 1u)) continue;
+        if (val[j] > border + 2.f * slack)
+            sure |= 1u << j;
+        else if (val[j] >= border - 2.f * slack)
+            doubt |= 1u << j;
+    }
+    const int n_sure = __reduce_add_sync(0xFFFFFFFFu, __popc(sure));
+    const int n_doubt = __reduce_add_sync(0xFFFFFFFFu, __popc(doubt));
+    // (a border that is not finite decides nothing: the fp32 choice stands)
+    if (n_sure + n_doubt > p.top && fabsf(border) < INFINITY) {
+        for (int e = 0; e < p.E; ++e) {
+            if (!(__shfl_sync(0xFFFFFFFFu, doubt, e & 31) >> (e >> 5) & 1u)) continue;
+            double d = precise_logit<BF16>(p.x + (size_t)t * p.K, p.w + (size_t)e * p.K, p.K);
+            if (p.bias) d = 1.0 / (1.0 + exp(-d)) + (double)p.bias[e];
+            if (lane == (e & 31)) keep[e] = d;
+        }
+        __syncwarp();
+        taken = sure;
+        for (int n = n_sure; n < p.top; ++n) {
+            double best = 0.0;
+            int at = 0x7FFFFFFF;
+            for (uint32_t m = doubt; m; m &= m - 1u) {
+                const int e = (__ffs(m) - 1) * 32 + lane;
+                if (at == 0x7FFFFFFF || keep[e] > best) {
+                    best = keep[e];
+                    at = e;
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double b = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+                const int a = __shfl_xor_sync(0xFFFFFFFFu, at, o);
+                if (a != 0x7FFFFFFF &&
+                    (at == 0x7FFFFFFF || b > best || (b == best && a < at))) {
+                    best = b;
+                    at = a;
+                }
+            }
+            if (lane == (at & 31)) {
+                doubt &= ~(1u << (at >> 5));
+                taken |= 1u << (at >> 5);
+            }
+        }
+    }
+
+    // weights: with m the largest (chosen) logit, exp(l - m); sigmoids times
+    // exp(-min(m, 0)), so that a sum of tiny ones does not vanish
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kLanes; ++j)
+        if ((sigmoid || p.normalize ? taken : open) >> j & 1u) m = fmaxf(m, logit[j]);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    if (sigmoid) m = p.normalize ? fminf(m, 0.f) : 0.f;
+    float sum = 0.f;
+    const uint32_t over = p.normalize ? taken : open;
+#pragma unroll
+    for (int j = 0; j < kLanes; ++j) {
+        // sigmoid: exp(-m) / (1 + exp(-l)), for l < 0 as exp(l - m) / (1 + exp(l))
+        const float l = logit[j];
+        val[j] = !sigmoid ? expf(l - m)
+                 : l < 0.f ? expf(l - m) / (1.f + expf(l))
+                           : expf(-m) / (1.f + expf(-l));
+        if (over >> j & 1u) sum += val[j];
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (sigmoid && !p.normalize) sum = 1.f;
+    int before = 0;
+#pragma unroll
+    for (int j = 0; j < kLanes; ++j) {
+        const uint32_t on = __ballot_sync(0xFFFFFFFFu, taken >> j & 1u);
+        if (taken >> j & 1u) {
+            const size_t at = (size_t)t * p.top + before + __popc(on & ((1u << lane) - 1u));
+            p.ids[at] = j * 32 + lane;
+            p.weights[at] = val[j] / sum * p.scale;
+        }
+        before += __popc(on);
+    }
+}
+
+template <bool BF16, int NB>
+__global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteParams p) {
+    constexpr int TOKENS = 8 * NB, MINE = TOKENS / kCluster;  // a CTA chooses for MINE tokens
+    extern __shared__ __align__(16) uint8_t dyn[];
+    // [kWarps][NB][2][32] float4 of the CTA's own sums; [MINE][slices][2][E]
+    // parts from all CTAs; [MINE][E] doubles
+    float4 *red = reinterpret_cast<float4 *>(dyn);
+    float *parts = reinterpret_cast<float *>(red + kWarps * NB * 2 * 32);
+    double *keep = reinterpret_cast<double *>(
+        reinterpret_cast<uint8_t *>(parts) + ((MINE * p.slices * 2 * p.E * 4 + 15) & ~15));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+    const int rank = (int)cluster_ctarank();
+    const int t0 = (int)(blockIdx.x / kCluster) * TOKENS;
+    const int slice = rank / p.tiles;
+    launch_dependents();
+    cluster_sync();  // every CTA of the cluster runs before its shared memory is written
+    grid_dependency_wait();
+
+    // the warp's 32-value steps of K
+    const int steps = p.K / 32, parts_k = p.slices * kWarps, me = slice * kWarps + warp;
+    const int k_beg = (int)((int64_t)steps * me / parts_k);
+    const int k_end = (int)((int64_t)steps * (me + 1) / parts_k);
+    for (int tile = rank % p.tiles; tile * 16 < p.E; tile += p.tiles) {
+        const int ra = min(tile * 16 + g, p.E - 1), rb = min(tile * 16 + 8 + g, p.E - 1);
+        const uint16_t *wa = p.w + (size_t)ra * p.K + 8 * q, *wb = p.w + (size_t)rb * p.K + 8 * q;
+        const uint16_t *xs[NB];
+        float d[NB][4], m[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            xs[nb] = p.x + (size_t)min(t0 + nb * 8 + g, p.T - 1) * p.K + 8 * q;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[nb][i] = m[nb][i] = 0.f;
+        }
+#pragma unroll 4
+        for (int k = k_beg; k < k_end; ++k) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(wa + 32 * k);
+            const uint4 b = *reinterpret_cast<const uint4 *>(wb + 32 * k);
+            constexpr uint32_t kAbs = 0x7FFF7FFFu;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(xs[nb] + 32 * k);
+                mma_x<BF16>(d[nb], a.x, b.x, a.y, b.y, x.x, x.y);
+                mma_x<BF16>(d[nb], a.z, b.z, a.w, b.w, x.z, x.w);
+                mma_x<BF16>(m[nb], a.x & kAbs, b.x & kAbs, a.y & kAbs, b.y & kAbs, x.x & kAbs,
+                            x.y & kAbs);
+                mma_x<BF16>(m[nb], a.z & kAbs, b.z & kAbs, a.w & kAbs, b.w & kAbs, x.z & kAbs,
+                            x.w & kAbs);
+            }
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            red[((warp * NB + nb) * 2) * 32 + lane] = make_float4(d[nb][0], d[nb][1], d[nb][2], d[nb][3]);
+            red[((warp * NB + nb) * 2 + 1) * 32 + lane] = make_float4(m[nb][0], m[nb][1], m[nb][2], m[nb][3]);
+        }
+        __syncthreads();
+        // add the warps' sums in order and send them to the token's CTA
+        for (int i = tid; i < NB * 2 * 32; i += kThreads) {
+            float4 s = red[i];
+            for (int w = 1; w < kWarps; ++w) {
+                const float4 v = red[w * NB * 2 * 32 + i];
+                s.x += v.x;
+                s.y += v.y;
+                s.z += v.z;
+                s.w += v.w;
+            }
+            const int ln = i & 31, which = (i >> 5) & 1, nb = i >> 6;
+            const float val[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int e = tile * 16 + (ln >> 2) + 8 * (j >> 1), n = nb * 8 + 2 * (ln & 3) + (j & 1);
+                if (e >= p.E) continue;
+                const float *to = parts + ((size_t)((n / kCluster) * p.slices + slice) * 2 + which) * p.E + e;
+                st_dsmem_f32(map_to_rank(smem_u32(to), (uint32_t)(n % kCluster)), val[j]);
+            }
+        }
+        __syncthreads();
+    }
+    cluster_sync();
+    if (warp < MINE) {
+        const int t = t0 + warp * kCluster + rank;
+        if (t < p.T) choose<BF16>(p, t, parts + (size_t)warp * p.slices * 2 * p.E, keep + (size_t)warp * p.E);
+    }
+}
+
+// y[t] = sum over j of weight * d[t * top + j], entries without an expert left
+// out, in j's order; four columns a thread.
+struct CombineParams {
+    const int32_t *ids;
+    const float *weights, *parts;
+    void *out;
+    int T, top, E, H, dtype;
+};
+
+__global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant__ CombineParams p) {
+    launch_dependents();
+    grid_dependency_wait();
+    const int per = p.H / 4;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= (int64_t)p.T * per) return;
+    const int t = (int)(i / per), c = (int)(i - (int64_t)t * per);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < p.top; ++j) {
+        const int64_t at = (int64_t)t * p.top + j;
+        const int e = p.ids[at];
+        if (e < 0 || e >= p.E) continue;
+        const float w = p.weights[at];
+        const float4 v = reinterpret_cast<const float4 *>(p.parts)[at * per + c];
+        s.x = fmaf(w, v.x, s.x);
+        s.y = fmaf(w, v.y, s.y);
+        s.z = fmaf(w, v.z, s.z);
+        s.w = fmaf(w, v.w, s.w);
+    }
+    uint2 o;
+    if (p.dtype == AQ_BF16) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(s.x, s.y), b = __floats2bfloat162_rn(s.z, s.w);
+        o = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    } else {
+        o = make_uint2(pack_half2(s.x, s.y), pack_half2(s.z, s.w));
+    }
+    reinterpret_cast<uint2 *>(p.out)[i] = o;
+}
+
+template <bool BF16, int NB>
+cudaError_t route_run(const RouteParams &p, cudaStream_t stream) {
+    const int mine = 8 * NB / kCluster;
+    const size_t smem = (size_t)kWarps * NB * 2 * 32 * 16 +
+                        (((size_t)mine * p.slices * 2 * p.E * 4 + 15) & ~(size_t)15) +
+                        (size_t)mine * p.E * 8;
+    const unsigned blocks = (unsigned)((p.T + 8 * NB - 1) / (8 * NB)) * kCluster;
+    auto *kern = route_kernel<BF16, NB>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return moe_launch(kern, dim3(blocks), kThreads, smem, kCluster, stream, p);
+}
+
+}  // namespace
+
+cudaError_t moe_route_launch(const RouteArgs &a) {
+    const aq_router &r = *a.router;
+    RouteParams p = {};
+    p.x = static_cast<const uint16_t *>(a.x);
+    p.w = static_cast<const uint16_t *>(r.weight_dev);
+    p.bias = r.bias_dev;
+    p.ids = a.ids;
+    p.weights = a.weights;
+    p.T = (int)a.T;
+    p.E = (int)r.E;
+    p.K = (int)r.K;
+    p.top = r.top_k;
+    p.score = r.score;
+    p.normalize = r.normalize;
+    p.scale = r.scale;
+    p.tiles = 1;
+    while (p.tiles < kCluster && p.tiles * 16 < p.E) p.tiles *= 2;
+    p.slices = kCluster / p.tiles;
+    const bool bf16 = r.dtype == AQ_BF16;
+    if (a.T > 64) return bf16 ? route_run<true, 4>(p, a.stream) : route_run<false, 4>(p, a.stream);
+    return bf16 ? route_run<true, 1>(p, a.stream) : route_run<false, 1>(p, a.stream);
+}
+
+namespace {
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+}  // namespace
+
+// h [T * top][I] and the down products [T * top][K], fp32.
+size_t moe_workspace_bytes(const aq_experts *x, int64_t T, int top_k) {
+    return round256((size_t)T * top_k * x->I * 4) + round256((size_t)T * top_k * x->K * 4);
+}
+
+cudaError_t moe_experts_launch(const ExpertsArgs &a) {
+    const aq_experts &x = *a.experts;
+    float *h = static_cast<float *>(a.ws);
+    float *parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) +
+                                             round256((size_t)a.T * a.top_k * x.I * 4));
+    cudaError_t (*product)(const MoeParams &, bool, cudaStream_t) =
+        x.bits == 2   ? moe_product_b2
+        : x.bits == 3 ? moe_product_b3
+        : x.bits == 4 ? moe_product_b4
+        : x.bits == 5 ? moe_product_b5
+        : x.bits == 6 ? moe_product_b6
+                      : moe_product_b8;
+    MoeParams p = {x.gate_words_dev, x.up_words_dev, x.gate_scales_dev, x.up_scales_dev,
+                   x.gate_biases_dev, x.up_biases_dev, a.ids, a.x, h, (int)a.T, a.top_k, (int)x.E,
+                   (int)x.I, (int)x.K, x.group_size, a.dtype};
+    cudaError_t e = product(p, true, a.stream);
+    if (e != cudaSuccess) return e;
+    p.w0 = p.w1 = x.down_words_dev;
+    p.s0 = p.s1 = x.down_scales_dev;
+    p.b0 = p.b1 = x.down_biases_dev;
+    p.src = h;
+    p.dst = parts;
+    p.R = (int)x.K;
+    p.K = (int)x.I;
+    e = product(p, false, a.stream);
+    if (e != cudaSuccess) return e;
+    const CombineParams c = {a.ids, a.weights, parts, a.out, (int)a.T, a.top_k, (int)x.E, (int)x.K,
+                             a.dtype};
+    const int64_t threads = a.T * (x.K / 4);
+    return moe_launch(combine_kernel, dim3((unsigned)((threads + kThreads - 1) / kThreads)), kThreads,
+                      0, 1, a.stream, c);
+}
+
+}  // namespace aq
