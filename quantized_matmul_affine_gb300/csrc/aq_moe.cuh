@@ -40,65 +40,113 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <cmath>
+#include <type_traits>
 
 namespace aq {
 namespace moe_detail {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxTiles = 16;      // tiles of a pass
-constexpr int kDynamic = 90112;    // dynamic shared memory: two CTAs an SM
+constexpr int kMaxTiles = 16;        // tiles of a pass
+constexpr int kRing = 6144;          // bytes of codes in flight a warp
+constexpr int kDynamic = 110592;     // dynamic shared memory: two CTAs an SM
 constexpr uint16_t kNone = 0xFFFF;
 constexpr int kMaxEntries = AQ_MOE_MAX_TOKENS * AQ_MOE_MAX_TOP;
 
-// How the 16 codes of a lane's segment land in the 8 registers of fp16 pairs:
-// register p holds codes lo(p) and hi(p) at bit position pre(p).
-template <int B>
+// A lane's 16 codes of one row and unit are codes [16q, 16q + 16), or with
+// groups of 32 codes [8q, 8q + 8) of either group, so that the MMA's first two
+// k steps are one group and the last two the other.  Order says how they land
+// in 8 registers of fp16 pairs: register p holds codes lo(p) and hi(p) of the
+// lane's 16, at bit position pre(p).
+template <int B, bool G32>
 struct Order {
+    static constexpr int kHalf = G32 ? 4 : 8;  // distance of a pair's codes in the odd widths
     __host__ __device__ static constexpr int lo(int p) {
-        return B == 4 ? (p / 4) * 8 + p % 4 : B == 8 ? (p / 2) * 4 + p % 2 : p;
+        return B == 4 ? (p / 4) * 8 + p % 4 : B == 8 ? (p / 2) * 4 + p % 2 : (p / kHalf) * 8 + p % kHalf;
     }
     __host__ __device__ static constexpr int hi(int p) {
-        return B == 4 ? lo(p) + 4 : B == 8 ? lo(p) + 2 : p + 8;
+        return lo(p) + (B == 4 ? 4 : B == 8 ? 2 : kHalf);
     }
     __host__ __device__ static constexpr int pre(int p) {
-        return B == 2   ? (p < 5 ? 2 * p : 2 * (p - 5))
-               : B == 3 ? (p < 3 ? 3 * p : p < 5 ? 3 * (p - 3) : 3 * (p - 5))
+        const int k = p % kHalf;
+        return B == 2   ? (k < 5 ? 2 * k : 2 * (k - 5))
+               : B == 3 ? (k < 3 ? 3 * k : k < 5 ? 3 * (k - 3) : 3 * (k - 5))
                : B == 4 ? 4 * (p & 1)
-               : B == 5 ? (p % 3 == 1 ? 5 : 0)
+               : B == 5 ? (k % 3 == 1 ? 5 : 0)
                         : 0;
     }
 };
 
-// 32-bit words that hold a lane's 16 codes of one row and unit (odd widths
-// start in the middle of a word in odd lanes).
+// 32-bit words that hold a lane's 16 codes (codes that start or end inside a
+// word bring their neighbours along).
+template <int B, bool G32>
+constexpr int kWords = B == 8 ? 4 : B == 4 ? 2 : G32 ? (B == 2 ? 2 : 4) : (B == 2 ? 1 : B == 3 ? 2 : 3);
+// Units of 64 values taken in one step: two where that makes a row's codes of
+// a step whole 16-byte pieces.
 template <int B>
-constexpr int kWords = B == 2 ? 1 : B == 3 || B == 4 ? 2 : B == 8 ? 4 : 3;
-// Units in flight a lane: about 32 registers.
-template <int B>
-constexpr int kAhead = B == 8 ? 4 : kWords<B> == 3 ? 5 : 8;
+constexpr int kUnits = B == 6 || B == 8 ? 1 : 2;
 
-template <int B>
-__device__ __forceinline__ void load_codes(const uint32_t *p, uint32_t (&w)[kWords<B>]) {
-    if constexpr (B == 4) {
-        asm("ld.global.nc.L1::no_allocate.L2::128B.v2.u32 {%0, %1}, [%2];"
-            : "=r"(w[0]), "=r"(w[1])
-            : "l"(p));
-    } else if constexpr (B == 8) {
-        asm("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
-            : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-            : "l"(p));
+// First bit of the lane's codes in a unit's row (with groups of 32 the second
+// group's lie B words on).
+template <int B, bool G32>
+__device__ __forceinline__ int first_bit(int q) {
+    return (G32 ? 8 : 16) * B * q;
+}
+
+// Shared memory by 32-bit address: the loop's addresses stay in one register.
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+template <int N>
+__device__ __forceinline__ void lds(uint32_t a, uint32_t *v) {
+    if constexpr (N == 4) {
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(a)
+                     : "memory");
+    } else if constexpr (N == 2) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a) : "memory");
     } else {
-#pragma unroll
-        for (int i = 0; i < kWords<B>; ++i)
-            asm("ld.global.nc.L2::128B.u32 %0, [%1];" : "=r"(w[i]) : "l"(p + i));
+        static_assert(N == 1, "1, 2 or 4 words");
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(a) : "memory");
     }
 }
 
-// A lane's 16 codes as 8 registers of two fp16 subnormals each; sh: 0, or 16
-// where the codes start in the upper half of the first word.
-template <int B>
-__device__ __forceinline__ void decode(const uint32_t (&w)[kWords<B>], uint32_t sh,
+// The words of a lane's codes of one row and unit.
+template <int B, bool G32>
+__device__ __forceinline__ void load_codes(uint32_t a, uint32_t (&w)[kWords<B, G32>]) {
+    constexpr int N = kWords<B, G32>;
+    if constexpr (!G32 && (B == 4 || B == 8)) {
+        lds<N>(a, w);
+    } else if constexpr (!G32) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) lds<1>(a + 4 * i, w + i);
+    } else if constexpr (B == 8) {
+        lds<2>(a, w);
+        lds<2>(a + 32, w + 2);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) lds<1>(a + 4 * (B * h + i), w + h * (N / 2) + i);
+    }
+}
+
+// A lane's 16 codes as 8 registers of two fp16 subnormals each; sh: where they
+// start in the first word.
+template <int B, bool G32>
+__device__ __forceinline__ void decode(const uint32_t (&w)[kWords<B, G32>], uint32_t sh,
                                        uint32_t (&r)[8]) {
     if constexpr (B == 4) {
 #pragma unroll
@@ -114,6 +162,44 @@ __device__ __forceinline__ void decode(const uint32_t (&w)[kWords<B>], uint32_t 
         for (int i = 0; i < 4; ++i) {
             r[2 * i] = w[i] & 0x00FF00FFu;
             r[2 * i + 1] = prmt(w[i], 0u, 0x4341u);  // bytes 1 and 3
+        }
+    } else if constexpr (G32) {
+        // 8 codes of each group: the first four and the last four side by side
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t *o = r + 4 * h;
+            if constexpr (B == 2) {
+                const uint32_t a = w[h] >> sh, x = prmt(a, a >> 8, 0x5410u);
+                o[0] = x & 0x00030003u;
+                o[1] = x & 0x000C000Cu;
+                o[2] = x & 0x00300030u;
+                o[3] = x & 0x00C000C0u;
+            } else {
+                const uint32_t a = __funnelshift_r(w[2 * h], w[2 * h + 1], sh);
+                if constexpr (B == 3) {
+                    const uint32_t x = prmt(a, a >> 12, 0x5410u);
+                    o[0] = x & 0x00070007u;
+                    o[1] = x & 0x00380038u;
+                    o[2] = x & 0x01C001C0u;
+                    o[3] = (x >> 9) & 0x00070007u;
+                } else {
+                    const uint32_t b = w[2 * h + 1] >> sh;
+                    const uint32_t t = __funnelshift_r(a, b, 4 * B);
+                    uint32_t x = prmt(a, t, 0x5410u);
+                    if constexpr (B == 5) {
+                        o[0] = x & 0x001F001Fu;
+                        o[1] = x & 0x03E003E0u;
+                        o[2] = (x >> 10) & 0x001F001Fu;
+                        o[3] = prmt(a >> 15, t >> 15, 0x5410u) & 0x001F001Fu;
+                    } else {
+                        o[0] = x & 0x003F003Fu;
+                        o[1] = (x >> 6) & 0x003F003Fu;
+                        x = prmt(a >> 12, t >> 12, 0x5410u);
+                        o[2] = x & 0x003F003Fu;
+                        o[3] = (x >> 6) & 0x003F003Fu;
+                    }
+                }
+            }
         }
     } else if constexpr (B == 2) {
         const uint32_t v = w[0] >> 10;
@@ -166,6 +252,14 @@ __device__ __forceinline__ void decode(const uint32_t (&w)[kWords<B>], uint32_t 
     }
 }
 
+// d = a b + d, or without d.
+__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                     uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
@@ -174,57 +268,53 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 source values, from x (fp16 or bf16) or h (fp32).
+// The words of 8 source values, from x (fp16 or bf16) or h (fp32); ordinary
+// loads, since this grid may have started before they were written.
 template <bool PAIRS>
-__device__ __forceinline__ void source16(const MoeParams &p, size_t at, float (&v)[16]) {
-    if constexpr (PAIRS) {
-        const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.src) + at);
-        const uint4 a = s[0], b = s[1];
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void source8(const MoeParams &p, size_t at, uint32_t *w) {
+    const uint8_t *s = static_cast<const uint8_t *>(p.src) + at * (PAIRS ? 2 : 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (p.dtype == AQ_BF16) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            } else {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-                v[2 * i] = f.x;
-                v[2 * i + 1] = f.y;
-            }
-        }
-    } else {
-        const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p.src) + at);
+    for (int i = 0; i < (PAIRS ? 1 : 2); ++i)
+        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                     : "l"(s + 16 * i)
+                     : "memory");
+}
+template <bool PAIRS>
+__device__ __forceinline__ void widen16(const MoeParams &p, const uint32_t (&w)[PAIRS ? 8 : 16], float (&v)[16]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 f = s[i];
-            v[4 * i] = f.x;
-            v[4 * i + 1] = f.y;
-            v[4 * i + 2] = f.z;
-            v[4 * i + 3] = f.w;
+    for (int i = 0; i < 16; ++i) {
+        if constexpr (!PAIRS) {
+            v[i] = __uint_as_float(w[i]);
+        } else if (p.dtype == AQ_BF16) {
+            v[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+        } else {
+            const __half2 h = *reinterpret_cast<const __half2 *>(&w[i / 2]);
+            v[i] = i & 1 ? __high2float(h) : __low2float(h);
         }
     }
 }
 
 struct Shared {
-    uint16_t act[AQ_MOE_MAX_EXPERTS];  // the busy experts, ascending
-    uint16_t ids[kMaxEntries];         // every entry's expert, kNone without one
-    uint16_t list[kMaxEntries];        // entries t * top + j of the current expert
     int count[AQ_MOE_MAX_EXPERTS];     // entries of each expert
+    uint16_t act[AQ_MOE_MAX_EXPERTS];  // the busy experts, ascending
+    uint16_t list[32];                 // entries t * top + j of the current columns
     uint32_t peak[32];                 // a column's largest magnitude, as bits
     float undo[32];                    // a column's inverse power of two
     int warp_sum[kWarps];
-    int busy, listed;
+    int busy;
 };
 
-// Counts the entries of every expert and lists the busy experts in order.
-__device__ __forceinline__ void plan(const MoeParams &p, Shared &sh) {
+// Counts the entries of every expert, lists the busy experts in order and
+// keeps every entry's expert in ids (kNone without one).
+__device__ __forceinline__ void plan(const MoeParams &p, Shared &sh, uint16_t *ids) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int e = tid; e < p.E; e += kThreads) sh.count[e] = 0;
     __syncthreads();
     for (int i = tid; i < p.T * p.top; i += kThreads) {
         const int e = __ldcg(p.ids + i);  // from L2: another grid may have just written them
         const bool on = e >= 0 && e < p.E;
-        sh.ids[i] = on ? (uint16_t)e : kNone;
+        ids[i] = on ? (uint16_t)e : kNone;
         if (on) atomicAdd(&sh.count[e], 1);
     }
     __syncthreads();
@@ -247,254 +337,491 @@ __device__ __forceinline__ void plan(const MoeParams &p, Shared &sh) {
     __syncthreads();
 }
 
-// The entries of expert e, in order.
-__device__ __forceinline__ void list_entries(const MoeParams &p, int e, Shared &sh) {
+// Entries first .. first + MOST - 1 of expert e, in order.
+template <int MOST>
+__device__ __forceinline__ void list_entries(const MoeParams &p, int e, int first, Shared &sh,
+                                             const uint16_t *ids) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int before = 0;
-    for (int i0 = 0; i0 < p.T * p.top; i0 += kThreads) {
+    int before = -first;
+    for (int i0 = 0; i0 < p.T * p.top && before < MOST; i0 += kThreads) {
         const int i = i0 + tid;
-        const bool on = i < p.T * p.top && sh.ids[i] == e;
+        const bool on = i < p.T * p.top && ids[i] == e;
         const uint32_t m = __ballot_sync(0xFFFFFFFFu, on);
         if (lane == 0) sh.warp_sum[warp] = __popc(m);
         __syncthreads();
-        int at = before;
+        int at = before + __popc(m & ((1u << lane) - 1u));
         for (int w = 0; w < kWarps; ++w) {
             if (w < warp) at += sh.warp_sum[w];
             before += sh.warp_sum[w];
         }
-        if (on) sh.list[at + __popc(m & ((1u << lane) - 1u))] = (uint16_t)i;
+        if (on && at >= 0 && at < MOST) sh.list[at] = (uint16_t)i;
         __syncthreads();
     }
 }
 
-// 64-value units of K whose activations, group sums and scales fit in shared
-// memory beside the slots and totals of nt tiles.
-__host__ __device__ constexpr int units_that_fit(int nt, int ncols, int nb, int sets) {
-    const int fixed = (2 * nt + kWarps - 1) * nb * 512 + 128 + nt * 16 * 8 + ncols * 64 + 64;
-    const int each = 8 * nb * sets * 4 + nt * 16 * sets * 4 + ncols * 128;
-    return (kDynamic - fixed) / each;
-}
-// With 32 columns and groups of 32 (the most a unit takes), four tiles still
-// leave chunks of 8 units and more.
-static_assert(units_that_fit(4, 32, 4, 2) >= 8 && units_that_fit(8, 16, 2, 2) >= 8, "chunks");
-
-// A pass: tiles tile0 .. tile0 + nt - 1 of expert e for the ncols entries at
-// list[col0].
+// A pass: tiles tile0 .. tile0 + nt - 1 of expert e for the ncols listed
+// entries.  flat: the (tile, step) pairs are dealt to the warps in even runs;
+// otherwise each warp, or `share` warps, keep TT tiles for the whole of K.
 struct Pass {
-    int e, tile0, nt, col0, ncols;
+    int e, tile0, nt, ncols;
 };
 
-template <int BITS, bool G32, bool PAIRS, int NB>
-__device__ __forceinline__ void run_pass(const MoeParams &p, const Pass &ps, Shared &sh,
-                                         uint8_t *dyn, bool wait) {
-    constexpr int NW = kWords<BITS>, AHEAD = kAhead<BITS>, C = 8 * NB;
-    constexpr int SETS = G32 ? 2 : 1;  // groups of a unit whose sums are kept apart
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-    const int U = p.K / 64, nt = ps.nt;
-    const int groups = p.K / p.group;
+// 64-value units of K (a multiple of 4) whose activations, group sums and
+// scales fit in `room` bytes of shared memory.
+__host__ __device__ constexpr int units_that_fit(int room, bool flat, int tt, int nb, int nt,
+                                                 int ncols, int sets) {
+    const int sums = flat ? (nt + (nt + tt - 1) / tt * tt + (kWarps - 1) * tt) * nb * 512 : 0;
+    const int fixed = sums + nt * 1024 + ncols * 64;
+    const int each = 8 * nb * sets * 4 + nt * 16 * sets * 4 + ncols * 128;
+    return (room - fixed) / each & ~3;
+}
+constexpr int kRoom = kDynamic - kWarps * kRing;  // less the entries' experts
+// The most a unit takes, beside the most entries, still leaves chunks of 4.
+static_assert(units_that_fit(kRoom - 2 * kMaxEntries, false, 2, 4, 16, 32, 2) >= 4 &&
+              units_that_fit(kRoom - 2 * kMaxEntries, true, 2, 1, 16, 8, 2) >= 4 &&
+              kRoom - 2 * kMaxEntries >= kWarps * 2 * 4 * 512, "chunks");
 
-    // shared memory: slots, totals, group sums, zeros, (scale, bias) pairs, activations
-    float4 *slots = reinterpret_cast<float4 *>(dyn);
-    float4 *total = slots + (nt + kWarps - 1) * NB * 32;
-    int cu = units_that_fit(nt, ps.ncols, NB, SETS);  // units of a chunk; even: whole groups of 128
-    cu = cu >= U ? U : cu & ~1;
-    const int ng_all = p.group == 128 ? (cu + 1) / 2 : cu * SETS;
-    const int sp = ng_all | 1;  // pairs of a row: an odd pitch keeps the 8 rows on 8 banks
-    const int pitch = cu * 128 + 64;
-    float *sums = reinterpret_cast<float *>(total + nt * NB * 32);
-    uint4 *zeros = reinterpret_cast<uint4 *>(sums + cu * SETS * C);
-    __half2 *pairs = reinterpret_cast<__half2 *>(zeros + 8);
-    uint8_t *act = reinterpret_cast<uint8_t *>(pairs) + ((nt * 16 * sp * 4 + 15) & ~15);
+// Copies P bytes (a plain load and store for 2), asynchronously from 4 up.
+template <int P>
+__device__ __forceinline__ void copy_piece(uint32_t to, const uint8_t *from) {
+    if constexpr (P == 16)
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else if constexpr (P == 8)
+        asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+    else if constexpr (P == 4)
+        asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+    else
+        asm volatile("{\n\t.reg .b16 v;\n\tld.global.b16 v, [%1];\n\tst.shared.b16 [%0], v;\n\t}" ::"r"(to),
+                     "l"(from)
+                     : "memory");
+}
 
-    const int64_t row_words = (int64_t)p.K * BITS / 32;
-    const uint32_t shift = BITS & 1 ? (uint32_t)(q & 1) * 16u : 0u;
-    for (int u0 = 0; u0 < U; u0 += cu) {
-        const int n = U - u0 < cu ? U - u0 : cu;  // units of this chunk
-        const int total_units = nt * n;
-        const int beg = total_units * warp / kWarps, end = total_units * (warp + 1) / kWarps;
-        int t = beg / n, u = beg - t * n;
-
-        // codes: pointers of the loads in flight, one unit after the other
-        const int64_t row0 = (int64_t)ps.e * p.R + (int64_t)(ps.tile0 + t) * (PAIRS ? 8 : 16) + g;
-        const int64_t off = row0 * row_words + (int64_t)(u0 + u) * (2 * BITS) + BITS * q / 2;
-        const uint32_t *pa = p.w0 + off;
-        const uint32_t *pb = (PAIRS ? p.w1 : p.w0 + 8 * row_words) + off;
-        const int64_t jump = (PAIRS ? 8 : 16) * row_words - (int64_t)n * (2 * BITS);
-        int pu = u;
-        uint32_t wa[AHEAD][NW], wb[AHEAD][NW];
-        auto fetch = [&](uint32_t(&a)[NW], uint32_t(&b)[NW]) {
-            load_codes<BITS>(pa, a);
-            load_codes<BITS>(pb, b);
-            pa += 2 * BITS;
-            pb += 2 * BITS;
-            if (++pu == n) {
-                pu = 0;
-                pa += jump;
-                pb += jump;
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-            if (beg + i < end) fetch(wa[i], wb[i]);
-
-        if (wait && u0 == 0) grid_dependency_wait();
-        if (u0 == 0 && tid < 32) sh.peak[tid] = 0u;
-        __syncthreads();  // the last chunk's or pass's readers are done
-
-        // (scale, bias) of the pass's rows
-        const int g0 = (int)((int64_t)u0 * 64 / p.group), ng = (n * 64 + p.group - 1) / p.group;
-        for (int i = tid; i < nt * 16 * ng; i += kThreads) {
-            const int row = i / ng, k = i - row * ng, r = row & 15;
-            const bool second = PAIRS && r >= 8;
-            const int64_t at =
-                ((int64_t)ps.e * p.R + (int64_t)(ps.tile0 + (row >> 4)) * (PAIRS ? 8 : 16) +
-                 (PAIRS ? r & 7 : r)) * groups + g0 + k;
-            const __half s = static_cast<const __half *>(second ? p.s1 : p.s0)[at];
-            const __half b = static_cast<const __half *>(second ? p.b1 : p.b0)[at];
-            pairs[row * sp + k] = __halves2half2(s, b);
+// The scales and biases of the pass's rows for the groups of units u0 .. u0 +
+// n - 1: each row's scales, sp bytes on its biases, zeros up to `padded` units.
+template <bool PAIRS, int P>
+__device__ __forceinline__ void copy_scales(const MoeParams &p, const Pass &ps, int g0, int bytes, int groups,
+                                            uint32_t scales, int sp) {
+    const int per = (bytes + P - 1) / P, rows = ps.nt * 16;
+    // rows by threads, so that a row's pieces need no division; a wide row is
+    // shared by several
+    const int tid = threadIdx.x;
+    int lanes = 1;
+    while (lanes < 32 && lanes < per) lanes *= 2;
+    for (int row = tid / lanes; row < rows; row += kThreads / lanes) {
+        const int r = row & 15;
+        const bool second = PAIRS && r >= 8;
+        const int64_t at = (((int64_t)ps.e * p.R + (int64_t)(ps.tile0 + (row >> 4)) * (PAIRS ? 8 : 16) +
+                             (PAIRS ? r & 7 : r)) * groups + g0) * 2;
+        const uint8_t *s = static_cast<const uint8_t *>(second ? p.s1 : p.s0) + at;
+        const uint8_t *b = static_cast<const uint8_t *>(second ? p.b1 : p.b0) + at;
+        for (int k = tid % lanes; k < per; k += lanes) {
+            copy_piece<P>(scales + (uint32_t)(2 * row * sp + k * P), s + k * P);
+            copy_piece<P>(scales + (uint32_t)((2 * row + 1) * sp + k * P), b + k * P);
         }
-        // the columns' largest magnitudes
-        if (u0 == 0) {
-            for (int i = tid; i < ps.ncols * U * 4; i += kThreads) {
-                const int c = i / (U * 4);
-                const int entry = sh.list[ps.col0 + c];
-                float v[16];
-                source16<PAIRS>(p, (size_t)(PAIRS ? entry / p.top : entry) * p.K +
-                                       (size_t)(i - c * U * 4) * 16, v);
-                float m = 0.f;
+    }
+}
+template <bool PAIRS, int SETS>
+__device__ __forceinline__ void stage_scales(const MoeParams &p, const Pass &ps, int u0, int n, int padded,
+                                             int groups, uint32_t scales, int sp) {
+    const int wide = p.group == 128;
+    const int g0 = wide ? u0 / 2 : u0 * SETS, ng = wide ? n / 2 : n * SETS;
+    // the largest piece that the rows' starts and lengths allow
+    const uint32_t all = (uint32_t)(reinterpret_cast<uintptr_t>(p.s0) | reinterpret_cast<uintptr_t>(p.b0) |
+                                    reinterpret_cast<uintptr_t>(p.s1) | reinterpret_cast<uintptr_t>(p.b1)) |
+                         (uint32_t)(groups * 2) | (uint32_t)(g0 * 2) | (uint32_t)(ng * 2);
+    if ((all & 15) == 0)
+        copy_scales<PAIRS, 16>(p, ps, g0, ng * 2, groups, scales, sp);
+    else if ((all & 7) == 0)
+        copy_scales<PAIRS, 8>(p, ps, g0, ng * 2, groups, scales, sp);
+    else if ((all & 3) == 0)
+        copy_scales<PAIRS, 4>(p, ps, g0, ng * 2, groups, scales, sp);
+    else
+        copy_scales<PAIRS, 2>(p, ps, g0, ng * 2, groups, scales, sp);
+    const int zeros = (wide ? (padded + 1) / 2 : padded * SETS) - ng;
+    for (int i = threadIdx.x; i < ps.nt * 32 * zeros; i += kThreads)
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(scales + (uint32_t)(i / zeros * sp + (ng + i % zeros) * 2)),
+                     "h"((short)0)
+                     : "memory");
+}
+
+// The pass's columns as fp16 in MMA order, with their group sums.
+template <int BITS, bool G32, bool PAIRS, int C>
+__device__ __forceinline__ void stage_columns(const MoeParams &p, const Pass &ps, Shared &sh, int u0,
+                                              int n, int padded, int pitch, float *sums, uint8_t *act) {
+    using Ord = Order<BITS, G32>;
+    constexpr int SETS = G32 ? 2 : 1, KEPT = 2;  // quarters a thread has in flight
+    const int tid = threadIdx.x, lane = tid & 31, U = p.K / 64;
+    const uint32_t quad = 0xFu << (lane & ~3);  // a unit's four lanes come together
+    // a unit's quarter (column c, quarter k of K): 16 values in two pieces
+    auto source = [&](int c, int k, size_t &second) {
+        const int entry = sh.list[c];
+        second = G32 ? 32 : 8;
+        return (size_t)(PAIRS ? entry / p.top : entry) * p.K +
+               (G32 ? (size_t)(k >> 2) * 64 + (k & 3) * 8 : (size_t)k * 16);
+    };
+    uint32_t raw[KEPT][PAIRS ? 8 : 16];
+    auto load = [&](int c, int k, uint32_t(&w)[PAIRS ? 8 : 16]) {
+        size_t second;
+        const size_t at = source(c, k, second);
+        source8<PAIRS>(p, at, w);
+        source8<PAIRS>(p, at + second, w + (PAIRS ? 4 : 8));
+    };
+    const int peak_items = ps.ncols * U * 4;
+    const bool kept = u0 == 0 && n == U && n == padded && peak_items <= KEPT * kThreads;
+    if (u0 == 0) {  // the columns' largest magnitudes
+        if (tid < 32) sh.peak[tid] = 0u;
+        __syncthreads();
+        for (int i0 = tid; i0 < peak_items; i0 += KEPT * kThreads) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) m = fmaxf(m, fabsf(v[k]));
-                atomicMax(&sh.peak[c], __float_as_uint(m));
+            for (int r = 0; r < KEPT; ++r) {
+                const int i = i0 + r * kThreads, c = i / (U * 4);
+                if (i < peak_items) load(c, i - c * U * 4, raw[r]);
             }
-            if (tid < 8) zeros[tid] = make_uint4(0u, 0u, 0u, 0u);
-            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < KEPT; ++r) {
+                const int i = i0 + r * kThreads, c = i / (U * 4);
+                if (i < peak_items) {
+                    float v[16], m = 0.f;
+                    widen16<PAIRS>(p, raw[r], v);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) m = fmaxf(m, fabsf(v[k]));
+                    m = fmaxf(m, __shfl_xor_sync(quad, m, 1));
+                    m = fmaxf(m, __shfl_xor_sync(quad, m, 2));
+                    if ((i & 3) == 0) atomicMax(&sh.peak[c], __float_as_uint(m));
+                }
+            }
         }
-        // the columns in MMA order, with their group sums
-        for (int i = tid; i < ps.ncols * n * 4; i += kThreads) {
-            const int c = i / (n * 4), r = i - c * n * 4, uu = r >> 2, qq = r & 3;
-            const int entry = sh.list[ps.col0 + c];
+        __syncthreads();
+    }
+    const int items = ps.ncols * padded * 4;
+    for (int i0 = tid; i0 < items; i0 += KEPT * kThreads) {
+        if (!kept) {
+#pragma unroll
+            for (int r = 0; r < KEPT; ++r) {
+                const int i = i0 + r * kThreads, c = i / (padded * 4), k = i - c * padded * 4;
+                if (i < items && (k >> 2) < n) load(c, u0 * 4 + k, raw[r]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < KEPT; ++r) {
+            const int i = i0 + r * kThreads, c = i / (padded * 4), k = i - c * padded * 4;
+            if (i >= items) continue;
+            const int uu = k >> 2, qq = k & 3;
+            uint4 *dst = reinterpret_cast<uint4 *>(act + (size_t)c * pitch + uu * 128) + qq;
+            if (uu >= n) {  // past the end
+                dst[0] = dst[4] = make_uint4(0u, 0u, 0u, 0u);
+                if (qq < SETS) sums[(uu * SETS + qq) * C + c] = 0.f;
+                continue;
+            }
             float v[16];
-            source16<PAIRS>(p, (size_t)(PAIRS ? entry / p.top : entry) * p.K +
-                                   (size_t)(u0 * 4 + r) * 16, v);
+            widen16<PAIRS>(p, raw[r], v);
             // 2^up puts the largest magnitude into [2^14, 2^15)
             const int ex = (int)(sh.peak[c] >> 23);
             int up = ex == 0 || ex == 255 ? 0 : 14 + 127 - ex;
             up = up > 100 ? 100 : up;
             const float f = __int_as_float((127 + up) << 23);
-            if (r == 0) sh.undo[c] = __int_as_float((127 - up) << 23);
-            float s = 0.f;
+            if (k == 0) sh.undo[c] = __int_as_float((127 - up) << 23);
+            float s = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int m = 0; m < 16; ++m) {
+                v[m] *= f;
+                const float h = __half2float(__float2half_rn(v[m]));
+                if (G32 && m >= 8)
+                    s2 += h;
+                else
+                    s += h;
+            }
             uint32_t o[8];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                v[k] *= f;
-                s += __half2float(__float2half_rn(v[k]));
+            for (int m = 0; m < 8; ++m) {
+                const float down = 1.f / (float)(1 << Ord::pre(m));
+                o[m] = pack_half2(v[Ord::lo(m)] * down, v[Ord::hi(m)] * down);
             }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float down = 1.f / (float)(1 << Order<BITS>::pre(k));
-                o[k] = pack_half2(v[Order<BITS>::lo(k)] * down, v[Order<BITS>::hi(k)] * down);
-            }
-            uint4 *dst = reinterpret_cast<uint4 *>(act + (size_t)c * pitch + uu * 128) + qq;
             dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
             dst[4] = make_uint4(o[4], o[5], o[6], o[7]);
-            const uint32_t quad = 0xFu << (lane & ~3);  // a unit's four lanes come together
             s += __shfl_xor_sync(quad, s, 1);
-            if (!G32) s += __shfl_xor_sync(quad, s, 2);
-            if (G32 ? (qq & 1) == 0 : qq == 0)
-                sums[(uu * SETS + (G32 ? qq >> 1 : 0)) * C + c] = s * 5.9604644775390625e-08f;
-        }
-        __syncthreads();
-
-        const uint8_t *bp[NB][SETS];
-        uint32_t step[SETS];
-#pragma unroll
-        for (int h = 0; h < SETS; ++h) {
-            const bool mine = !G32 || (q >> 1) == h;
-            step[h] = mine ? 128u : 0u;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                const int c = nb * 8 + g;
-                bp[nb][h] = mine ? act + (size_t)(c < ps.ncols ? c : 0) * pitch + q * 16
-                                 : reinterpret_cast<const uint8_t *>(zeros);
+            s += __shfl_xor_sync(quad, s, 2);
+            if (G32) {
+                s2 += __shfl_xor_sync(quad, s2, 1);
+                s2 += __shfl_xor_sync(quad, s2, 2);
             }
+            if (qq < SETS) sums[(uu * SETS + qq) * C + c] = (qq ? s2 : s) * 5.9604644775390625e-08f;
         }
-        float acc[NB][4];
+    }
+}
+
+// TT tiles side by side share the activations that a step reads from shared
+// memory; 8 NB columns.  (With an odd number of tiles the last one is taken
+// twice and counted once.)  staged: the last pass left these columns, for all
+// of K, in shared memory; returned is whether this one does.
+template <int BITS, bool G32, bool PAIRS, bool FLAT, int TT, int NB>
+__device__ __forceinline__ bool run_pass(const MoeParams &p, const Pass &ps, Shared &sh, uint8_t *dyn,
+                                         int room, bool wait, bool staged) {
+    constexpr int NW = kWords<BITS, G32>, UU = kUnits<BITS>, C = 8 * NB;
+    constexpr int SETS = G32 ? 2 : 1;      // groups of a unit whose sums are kept apart
+    constexpr int ROWS = PAIRS ? 8 : 16;   // rows of a matrix in a tile
+    constexpr int UNIT = 8 * BITS;         // bytes of a unit's row
+    constexpr int CELL = 16 * UNIT, STAGE = TT * UU * CELL;
+    constexpr int STAGES = kRing / STAGE < 8 ? kRing / STAGE : 8;
+    constexpr bool SPLIT = BITS % 2 == 0;  // units apart in shared memory, else rows whole
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+    const int U = p.K / 64, nt = ps.nt, ns = (nt + TT - 1) / TT;
+    const int groups = p.K / p.group;
+    const bool wide = p.group == 128;
+
+    int cu = units_that_fit(room, FLAT, TT, NB, nt, ps.ncols, SETS);  // units of a chunk
+    if (cu >= U) cu = U;
+    const int padded = (cu + UU - 1) / UU * UU;  // whole steps: units past the end count as zeros
+    const uint32_t ring = smem_u32(dyn + warp * kRing);
+    // shared memory behind the rings: activations, group sums, scales, biases,
+    // totals, slots
+    const int pitch = padded * 128 + 64;
+    uint8_t *act = dyn + kWarps * kRing;
+    float *sums = reinterpret_cast<float *>(act + ps.ncols * pitch);
+    // bytes of a row: a pitch of an odd number of 16 bytes spreads 8 rows over all banks
+    const int sp = ((padded * SETS + 7) / 8 | 1) * 16;
+    uint8_t *scales = reinterpret_cast<uint8_t *>(sums + padded * SETS * C);
+    float4 *total = reinterpret_cast<float4 *>(scales + nt * 32 * sp);  // a row's scales, then its biases
+    float4 *slots = FLAT ? total + nt * NB * 32 : reinterpret_cast<float4 *>(act);
+
+    const int64_t row_bytes = (int64_t)p.K * BITS / 8;
+    const int64_t to_b = PAIRS ? reinterpret_cast<const uint8_t *>(p.w1) - reinterpret_cast<const uint8_t *>(p.w0)
+                               : 8 * row_bytes;
+    const int64_t to_t = ROWS * row_bytes;
+    const uint8_t *w0 = reinterpret_cast<const uint8_t *>(p.w0) +
+                        ((int64_t)ps.e * p.R + (int64_t)ps.tile0 * ROWS) * row_bytes;
+    // what a lane copies of a tile's step: pieces of 16 bytes, PER a row (of 8
+    // bytes where an odd width's rows are not multiples of 16: fine)
+    constexpr int PER = UU * UNIT / 16, PIECES = (16 * PER + 31) / 32;
+    const bool fine = !SPLIT && (row_bytes & 8);
+    auto piece_at = [&](int i) { return (lane + 32 * i) % PER * 16; };  // byte of the row's step
+    auto piece_to = [&](int row, int at) {
+        return (uint32_t)(SPLIT ? at / UNIT * CELL + row * UNIT + at % UNIT : row * UU * UNIT + at);
+    };
+    int64_t from[PIECES];
+    uint32_t to[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int row = (lane + 32 * i) / PER;
+        from[i] = (row & 7) * row_bytes + (row >= 8 ? to_b : 0) + piece_at(i);
+        to[i] = piece_to(row, piece_at(i));
+    }
+    const uint32_t shift = (uint32_t)first_bit<BITS, G32>(q) & 31u;
+    const uint32_t mine = (uint32_t)(g * (SPLIT ? UNIT : UU * UNIT) + first_bit<BITS, G32>(q) / 32 * 4);
+    const int share = FLAT ? 1 : ns >= 5 ? 1 : ns >= 3 ? 2 : ns == 2 ? 4 : 8;
+
+    float acc[TT][NB][4];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[nb][i] = 0.f;
+            for (int i = 0; i < 4; ++i) acc[t][nb][i] = 0.f;
 
-        auto flush = [&]() {
+    for (int u0 = 0; u0 < U; u0 += cu) {
+        const int n = U - u0 < cu ? U - u0 : cu;     // units of this chunk
+        const int nq = (n + UU - 1) / UU;            // steps of a tile
+        int st, beg, end;                            // first tile (of TT), steps counted from it
+        if (FLAT) {
+            beg = ns * nq * warp / kWarps;
+            end = ns * nq * (warp + 1) / kWarps;
+            st = beg / nq;
+            beg -= st * nq;
+            end -= st * nq;
+        } else {
+            st = warp / share;
+            beg = nq * (warp % share) / share;
+            end = st < ns ? nq * (warp % share + 1) / share : beg;
+        }
+
+        // the step to fetch next: its tiles, its first unit
+        int fs = st, fu = beg * UU, fk = beg;
+        const uint8_t *src = w0 + (int64_t)(st * TT) * to_t + (int64_t)(u0 + fu) * UNIT;
+        int64_t next = TT == 2 && st * 2 + 1 < nt ? to_t : 0;
+        const int64_t wrap = TT * to_t - (int64_t)nq * UU * UNIT;
+        uint32_t fr = ring;
+        auto fetch = [&]() {
+            if (fk < end) {
+                const int left = (n - fu) * UNIT;  // bytes of the row up to the chunk's end
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                slots[((t + warp) * NB + nb) * 32 + lane] =
-                    make_float4(acc[nb][0], acc[nb][1], acc[nb][2], acc[nb][3]);
+                for (int t = 0; t < TT; ++t) {
+                    const uint8_t *s = src + (t ? next : 0);
+                    if (SPLIT || !fine) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[nb][i] = 0.f;
-            }
-        };
-        for (int base = beg; base < end; base += AHEAD) {
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                if (base + i < end) {
-                    uint32_t ra[8], rb[8];
-                    decode<BITS>(wa[i], shift, ra);
-                    decode<BITS>(wb[i], shift, rb);
-                    if (base + i + AHEAD < end) fetch(wa[i], wb[i]);
-#pragma unroll
-                    for (int h = 0; h < SETS; ++h) {
-                        const int gi = p.group == 128 ? u >> 1 : u * SETS + h;
-                        const float2 sa = __half22float2(pairs[(t * 16 + g) * sp + gi]);
-                        const float2 sb = __half22float2(pairs[(t * 16 + 8 + g) * sp + gi]);
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            const uint8_t *b = bp[nb][h] + u * step[h];
-                            const uint4 x = *reinterpret_cast<const uint4 *>(b);
-                            const uint4 y = *reinterpret_cast<const uint4 *>(b + 64);
-                            float d[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma(d, ra[0], rb[0], ra[1], rb[1], x.x, x.y);
-                            mma(d, ra[2], rb[2], ra[3], rb[3], x.z, x.w);
-                            mma(d, ra[4], rb[4], ra[5], rb[5], y.x, y.y);
-                            mma(d, ra[6], rb[6], ra[7], rb[7], y.z, y.w);
-                            const float2 s = *reinterpret_cast<const float2 *>(
-                                sums + (u * SETS + h) * C + nb * 8 + 2 * q);
-                            acc[nb][0] = fmaf(sa.x, d[0], fmaf(sa.y, s.x, acc[nb][0]));
-                            acc[nb][1] = fmaf(sa.x, d[1], fmaf(sa.y, s.y, acc[nb][1]));
-                            acc[nb][2] = fmaf(sb.x, d[2], fmaf(sb.y, s.x, acc[nb][2]));
-                            acc[nb][3] = fmaf(sb.x, d[3], fmaf(sb.y, s.y, acc[nb][3]));
+                        for (int i = 0; i < PIECES; ++i)
+                            if ((16 * PER % 32 == 0 || lane + 32 * i < 16 * PER) && (UU == 1 || piece_at(i) < left))
+                                copy_piece<16>(fr + t * UU * CELL + to[i], s + from[i]);
+                    } else {
+                        for (int k = lane; k < 32 * PER; k += 32) {
+                            const int row = k / (2 * PER), at = k % (2 * PER) * 8;
+                            if (at < left)
+                                copy_piece<8>(fr + t * UU * CELL + piece_to(row, at),
+                                              s + (row & 7) * row_bytes + (row >= 8 ? to_b : 0) + at);
                         }
                     }
-                    if (++u == n) {
-                        flush();
-                        u = 0;
-                        ++t;
+                }
+                fu += UU;
+                src += UU * UNIT;
+                if (fu >= n) {
+                    fu = 0;
+                    ++fs;
+                    src += wrap;
+                    if (TT == 2) next = fs * 2 + 1 < nt ? to_t : 0;
+                }
+                ++fk;
+                fr = fr + STAGE == ring + STAGES * STAGE ? ring : fr + STAGE;
+            }
+            cp_async_commit();
+        };
+        __syncthreads();  // the last chunk's or pass's readers are done
+        const uint32_t scale0 = smem_u32(scales);
+        stage_scales<PAIRS, SETS>(p, ps, u0, n, nq * UU, groups, scale0, sp);
+        cp_async_commit();
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) fetch();
+        if (wait && u0 == 0) grid_dependency_wait();
+        if (!(FLAT && staged && cu == U))
+            stage_columns<BITS, G32, PAIRS, C>(p, ps, sh, u0, n, nq * UU, pitch, sums, act);
+        cp_async_wait<STAGES>();  // the scales
+        __syncthreads();
+
+        uint32_t xs[NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            const int c = nb * 8 + g;
+            xs[nb] = smem_u32(act) + (uint32_t)((c < ps.ncols ? c : 0) * pitch + q * 16);
+        }
+        const uint32_t sum0 = smem_u32(sums) + 8u * (uint32_t)q;
+        int u = beg * UU;
+        uint32_t rd = ring + mine;
+        // the scales of rows g and g + 8 of the warp's tiles
+        uint32_t sc0 = scale0 + (uint32_t)((st * TT * 32 + 2 * g) * sp);
+        uint32_t sc1 = TT == 2 && st * 2 + 1 < nt ? (uint32_t)(32 * sp) : 0u;
+        for (int k = beg; k < end; ++k) {
+            cp_async_wait<STAGES - 1>();
+            __syncwarp();
+            // scales and biases of the step's groups: rows g and g + 8 of each
+            // tile; the words that hold them, and which half is unit 0's (with
+            // one group a step also unit 1's)
+            constexpr int W = UU * SETS == 4 ? 2 : 1;
+            const int at = wide ? u >> 1 : u * SETS;
+            const uint32_t pick = UU * SETS > 1 && !wide ? 0x3210u : at & 1 ? 0x3232u : 0x1010u;
+            uint32_t sc[TT][2][2][W];
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const uint32_t o = sc0 + (t ? sc1 : 0u) + (uint32_t)(b * 16 * sp) + (uint32_t)(at & ~1) * 2u;
+                    lds<W>(o, sc[t][b][0]);
+                    lds<W>(o + (uint32_t)sp, sc[t][b][1]);
+                    if (UU * SETS < 4) {
+                        sc[t][b][0][0] = prmt(sc[t][b][0][0], 0u, pick);
+                        sc[t][b][1][0] = prmt(sc[t][b][1][0], 0u, pick);
                     }
                 }
             }
+#pragma unroll
+            for (int i = 0; i < UU; ++i) {
+                uint32_t ra[TT][8], rb[TT][8];
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    uint32_t w[NW];
+                    const uint32_t a = rd + (uint32_t)((t * UU + (SPLIT ? i : 0)) * CELL + (SPLIT ? 0 : i * UNIT));
+                    load_codes<BITS, G32>(a, w);
+                    decode<BITS, G32>(w, shift, ra[t]);
+                    load_codes<BITS, G32>(a + 8 * (SPLIT ? UNIT : UU * UNIT), w);
+                    decode<BITS, G32>(w, shift, rb[t]);
+                }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    const uint4 x = lds16(xs[nb] + (uint32_t)(u + i) * 128u);
+                    const uint4 y = lds16(xs[nb] + (uint32_t)(u + i) * 128u + 64u);
+                    float2 s[SETS];
+#pragma unroll
+                    for (int h = 0; h < SETS; ++h)
+                        s[h] = lds_f2(sum0 + (uint32_t)(((u + i) * SETS + h) * C + nb * 8) * 4u);
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) {
+                        float d[SETS][4];
+                        mma0(d[0], ra[t][0], rb[t][0], ra[t][1], rb[t][1], x.x, x.y);
+                        mma(d[0], ra[t][2], rb[t][2], ra[t][3], rb[t][3], x.z, x.w);
+                        if constexpr (G32)
+                            mma0(d[SETS - 1], ra[t][4], rb[t][4], ra[t][5], rb[t][5], y.x, y.y);
+                        else
+                            mma(d[0], ra[t][4], rb[t][4], ra[t][5], rb[t][5], y.x, y.y);
+                        mma(d[SETS - 1], ra[t][6], rb[t][6], ra[t][7], rb[t][7], y.z, y.w);
+                        float(&o)[4] = acc[t][nb];
+#pragma unroll
+                        for (int h = 0; h < SETS; ++h) {
+                            const int z = i * SETS + h;
+                            auto half = [&](int b, int v) {
+                                const __half2 p2 = *reinterpret_cast<const __half2 *>(&sc[t][b][v][z / 2]);
+                                return z & 1 ? __high2float(p2) : __low2float(p2);
+                            };
+                            const float2 sa = make_float2(half(0, 0), half(0, 1));
+                            const float2 sb = make_float2(half(1, 0), half(1, 1));
+                            o[0] = fmaf(sa.x, d[h][0], fmaf(sa.y, s[h].x, o[0]));
+                            o[1] = fmaf(sa.x, d[h][1], fmaf(sa.y, s[h].y, o[1]));
+                            o[2] = fmaf(sb.x, d[h][2], fmaf(sb.y, s[h].x, o[2]));
+                            o[3] = fmaf(sb.x, d[h][3], fmaf(sb.y, s[h].y, o[3]));
+                        }
+                    }
+                }
+            }
+            __syncwarp();  // the stage is read: it may be filled again
+            fetch();
+            rd += STAGE;
+            if (rd >= ring + STAGES * STAGE) rd -= STAGES * STAGE;
+            u += UU;
+            if (FLAT && (u >= n || k + 1 == end)) {
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        float(&o)[4] = acc[t][nb];
+                        slots[(((st + warp) * TT + t) * NB + nb) * 32 + lane] =
+                            make_float4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[i] = 0.f;
+                    }
+                u = 0;
+                ++st;
+                sc0 += (uint32_t)(TT * 32 * sp);
+                if (TT == 2) sc1 = st * 2 + 1 < nt ? (uint32_t)(32 * sp) : 0u;
+            }
         }
-        if (u != 0 && beg < end) flush();
         __syncthreads();
+        const bool done = u0 + n >= U;
+        if (!FLAT) {
+            if (!done) continue;
+#pragma unroll
+            for (int t = 0; t < TT; ++t)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                    slots[((warp * TT + t) * NB + nb) * 32 + lane] =
+                        make_float4(acc[t][nb][0], acc[t][nb][1], acc[t][nb][2], acc[t][nb][3]);
+            __syncthreads();
+        }
 
         // the tiles' sums, in warp order; after the last chunk the results
         for (int i = tid; i < nt * NB * 32; i += kThreads) {
-            const int tt = i / (NB * 32), nb = i / 32 % NB, ln = i & 31;
-            float4 s = u0 == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : total[i];
-            for (int w = 0; w < kWarps; ++w) {
-                const int b = max(total_units * w / kWarps, tt * n);
-                const int e = min(total_units * (w + 1) / kWarps, (tt + 1) * n);
-                if (b < e) {
-                    const float4 v = slots[((tt + w) * NB + nb) * 32 + ln];
+            const int tt = i / (NB * 32), s0 = tt / TT, nb = i / 32 % NB, ln = i & 31;
+            float4 s = !FLAT || u0 == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : total[i];
+            const int first = FLAT ? 0 : s0 * share, last = FLAT ? kWarps : first + share;
+            for (int w = first; w < last; ++w) {
+                if (!FLAT || max(ns * nq * w / kWarps, s0 * nq) < min(ns * nq * (w + 1) / kWarps, (s0 + 1) * nq)) {
+                    const float4 v = slots[(((FLAT ? s0 + w : w) * TT + tt % TT) * NB + nb) * 32 + ln];
                     s.x += v.x;
                     s.y += v.y;
                     s.z += v.z;
                     s.w += v.w;
                 }
             }
-            if (u0 + n < U) {
+            if (!done) {
                 total[i] = s;
                 continue;
             }
-            const int row = (ps.tile0 + tt) * (PAIRS ? 8 : 16) + (ln >> 2);
+            const int row = (ps.tile0 + tt) * ROWS + (ln >> 2);
             const float part[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -502,7 +829,7 @@ __device__ __forceinline__ void run_pass(const MoeParams &p, const Pass &ps, Sha
                 if (c >= ps.ncols) continue;
                 const float a = part[j] * 16777216.f * sh.undo[c];
                 const float b = part[2 + j] * 16777216.f * sh.undo[c];
-                float *to = p.dst + (size_t)sh.list[ps.col0 + c] * p.R + row;
+                float *to = p.dst + (size_t)sh.list[c] * p.R + row;
                 if constexpr (PAIRS) {
                     *to = a / (1.f + expf(-a)) * b;
                 } else {
@@ -512,62 +839,55 @@ __device__ __forceinline__ void run_pass(const MoeParams &p, const Pass &ps, Sha
             }
         }
     }
+    return FLAT && cu == U;
 }
 
-template <int BITS, bool G32, bool PAIRS>
+// A kernel takes columns 8 NB at a time; which one is launched is a matter of
+// sizes alone (variant below).
+template <int BITS, bool G32, bool PAIRS, bool FLAT, int TT, int NB>
 __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant__ MoeParams p) {
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ Shared sh;
-    // the ids are there before this grid's predecessor starts (down), or are
-    // what it writes (gate and up)
+    // The down grid reads ids and weights before it waits: this grid's
+    // predecessor lets it start only once all that came before is complete.
     if (PAIRS) {
         grid_dependency_wait();
         launch_dependents();
     }
-    plan(p, sh);
-    const int per = p.R / (PAIRS ? 8 : 16);
+    // behind the rings: room for the passes, at the end the entries' experts
+    const int room = kRoom - ((p.T * p.top * 2 + 15) & ~15);
+    uint16_t *ids = reinterpret_cast<uint16_t *>(dyn + kWarps * kRing + room);
+    plan(p, sh, ids);
+    const int per = p.R / (PAIRS ? 8 : 16);  // tiles of an expert
     const int64_t tiles = (int64_t)sh.busy * per;
     int64_t lo = tiles * blockIdx.x / gridDim.x;
     const int64_t hi = tiles * (blockIdx.x + 1) / gridDim.x;
     bool wait = !PAIRS;
     if (wait && lo >= hi) grid_dependency_wait();
-    int last = -1;
     while (lo < hi) {
-        const int a = (int)(lo / per);
-        Pass ps;
-        ps.e = sh.act[a];
-        ps.tile0 = (int)(lo - (int64_t)a * per);
-        int left = per - ps.tile0;
-        if (hi - lo < left) left = (int)(hi - lo);
-        if (ps.e != last) list_entries(p, ps.e, sh);
-        last = ps.e;
-        const int count = sh.count[ps.e];
-        // as many tiles as leave the whole of K in one chunk, else a few
-        const int most = count < 32 ? count : 32, nb = most <= 8 ? 1 : most <= 16 ? 2 : 4;
-        ps.nt = left < kMaxTiles ? left : kMaxTiles;
-        while (ps.nt > 1 && units_that_fit(ps.nt, most, nb, G32 ? 2 : 1) < p.K / 64) --ps.nt;
-        if (units_that_fit(ps.nt, most, nb, G32 ? 2 : 1) < p.K / 64) {
-            ps.nt = nb == 4 ? 4 : 8;
-            if (left < ps.nt) ps.nt = left;
+        const int a = (int)(lo / per), e = sh.act[a], count = sh.count[e];
+        const int from = (int)(lo - (int64_t)a * per);
+        const int to = hi - lo < per - from ? from + (int)(hi - lo) : per;  // tiles of this expert
+        for (int col0 = 0; col0 < count; col0 += 8 * NB) {
+            list_entries<8 * NB>(p, e, col0, sh, ids);
+            Pass ps;
+            ps.e = e;
+            ps.ncols = count - col0 < 8 * NB ? count - col0 : 8 * NB;
+            bool staged = false;
+            for (ps.tile0 = from; ps.tile0 < to; ps.tile0 += ps.nt) {
+                ps.nt = to - ps.tile0 < kMaxTiles ? to - ps.tile0 : kMaxTiles;
+                staged = run_pass<BITS, G32, PAIRS, FLAT, TT, NB>(p, ps, sh, dyn, room, wait, staged);
+                wait = false;
+            }
         }
-        for (ps.col0 = 0; ps.col0 < count; ps.col0 += 32) {
-            ps.ncols = count - ps.col0 < 32 ? count - ps.col0 : 32;
-            if (ps.ncols <= 8)
-                run_pass<BITS, G32, PAIRS, 1>(p, ps, sh, dyn, wait);
-            else if (ps.ncols <= 16)
-                run_pass<BITS, G32, PAIRS, 2>(p, ps, sh, dyn, wait);
-            else
-                run_pass<BITS, G32, PAIRS, 4>(p, ps, sh, dyn, wait);
-            wait = false;
-        }
-        lo += ps.nt;
+        lo += to - from;
     }
 }
 
 // The grid: two CTAs an SM, each with an even run of tiles.
-template <int BITS, bool G32, bool PAIRS>
+template <int BITS, bool G32, bool PAIRS, bool FLAT, int TT, int NB>
 cudaError_t launch_one(const MoeParams &p, cudaStream_t stream) {
-    auto *kern = moe_kernel<BITS, G32, PAIRS>;
+    auto *kern = moe_kernel<BITS, G32, PAIRS, FLAT, TT, NB>;
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised, one bit each
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -581,13 +901,28 @@ cudaError_t launch_one(const MoeParams &p, cudaStream_t stream) {
     return moe_launch(kern, dim3(2u * (unsigned)num_sms()), kThreads, kDynamic, 1, stream, p);
 }
 
+// Which kernel: by the tokens a busy expert has on average and the tiles a CTA
+// gets, were all experts picked alike.
+template <int BITS, bool G32, bool PAIRS>
+cudaError_t launch_sized(const MoeParams &p, cudaStream_t stream) {
+    const double picked = (double)p.T * p.top;
+    const double busy = p.E * -std::expm1(p.T * std::log1p(-(double)(p.top < p.E ? p.top : p.E - 0.5) / p.E));
+    const double tokens = picked / busy, tiles = busy * (p.R / (PAIRS ? 8 : 16)) / (2.0 * num_sms());
+    if (p.T <= 8 || tokens <= 6.0) {
+        if (tiles <= 3.0) return launch_one<BITS, G32, PAIRS, true, 1, 1>(p, stream);
+        return launch_one<BITS, G32, PAIRS, true, 2, 1>(p, stream);
+    }
+    if (p.T <= 16 || tokens <= 12.0) return launch_one<BITS, G32, PAIRS, false, 2, 2>(p, stream);
+    return launch_one<BITS, G32, PAIRS, false, 2, 4>(p, stream);
+}
+
 template <int BITS>
 cudaError_t launch(const MoeParams &p, bool pairs, cudaStream_t stream) {
     if (p.group == 32)
-        return pairs ? launch_one<BITS, true, true>(p, stream)
-                     : launch_one<BITS, true, false>(p, stream);
-    return pairs ? launch_one<BITS, false, true>(p, stream)
-                 : launch_one<BITS, false, false>(p, stream);
+        return pairs ? launch_sized<BITS, true, true>(p, stream)
+                     : launch_sized<BITS, true, false>(p, stream);
+    return pairs ? launch_sized<BITS, false, true>(p, stream)
+                 : launch_sized<BITS, false, false>(p, stream);
 }
 
 }  // namespace moe_detail
