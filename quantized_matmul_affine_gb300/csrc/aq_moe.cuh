@@ -50,7 +50,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxTiles = 16;        // tiles of a pass
 constexpr int kRing = 6144;          // bytes of codes in flight a warp
-constexpr int kDynamic = 110592;     // dynamic shared memory: two CTAs an SM
+constexpr int kDynamic = 109568;     // dynamic shared memory: two CTAs an SM
 constexpr uint16_t kNone = 0xFFFF;
 constexpr int kMaxEntries = AQ_MOE_MAX_TOKENS * AQ_MOE_MAX_TOP;
 
@@ -297,18 +297,29 @@ __device__ __forceinline__ void widen16(const MoeParams &p, const uint32_t (&w)[
 
 struct Shared {
     int count[AQ_MOE_MAX_EXPERTS];     // entries of each expert
+    int before[AQ_MOE_MAX_EXPERTS];    // cost of a tile of the busy experts before each
     uint16_t act[AQ_MOE_MAX_EXPERTS];  // the busy experts, ascending
     uint16_t list[32];                 // entries t * top + j of the current columns
     uint32_t peak[32];                 // a column's largest magnitude, as bits
     float undo[32];                    // a column's inverse power of two
     int warp_sum[kWarps];
-    int busy;
+    int busy, cost;
 };
+static_assert(2 * (kDynamic + sizeof(Shared) + 1024) <= 228 * 1024, "two CTAs an SM");
 
-// Counts the entries of every expert, lists the busy experts in order and
-// keeps every entry's expert in ids (kNone without one).
+// What a tile of an expert with n entries costs, in columns' products: the
+// codes are decoded once for every C columns, as much work as about four
+// products with 8 columns.
+template <int C>
+__device__ __forceinline__ int tile_cost(int n) {
+    return 4 * ((n + C - 1) / C) + (n + 7) / 8;
+}
+
+// Counts the entries of every expert, lists the busy experts in order with the
+// costs before them, and keeps every entry's expert in ids (kNone without one).
+template <int C>
 __device__ __forceinline__ void plan(const MoeParams &p, Shared &sh, uint16_t *ids) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
     for (int e = tid; e < p.E; e += kThreads) sh.count[e] = 0;
     __syncthreads();
     for (int i = tid; i < p.T * p.top; i += kThreads) {
@@ -318,22 +329,30 @@ __device__ __forceinline__ void plan(const MoeParams &p, Shared &sh, uint16_t *i
         if (on) atomicAdd(&sh.count[e], 1);
     }
     __syncthreads();
-    int before = 0;
-    for (int e0 = 0; e0 < p.E; e0 += kThreads) {
-        const int e = e0 + tid;
-        const bool on = e < p.E && sh.count[e] > 0;
-        const uint32_t m = __ballot_sync(0xFFFFFFFFu, on);
-        if (lane == 0) sh.warp_sum[warp] = __popc(m);
-        __syncthreads();
-        int at = before;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) at += sh.warp_sum[w];
-            before += sh.warp_sum[w];
+    if (tid < 32) {
+        int busy = 0, cost = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int n = e0 + lane < p.E ? sh.count[e0 + lane] : 0;
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, n > 0);
+            int c = n > 0 ? tile_cost<C>(n) : 0, sum = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (n > 0) {
+                const int at = busy + __popc(m & ((1u << lane) - 1u));
+                sh.act[at] = (uint16_t)(e0 + lane);
+                sh.before[at] = cost + sum - c;
+            }
+            busy += __popc(m);
+            cost += __shfl_sync(0xFFFFFFFFu, sum, 31);
         }
-        if (on) sh.act[at + __popc(m & ((1u << lane) - 1u))] = (uint16_t)e;
-        __syncthreads();
+        if (lane == 0) {
+            sh.busy = busy;
+            sh.cost = cost;
+        }
     }
-    if (tid == 0) sh.busy = before;
     __syncthreads();
 }
 
@@ -366,20 +385,50 @@ struct Pass {
     int e, tile0, nt, ncols;
 };
 
-// 64-value units of K (a multiple of 4) whose activations, group sums and
-// scales fit in `room` bytes of shared memory.
-__host__ __device__ constexpr int units_that_fit(int room, bool flat, int tt, int nb, int nt,
-                                                 int ncols, int sets) {
-    const int sums = flat ? (nt + (nt + tt - 1) / tt * tt + (kWarps - 1) * tt) * nb * 512 : 0;
-    const int fixed = sums + nt * 1024 + ncols * 64;
-    const int each = 8 * nb * sets * 4 + nt * 16 * sets * 4 + ncols * 128;
-    return (room - fixed) / each & ~3;
+// Shared memory behind the rings for a chunk of `units` 64-value units: the
+// columns (fp16 in MMA order, 64 bytes of pitch so that two rows' 16-byte reads
+// differ in banks), their group sums (two fp16 parts, a whole MMA step of 16
+// groups), the tiles' scales and biases, and what sums need.  Pitches of an odd
+// number of 16 bytes put 8 rows on all banks.
+struct Layout {
+    int pitch, sum_lo, sum_pitch, bias_at, scale_pitch;
+    int sums, scales, total, slots, end;  // byte offsets
+};
+__host__ __device__ constexpr Layout layout(bool flat, int tt, int uu, int nb, int nt, int ncols, int group,
+                                            int units) {
+    Layout l = {};
+    const int padded = (units + uu - 1) / uu * uu;  // whole steps: units past the end count as zeros
+    const int have = group == 32 ? padded * 2 : group == 64 ? padded : (padded + 1) / 2;
+    const int steps = (have + 15) / 16 * 32;  // bytes of whole MMA steps
+    l.pitch = padded * 128 + 64;
+    l.sum_lo = steps;
+    l.sum_pitch = 2 * steps + 16;
+    l.bias_at = (have * 2 + 15) / 16 * 16;
+    l.scale_pitch = ((l.bias_at + steps) / 16 | 1) * 16;
+    l.sums = ncols * l.pitch;
+    l.scales = l.sums + ncols * l.sum_pitch;
+    l.total = l.scales + nt * 16 * l.scale_pitch;
+    l.slots = flat ? l.total + nt * nb * 512 : 0;
+    l.end = flat ? l.slots + ((nt + tt - 1) / tt + kWarps - 1) * tt * nb * 512 : l.total;
+    return l;
 }
 constexpr int kRoom = kDynamic - kWarps * kRing;  // less the entries' experts
-// The most a unit takes, beside the most entries, still leaves chunks of 4.
-static_assert(units_that_fit(kRoom - 2 * kMaxEntries, false, 2, 4, 16, 32, 2) >= 4 &&
-              units_that_fit(kRoom - 2 * kMaxEntries, true, 2, 1, 16, 8, 2) >= 4 &&
-              kRoom - 2 * kMaxEntries >= kWarps * 2 * 4 * 512, "chunks");
+// The most that 4 units take fits beside the most entries, and so do the slots
+// of warps that keep their tiles.
+static_assert(layout(false, 2, 2, 4, kMaxTiles, 32, 32, 4).end <= kRoom - 2 * kMaxEntries &&
+              layout(true, 2, 2, 1, kMaxTiles, 8, 32, 4).end <= kRoom - 2 * kMaxEntries &&
+              kWarps * 2 * 4 * 512 <= kRoom - 2 * kMaxEntries, "chunks");
+
+// Units of a chunk: all, or the most that fit, steps of 16 where there are as
+// many (the sums' MMA steps are whole then), else of 4.
+__device__ __forceinline__ int chunk_units(bool flat, int tt, int uu, int nb, int nt, int ncols, int group,
+                                           int U, int room) {
+    if (layout(flat, tt, uu, nb, nt, ncols, group, U).end <= room) return U;
+    int n = 4;
+    while (n + 16 < U && layout(flat, tt, uu, nb, nt, ncols, group, n < 16 ? 16 : n + 16).end <= room)
+        n = n < 16 ? 16 : n + 16;
+    return n;
+}
 
 // Copies P bytes (a plain load and store for 2), asynchronously from 4 up.
 template <int P>
@@ -397,10 +446,11 @@ __device__ __forceinline__ void copy_piece(uint32_t to, const uint8_t *from) {
 }
 
 // The scales and biases of the pass's rows for the groups of units u0 .. u0 +
-// n - 1: each row's scales, sp bytes on its biases, zeros up to `padded` units.
+// n - 1: each row's scales, at bias_at its biases, both with zeros up to the
+// end of their room.
 template <bool PAIRS, int P>
 __device__ __forceinline__ void copy_scales(const MoeParams &p, const Pass &ps, int g0, int bytes, int groups,
-                                            uint32_t scales, int sp) {
+                                            uint32_t scales, const Layout &l) {
     const int per = (bytes + P - 1) / P, rows = ps.nt * 16;
     // rows by threads, so that a row's pieces need no division; a wide row is
     // shared by several
@@ -414,15 +464,16 @@ __device__ __forceinline__ void copy_scales(const MoeParams &p, const Pass &ps, 
                              (PAIRS ? r & 7 : r)) * groups + g0) * 2;
         const uint8_t *s = static_cast<const uint8_t *>(second ? p.s1 : p.s0) + at;
         const uint8_t *b = static_cast<const uint8_t *>(second ? p.b1 : p.b0) + at;
+        const uint32_t to = scales + (uint32_t)(row * l.scale_pitch);
         for (int k = tid % lanes; k < per; k += lanes) {
-            copy_piece<P>(scales + (uint32_t)(2 * row * sp + k * P), s + k * P);
-            copy_piece<P>(scales + (uint32_t)((2 * row + 1) * sp + k * P), b + k * P);
+            copy_piece<P>(to + k * P, s + k * P);
+            copy_piece<P>(to + l.bias_at + k * P, b + k * P);
         }
     }
 }
 template <bool PAIRS, int SETS>
-__device__ __forceinline__ void stage_scales(const MoeParams &p, const Pass &ps, int u0, int n, int padded,
-                                             int groups, uint32_t scales, int sp) {
+__device__ __forceinline__ void stage_scales(const MoeParams &p, const Pass &ps, int u0, int n, int groups,
+                                             uint32_t scales, const Layout &l) {
     const int wide = p.group == 128;
     const int g0 = wide ? u0 / 2 : u0 * SETS, ng = wide ? n / 2 : n * SETS;
     // the largest piece that the rows' starts and lengths allow
@@ -430,27 +481,33 @@ __device__ __forceinline__ void stage_scales(const MoeParams &p, const Pass &ps,
                                     reinterpret_cast<uintptr_t>(p.s1) | reinterpret_cast<uintptr_t>(p.b1)) |
                          (uint32_t)(groups * 2) | (uint32_t)(g0 * 2) | (uint32_t)(ng * 2);
     if ((all & 15) == 0)
-        copy_scales<PAIRS, 16>(p, ps, g0, ng * 2, groups, scales, sp);
+        copy_scales<PAIRS, 16>(p, ps, g0, ng * 2, groups, scales, l);
     else if ((all & 7) == 0)
-        copy_scales<PAIRS, 8>(p, ps, g0, ng * 2, groups, scales, sp);
+        copy_scales<PAIRS, 8>(p, ps, g0, ng * 2, groups, scales, l);
     else if ((all & 3) == 0)
-        copy_scales<PAIRS, 4>(p, ps, g0, ng * 2, groups, scales, sp);
+        copy_scales<PAIRS, 4>(p, ps, g0, ng * 2, groups, scales, l);
     else
-        copy_scales<PAIRS, 2>(p, ps, g0, ng * 2, groups, scales, sp);
-    const int zeros = (wide ? (padded + 1) / 2 : padded * SETS) - ng;
-    for (int i = threadIdx.x; i < ps.nt * 32 * zeros; i += kThreads)
-        asm volatile("st.shared.b16 [%0], %1;" ::"r"(scales + (uint32_t)(i / zeros * sp + (ng + i % zeros) * 2)),
-                     "h"((short)0)
-                     : "memory");
+        copy_scales<PAIRS, 2>(p, ps, g0, ng * 2, groups, scales, l);
+    auto zero = [&](int from, int to) {
+        const int each = (to - from) / 2;
+        for (int i = threadIdx.x; i < ps.nt * 16 * each; i += kThreads)
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(scales + (uint32_t)(i / each * l.scale_pitch + from + i % each * 2)),
+                         "h"((short)0)
+                         : "memory");
+    };
+    zero(2 * ng, l.bias_at);
+    zero(l.bias_at + 2 * ng, l.bias_at + l.sum_lo);
 }
 
-// The pass's columns as fp16 in MMA order, with their group sums.
-template <int BITS, bool G32, bool PAIRS, int C>
+// The pass's columns as fp16 in MMA order, with their group sums times 2^-8 as
+// two fp16 parts (22 bits).
+template <int BITS, bool G32, bool PAIRS>
 __device__ __forceinline__ void stage_columns(const MoeParams &p, const Pass &ps, Shared &sh, int u0,
-                                              int n, int padded, int pitch, float *sums, uint8_t *act) {
+                                              int n, int padded, uint8_t *act, const Layout &l) {
     using Ord = Order<BITS, G32>;
     constexpr int SETS = G32 ? 2 : 1, KEPT = 2;  // quarters a thread has in flight
     const int tid = threadIdx.x, lane = tid & 31, U = p.K / 64;
+    const bool wide = p.group == 128;
     const uint32_t quad = 0xFu << (lane & ~3);  // a unit's four lanes come together
     // a unit's quarter (column c, quarter k of K): 16 values in two pieces
     auto source = [&](int c, int k, size_t &second) {
@@ -507,10 +564,9 @@ __device__ __forceinline__ void stage_columns(const MoeParams &p, const Pass &ps
             const int i = i0 + r * kThreads, c = i / (padded * 4), k = i - c * padded * 4;
             if (i >= items) continue;
             const int uu = k >> 2, qq = k & 3;
-            uint4 *dst = reinterpret_cast<uint4 *>(act + (size_t)c * pitch + uu * 128) + qq;
+            uint4 *dst = reinterpret_cast<uint4 *>(act + (size_t)c * l.pitch + uu * 128) + qq;
             if (uu >= n) {  // past the end
                 dst[0] = dst[4] = make_uint4(0u, 0u, 0u, 0u);
-                if (qq < SETS) sums[(uu * SETS + qq) * C + c] = 0.f;
                 continue;
             }
             float v[16];
@@ -545,8 +601,25 @@ __device__ __forceinline__ void stage_columns(const MoeParams &p, const Pass &ps
                 s2 += __shfl_xor_sync(quad, s2, 1);
                 s2 += __shfl_xor_sync(quad, s2, 2);
             }
-            if (qq < SETS) sums[(uu * SETS + qq) * C + c] = (qq ? s2 : s) * 5.9604644775390625e-08f;
+            int at = G32 ? uu * 2 + qq : uu;  // its group
+            if (!G32 && wide) {               // the other unit of the group: n is even, as is the lane's part
+                s += __shfl_xor_sync(0xFFu << (lane & ~7), s, 4);
+                at = uu >> 1;
+            }
+            if (qq < SETS && !(wide && (uu & 1))) {
+                const float v = (qq ? s2 : s) * 0.00390625f;
+                const __half hi = __float2half_rn(v);
+                __half *to = reinterpret_cast<__half *>(act + l.sums + (size_t)c * l.sum_pitch) + at;
+                to[0] = hi;
+                to[l.sum_lo / 2] = __float2half_rn(v - __half2float(hi));
+            }
         }
+    }
+    // zeros up to the last MMA step's end
+    const int have = wide ? n / 2 : n * SETS, rest = l.sum_lo / 2 - have;
+    for (int i = tid; i < ps.ncols * rest; i += kThreads) {
+        __half *to = reinterpret_cast<__half *>(act + l.sums + (size_t)(i / rest) * l.sum_pitch) + have + i % rest;
+        to[0] = to[l.sum_lo / 2] = __half(0.f);
     }
 }
 
@@ -557,7 +630,7 @@ __device__ __forceinline__ void stage_columns(const MoeParams &p, const Pass &ps
 template <int BITS, bool G32, bool PAIRS, bool FLAT, int TT, int NB>
 __device__ __forceinline__ bool run_pass(const MoeParams &p, const Pass &ps, Shared &sh, uint8_t *dyn,
                                          int room, bool wait, bool staged) {
-    constexpr int NW = kWords<BITS, G32>, UU = kUnits<BITS>, C = 8 * NB;
+    constexpr int NW = kWords<BITS, G32>, UU = kUnits<BITS>;
     constexpr int SETS = G32 ? 2 : 1;      // groups of a unit whose sums are kept apart
     constexpr int ROWS = PAIRS ? 8 : 16;   // rows of a matrix in a tile
     constexpr int UNIT = 8 * BITS;         // bytes of a unit's row
@@ -569,20 +642,12 @@ __device__ __forceinline__ bool run_pass(const MoeParams &p, const Pass &ps, Sha
     const int groups = p.K / p.group;
     const bool wide = p.group == 128;
 
-    int cu = units_that_fit(room, FLAT, TT, NB, nt, ps.ncols, SETS);  // units of a chunk
-    if (cu >= U) cu = U;
-    const int padded = (cu + UU - 1) / UU * UU;  // whole steps: units past the end count as zeros
+    const int cu = chunk_units(FLAT, TT, UU, NB, nt, ps.ncols, p.group, U, room);
+    const Layout l = layout(FLAT, TT, UU, NB, nt, ps.ncols, p.group, cu);
     const uint32_t ring = smem_u32(dyn + warp * kRing);
-    // shared memory behind the rings: activations, group sums, scales, biases,
-    // totals, slots
-    const int pitch = padded * 128 + 64;
     uint8_t *act = dyn + kWarps * kRing;
-    float *sums = reinterpret_cast<float *>(act + ps.ncols * pitch);
-    // bytes of a row: a pitch of an odd number of 16 bytes spreads 8 rows over all banks
-    const int sp = ((padded * SETS + 7) / 8 | 1) * 16;
-    uint8_t *scales = reinterpret_cast<uint8_t *>(sums + padded * SETS * C);
-    float4 *total = reinterpret_cast<float4 *>(scales + nt * 32 * sp);  // a row's scales, then its biases
-    float4 *slots = FLAT ? total + nt * NB * 32 : reinterpret_cast<float4 *>(act);
+    float4 *total = reinterpret_cast<float4 *>(act + l.total);
+    float4 *slots = reinterpret_cast<float4 *>(act + l.slots);
 
     const int64_t row_bytes = (int64_t)p.K * BITS / 8;
     const int64_t to_b = PAIRS ? reinterpret_cast<const uint8_t *>(p.w1) - reinterpret_cast<const uint8_t *>(p.w0)
@@ -674,14 +739,14 @@ __device__ __forceinline__ bool run_pass(const MoeParams &p, const Pass &ps, Sha
             cp_async_commit();
         };
         __syncthreads();  // the last chunk's or pass's readers are done
-        const uint32_t scale0 = smem_u32(scales);
-        stage_scales<PAIRS, SETS>(p, ps, u0, n, nq * UU, groups, scale0, sp);
+        const uint32_t scale0 = smem_u32(act + l.scales);
+        stage_scales<PAIRS, SETS>(p, ps, u0, n, groups, scale0, l);
         cp_async_commit();
 #pragma unroll
         for (int i = 0; i < STAGES; ++i) fetch();
         if (wait && u0 == 0) grid_dependency_wait();
         if (!(FLAT && staged && cu == U))
-            stage_columns<BITS, G32, PAIRS, C>(p, ps, sh, u0, n, nq * UU, pitch, sums, act);
+            stage_columns<BITS, G32, PAIRS>(p, ps, sh, u0, n, nq * UU, act, l);
         cp_async_wait<STAGES>();  // the scales
         __syncthreads();
 
@@ -689,37 +754,67 @@ __device__ __forceinline__ bool run_pass(const MoeParams &p, const Pass &ps, Sha
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             const int c = nb * 8 + g;
-            xs[nb] = smem_u32(act) + (uint32_t)((c < ps.ncols ? c : 0) * pitch + q * 16);
+            xs[nb] = smem_u32(act) + (uint32_t)((c < ps.ncols ? c : 0) * l.pitch + q * 16);
         }
-        const uint32_t sum0 = smem_u32(sums) + 8u * (uint32_t)q;
         int u = beg * UU;
         uint32_t rd = ring + mine;
         // the scales of rows g and g + 8 of the warp's tiles
-        uint32_t sc0 = scale0 + (uint32_t)((st * TT * 32 + 2 * g) * sp);
-        uint32_t sc1 = TT == 2 && st * 2 + 1 < nt ? (uint32_t)(32 * sp) : 0u;
+        const uint32_t sp = (uint32_t)l.scale_pitch;
+        uint32_t sc0 = scale0 + (uint32_t)(st * TT * 16 + g) * sp;
+        uint32_t sc1 = TT == 2 && st * 2 + 1 < nt ? 16u * sp : 0u;
+        // The chunk's biases times group sums, 16 groups a product, by the warp
+        // that takes a tile's last step: acc is in 2^-24, these products in 2^-8.
+        auto add_biases = [&]() {
+            const uint32_t bias = (uint32_t)(l.bias_at + 4 * q);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                if (NB > 1 && nb * 8 >= ps.ncols) continue;
+                const int c = nb * 8 + g;
+                const uint32_t sum = smem_u32(act) + (uint32_t)(l.sums + (c < ps.ncols ? c : 0) * l.sum_pitch + 4 * q);
+                float d[TT][4];
+#pragma unroll
+                for (int t = 0; t < TT; ++t) d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.f;
+                for (int k = 0; k < l.sum_lo; k += 32) {
+                    uint32_t h0, h1, l0, l1;
+                    lds<1>(sum + k, &h0);
+                    lds<1>(sum + k + 16, &h1);
+                    lds<1>(sum + l.sum_lo + k, &l0);
+                    lds<1>(sum + l.sum_lo + k + 16, &l1);
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) {
+                        const uint32_t o = sc0 + (t ? sc1 : 0u) + bias + k;
+                        uint32_t a0, a1, a2, a3;
+                        lds<1>(o, &a0);
+                        lds<1>(o + 8u * sp, &a1);
+                        lds<1>(o + 16u, &a2);
+                        lds<1>(o + 8u * sp + 16u, &a3);
+                        mma(d[t], a0, a1, a2, a3, h0, h1);
+                        mma(d[t], a0, a1, a2, a3, l0, l1);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[t][nb][i] = fmaf(d[t][i], 1.52587890625e-05f, acc[t][nb][i]);
+            }
+        };
         for (int k = beg; k < end; ++k) {
             cp_async_wait<STAGES - 1>();
             __syncwarp();
-            // scales and biases of the step's groups: rows g and g + 8 of each
-            // tile; the words that hold them, and which half is unit 0's (with
-            // one group a step also unit 1's)
+            // scales of the step's groups, rows g and g + 8 of each tile: the words
+            // that hold them, and which half is unit 0's (with one group a step
+            // also unit 1's)
             constexpr int W = UU * SETS == 4 ? 2 : 1;
             const int at = wide ? u >> 1 : u * SETS;
             const uint32_t pick = UU * SETS > 1 && !wide ? 0x3210u : at & 1 ? 0x3232u : 0x1010u;
-            uint32_t sc[TT][2][2][W];
+            uint32_t sc[TT][2][W];
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
+            for (int t = 0; t < TT; ++t)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const uint32_t o = sc0 + (t ? sc1 : 0u) + (uint32_t)(b * 16 * sp) + (uint32_t)(at & ~1) * 2u;
-                    lds<W>(o, sc[t][b][0]);
-                    lds<W>(o + (uint32_t)sp, sc[t][b][1]);
-                    if (UU * SETS < 4) {
-                        sc[t][b][0][0] = prmt(sc[t][b][0][0], 0u, pick);
-                        sc[t][b][1][0] = prmt(sc[t][b][1][0], 0u, pick);
-                    }
+                    lds<W>(sc0 + (t ? sc1 : 0u) + (b ? 8u * sp : 0u) + (uint32_t)(at & ~1) * 2u, sc[t][b]);
+                    if (UU * SETS < 4) sc[t][b][0] = prmt(sc[t][b][0], 0u, pick);
                 }
-            }
 #pragma unroll
             for (int i = 0; i < UU; ++i) {
                 uint32_t ra[TT][8], rb[TT][8];
@@ -734,12 +829,9 @@ __device__ __forceinline__ bool run_pass(const MoeParams &p, const Pass &ps, Sha
                 }
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
+                    if (NB > 1 && nb * 8 >= ps.ncols) continue;
                     const uint4 x = lds16(xs[nb] + (uint32_t)(u + i) * 128u);
                     const uint4 y = lds16(xs[nb] + (uint32_t)(u + i) * 128u + 64u);
-                    float2 s[SETS];
-#pragma unroll
-                    for (int h = 0; h < SETS; ++h)
-                        s[h] = lds_f2(sum0 + (uint32_t)(((u + i) * SETS + h) * C + nb * 8) * 4u);
 #pragma unroll
                     for (int t = 0; t < TT; ++t) {
                         float d[SETS][4];
@@ -754,16 +846,15 @@ __device__ __forceinline__ bool run_pass(const MoeParams &p, const Pass &ps, Sha
 #pragma unroll
                         for (int h = 0; h < SETS; ++h) {
                             const int z = i * SETS + h;
-                            auto half = [&](int b, int v) {
-                                const __half2 p2 = *reinterpret_cast<const __half2 *>(&sc[t][b][v][z / 2]);
+                            auto half = [&](int b) {
+                                const __half2 p2 = *reinterpret_cast<const __half2 *>(&sc[t][b][z / 2]);
                                 return z & 1 ? __high2float(p2) : __low2float(p2);
                             };
-                            const float2 sa = make_float2(half(0, 0), half(0, 1));
-                            const float2 sb = make_float2(half(1, 0), half(1, 1));
-                            o[0] = fmaf(sa.x, d[h][0], fmaf(sa.y, s[h].x, o[0]));
-                            o[1] = fmaf(sa.x, d[h][1], fmaf(sa.y, s[h].y, o[1]));
-                            o[2] = fmaf(sb.x, d[h][2], fmaf(sb.y, s[h].x, o[2]));
-                            o[3] = fmaf(sb.x, d[h][3], fmaf(sb.y, s[h].y, o[3]));
+                            const float sa = half(0), sb = half(1);
+                            o[0] = fmaf(sa, d[h][0], o[0]);
+                            o[1] = fmaf(sa, d[h][1], o[1]);
+                            o[2] = fmaf(sb, d[h][2], o[2]);
+                            o[3] = fmaf(sb, d[h][3], o[3]);
                         }
                     }
                 }
@@ -773,6 +864,7 @@ __device__ __forceinline__ bool run_pass(const MoeParams &p, const Pass &ps, Sha
             rd += STAGE;
             if (rd >= ring + STAGES * STAGE) rd -= STAGES * STAGE;
             u += UU;
+            if (u >= n) add_biases();
             if (FLAT && (u >= n || k + 1 == end)) {
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
@@ -786,8 +878,8 @@ __device__ __forceinline__ bool run_pass(const MoeParams &p, const Pass &ps, Sha
                     }
                 u = 0;
                 ++st;
-                sc0 += (uint32_t)(TT * 32 * sp);
-                if (TT == 2) sc1 = st * 2 + 1 < nt ? (uint32_t)(32 * sp) : 0u;
+                sc0 += (uint32_t)(TT * 16) * sp;
+                if (TT == 2) sc1 = st * 2 + 1 < nt ? 16u * sp : 0u;
             }
         }
         __syncthreads();
@@ -857,17 +949,22 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
     // behind the rings: room for the passes, at the end the entries' experts
     const int room = kRoom - ((p.T * p.top * 2 + 15) & ~15);
     uint16_t *ids = reinterpret_cast<uint16_t *>(dyn + kWarps * kRing + room);
-    plan(p, sh, ids);
+    plan<8 * NB>(p, sh, ids);
     const int per = p.R / (PAIRS ? 8 : 16);  // tiles of an expert
-    const int64_t tiles = (int64_t)sh.busy * per;
-    int64_t lo = tiles * blockIdx.x / gridDim.x;
-    const int64_t hi = tiles * (blockIdx.x + 1) / gridDim.x;
+    // this CTA takes the tiles that start at costs lo .. hi - 1 (at most 2^30)
+    const int all = sh.cost * per, G = (int)gridDim.x, each = all / G, rest = all - each * G;
+    const int lo = each * (int)blockIdx.x + rest * (int)blockIdx.x / G;
+    const int hi = each * ((int)blockIdx.x + 1) + rest * ((int)blockIdx.x + 1) / G;
     bool wait = !PAIRS;
-    if (wait && lo >= hi) grid_dependency_wait();
-    while (lo < hi) {
-        const int a = (int)(lo / per), e = sh.act[a], count = sh.count[e];
-        const int from = (int)(lo - (int64_t)a * per);
-        const int to = hi - lo < per - from ? from + (int)(hi - lo) : per;  // tiles of this expert
+    int a = 0;  // the last busy expert that starts at or before lo
+    for (int step = AQ_MOE_MAX_EXPERTS / 2; step > 0; step >>= 1)
+        if (a + step < sh.busy && sh.before[a + step] * per <= lo) a += step;
+    for (; a < sh.busy && sh.before[a] * per < hi; ++a) {
+        const int e = sh.act[a], count = sh.count[e], cost = tile_cost<8 * NB>(count);
+        const int start = sh.before[a] * per;
+        const int from = lo > start ? (lo - start + cost - 1) / cost : 0;
+        const int to = min((hi - start + cost - 1) / cost, per);
+        if (from >= to) continue;
         for (int col0 = 0; col0 < count; col0 += 8 * NB) {
             list_entries<8 * NB>(p, e, col0, sh, ids);
             Pass ps;
@@ -876,12 +973,17 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
             bool staged = false;
             for (ps.tile0 = from; ps.tile0 < to; ps.tile0 += ps.nt) {
                 ps.nt = to - ps.tile0 < kMaxTiles ? to - ps.tile0 : kMaxTiles;
+                // fewer tiles where 16 leave no room for chunks of 16 units
+                if (ps.nt > kMaxTiles / 2 &&
+                    chunk_units(FLAT, TT, kUnits<BITS>, NB, ps.nt, ps.ncols, p.group, p.K / 64, room) <
+                        (p.K < 1024 ? p.K / 64 : 16))
+                    ps.nt = kMaxTiles / 2;
                 staged = run_pass<BITS, G32, PAIRS, FLAT, TT, NB>(p, ps, sh, dyn, room, wait, staged);
                 wait = false;
             }
         }
-        lo += to - from;
     }
+    if (wait) grid_dependency_wait();
 }
 
 // The grid: two CTAs an SM, each with an even run of tiles.
@@ -908,11 +1010,12 @@ cudaError_t launch_sized(const MoeParams &p, cudaStream_t stream) {
     const double picked = (double)p.T * p.top;
     const double busy = p.E * -std::expm1(p.T * std::log1p(-(double)(p.top < p.E ? p.top : p.E - 0.5) / p.E));
     const double tokens = picked / busy, tiles = busy * (p.R / (PAIRS ? 8 : 16)) / (2.0 * num_sms());
-    if (p.T <= 8 || tokens <= 6.0) {
+    if (p.T <= 8 || tokens <= 2.0) {
         if (tiles <= 3.0) return launch_one<BITS, G32, PAIRS, true, 1, 1>(p, stream);
-        return launch_one<BITS, G32, PAIRS, true, 2, 1>(p, stream);
+        if (tiles <= 8.0) return launch_one<BITS, G32, PAIRS, true, 2, 1>(p, stream);
+        return launch_one<BITS, G32, PAIRS, false, 2, 1>(p, stream);
     }
-    if (p.T <= 16 || tokens <= 12.0) return launch_one<BITS, G32, PAIRS, false, 2, 2>(p, stream);
+    if (p.T <= 16 || tokens <= 10.0) return launch_one<BITS, G32, PAIRS, false, 2, 2>(p, stream);
     return launch_one<BITS, G32, PAIRS, false, 2, 4>(p, stream);
 }
 
