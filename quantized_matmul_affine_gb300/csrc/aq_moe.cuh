@@ -48,8 +48,6 @@ namespace moe_detail {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxTiles = 16;        // tiles of a pass
-constexpr int kRing = 6144;          // bytes of codes in flight a warp
 constexpr int kDynamic = 109568;     // dynamic shared memory: two CTAs an SM
 constexpr uint16_t kNone = 0xFFFF;
 constexpr int kMaxEntries = AQ_MOE_MAX_TOKENS * AQ_MOE_MAX_TOP;
@@ -268,6 +266,12 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(b0));
+}
+
 // The words of 8 source values, from x (fp16 or bf16) or h (fp32); ordinary
 // loads, since this grid may have started before they were written.
 template <bool PAIRS>
@@ -378,131 +382,65 @@ __device__ __forceinline__ void list_entries(const MoeParams &p, int e, int firs
     }
 }
 
-// A pass: tiles tile0 .. tile0 + nt - 1 of expert e for the ncols listed
-// entries.  flat: the (tile, step) pairs are dealt to the warps in even runs;
-// otherwise each warp, or `share` warps, keep TT tiles for the whole of K.
-struct Pass {
-    int e, tile0, nt, ncols;
-};
-
-// Shared memory behind the rings for a chunk of `units` 64-value units: the
-// columns (fp16 in MMA order, 64 bytes of pitch so that two rows' 16-byte reads
-// differ in banks), their group sums (two fp16 parts, a whole MMA step of 16
-// groups), the tiles' scales and biases, and what sums need.  Pitches of an odd
-// number of 16 bytes put 8 rows on all banks.
-struct Layout {
-    int pitch, sum_lo, sum_pitch, bias_at, scale_pitch;
-    int sums, scales, total, slots, end;  // byte offsets
-};
-__host__ __device__ constexpr Layout layout(bool flat, int tt, int uu, int nb, int nt, int ncols, int group,
-                                            int units) {
-    Layout l = {};
-    const int padded = (units + uu - 1) / uu * uu;  // whole steps: units past the end count as zeros
-    const int have = group == 32 ? padded * 2 : group == 64 ? padded : (padded + 1) / 2;
-    const int steps = (have + 15) / 16 * 32;  // bytes of whole MMA steps
-    l.pitch = padded * 128 + 64;
-    l.sum_lo = steps;
-    l.sum_pitch = 2 * steps + 16;
-    l.bias_at = (have * 2 + 15) / 16 * 16;
-    l.scale_pitch = ((l.bias_at + steps) / 16 | 1) * 16;
-    l.sums = ncols * l.pitch;
-    l.scales = l.sums + ncols * l.sum_pitch;
-    l.total = l.scales + nt * 16 * l.scale_pitch;
-    l.slots = flat ? l.total + nt * nb * 512 : 0;
-    l.end = flat ? l.slots + ((nt + tt - 1) / tt + kWarps - 1) * tt * nb * 512 : l.total;
-    return l;
-}
-constexpr int kRoom = kDynamic - kWarps * kRing;  // less the entries' experts
-// The most that 4 units take fits beside the most entries, and so do the slots
-// of warps that keep their tiles.
-static_assert(layout(false, 2, 2, 4, kMaxTiles, 32, 32, 4).end <= kRoom - 2 * kMaxEntries &&
-              layout(true, 2, 2, 1, kMaxTiles, 8, 32, 4).end <= kRoom - 2 * kMaxEntries &&
-              kWarps * 2 * 4 * 512 <= kRoom - 2 * kMaxEntries, "chunks");
-
-// Units of a chunk: all, or the most that fit, steps of 16 where there are as
-// many (the sums' MMA steps are whole then), else of 4.
-__device__ __forceinline__ int chunk_units(bool flat, int tt, int uu, int nb, int nt, int ncols, int group,
-                                           int U, int room) {
-    if (layout(flat, tt, uu, nb, nt, ncols, group, U).end <= room) return U;
-    int n = 4;
-    while (n + 16 < U && layout(flat, tt, uu, nb, nt, ncols, group, n < 16 ? 16 : n + 16).end <= room)
-        n = n < 16 ? 16 : n + 16;
-    return n;
-}
-
-// Copies P bytes (a plain load and store for 2), asynchronously from 4 up.
+// Copies 16 (or 8) bytes of codes where `on`, without a branch: the lanes that
+// have nothing to copy stay with the others.
 template <int P>
-__device__ __forceinline__ void copy_piece(uint32_t to, const uint8_t *from) {
+__device__ __forceinline__ void copy_codes(uint32_t to, const uint8_t *from, bool on) {
+    static_assert(P == 16 || P == 8, "16 or 8 bytes");
     if constexpr (P == 16)
-        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-    else if constexpr (P == 8)
-        asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
-    else if constexpr (P == 4)
-        asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+                     "@p cp.async.cg.shared.global.L2::128B [%0], [%1], 16;\n\t}" ::"r"(to),
+                     "l"(from), "r"((uint32_t)on)
+                     : "memory");
     else
-        asm volatile("{\n\t.reg .b16 v;\n\tld.global.b16 v, [%1];\n\tst.shared.b16 [%0], v;\n\t}" ::"r"(to),
-                     "l"(from)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+                     "@p cp.async.ca.shared.global.L2::128B [%0], [%1], 8;\n\t}" ::"r"(to),
+                     "l"(from), "r"((uint32_t)on)
                      : "memory");
 }
-
-// The scales and biases of the pass's rows for the groups of units u0 .. u0 +
-// n - 1: each row's scales, at bias_at its biases, both with zeros up to the
-// end of their room.
-template <bool PAIRS, int P>
-__device__ __forceinline__ void copy_scales(const MoeParams &p, const Pass &ps, int g0, int bytes, int groups,
-                                            uint32_t scales, const Layout &l) {
-    const int per = (bytes + P - 1) / P, rows = ps.nt * 16;
-    // rows by threads, so that a row's pieces need no division; a wide row is
-    // shared by several
-    const int tid = threadIdx.x;
-    int lanes = 1;
-    while (lanes < 32 && lanes < per) lanes *= 2;
-    for (int row = tid / lanes; row < rows; row += kThreads / lanes) {
-        const int r = row & 15;
-        const bool second = PAIRS && r >= 8;
-        const int64_t at = (((int64_t)ps.e * p.R + (int64_t)(ps.tile0 + (row >> 4)) * (PAIRS ? 8 : 16) +
-                             (PAIRS ? r & 7 : r)) * groups + g0) * 2;
-        const uint8_t *s = static_cast<const uint8_t *>(second ? p.s1 : p.s0) + at;
-        const uint8_t *b = static_cast<const uint8_t *>(second ? p.b1 : p.b0) + at;
-        const uint32_t to = scales + (uint32_t)(row * l.scale_pitch);
-        for (int k = tid % lanes; k < per; k += lanes) {
-            copy_piece<P>(to + k * P, s + k * P);
-            copy_piece<P>(to + l.bias_at + k * P, b + k * P);
-        }
+// Copies P bytes of scales, or writes P bytes of zeros (and reads nothing).
+template <int P>
+__device__ __forceinline__ void copy_scales(uint32_t to, const uint8_t *from, bool on) {
+    if constexpr (P == 16) {
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+                     "r"(on ? 16u : 0u)
+                     : "memory");
+    } else if constexpr (P == 8 || P == 4) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(P),
+                     "r"(on ? (uint32_t)P : 0u)
+                     : "memory");
+    } else {
+        uint16_t v = 0;
+        if (on) asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(from) : "memory");
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(v) : "memory");
     }
 }
-template <bool PAIRS, int SETS>
-__device__ __forceinline__ void stage_scales(const MoeParams &p, const Pass &ps, int u0, int n, int groups,
-                                             uint32_t scales, const Layout &l) {
-    const int wide = p.group == 128;
-    const int g0 = wide ? u0 / 2 : u0 * SETS, ng = wide ? n / 2 : n * SETS;
-    // the largest piece that the rows' starts and lengths allow
-    const uint32_t all = (uint32_t)(reinterpret_cast<uintptr_t>(p.s0) | reinterpret_cast<uintptr_t>(p.b0) |
-                                    reinterpret_cast<uintptr_t>(p.s1) | reinterpret_cast<uintptr_t>(p.b1)) |
-                         (uint32_t)(groups * 2) | (uint32_t)(g0 * 2) | (uint32_t)(ng * 2);
-    if ((all & 15) == 0)
-        copy_scales<PAIRS, 16>(p, ps, g0, ng * 2, groups, scales, l);
-    else if ((all & 7) == 0)
-        copy_scales<PAIRS, 8>(p, ps, g0, ng * 2, groups, scales, l);
-    else if ((all & 3) == 0)
-        copy_scales<PAIRS, 4>(p, ps, g0, ng * 2, groups, scales, l);
-    else
-        copy_scales<PAIRS, 2>(p, ps, g0, ng * 2, groups, scales, l);
-    auto zero = [&](int from, int to) {
-        const int each = (to - from) / 2;
-        for (int i = threadIdx.x; i < ps.nt * 16 * each; i += kThreads)
-            asm volatile("st.shared.b16 [%0], %1;" ::"r"(scales + (uint32_t)(i / each * l.scale_pitch + from + i % each * 2)),
-                         "h"((short)0)
-                         : "memory");
-    };
-    zero(2 * ng, l.bias_at);
-    zero(l.bias_at + 2 * ng, l.bias_at + l.sum_lo);
+
+// Where a chunk of `units` 64-value units of ncols columns lies: the columns,
+// fp16 in MMA order (64 bytes of pitch: two rows' 16-byte reads differ in
+// banks), then their group sums, two fp16 parts, whole blocks of scales. An
+// odd number of 16 bytes as the sums' pitch puts 8 columns on all banks.
+struct Layout {
+    int pitch, sums, sum_lo, sum_pitch;
+};
+template <int UU, int BU>
+__host__ __device__ constexpr Layout layout(int ncols, int units) {
+    Layout l = {};
+    l.pitch = (units + UU - 1) / UU * UU * 128 + 64;  // whole steps: units past the end count as zeros
+    l.sums = ncols * l.pitch;
+    l.sum_lo = (units + BU - 1) / BU * 16;
+    l.sum_pitch = 2 * l.sum_lo + 16;
+    return l;
+}
+template <int UU, int BU>
+__host__ __device__ constexpr int layout_bytes(int ncols, int units) {
+    return layout<UU, BU>(ncols, units).sums + ncols * layout<UU, BU>(ncols, units).sum_pitch;
 }
 
-// The pass's columns as fp16 in MMA order, with their group sums times 2^-8 as
-// two fp16 parts (22 bits).
+// The listed columns for units u0 .. u0 + n - 1 as fp16 in MMA order, with
+// their group sums times 2^-8 as two fp16 parts (22 bits).
 template <int BITS, bool G32, bool PAIRS>
-__device__ __forceinline__ void stage_columns(const MoeParams &p, const Pass &ps, Shared &sh, int u0,
+__device__ __forceinline__ void stage_columns(const MoeParams &p, int ncols, Shared &sh, int u0,
                                               int n, int padded, uint8_t *act, const Layout &l) {
     using Ord = Order<BITS, G32>;
     constexpr int SETS = G32 ? 2 : 1, KEPT = 2;  // quarters a thread has in flight
@@ -523,7 +461,7 @@ __device__ __forceinline__ void stage_columns(const MoeParams &p, const Pass &ps
         source8<PAIRS>(p, at, w);
         source8<PAIRS>(p, at + second, w + (PAIRS ? 4 : 8));
     };
-    const int peak_items = ps.ncols * U * 4;
+    const int peak_items = ncols * U * 4;
     const bool kept = u0 == 0 && n == U && n == padded && peak_items <= KEPT * kThreads;
     if (u0 == 0) {  // the columns' largest magnitudes
         if (tid < 32) sh.peak[tid] = 0u;
@@ -550,7 +488,7 @@ __device__ __forceinline__ void stage_columns(const MoeParams &p, const Pass &ps
         }
         __syncthreads();
     }
-    const int items = ps.ncols * padded * 4;
+    const int items = ncols * padded * 4;
     for (int i0 = tid; i0 < items; i0 += KEPT * kThreads) {
         if (!kept) {
 #pragma unroll
@@ -601,10 +539,10 @@ __device__ __forceinline__ void stage_columns(const MoeParams &p, const Pass &ps
                 s2 += __shfl_xor_sync(quad, s2, 1);
                 s2 += __shfl_xor_sync(quad, s2, 2);
             }
-            int at = G32 ? uu * 2 + qq : uu;  // its group
+            int at = G32 ? uu * 2 + qq : uu;  // its group's place
             if (!G32 && wide) {               // the other unit of the group: n is even, as is the lane's part
                 s += __shfl_xor_sync(0xFFu << (lane & ~7), s, 4);
-                at = uu >> 1;
+                at = (uu >> 3) * 8 + ((uu & 7) >> 1);
             }
             if (qq < SETS && !(wide && (uu & 1))) {
                 const float v = (qq ? s2 : s) * 0.00390625f;
@@ -615,329 +553,387 @@ __device__ __forceinline__ void stage_columns(const MoeParams &p, const Pass &ps
             }
         }
     }
-    // zeros up to the last MMA step's end
-    const int have = wide ? n / 2 : n * SETS, rest = l.sum_lo / 2 - have;
-    for (int i = tid; i < ps.ncols * rest; i += kThreads) {
-        __half *to = reinterpret_cast<__half *>(act + l.sums + (size_t)(i / rest) * l.sum_pitch) + have + i % rest;
-        to[0] = to[l.sum_lo / 2] = __half(0.f);
-    }
+    // zeros in what is left of the blocks
+    const int all = l.sum_lo / 2;
+    if (wide || n * SETS < all)
+        for (int i = tid; i < ncols * all; i += kThreads) {
+            const int c = i / all, k = i - c * all;
+            if (wide ? (k & 7) >= 4 || (k >> 3) * 8 + (k & 7) * 2 >= n : k >= n * SETS) {
+                __half *to = reinterpret_cast<__half *>(act + l.sums + (size_t)c * l.sum_pitch) + k;
+                to[0] = to[all] = __half(0.f);
+            }
+        }
 }
 
-// TT tiles side by side share the activations that a step reads from shared
-// memory; 8 NB columns.  (With an odd number of tiles the last one is taken
-// twice and counted once.)  staged: the last pass left these columns, for all
-// of K, in shared memory; returned is whether this one does.
-template <int BITS, bool G32, bool PAIRS, bool FLAT, int TT, int NB>
-__device__ __forceinline__ bool run_pass(const MoeParams &p, const Pass &ps, Shared &sh, uint8_t *dyn,
-                                         int room, bool wait, bool staged) {
-    constexpr int NW = kWords<BITS, G32>, UU = kUnits<BITS>;
-    constexpr int SETS = G32 ? 2 : 1;      // groups of a unit whose sums are kept apart
-    constexpr int ROWS = PAIRS ? 8 : 16;   // rows of a matrix in a tile
-    constexpr int UNIT = 8 * BITS;         // bytes of a unit's row
-    constexpr int CELL = 16 * UNIT, STAGE = TT * UU * CELL;
-    constexpr int STAGES = kRing / STAGE < 8 ? kRing / STAGE : 8;
-    constexpr bool SPLIT = BITS % 2 == 0;  // units apart in shared memory, else rows whole
+// The sizes of a kernel.  TT tiles side by side share the activations that a
+// step of UU units reads from shared memory; 8 NB columns.
+template <int BITS, bool G32, bool PAIRS, int TT_, int NB_>
+struct Kernel {
+    static constexpr int TT = TT_, NB = NB_, C = 8 * NB, UU = kUnits<BITS>, NW = kWords<BITS, G32>;
+    static constexpr int SETS = G32 ? 2 : 1;     // groups of a unit whose sums are kept apart
+    static constexpr int BU = G32 ? 4 : 8;       // units of a block of scales: 8 groups, 4 of 128
+    static constexpr int ROWS = PAIRS ? 8 : 16;  // rows of a matrix in a tile
+    static constexpr int UNIT = 8 * BITS;        // bytes of a unit's row
+    static constexpr int CELL = 16 * UNIT, STAGE = TT * UU * CELL;
+    // steps in flight, two at least; a block of scales for each and the one at work
+    static constexpr int STAGES = TT == 1 || (STAGE <= 1536 && NB < 4) ? 3 : 2, BLOCKS = STAGES + 1;
+    static constexpr int BLOCK = TT * 512;  // bytes: 16 scales and biases of 8 groups a tile
+    static constexpr int RING = STAGES * STAGE + BLOCKS * BLOCK;  // a warp's
+    static constexpr bool SPLIT = BITS % 2 == 0;  // units apart in shared memory, else rows whole
+    static constexpr int ROOM = kDynamic - kWarps * RING;  // for columns, less the entries' experts
+    // 8 units of all columns fit beside the most entries, and the partial
+    // sums of shared tiles where the rings were
+    static_assert(layout_bytes<UU, BU>(C, 8) <= ROOM - 2 * kMaxEntries && TT * NB * 512 <= RING, "room");
+};
+
+// Tiles from .. to - 1 of expert e for the ncols listed entries.  The tiles, TT
+// a group, go round the warps; the groups of the last, unfull round are shared
+// by 2, 4 or 8 warps, which split K.  Each warp has its codes and scales copied
+// to shared memory a few steps ahead, from one group to the next without a
+// stop; the warps meet only where columns are staged.
+template <class S, int BITS, bool G32, bool PAIRS>
+__device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, int to, int ncols, Shared &sh,
+                                          uint8_t *dyn, int room, bool wait) {
+    constexpr int TT = S::TT, NB = S::NB, UU = S::UU, BU = S::BU, SETS = S::SETS, STAGES = S::STAGES;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-    const int U = p.K / 64, nt = ps.nt, ns = (nt + TT - 1) / TT;
-    const int groups = p.K / p.group;
+    const int U = p.K / 64, groups = p.K / p.group;
     const bool wide = p.group == 128;
 
-    const int cu = chunk_units(FLAT, TT, UU, NB, nt, ps.ncols, p.group, U, room);
-    const Layout l = layout(FLAT, TT, UU, NB, nt, ps.ncols, p.group, cu);
-    const uint32_t ring = smem_u32(dyn + warp * kRing);
-    uint8_t *act = dyn + kWarps * kRing;
-    float4 *total = reinterpret_cast<float4 *>(act + l.total);
-    float4 *slots = reinterpret_cast<float4 *>(act + l.slots);
+    // all of K's columns at once, or as many units of them as fit, a multiple of 8
+    int cu = U;
+    if (layout_bytes<UU, BU>(ncols, U) > room) {
+        cu = (room - ncols * 128) / (ncols * (128 + 4 * SETS)) & ~7;
+        cu = cu < 8 ? 8 : cu;
+    }
+    const Layout l = layout<UU, BU>(ncols, cu);
+    uint8_t *act = dyn + kWarps * S::RING;
+    const uint32_t ring = smem_u32(dyn + warp * S::RING), blocks = ring + STAGES * S::STAGE;
+    float4 *slots = reinterpret_cast<float4 *>(dyn);
 
+    const int ngroups = (to - from + TT - 1) / TT, full = ngroups / kWarps, rest = ngroups - full * kWarps;
+    const int share = rest >= 5 ? 1 : rest >= 3 ? 2 : rest == 2 ? 4 : 8;
+    const int rounds = full + (rest > 0);
+
+    // what a lane copies of a tile's step: pieces of 16 bytes, PER a row (of 8
+    // bytes where an odd width's rows are not multiples of 16: fine)
+    constexpr int UNIT = S::UNIT, CELL = S::CELL, PER = UU * UNIT / 16, PIECES = (16 * PER + 31) / 32;
     const int64_t row_bytes = (int64_t)p.K * BITS / 8;
     const int64_t to_b = PAIRS ? reinterpret_cast<const uint8_t *>(p.w1) - reinterpret_cast<const uint8_t *>(p.w0)
                                : 8 * row_bytes;
-    const int64_t to_t = ROWS * row_bytes;
-    const uint8_t *w0 = reinterpret_cast<const uint8_t *>(p.w0) +
-                        ((int64_t)ps.e * p.R + (int64_t)ps.tile0 * ROWS) * row_bytes;
-    // what a lane copies of a tile's step: pieces of 16 bytes, PER a row (of 8
-    // bytes where an odd width's rows are not multiples of 16: fine)
-    constexpr int PER = UU * UNIT / 16, PIECES = (16 * PER + 31) / 32;
-    const bool fine = !SPLIT && (row_bytes & 8);
+    const int64_t to_t = S::ROWS * row_bytes;
+    const bool fine = !S::SPLIT && (row_bytes & 8);
     auto piece_at = [&](int i) { return (lane + 32 * i) % PER * 16; };  // byte of the row's step
     auto piece_to = [&](int row, int at) {
-        return (uint32_t)(SPLIT ? at / UNIT * CELL + row * UNIT + at % UNIT : row * UU * UNIT + at);
+        return (uint32_t)(S::SPLIT ? at / UNIT * CELL + row * UNIT + at % UNIT : row * UU * UNIT + at);
     };
-    int64_t from[PIECES];
-    uint32_t to[PIECES];
+    int64_t code_from[PIECES];
+    uint32_t code_to[PIECES];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
         const int row = (lane + 32 * i) / PER;
-        from[i] = (row & 7) * row_bytes + (row >= 8 ? to_b : 0) + piece_at(i);
-        to[i] = piece_to(row, piece_at(i));
+        code_from[i] = (row & 7) * row_bytes + (row >= 8 ? to_b : 0) + piece_at(i);
+        code_to[i] = piece_to(row, piece_at(i));
     }
+    // and of a tile's block of scales: a row's scales or biases (16 rows of 16
+    // bytes each), whole where rows allow, else in smaller pieces
+    const int block_bytes = wide ? 8 : 16;
+    const uint32_t even = (uint32_t)(reinterpret_cast<uintptr_t>(p.s0) | reinterpret_cast<uintptr_t>(p.b0) |
+                                     reinterpret_cast<uintptr_t>(p.s1) | reinterpret_cast<uintptr_t>(p.b1)) |
+                          (uint32_t)(groups * 2) | (uint32_t)block_bytes;
+    const uint8_t *scale_row;  // the lane's row of the expert's first tile of the run
+    {
+        const int r = lane & 15;
+        const bool second = PAIRS && r >= 8;
+        const void *m = lane < 16 ? (second ? p.s1 : p.s0) : (second ? p.b1 : p.b0);
+        scale_row = static_cast<const uint8_t *>(m) +
+                    (((int64_t)e * p.R + (int64_t)from * S::ROWS + (PAIRS ? r & 7 : r)) * groups) * 2;
+    }
+    const uint8_t *w0 = reinterpret_cast<const uint8_t *>(p.w0) +
+                        ((int64_t)e * p.R + (int64_t)from * S::ROWS) * row_bytes;
     const uint32_t shift = (uint32_t)first_bit<BITS, G32>(q) & 31u;
-    const uint32_t mine = (uint32_t)(g * (SPLIT ? UNIT : UU * UNIT) + first_bit<BITS, G32>(q) / 32 * 4);
-    const int share = FLAT ? 1 : ns >= 5 ? 1 : ns >= 3 ? 2 : ns == 2 ? 4 : 8;
+    const uint32_t mine = (uint32_t)(g * (S::SPLIT ? UNIT : UU * UNIT) + first_bit<BITS, G32>(q) / 32 * 4);
 
     float acc[TT][NB][4];
+    auto clear = [&]() {
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][nb][i] = 0.f;
-
-    for (int u0 = 0; u0 < U; u0 += cu) {
-        const int n = U - u0 < cu ? U - u0 : cu;     // units of this chunk
-        const int nq = (n + UU - 1) / UU;            // steps of a tile
-        int st, beg, end;                            // first tile (of TT), steps counted from it
-        if (FLAT) {
-            beg = ns * nq * warp / kWarps;
-            end = ns * nq * (warp + 1) / kWarps;
-            st = beg / nq;
-            beg -= st * nq;
-            end -= st * nq;
+                for (int i = 0; i < 4; ++i) acc[t][nb][i] = 0.f;
+    };
+    // acc is in 2^-24 of the column's units
+    auto write = [&](int tile, int c, float a, float b) {
+        const float f = sh.undo[c];
+        a = a * 16777216.f * f;
+        b = b * 16777216.f * f;
+        float *o = p.dst + (size_t)sh.list[c] * p.R + tile * S::ROWS + g;
+        if constexpr (PAIRS) {
+            *o = a / (1.f + expf(-a)) * b;
         } else {
-            st = warp / share;
-            beg = nq * (warp % share) / share;
-            end = st < ns ? nq * (warp % share + 1) / share : beg;
+            o[0] = a;
+            o[8] = b;
         }
+    };
+    // The warp's group in a round and its steps of a chunk with nq steps.
+    auto place = [&](int round, int nq, int &group, int &beg, int &end) {
+        if (round < full) {
+            group = round * kWarps + warp;
+            beg = 0;
+            end = nq;
+        } else {
+            const int i = warp / share, part = warp - i * share;
+            group = full * kWarps + i;
+            beg = nq * part / share;
+            end = i < rest ? nq * (part + 1) / share : beg;
+        }
+    };
 
-        // the step to fetch next: its tiles, its first unit
-        int fs = st, fu = beg * UU, fk = beg;
-        const uint8_t *src = w0 + (int64_t)(st * TT) * to_t + (int64_t)(u0 + fu) * UNIT;
-        int64_t next = TT == 2 && st * 2 + 1 < nt ? to_t : 0;
-        const int64_t wrap = TT * to_t - (int64_t)nq * UU * UNIT;
+    // Units u0 .. u0 + n - 1 of K for rounds r0 .. r1 - 1.
+    auto stream = [&](int r0, int r1, int u0, int n) {
+        const int nq = (n + UU - 1) / UU;
+        // the step to fetch next
+        int fround = r0, fgroup, fk, fend, fu, fblock = 0;
+        const uint8_t *src = nullptr;
+        int64_t next = 0;
+        bool fresh = true;  // the first step of a group
         uint32_t fr = ring;
+        auto enter = [&]() {
+            place(fround, nq, fgroup, fk, fend);
+            while (fk >= fend && ++fround < r1) place(fround, nq, fgroup, fk, fend);
+            fu = fk * UU;
+            src = w0 + (int64_t)(fgroup * TT) * to_t + (int64_t)(u0 + fu) * UNIT;
+            next = TT == 2 && from + fgroup * 2 + 1 < to ? to_t : 0;
+            fresh = true;
+        };
+        enter();
         auto fetch = [&]() {
-            if (fk < end) {
+            if (fround < r1) {
                 const int left = (n - fu) * UNIT;  // bytes of the row up to the chunk's end
 #pragma unroll
                 for (int t = 0; t < TT; ++t) {
                     const uint8_t *s = src + (t ? next : 0);
-                    if (SPLIT || !fine) {
+                    if (S::SPLIT || !fine) {
 #pragma unroll
                         for (int i = 0; i < PIECES; ++i)
-                            if ((16 * PER % 32 == 0 || lane + 32 * i < 16 * PER) && (UU == 1 || piece_at(i) < left))
-                                copy_piece<16>(fr + t * UU * CELL + to[i], s + from[i]);
+                            copy_codes<16>(fr + t * UU * CELL + code_to[i], s + code_from[i],
+                                           (16 * PER % 32 == 0 || lane + 32 * i < 16 * PER) &&
+                                               (UU == 1 || piece_at(i) < left));
                     } else {
                         for (int k = lane; k < 32 * PER; k += 32) {
                             const int row = k / (2 * PER), at = k % (2 * PER) * 8;
-                            if (at < left)
-                                copy_piece<8>(fr + t * UU * CELL + piece_to(row, at),
-                                              s + (row & 7) * row_bytes + (row >= 8 ? to_b : 0) + at);
+                            copy_codes<8>(fr + t * UU * CELL + piece_to(row, at),
+                                          s + (row & 7) * row_bytes + (row >= 8 ? to_b : 0) + at, at < left);
                         }
                     }
+                }
+                if (fresh || (fu & (BU - 1)) == 0) {
+                    // the block of scales that this step lies in
+                    const int b0 = (u0 + fu) / BU * block_bytes;  // of the row's bytes
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) {
+                        const int tile = fgroup * TT + (t && next ? 1 : 0);
+                        const uint8_t *s = scale_row + (int64_t)tile * (S::ROWS * 2) * groups + b0;
+                        const uint32_t to_s = blocks + (uint32_t)(fblock * S::BLOCK + t * 512 + lane * 16);
+                        const int have = groups * 2 - b0;  // bytes of the row from here on
+                        if ((even & 15) == 0) {
+                            copy_scales<16>(to_s, s, true);
+                        } else if ((even & 7) == 0) {
+                            copy_scales<8>(to_s, s, true);
+                            copy_scales<8>(to_s + 8, s + 8, !wide && have >= 16);
+                        } else if ((even & 3) == 0) {
+#pragma unroll
+                            for (int k = 0; k < 16; k += 4)
+                                copy_scales<4>(to_s + k, s + k, k < block_bytes && have >= k + 4);
+                        } else {
+                            for (int k = 0; k < 16; k += 2)
+                                copy_scales<2>(to_s + k, s + k, k < block_bytes && have >= k + 2);
+                        }
+                    }
+                    fblock = fblock + 1 == S::BLOCKS ? 0 : fblock + 1;
+                    fresh = false;
                 }
                 fu += UU;
                 src += UU * UNIT;
-                if (fu >= n) {
-                    fu = 0;
-                    ++fs;
-                    src += wrap;
-                    if (TT == 2) next = fs * 2 + 1 < nt ? to_t : 0;
-                }
-                ++fk;
-                fr = fr + STAGE == ring + STAGES * STAGE ? ring : fr + STAGE;
+                fr = fr + S::STAGE == ring + STAGES * S::STAGE ? ring : fr + S::STAGE;
+                if (++fk >= fend && ++fround < r1) enter();
             }
             cp_async_commit();
         };
-        __syncthreads();  // the last chunk's or pass's readers are done
-        const uint32_t scale0 = smem_u32(act + l.scales);
-        stage_scales<PAIRS, SETS>(p, ps, u0, n, groups, scale0, l);
-        cp_async_commit();
 #pragma unroll
         for (int i = 0; i < STAGES; ++i) fetch();
-        if (wait && u0 == 0) grid_dependency_wait();
-        if (!(FLAT && staged && cu == U))
-            stage_columns<BITS, G32, PAIRS>(p, ps, sh, u0, n, nq * UU, act, l);
-        cp_async_wait<STAGES>();  // the scales
+
+        if (wait) grid_dependency_wait();
+        wait = false;
+        __syncthreads();  // the last columns' readers are done
+        stage_columns<BITS, G32, PAIRS>(p, ncols, sh, u0, n, nq * UU, act, l);
         __syncthreads();
 
-        uint32_t xs[NB];
+        uint32_t xs[NB], ss[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-            const int c = nb * 8 + g;
-            xs[nb] = smem_u32(act) + (uint32_t)((c < ps.ncols ? c : 0) * l.pitch + q * 16);
+            const int c = nb * 8 + g < ncols ? nb * 8 + g : 0;
+            xs[nb] = smem_u32(act) + (uint32_t)(c * l.pitch + q * 16);
+            ss[nb] = smem_u32(act) + (uint32_t)(l.sums + c * l.sum_pitch + 4 * q);
         }
-        int u = beg * UU;
         uint32_t rd = ring + mine;
-        // the scales of rows g and g + 8 of the warp's tiles
-        const uint32_t sp = (uint32_t)l.scale_pitch;
-        uint32_t sc0 = scale0 + (uint32_t)(st * TT * 16 + g) * sp;
-        uint32_t sc1 = TT == 2 && st * 2 + 1 < nt ? 16u * sp : 0u;
-        // The chunk's biases times group sums, 16 groups a product, by the warp
-        // that takes a tile's last step: acc is in 2^-24, these products in 2^-8.
-        auto add_biases = [&]() {
-            const uint32_t bias = (uint32_t)(l.bias_at + 4 * q);
+        int block = -1;
+        for (int round = r0; round < r1; ++round) {
+            int group, beg, end;
+            place(round, nq, group, beg, end);
+            uint32_t sc = 0;
+            for (int k = beg, u = beg * UU; k < end; ++k, u += UU) {
+                cp_async_wait<STAGES - 1>();
+                __syncwarp();
+                if (k == beg || (u & (BU - 1)) == 0) {
+                    block = block + 1 == S::BLOCKS ? 0 : block + 1;
+                    sc = blocks + (uint32_t)(block * S::BLOCK);
+                    if ((u & (BU - 1)) == 0) {
+                        // the block's biases times the columns' group sums: acc is in
+                        // 2^-24, these products in 2^-8
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                if (NB > 1 && nb * 8 >= ps.ncols) continue;
-                const int c = nb * 8 + g;
-                const uint32_t sum = smem_u32(act) + (uint32_t)(l.sums + (c < ps.ncols ? c : 0) * l.sum_pitch + 4 * q);
-                float d[TT][4];
+                        for (int nb = 0; nb < NB; ++nb) {
+                            if (NB > 1 && nb * 8 >= ncols) continue;
+                            uint32_t hi, lo;
+                            lds<1>(ss[nb] + (uint32_t)(u / BU * 16), &hi);
+                            lds<1>(ss[nb] + (uint32_t)(l.sum_lo + u / BU * 16), &lo);
 #pragma unroll
-                for (int t = 0; t < TT; ++t) d[t][0] = d[t][1] = d[t][2] = d[t][3] = 0.f;
-                for (int k = 0; k < l.sum_lo; k += 32) {
-                    uint32_t h0, h1, l0, l1;
-                    lds<1>(sum + k, &h0);
-                    lds<1>(sum + k + 16, &h1);
-                    lds<1>(sum + l.sum_lo + k, &l0);
-                    lds<1>(sum + l.sum_lo + k + 16, &l1);
+                            for (int t = 0; t < TT; ++t) {
+                                uint32_t a0, a1;
+                                lds<1>(sc + (uint32_t)(t * 512 + 256 + g * 16 + 4 * q), &a0);
+                                lds<1>(sc + (uint32_t)(t * 512 + 384 + g * 16 + 4 * q), &a1);
+                                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma_k8(d, a0, a1, hi);
+                                mma_k8(d, a0, a1, lo);
 #pragma unroll
-                    for (int t = 0; t < TT; ++t) {
-                        const uint32_t o = sc0 + (t ? sc1 : 0u) + bias + k;
-                        uint32_t a0, a1, a2, a3;
-                        lds<1>(o, &a0);
-                        lds<1>(o + 8u * sp, &a1);
-                        lds<1>(o + 16u, &a2);
-                        lds<1>(o + 8u * sp + 16u, &a3);
-                        mma(d[t], a0, a1, a2, a3, h0, h1);
-                        mma(d[t], a0, a1, a2, a3, l0, l1);
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < TT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[t][nb][i] = fmaf(d[t][i], 1.52587890625e-05f, acc[t][nb][i]);
-            }
-        };
-        for (int k = beg; k < end; ++k) {
-            cp_async_wait<STAGES - 1>();
-            __syncwarp();
-            // scales of the step's groups, rows g and g + 8 of each tile: the words
-            // that hold them, and which half is unit 0's (with one group a step
-            // also unit 1's)
-            constexpr int W = UU * SETS == 4 ? 2 : 1;
-            const int at = wide ? u >> 1 : u * SETS;
-            const uint32_t pick = UU * SETS > 1 && !wide ? 0x3210u : at & 1 ? 0x3232u : 0x1010u;
-            uint32_t sc[TT][2][W];
-#pragma unroll
-            for (int t = 0; t < TT; ++t)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    lds<W>(sc0 + (t ? sc1 : 0u) + (b ? 8u * sp : 0u) + (uint32_t)(at & ~1) * 2u, sc[t][b]);
-                    if (UU * SETS < 4) sc[t][b][0] = prmt(sc[t][b][0], 0u, pick);
-                }
-#pragma unroll
-            for (int i = 0; i < UU; ++i) {
-                uint32_t ra[TT][8], rb[TT][8];
-#pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    uint32_t w[NW];
-                    const uint32_t a = rd + (uint32_t)((t * UU + (SPLIT ? i : 0)) * CELL + (SPLIT ? 0 : i * UNIT));
-                    load_codes<BITS, G32>(a, w);
-                    decode<BITS, G32>(w, shift, ra[t]);
-                    load_codes<BITS, G32>(a + 8 * (SPLIT ? UNIT : UU * UNIT), w);
-                    decode<BITS, G32>(w, shift, rb[t]);
-                }
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    if (NB > 1 && nb * 8 >= ps.ncols) continue;
-                    const uint4 x = lds16(xs[nb] + (uint32_t)(u + i) * 128u);
-                    const uint4 y = lds16(xs[nb] + (uint32_t)(u + i) * 128u + 64u);
-#pragma unroll
-                    for (int t = 0; t < TT; ++t) {
-                        float d[SETS][4];
-                        mma0(d[0], ra[t][0], rb[t][0], ra[t][1], rb[t][1], x.x, x.y);
-                        mma(d[0], ra[t][2], rb[t][2], ra[t][3], rb[t][3], x.z, x.w);
-                        if constexpr (G32)
-                            mma0(d[SETS - 1], ra[t][4], rb[t][4], ra[t][5], rb[t][5], y.x, y.y);
-                        else
-                            mma(d[0], ra[t][4], rb[t][4], ra[t][5], rb[t][5], y.x, y.y);
-                        mma(d[SETS - 1], ra[t][6], rb[t][6], ra[t][7], rb[t][7], y.z, y.w);
-                        float(&o)[4] = acc[t][nb];
-#pragma unroll
-                        for (int h = 0; h < SETS; ++h) {
-                            const int z = i * SETS + h;
-                            auto half = [&](int b) {
-                                const __half2 p2 = *reinterpret_cast<const __half2 *>(&sc[t][b][z / 2]);
-                                return z & 1 ? __high2float(p2) : __low2float(p2);
-                            };
-                            const float sa = half(0), sb = half(1);
-                            o[0] = fmaf(sa, d[h][0], o[0]);
-                            o[1] = fmaf(sa, d[h][1], o[1]);
-                            o[2] = fmaf(sb, d[h][2], o[2]);
-                            o[3] = fmaf(sb, d[h][3], o[3]);
+                                for (int i = 0; i < 4; ++i)
+                                    acc[t][nb][i] = fmaf(d[i], 1.52587890625e-05f, acc[t][nb][i]);
+                            }
                         }
                     }
                 }
-            }
-            __syncwarp();  // the stage is read: it may be filled again
-            fetch();
-            rd += STAGE;
-            if (rd >= ring + STAGES * STAGE) rd -= STAGES * STAGE;
-            u += UU;
-            if (u >= n) add_biases();
-            if (FLAT && (u >= n || k + 1 == end)) {
+                // scales of the step's groups, rows g and g + 8 of each tile: the words
+                // that hold them, and which half is unit 0's (with one group a step
+                // also unit 1's)
+                constexpr int W = UU * SETS == 4 ? 2 : 1;
+                const int at = wide ? (u & 7) >> 1 : (u & (BU - 1)) * SETS;
+                const uint32_t pick = UU * SETS > 1 && !wide ? 0x3210u : at & 1 ? 0x3232u : 0x1010u;
+                uint32_t sv[TT][2][W];
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        float(&o)[4] = acc[t][nb];
-                        slots[(((st + warp) * TT + t) * NB + nb) * 32 + lane] =
-                            make_float4(o[0], o[1], o[2], o[3]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[i] = 0.f;
+                    for (int b = 0; b < 2; ++b) {
+                        lds<W>(sc + (uint32_t)(t * 512 + b * 128 + g * 16 + (at & ~1) * 2), sv[t][b]);
+                        if (UU * SETS < 4) sv[t][b][0] = prmt(sv[t][b][0], 0u, pick);
                     }
-                u = 0;
-                ++st;
-                sc0 += (uint32_t)(TT * 16) * sp;
-                if (TT == 2) sc1 = st * 2 + 1 < nt ? 16u * sp : 0u;
+#pragma unroll
+                for (int i = 0; i < UU; ++i) {
+                    uint32_t ra[TT][8], rb[TT][8];
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) {
+                        uint32_t w[S::NW];
+                        const uint32_t a = rd + (uint32_t)((t * UU + (S::SPLIT ? i : 0)) * CELL + (S::SPLIT ? 0 : i * UNIT));
+                        load_codes<BITS, G32>(a, w);
+                        decode<BITS, G32>(w, shift, ra[t]);
+                        load_codes<BITS, G32>(a + 8 * (S::SPLIT ? UNIT : UU * UNIT), w);
+                        decode<BITS, G32>(w, shift, rb[t]);
+                    }
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) {
+                        if (NB > 1 && nb * 8 >= ncols) continue;
+                        const uint4 x = lds16(xs[nb] + (uint32_t)(u + i) * 128u);
+                        const uint4 y = lds16(xs[nb] + (uint32_t)(u + i) * 128u + 64u);
+#pragma unroll
+                        for (int t = 0; t < TT; ++t) {
+                            float d[SETS][4];
+                            mma0(d[0], ra[t][0], rb[t][0], ra[t][1], rb[t][1], x.x, x.y);
+                            mma(d[0], ra[t][2], rb[t][2], ra[t][3], rb[t][3], x.z, x.w);
+                            if constexpr (G32)
+                                mma0(d[SETS - 1], ra[t][4], rb[t][4], ra[t][5], rb[t][5], y.x, y.y);
+                            else
+                                mma(d[0], ra[t][4], rb[t][4], ra[t][5], rb[t][5], y.x, y.y);
+                            mma(d[SETS - 1], ra[t][6], rb[t][6], ra[t][7], rb[t][7], y.z, y.w);
+                            float(&o)[4] = acc[t][nb];
+#pragma unroll
+                            for (int h = 0; h < SETS; ++h) {
+                                const int z = i * SETS + h;
+                                auto half = [&](int b) {
+                                    const __half2 v = *reinterpret_cast<const __half2 *>(&sv[t][b][z / 2]);
+                                    return z & 1 ? __high2float(v) : __low2float(v);
+                                };
+                                const float sa = half(0), sb = half(1);
+                                o[0] = fmaf(sa, d[h][0], o[0]);
+                                o[1] = fmaf(sa, d[h][1], o[1]);
+                                o[2] = fmaf(sb, d[h][2], o[2]);
+                                o[3] = fmaf(sb, d[h][3], o[3]);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();  // the stage is read: it may be filled again
+                fetch();
+                rd += S::STAGE;
+                if (rd >= ring + STAGES * S::STAGE) rd -= STAGES * S::STAGE;
+            }
+            if (u0 + n >= U && (round < full || share == 1) && end > beg) {  // the group is whole
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    const int tile = from + group * TT + t;
+                    if (tile >= to) continue;
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int c = nb * 8 + 2 * q + j;
+                            if (c < ncols) write(tile, c, acc[t][nb][j], acc[t][nb][2 + j]);
+                        }
+                }
+                clear();
             }
         }
-        __syncthreads();
-        const bool done = u0 + n >= U;
-        if (!FLAT) {
-            if (!done) continue;
-#pragma unroll
-            for (int t = 0; t < TT; ++t)
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-                    slots[((warp * TT + t) * NB + nb) * 32 + lane] =
-                        make_float4(acc[t][nb][0], acc[t][nb][1], acc[t][nb][2], acc[t][nb][3]);
-            __syncthreads();
-        }
+    };
 
-        // the tiles' sums, in warp order; after the last chunk the results
-        for (int i = tid; i < nt * NB * 32; i += kThreads) {
-            const int tt = i / (NB * 32), s0 = tt / TT, nb = i / 32 % NB, ln = i & 31;
-            float4 s = !FLAT || u0 == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : total[i];
-            const int first = FLAT ? 0 : s0 * share, last = FLAT ? kWarps : first + share;
-            for (int w = first; w < last; ++w) {
-                if (!FLAT || max(ns * nq * w / kWarps, s0 * nq) < min(ns * nq * (w + 1) / kWarps, (s0 + 1) * nq)) {
-                    const float4 v = slots[(((FLAT ? s0 + w : w) * TT + tt % TT) * NB + nb) * 32 + ln];
-                    s.x += v.x;
-                    s.y += v.y;
-                    s.z += v.z;
-                    s.w += v.w;
-                }
-            }
-            if (!done) {
-                total[i] = s;
-                continue;
-            }
-            const int row = (ps.tile0 + tt) * ROWS + (ln >> 2);
-            const float part[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int c = nb * 8 + 2 * (ln & 3) + j;
-                if (c >= ps.ncols) continue;
-                const float a = part[j] * 16777216.f * sh.undo[c];
-                const float b = part[2 + j] * 16777216.f * sh.undo[c];
-                float *to = p.dst + (size_t)sh.list[c] * p.R + row;
-                if constexpr (PAIRS) {
-                    *to = a / (1.f + expf(-a)) * b;
-                } else {
-                    to[0] = a;
-                    to[8] = b;
-                }
-            }
-        }
+    clear();
+    for (int r0 = 0; r0 < rounds;) {
+        const int r1 = cu == U ? rounds : r0 + 1;
+        for (int u0 = 0; u0 < U; u0 += cu) stream(r0, r1, u0, U - u0 < cu ? U - u0 : cu);
+        r0 = r1;
     }
-    return FLAT && cu == U;
+    if (rest > 0 && share > 1) {
+        // the warps' parts of the shared tiles, added in order
+        __syncthreads();  // no copies are in flight, and the rings are read
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+                slots[((warp * TT + t) * NB + nb) * 32 + lane] =
+                    make_float4(acc[t][nb][0], acc[t][nb][1], acc[t][nb][2], acc[t][nb][3]);
+        __syncthreads();
+        for (int i = warp; i < rest * TT * NB; i += kWarps) {
+            const int grp = i / (TT * NB), t = i / NB % TT, nb = i % NB;
+            const int tile = from + (full * kWarps + grp) * TT + t;
+            if (tile >= to) continue;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = grp * share; w < (grp + 1) * share; ++w) {
+                const float4 v = slots[((w * TT + t) * NB + nb) * 32 + lane];
+                s.x += v.x;
+                s.y += v.y;
+                s.z += v.z;
+                s.w += v.w;
+            }
+            const int c = nb * 8 + 2 * q;
+            if (c < ncols) write(tile, c, s.x, s.z);
+            if (c + 1 < ncols) write(tile, c + 1, s.y, s.w);
+        }
+        __syncthreads();  // before the rings are filled again
+    }
 }
 
 // A kernel takes columns 8 NB at a time; which one is launched is a matter of
-// sizes alone (variant below).
-template <int BITS, bool G32, bool PAIRS, bool FLAT, int TT, int NB>
+// sizes alone (launch_sized below).
+template <int BITS, bool G32, bool PAIRS, int TT, int NB>
 __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant__ MoeParams p) {
+    using S = Kernel<BITS, G32, PAIRS, TT, NB>;
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ Shared sh;
     // The down grid reads ids and weights before it waits: this grid's
@@ -946,11 +942,11 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
         grid_dependency_wait();
         launch_dependents();
     }
-    // behind the rings: room for the passes, at the end the entries' experts
-    const int room = kRoom - ((p.T * p.top * 2 + 15) & ~15);
-    uint16_t *ids = reinterpret_cast<uint16_t *>(dyn + kWarps * kRing + room);
-    plan<8 * NB>(p, sh, ids);
-    const int per = p.R / (PAIRS ? 8 : 16);  // tiles of an expert
+    // behind the rings: the columns, at the end the entries' experts
+    const int room = S::ROOM - ((p.T * p.top * 2 + 15) & ~15);
+    uint16_t *ids = reinterpret_cast<uint16_t *>(dyn + kWarps * S::RING + room);
+    plan<S::C>(p, sh, ids);
+    const int per = p.R / S::ROWS;  // tiles of an expert
     // this CTA takes the tiles that start at costs lo .. hi - 1 (at most 2^30)
     const int all = sh.cost * per, G = (int)gridDim.x, each = all / G, rest = all - each * G;
     const int lo = each * (int)blockIdx.x + rest * (int)blockIdx.x / G;
@@ -960,36 +956,25 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
     for (int step = AQ_MOE_MAX_EXPERTS / 2; step > 0; step >>= 1)
         if (a + step < sh.busy && sh.before[a + step] * per <= lo) a += step;
     for (; a < sh.busy && sh.before[a] * per < hi; ++a) {
-        const int e = sh.act[a], count = sh.count[e], cost = tile_cost<8 * NB>(count);
+        const int e = sh.act[a], count = sh.count[e], cost = tile_cost<S::C>(count);
         const int start = sh.before[a] * per;
         const int from = lo > start ? (lo - start + cost - 1) / cost : 0;
         const int to = min((hi - start + cost - 1) / cost, per);
         if (from >= to) continue;
-        for (int col0 = 0; col0 < count; col0 += 8 * NB) {
-            list_entries<8 * NB>(p, e, col0, sh, ids);
-            Pass ps;
-            ps.e = e;
-            ps.ncols = count - col0 < 8 * NB ? count - col0 : 8 * NB;
-            bool staged = false;
-            for (ps.tile0 = from; ps.tile0 < to; ps.tile0 += ps.nt) {
-                ps.nt = to - ps.tile0 < kMaxTiles ? to - ps.tile0 : kMaxTiles;
-                // fewer tiles where 16 leave no room for chunks of 16 units
-                if (ps.nt > kMaxTiles / 2 &&
-                    chunk_units(FLAT, TT, kUnits<BITS>, NB, ps.nt, ps.ncols, p.group, p.K / 64, room) <
-                        (p.K < 1024 ? p.K / 64 : 16))
-                    ps.nt = kMaxTiles / 2;
-                staged = run_pass<BITS, G32, PAIRS, FLAT, TT, NB>(p, ps, sh, dyn, room, wait, staged);
-                wait = false;
-            }
+        for (int col0 = 0; col0 < count; col0 += S::C) {
+            list_entries<S::C>(p, e, col0, sh, ids);
+            run_tiles<S, BITS, G32, PAIRS>(p, e, from, to, count - col0 < S::C ? count - col0 : S::C, sh, dyn,
+                                           room, wait);
+            wait = false;
         }
     }
     if (wait) grid_dependency_wait();
 }
 
 // The grid: two CTAs an SM, each with an even run of tiles.
-template <int BITS, bool G32, bool PAIRS, bool FLAT, int TT, int NB>
+template <int BITS, bool G32, bool PAIRS, int TT, int NB>
 cudaError_t launch_one(const MoeParams &p, cudaStream_t stream) {
-    auto *kern = moe_kernel<BITS, G32, PAIRS, FLAT, TT, NB>;
+    auto *kern = moe_kernel<BITS, G32, PAIRS, TT, NB>;
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised, one bit each
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1010,13 +995,11 @@ cudaError_t launch_sized(const MoeParams &p, cudaStream_t stream) {
     const double picked = (double)p.T * p.top;
     const double busy = p.E * -std::expm1(p.T * std::log1p(-(double)(p.top < p.E ? p.top : p.E - 0.5) / p.E));
     const double tokens = picked / busy, tiles = busy * (p.R / (PAIRS ? 8 : 16)) / (2.0 * num_sms());
-    if (p.T <= 8 || tokens <= 2.0) {
-        if (tiles <= 3.0) return launch_one<BITS, G32, PAIRS, true, 1, 1>(p, stream);
-        if (tiles <= 8.0) return launch_one<BITS, G32, PAIRS, true, 2, 1>(p, stream);
-        return launch_one<BITS, G32, PAIRS, false, 2, 1>(p, stream);
-    }
-    if (p.T <= 16 || tokens <= 10.0) return launch_one<BITS, G32, PAIRS, false, 2, 2>(p, stream);
-    return launch_one<BITS, G32, PAIRS, false, 2, 4>(p, stream);
+    if (p.T <= 8 || tokens <= 2.0)
+        return tiles <= 4.0 ? launch_one<BITS, G32, PAIRS, 1, 1>(p, stream)
+                            : launch_one<BITS, G32, PAIRS, 2, 1>(p, stream);
+    if (p.T <= 16 || tokens <= 10.0) return launch_one<BITS, G32, PAIRS, 2, 2>(p, stream);
+    return launch_one<BITS, G32, PAIRS, BITS == 5 ? 1 : 2, 4>(p, stream);  // (room for 32 columns)
 }
 
 template <int BITS>
