@@ -48,7 +48,6 @@ namespace moe_detail {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kDynamic = 109568;     // dynamic shared memory: two CTAs an SM
 constexpr uint16_t kNone = 0xFFFF;
 constexpr int kMaxEntries = AQ_MOE_MAX_TOKENS * AQ_MOE_MAX_TOP;
 
@@ -309,7 +308,8 @@ struct Shared {
     int warp_sum[kWarps];
     int busy, cost;
 };
-static_assert(2 * (kDynamic + sizeof(Shared) + 1024) <= 228 * 1024, "two CTAs an SM");
+// Dynamic shared memory of a CTA, n of them an SM.
+constexpr int dynamic_bytes(int n) { return (228 * 1024 / n - 1024 - (int)sizeof(Shared)) & ~127; }
 
 // What a tile of an expert with n entries costs, in columns' products: the
 // codes are decoded once for every C columns, as much work as about four
@@ -575,12 +575,15 @@ struct Kernel {
     static constexpr int ROWS = PAIRS ? 8 : 16;  // rows of a matrix in a tile
     static constexpr int UNIT = 8 * BITS;        // bytes of a unit's row
     static constexpr int CELL = 16 * UNIT, STAGE = TT * UU * CELL;
-    // steps in flight, two at least; a block of scales for each and the one at work
-    static constexpr int STAGES = TT == 1 || (STAGE <= 1536 && NB < 4) ? 3 : 2, BLOCKS = STAGES + 1;
+    // steps in flight, and a block of scales for each
+    static constexpr int STAGES = STAGE <= 1024 ? 3 : 2, BLOCKS = STAGES;
     static constexpr int BLOCK = TT * 512;  // bytes: 16 scales and biases of 8 groups a tile
     static constexpr int RING = STAGES * STAGE + BLOCKS * BLOCK;  // a warp's
     static constexpr bool SPLIT = BITS % 2 == 0;  // units apart in shared memory, else rows whole
-    static constexpr int ROOM = kDynamic - kWarps * RING;  // for columns, less the entries' experts
+    // CTAs an SM: what registers and shared memory allow
+    static constexpr int CTAS = NB > 1 || BITS == 5 ? 2 : 3;
+    static constexpr int DYNAMIC = dynamic_bytes(CTAS);
+    static constexpr int ROOM = DYNAMIC - kWarps * RING;  // for columns, less the entries' experts
     // 8 units of all columns fit beside the most entries, and the partial
     // sums of shared tiles where the rings were
     static_assert(layout_bytes<UU, BU>(C, 8) <= ROOM - 2 * kMaxEntries && TT * NB * 512 <= RING, "room");
@@ -595,7 +598,9 @@ template <class S, int BITS, bool G32, bool PAIRS>
 __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, int to, int ncols, Shared &sh,
                                           uint8_t *dyn, int room, bool wait) {
     constexpr int TT = S::TT, NB = S::NB, UU = S::UU, BU = S::BU, SETS = S::SETS, STAGES = S::STAGES;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, q = lane & 3;
+    // (the shuffle tells the compiler that a warp's lanes agree on it)
+    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
     const int U = p.K / 64, groups = p.K / p.group;
     const bool wide = p.group == 128;
 
@@ -932,7 +937,7 @@ __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, i
 // A kernel takes columns 8 NB at a time; which one is launched is a matter of
 // sizes alone (launch_sized below).
 template <int BITS, bool G32, bool PAIRS, int TT, int NB>
-__global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant__ MoeParams p) {
+__global__ void __launch_bounds__(kThreads, Kernel<BITS, G32, PAIRS, TT, NB>::CTAS) moe_kernel(const __grid_constant__ MoeParams p) {
     using S = Kernel<BITS, G32, PAIRS, TT, NB>;
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ Shared sh;
@@ -971,9 +976,10 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const __grid_constant_
     if (wait) grid_dependency_wait();
 }
 
-// The grid: two CTAs an SM, each with an even run of tiles.
+// The grid: every SM full, each CTA with an even run of tiles.
 template <int BITS, bool G32, bool PAIRS, int TT, int NB>
 cudaError_t launch_one(const MoeParams &p, cudaStream_t stream) {
+    using S = Kernel<BITS, G32, PAIRS, TT, NB>;
     auto *kern = moe_kernel<BITS, G32, PAIRS, TT, NB>;
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised, one bit each
     int dev = 0;
@@ -981,11 +987,11 @@ cudaError_t launch_one(const MoeParams &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynamic);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::DYNAMIC);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    return moe_launch(kern, dim3(2u * (unsigned)num_sms()), kThreads, kDynamic, 1, stream, p);
+    return moe_launch(kern, dim3((unsigned)(S::CTAS * num_sms())), kThreads, S::DYNAMIC, 1, stream, p);
 }
 
 // Which kernel: by the tokens a busy expert has on average and the tiles a CTA
@@ -994,7 +1000,7 @@ template <int BITS, bool G32, bool PAIRS>
 cudaError_t launch_sized(const MoeParams &p, cudaStream_t stream) {
     const double picked = (double)p.T * p.top;
     const double busy = p.E * -std::expm1(p.T * std::log1p(-(double)(p.top < p.E ? p.top : p.E - 0.5) / p.E));
-    const double tokens = picked / busy, tiles = busy * (p.R / (PAIRS ? 8 : 16)) / (2.0 * num_sms());
+    const double tokens = picked / busy, tiles = busy * (p.R / (PAIRS ? 8 : 16)) / (3.0 * num_sms());
     if (p.T <= 8 || tokens <= 2.0)
         return tiles <= 4.0 ? launch_one<BITS, G32, PAIRS, 1, 1>(p, stream)
                             : launch_one<BITS, G32, PAIRS, 2, 1>(p, stream);
