@@ -28,7 +28,6 @@ namespace {
 constexpr int kCluster = 8;
 constexpr int kWarps = 8;
 constexpr int kThreads = 256;
-constexpr int kLanes = AQ_MOE_MAX_EXPERTS / 32;  // experts a lane chooses from
 
 struct RouteParams {
     const uint16_t *x, *w;
@@ -72,13 +71,25 @@ __device__ __forceinline__ void two_sum(float &s, float &e, float v) {
     s = t;
 }
 
-// One logit to about 2^-46 of its sum of magnitudes, in every lane.
+// One logit to about 2^-46 of its sum of magnitudes, in every lane.  Four sums
+// a lane, so that the additions of one do not wait for another's.
 template <bool BF16>
-__device__ double precise_logit(const uint16_t *x, const uint16_t *w, int K) {
+__device__ __noinline__ double precise_logit(const uint16_t *x, const uint16_t *w, int K) {
     const int lane = threadIdx.x & 31;
-    float s = 0.f, e = 0.f;
-    for (int k = lane; k < K; k += 32) two_sum(s, e, __fmul_rn(value<BF16>(x[k]), value<BF16>(w[k])));
-    double d = (double)s + (double)e;
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int k = lane * 8; k < K; k += 256) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(x + k), b = *reinterpret_cast<const uint4 *>(w + k);
+        const uint32_t xa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            two_sum(s[i], e[i], __fmul_rn(value<BF16>((uint16_t)xa[i]), value<BF16>((uint16_t)wb[i])));
+            two_sum(s[i], e[i], __fmul_rn(value<BF16>((uint16_t)(xa[i] >> 16)), value<BF16>((uint16_t)(wb[i] >> 16))));
+        }
+    }
+    double d = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d += (double)s[i] + (double)e[i];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
     return d;
@@ -91,14 +102,14 @@ __device__ __forceinline__ uint32_t ordered(float v) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// The choice for token t by one warp.  parts: [slices][2][E], sums and sums of
+// The choice for token t by one warp, of up to 32 LANES experts.  parts: [slices][2][E], sums and sums of
 // magnitudes; keep: E doubles for values summed again.
-template <bool BF16>
+template <bool BF16, int LANES>
 __device__ void choose(const RouteParams &p, int t, const float *parts, double *keep) {
     const int lane = threadIdx.x & 31;
     const int per = (p.E + 31) / 32;
     const bool sigmoid = p.score == AQ_SCORE_SIGMOID;
-    float logit[kLanes], val[kLanes];
+    float logit[LANES], val[LANES];
     float slack = 0.f;      // the largest error bound of a value
     uint32_t open = 0u;     // experts not yet taken, by position
     // a slice's warp adds K / (16 * slices * 8) products of 16 and then 8 warps
@@ -106,7 +117,7 @@ __device__ void choose(const RouteParams &p, int t, const float *parts, double *
     // of the partial sum at most
     const float ulps = (float)(p.K / (16 * kWarps * p.slices) + 2 + kWarps + p.slices) * 2.384185791015625e-07f;
 #pragma unroll
-    for (int j = 0; j < kLanes; ++j) {
+    for (int j = 0; j < LANES; ++j) {
         logit[j] = val[j] = -INFINITY;
         const int e = j * 32 + lane;
         if (j < per && e < p.E) {
@@ -136,7 +147,7 @@ __device__ void choose(const RouteParams &p, int t, const float *parts, double *
         uint32_t best = 0u;
         int at = 0x7FFFFFFF;
 #pragma unroll
-        for (int j = 0; j < kLanes; ++j) {
+        for (int j = 0; j < LANES; ++j) {
             const uint32_t o = ordered(val[j]);
             if ((left >> j & 1u) && (at == 0x7FFFFFFF || o > best)) {
                 best = o;
@@ -154,7 +165,7 @@ __device__ void choose(const RouteParams &p, int t, const float *parts, double *
     // the k-th largest exact value lies within slack of the border
     uint32_t sure = 0u, doubt = 0u;
 #pragma unroll
-    for (int j = 0; j < kLanes; ++j) {
+    for (int j = 0; j < LANES; ++j) {
         if (!(open >> j & 1u)) continue;
         if (val[j] > border + 2.f * slack)
             sure |= 1u << j;
@@ -204,7 +215,7 @@ __device__ void choose(const RouteParams &p, int t, const float *parts, double *
     // exp(-min(m, 0)), so that a sum of tiny ones does not vanish
     float m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kLanes; ++j)
+    for (int j = 0; j < LANES; ++j)
         if ((sigmoid || p.normalize ? taken : open) >> j & 1u) m = fmaxf(m, logit[j]);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -212,7 +223,7 @@ __device__ void choose(const RouteParams &p, int t, const float *parts, double *
     float sum = 0.f;
     const uint32_t over = p.normalize ? taken : open;
 #pragma unroll
-    for (int j = 0; j < kLanes; ++j) {
+    for (int j = 0; j < LANES; ++j) {
         // sigmoid: exp(-m) / (1 + exp(-l)), for l < 0 as exp(l - m) / (1 + exp(l))
         const float l = logit[j];
         val[j] = !sigmoid ? expf(l - m)
@@ -225,7 +236,7 @@ __device__ void choose(const RouteParams &p, int t, const float *parts, double *
     if (sigmoid && !p.normalize) sum = 1.f;
     int before = 0;
 #pragma unroll
-    for (int j = 0; j < kLanes; ++j) {
+    for (int j = 0; j < LANES; ++j) {
         const uint32_t on = __ballot_sync(0xFFFFFFFFu, taken >> j & 1u);
         if (taken >> j & 1u) {
             const size_t at = (size_t)t * p.top + before + __popc(on & ((1u << lane) - 1u));
@@ -236,7 +247,7 @@ __device__ void choose(const RouteParams &p, int t, const float *parts, double *
     }
 }
 
-template <bool BF16, int NB>
+template <bool BF16, int NB, int LANES>
 __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteParams p) {
     constexpr int TOKENS = 8 * NB, MINE = TOKENS / kCluster;  // a CTA chooses for MINE tokens
     extern __shared__ __align__(16) uint8_t dyn[];
@@ -316,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
     cluster_sync();
     if (warp < MINE) {
         const int t = t0 + warp * kCluster + rank;
-        if (t < p.T) choose<BF16>(p, t, parts + (size_t)warp * p.slices * 2 * p.E, keep + (size_t)warp * p.E);
+        if (t < p.T) choose<BF16, LANES>(p, t, parts + (size_t)warp * p.slices * 2 * p.E, keep + (size_t)warp * p.E);
     }
 }
 
@@ -358,20 +369,28 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
     reinterpret_cast<uint2 *>(p.out)[i] = o;
 }
 
-template <bool BF16, int NB>
+template <bool BF16, int NB, int LANES>
 cudaError_t route_run(const RouteParams &p, cudaStream_t stream) {
     const int mine = 8 * NB / kCluster;
     const size_t smem = (size_t)kWarps * NB * 2 * 32 * 16 +
                         (((size_t)mine * p.slices * 2 * p.E * 4 + 15) & ~(size_t)15) +
                         (size_t)mine * p.E * 8;
     const unsigned blocks = (unsigned)((p.T + 8 * NB - 1) / (8 * NB)) * kCluster;
-    auto *kern = route_kernel<BF16, NB>;
+    auto *kern = route_kernel<BF16, NB, LANES>;
     if (smem > 48 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
     return moe_launch(kern, dim3(blocks), kThreads, smem, kCluster, stream, p);
+}
+
+// 8 tokens a cluster while the clusters fit on the device, else 32.
+template <bool BF16>
+cudaError_t route_sized(const RouteParams &p, cudaStream_t stream) {
+    if (p.T > 64)
+        return p.E <= 128 ? route_run<BF16, 4, 4>(p, stream) : route_run<BF16, 4, 16>(p, stream);
+    return p.E <= 128 ? route_run<BF16, 1, 4>(p, stream) : route_run<BF16, 1, 16>(p, stream);
 }
 
 }  // namespace
@@ -395,8 +414,7 @@ cudaError_t moe_route_launch(const RouteArgs &a) {
     while (p.tiles < kCluster && p.tiles * 16 < p.E) p.tiles *= 2;
     p.slices = kCluster / p.tiles;
     const bool bf16 = r.dtype == AQ_BF16;
-    if (a.T > 64) return bf16 ? route_run<true, 4>(p, a.stream) : route_run<false, 4>(p, a.stream);
-    return bf16 ? route_run<true, 1>(p, a.stream) : route_run<false, 1>(p, a.stream);
+    return bf16 ? route_sized<true>(p, a.stream) : route_sized<false>(p, a.stream);
 }
 
 namespace {

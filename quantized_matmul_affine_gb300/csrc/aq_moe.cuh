@@ -360,6 +360,28 @@ __device__ __forceinline__ void plan(const MoeParams &p, Shared &sh, uint16_t *i
     __syncthreads();
 }
 
+// The same for at most 32 entries, in registers of every warp (an entry a
+// lane) and without a barrier: the lanes that share the lane's expert, and,
+// in the lowest of those, the cost before it; returned is the whole cost.
+template <int C>
+__device__ __forceinline__ int plan_few(const MoeParams &p, int &e, uint32_t &same, int &before) {
+    const int lane = threadIdx.x & 31, n = p.T * p.top;
+    e = lane < n ? __ldcg(p.ids + lane) : -1;
+    if (e >= p.E) e = -1;
+    same = __match_any_sync(0xFFFFFFFFu, e);
+    const bool first = e >= 0 && (same & ((1u << lane) - 1u)) == 0;
+    const int cost = first ? tile_cost<C>(__popc(same)) : 0;
+    int sum = 0;
+    before = 0;
+    for (int i = 0; i < n; ++i) {
+        const int ei = __shfl_sync(0xFFFFFFFFu, e, i), ci = __shfl_sync(0xFFFFFFFFu, cost, i);
+        sum += ci;
+        before += ei < e ? ci : 0;
+    }
+    if (!first) before = -1;
+    return sum;
+}
+
 // Entries first .. first + MOST - 1 of expert e, in order.
 template <int MOST>
 __device__ __forceinline__ void list_entries(const MoeParams &p, int e, int first, Shared &sh,
@@ -567,7 +589,7 @@ __device__ __forceinline__ void stage_columns(const MoeParams &p, int ncols, Sha
 
 // The sizes of a kernel.  TT tiles side by side share the activations that a
 // step of UU units reads from shared memory; 8 NB columns.
-template <int BITS, bool G32, bool PAIRS, int TT_, int NB_>
+template <int BITS, bool G32, bool PAIRS, int TT_, int NB_, int CTAS_>
 struct Kernel {
     static constexpr int TT = TT_, NB = NB_, C = 8 * NB, UU = kUnits<BITS>, NW = kWords<BITS, G32>;
     static constexpr int SETS = G32 ? 2 : 1;     // groups of a unit whose sums are kept apart
@@ -580,8 +602,7 @@ struct Kernel {
     static constexpr int BLOCK = TT * 512;  // bytes: 16 scales and biases of 8 groups a tile
     static constexpr int RING = STAGES * STAGE + BLOCKS * BLOCK;  // a warp's
     static constexpr bool SPLIT = BITS % 2 == 0;  // units apart in shared memory, else rows whole
-    // CTAs an SM: what registers and shared memory allow
-    static constexpr int CTAS = NB > 1 || BITS == 5 ? 2 : 3;
+    static constexpr int CTAS = BITS == 5 && CTAS_ == 3 ? 2 : CTAS_;  // an SM
     static constexpr int DYNAMIC = dynamic_bytes(CTAS);
     static constexpr int ROOM = DYNAMIC - kWarps * RING;  // for columns, less the entries' experts
     // 8 units of all columns fit beside the most entries, and the partial
@@ -936,9 +957,9 @@ __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, i
 
 // A kernel takes columns 8 NB at a time; which one is launched is a matter of
 // sizes alone (launch_sized below).
-template <int BITS, bool G32, bool PAIRS, int TT, int NB>
-__global__ void __launch_bounds__(kThreads, Kernel<BITS, G32, PAIRS, TT, NB>::CTAS) moe_kernel(const __grid_constant__ MoeParams p) {
-    using S = Kernel<BITS, G32, PAIRS, TT, NB>;
+template <int BITS, bool G32, bool PAIRS, int TT, int NB, int CTAS>
+__global__ void __launch_bounds__(kThreads, Kernel<BITS, G32, PAIRS, TT, NB, CTAS>::CTAS) moe_kernel(const __grid_constant__ MoeParams p) {
+    using S = Kernel<BITS, G32, PAIRS, TT, NB, CTAS>;
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ Shared sh;
     // The down grid reads ids and weights before it waits: this grid's
@@ -950,24 +971,62 @@ __global__ void __launch_bounds__(kThreads, Kernel<BITS, G32, PAIRS, TT, NB>::CT
     // behind the rings: the columns, at the end the entries' experts
     const int room = S::ROOM - ((p.T * p.top * 2 + 15) & ~15);
     uint16_t *ids = reinterpret_cast<uint16_t *>(dyn + kWarps * S::RING + room);
-    plan<S::C>(p, sh, ids);
+    const bool few = p.T * p.top <= 32;
+    int mine = -1, mine_before = -1;
+    uint32_t same = 0u;
+    int cost_all;
+    if (few) {
+        cost_all = plan_few<S::C>(p, mine, same, mine_before);
+    } else {
+        plan<S::C>(p, sh, ids);
+        cost_all = sh.cost;
+    }
     const int per = p.R / S::ROWS;  // tiles of an expert
     // this CTA takes the tiles that start at costs lo .. hi - 1 (at most 2^30)
-    const int all = sh.cost * per, G = (int)gridDim.x, each = all / G, rest = all - each * G;
+    const int all = cost_all * per, G = (int)gridDim.x, each = all / G, rest = all - each * G;
     const int lo = each * (int)blockIdx.x + rest * (int)blockIdx.x / G;
     const int hi = each * ((int)blockIdx.x + 1) + rest * ((int)blockIdx.x + 1) / G;
     bool wait = !PAIRS;
-    int a = 0;  // the last busy expert that starts at or before lo
-    for (int step = AQ_MOE_MAX_EXPERTS / 2; step > 0; step >>= 1)
-        if (a + step < sh.busy && sh.before[a + step] * per <= lo) a += step;
-    for (; a < sh.busy && sh.before[a] * per < hi; ++a) {
-        const int e = sh.act[a], count = sh.count[e], cost = tile_cost<S::C>(count);
-        const int start = sh.before[a] * per;
+    uint32_t mask = 0u;  // few: the lanes whose expert has tiles here
+    int a = 0;           // else: the last busy expert that starts at or before lo
+    if (few) {
+        const int b = mine_before * per;
+        mask = __ballot_sync(0xFFFFFFFFu, mine_before >= 0 && b < hi && b + tile_cost<S::C>(__popc(same)) * per > lo);
+    } else {
+        for (int step = AQ_MOE_MAX_EXPERTS / 2; step > 0; step >>= 1)
+            if (a + step < sh.busy && sh.before[a + step] * per <= lo) a += step;
+    }
+    bool again = false;
+    for (;;) {
+        int e, count, start;
+        uint32_t entries = 0u;
+        if (few) {
+            if (mask == 0u) break;
+            const int i = __ffs(mask) - 1;
+            mask &= mask - 1u;
+            e = __shfl_sync(0xFFFFFFFFu, mine, i);
+            entries = __shfl_sync(0xFFFFFFFFu, same, i);
+            count = __popc(entries);
+            start = __shfl_sync(0xFFFFFFFFu, mine_before, i) * per;
+        } else {
+            if (a >= sh.busy || sh.before[a] * per >= hi) break;
+            e = sh.act[a];
+            count = sh.count[e];
+            start = sh.before[a++] * per;
+        }
+        const int cost = tile_cost<S::C>(count);
         const int from = lo > start ? (lo - start + cost - 1) / cost : 0;
         const int to = min((hi - start + cost - 1) / cost, per);
         if (from >= to) continue;
         for (int col0 = 0; col0 < count; col0 += S::C) {
-            list_entries<S::C>(p, e, col0, sh, ids);
+            if (few) {
+                if (again) __syncthreads();  // the last list's readers are done
+                again = true;
+                const int lane = threadIdx.x & 31, at = __popc(entries & ((1u << lane) - 1u)) - col0;
+                if (threadIdx.x < 32 && (entries >> lane & 1u) && at >= 0 && at < S::C) sh.list[at] = (uint16_t)lane;
+            } else {
+                list_entries<S::C>(p, e, col0, sh, ids);
+            }
             run_tiles<S, BITS, G32, PAIRS>(p, e, from, to, count - col0 < S::C ? count - col0 : S::C, sh, dyn,
                                            room, wait);
             wait = false;
@@ -977,10 +1036,10 @@ __global__ void __launch_bounds__(kThreads, Kernel<BITS, G32, PAIRS, TT, NB>::CT
 }
 
 // The grid: every SM full, each CTA with an even run of tiles.
-template <int BITS, bool G32, bool PAIRS, int TT, int NB>
+template <int BITS, bool G32, bool PAIRS, int TT, int NB, int CTAS>
 cudaError_t launch_one(const MoeParams &p, cudaStream_t stream) {
-    using S = Kernel<BITS, G32, PAIRS, TT, NB>;
-    auto *kern = moe_kernel<BITS, G32, PAIRS, TT, NB>;
+    using S = Kernel<BITS, G32, PAIRS, TT, NB, CTAS>;
+    auto *kern = moe_kernel<BITS, G32, PAIRS, TT, NB, CTAS>;
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised, one bit each
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1001,11 +1060,16 @@ cudaError_t launch_sized(const MoeParams &p, cudaStream_t stream) {
     const double picked = (double)p.T * p.top;
     const double busy = p.E * -std::expm1(p.T * std::log1p(-(double)(p.top < p.E ? p.top : p.E - 0.5) / p.E));
     const double tokens = picked / busy, tiles = busy * (p.R / (PAIRS ? 8 : 16)) / (3.0 * num_sms());
-    if (p.T <= 8 || tokens <= 2.0)
-        return tiles <= 4.0 ? launch_one<BITS, G32, PAIRS, 1, 1>(p, stream)
-                            : launch_one<BITS, G32, PAIRS, 2, 1>(p, stream);
-    if (p.T <= 16 || tokens <= 10.0) return launch_one<BITS, G32, PAIRS, 2, 2>(p, stream);
-    return launch_one<BITS, G32, PAIRS, BITS == 5 ? 1 : 2, 4>(p, stream);  // (room for 32 columns)
+    if (p.T <= 8 || tokens <= 2.0) {
+        if (tiles <= 4.0) return launch_one<BITS, G32, PAIRS, 1, 1, 3>(p, stream);
+        // three CTAs an SM, but two with more room each where the columns of
+        // a long K would not stay
+        using S = Kernel<BITS, G32, PAIRS, 2, 1, 3>;
+        if ((tokens + 1.0) * p.K * 2.1 <= S::ROOM) return launch_one<BITS, G32, PAIRS, 2, 1, 3>(p, stream);
+        return launch_one<BITS, G32, PAIRS, 2, 1, 2>(p, stream);
+    }
+    if (p.T <= 16 || tokens <= 10.0) return launch_one<BITS, G32, PAIRS, 2, 2, 2>(p, stream);
+    return launch_one<BITS, G32, PAIRS, BITS == 5 ? 1 : 2, 4, 2>(p, stream);  // (room for 32 columns)
 }
 
 template <int BITS>
