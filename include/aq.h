@@ -632,8 +632,8 @@ aq_status aq_moe(const aq_router *router, const aq_experts *experts, const void 
  *   Wq_dev      uint32 [N][K*bits/32]; scales_dev, biases_dev fp16
  *               [N][K/group_size].
  *   out_dev     [T][K], 16-byte aligned, written entirely.
- * Any N >= 1, T >= 0 (0 queues nothing) and K a multiple of 32 and of
- * group_size, T * K / 8 up to 2^38.
+ * Any N >= 1, T >= 0 (0 queues nothing), both up to 2^31, and K a multiple of
+ * 32 and of group_size, up to 2^24.
  * Errors: AQ_ERR_INVALID_ARG for bad sizes, widths, group or index sizes, a
  * scale that is not finite or NULL pointers; AQ_ERR_UNSUPPORTED past the
  * limits; AQ_ERR_MISALIGNED; AQ_ERR_CUDA.

@@ -725,7 +725,7 @@ aq_status aq_embed(int dtype, const void *ids_dev, int index_bytes, int64_t T,
         return AQ_ERR_INVALID_ARG;
     if (T == 0) return AQ_OK;
     if (!ids_dev || !Wq_dev || !scales_dev || !biases_dev || !out_dev) return AQ_ERR_INVALID_ARG;
-    if (K > (int64_t)1 << 26 || N > (int64_t)1 << 31 || T > ((int64_t)1 << 38) / (K / 8))
+    if (K > (int64_t)1 << 24 || N > (int64_t)1 << 31 || T > (int64_t)1 << 31)
         return AQ_ERR_UNSUPPORTED;
     if (!aligned(ids_dev, (uintptr_t)index_bytes) || !aligned(Wq_dev, 4) || !aligned(scales_dev, 2) ||
         !aligned(biases_dev, 2) || !aligned(out_dev, 16))

@@ -24,46 +24,76 @@ struct EmbedParams {
     float scale;
 };
 
+// 8 values of a row: the words of their codes, their scale and bias.
+struct Piece {
+    uint32_t w0, w1;
+    __half s, b;
+    bool live;
+};
+
 template <int B>
-__global__ void __launch_bounds__(256) embed_kernel(const __grid_constant__ EmbedParams p) {
-    const int per = p.K / 8;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t t = i / per;
-    if (t >= p.T) return;
-    const int c = (int)(i - t * per);
-    const int64_t id = p.wide ? static_cast<const int64_t *>(p.ids)[t]
-                              : (int64_t) static_cast<const int32_t *>(p.ids)[t];
-    if (id < 0 || id >= p.N) {
-        p.out[i] = make_uint4(0u, 0u, 0u, 0u);
-        return;
+__device__ __forceinline__ Piece load_piece(const EmbedParams &p, int64_t id, int c) {
+    Piece v = {0u, 0u, __half(0.f), __half(0.f), id >= 0 && id < p.N};
+    if (v.live) {
+        const int first = c * B / 4, sh = (c * B * 8) & 31;
+        const uint32_t *row = p.words + id * (p.K * B / 32);
+        v.w0 = row[first];
+        if (sh + 8 * B > 32) v.w1 = row[first + 1];
+        const int64_t at = id * (p.K / p.group) + c * 8 / p.group;
+        v.s = p.scales[at];
+        v.b = p.biases[at];
     }
-    const int row_words = p.K * B / 32, first = c * B / 4, sh = (c * B * 8) & 31;
-    const uint32_t *row = p.words + id * row_words;
-    const uint32_t w0 = row[first];
-    const uint32_t w1 = sh + 8 * B > 32 ? row[first + 1] : 0u;
-    const uint64_t codes = ((uint64_t)w1 << 32 | w0) >> sh;
-    const int64_t at = id * (p.K / p.group) + c * 8 / p.group;
-    const float s = __half2float(p.scales[at]), b = __half2float(p.biases[at]);
+    return v;
+}
+
+template <int B>
+__device__ __forceinline__ uint4 decode_piece(const EmbedParams &p, const Piece &v, int c) {
+    if (!v.live) return make_uint4(0u, 0u, 0u, 0u);
+    const uint64_t codes = ((uint64_t)v.w1 << 32 | v.w0) >> ((c * B * 8) & 31);
+    const float s = __half2float(v.s), b = __half2float(v.b);
     uint32_t o[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float lo = fmaf(s, (float)((uint32_t)(codes >> (2 * j * B)) & ((1u << B) - 1u)), b) * p.scale;
         const float hi = fmaf(s, (float)((uint32_t)(codes >> ((2 * j + 1) * B)) & ((1u << B) - 1u)), b) * p.scale;
         if (p.bf16) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-            o[j] = *reinterpret_cast<const uint32_t *>(&v);
+            const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+            o[j] = *reinterpret_cast<const uint32_t *>(&x);
         } else {
-            const __half2 v = __floats2half2_rn(lo, hi);
-            o[j] = *reinterpret_cast<const uint32_t *>(&v);
+            const __half2 x = __floats2half2_rn(lo, hi);
+            o[j] = *reinterpret_cast<const uint32_t *>(&x);
         }
     }
-    p.out[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// A block takes kRows tokens and a stretch of 8 * 256 columns: a thread has a
+// piece of each token's row in flight at once.
+constexpr int kRows = 4;
+template <int B>
+__global__ void __launch_bounds__(256) embed_kernel(const __grid_constant__ EmbedParams p) {
+    const int per = p.K / 8;
+    const int c = (int)blockIdx.y * 256 + (int)threadIdx.x;
+    if (c >= per) return;
+    const int64_t t0 = (int64_t)blockIdx.x * kRows;
+    Piece v[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+        int64_t id = -1;
+        if (t0 + r < p.T)
+            id = p.wide ? static_cast<const int64_t *>(p.ids)[t0 + r]
+                        : (int64_t) static_cast<const int32_t *>(p.ids)[t0 + r];
+        v[r] = load_piece<B>(p, id, c);
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+        if (t0 + r < p.T) p.out[(t0 + r) * per + c] = decode_piece<B>(p, v[r], c);
 }
 
 template <int B>
 cudaError_t run(const EmbedParams &p, cudaStream_t stream) {
-    const int64_t blocks = (p.T * (p.K / 8) + 255) / 256;
-    embed_kernel<B><<<(unsigned)blocks, 256, 0, stream>>>(p);
+    const dim3 grid((unsigned)((p.T + kRows - 1) / kRows), (unsigned)((p.K / 8 + 255) / 256));
+    embed_kernel<B><<<grid, 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

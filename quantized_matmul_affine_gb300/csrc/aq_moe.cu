@@ -22,6 +22,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cmath>
+#include <initializer_list>
+
 namespace aq {
 namespace {
 
@@ -421,27 +424,71 @@ namespace {
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 }  // namespace
 
-// h [T * top][I] and the down products [T * top][K], fp32.
+// Which kernel runs a product of R rows (tiles of 8 pairs, or of 16 rows) and
+// K columns: by the tokens a busy expert has on average and the tiles a CTA
+// gets, were all experts picked alike.
+static int moe_variant(const aq_experts *x, int64_t T, int top, int64_t tiles, int64_t K) {
+    const double E = (double)x->E;
+    const double busy = top >= E ? E : E * (1.0 - std::pow(1.0 - top / E, (double)T));
+    const double tokens = (double)T * top / busy;
+    if (T <= 8 || tokens <= 2.0) {
+        if (busy * (double)tiles <= 4.0 * 3.0 * num_sms()) return MOE_FEW;
+        // three CTAs an SM, but two with more room each, and packed rows, where
+        // the columns of a long K would not stay
+        return (tokens + 1.0) * (double)K * 2.1 <= 20480.0 ? MOE_8 : MOE_8_LONG;
+    }
+    return T <= 16 || tokens <= 10.0 ? MOE_16 : MOE_32;
+}
+static int up_variant(const aq_experts *x, int64_t T, int top) {
+    return moe_variant(x, T, top, x->I / 8, x->K);
+}
+static int down_variant(const aq_experts *x, int64_t T, int top) {
+    return moe_variant(x, T, top, x->K / 16, x->I);
+}
+
+namespace {
+struct Workspace {
+    size_t h, parts, x, hp, bytes;  // offsets of h, the down products, the packed rows
+};
+Workspace workspace(const aq_experts *x, int64_t T, int top) {
+    Workspace w;
+    w.h = 0;
+    w.parts = round256((size_t)T * top * x->I * 4);
+    w.x = w.parts + round256((size_t)T * top * x->K * 4);
+    w.hp = w.x + (moe_packed(up_variant(x, T, top)) ? (size_t)moe_pack(T, x->K, x->group_size).bytes : 0);
+    w.bytes = w.hp + (moe_packed(down_variant(x, T, top)) ? (size_t)moe_pack(T * top, x->I, x->group_size).bytes : 0);
+    return w;
+}
+}  // namespace
+
+// h [T * top][I] and the down products [T * top][K], fp32, and packed rows.
 size_t moe_workspace_bytes(const aq_experts *x, int64_t T, int top_k) {
-    return round256((size_t)T * top_k * x->I * 4) + round256((size_t)T * top_k * x->K * 4);
+    return workspace(x, T, top_k).bytes;
 }
 
 cudaError_t moe_experts_launch(const ExpertsArgs &a) {
     const aq_experts &x = *a.experts;
-    float *h = static_cast<float *>(a.ws);
-    float *parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) +
-                                             round256((size_t)a.T * a.top_k * x.I * 4));
-    cudaError_t (*product)(const MoeParams &, bool, cudaStream_t) =
-        x.bits == 2   ? moe_product_b2
-        : x.bits == 3 ? moe_product_b3
-        : x.bits == 4 ? moe_product_b4
-        : x.bits == 5 ? moe_product_b5
-        : x.bits == 6 ? moe_product_b6
-                      : moe_product_b8;
+    const Workspace w = workspace(&x, a.T, a.top_k);
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    float *h = reinterpret_cast<float *>(ws), *parts = reinterpret_cast<float *>(ws + w.parts);
+    typedef cudaError_t (*Product)(const MoeParams &, bool, int, cudaStream_t);
+    typedef cudaError_t (*Pack)(const MoeParams &, bool, uint8_t *, cudaStream_t);
+    const int at = x.bits == 8 ? 5 : x.bits - 2;
+    const Product product = std::initializer_list<Product>{moe_product_b2, moe_product_b3, moe_product_b4,
+                                                           moe_product_b5, moe_product_b6, moe_product_b8}.begin()[at];
+    const Pack pack = std::initializer_list<Pack>{moe_pack_b2, moe_pack_b3, moe_pack_b4,
+                                                  moe_pack_b5, moe_pack_b6, moe_pack_b8}.begin()[at];
     MoeParams p = {x.gate_words_dev, x.up_words_dev, x.gate_scales_dev, x.up_scales_dev,
                    x.gate_biases_dev, x.up_biases_dev, a.ids, a.x, h, (int)a.T, a.top_k, (int)x.E,
-                   (int)x.I, (int)x.K, x.group_size, a.dtype};
-    cudaError_t e = product(p, true, a.stream);
+                   (int)x.I, (int)x.K, x.group_size, a.dtype, nullptr};
+    cudaError_t e;
+    int variant = up_variant(&x, a.T, a.top_k);
+    if (moe_packed(variant)) {
+        e = pack(p, true, ws + w.x, a.stream);
+        if (e != cudaSuccess) return e;
+        p.packed = ws + w.x;
+    }
+    e = product(p, true, variant, a.stream);
     if (e != cudaSuccess) return e;
     p.w0 = p.w1 = x.down_words_dev;
     p.s0 = p.s1 = x.down_scales_dev;
@@ -450,7 +497,14 @@ cudaError_t moe_experts_launch(const ExpertsArgs &a) {
     p.dst = parts;
     p.R = (int)x.K;
     p.K = (int)x.I;
-    e = product(p, false, a.stream);
+    p.packed = nullptr;
+    variant = down_variant(&x, a.T, a.top_k);
+    if (moe_packed(variant)) {
+        e = pack(p, false, ws + w.hp, a.stream);
+        if (e != cudaSuccess) return e;
+        p.packed = ws + w.hp;
+    }
+    e = product(p, false, variant, a.stream);
     if (e != cudaSuccess) return e;
     const CombineParams c = {a.ids, a.weights, parts, a.out, (int)a.T, a.top_k, (int)x.E, (int)x.K,
                              a.dtype};

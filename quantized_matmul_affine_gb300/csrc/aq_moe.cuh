@@ -40,7 +40,6 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
-#include <cmath>
 #include <type_traits>
 
 namespace aq {
@@ -587,6 +586,37 @@ __device__ __forceinline__ void stage_columns(const MoeParams &p, int ncols, Sha
         }
 }
 
+// The same from packed rows: plain copies, asynchronous but for what is zero.
+template <bool G32, bool PAIRS>
+__device__ __forceinline__ void copy_columns(const MoeParams &p, int ncols, Shared &sh, int u0, int n, int padded,
+                                             uint8_t *act, const Layout &l) {
+    constexpr int BU = G32 ? 4 : 8;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0);
+    const MoePack m = moe_pack(PAIRS ? p.T : (int64_t)p.T * p.top, p.K, p.group);
+    const int sums = (n + BU - 1) / BU;  // pieces of either part
+    // a column a warp, or its halves, quarters or eighths where there are fewer
+    const int parts = ncols > 4 ? 1 : ncols > 2 ? 2 : ncols == 2 ? 4 : 8, part = warp % parts;
+    for (int c = warp / parts; c < ncols; c += kWarps / parts) {
+        const int64_t row = PAIRS ? sh.list[c] / p.top : sh.list[c];
+        const uint8_t *from = p.packed + row * p.K * 2 + (int64_t)u0 * 128;
+        const uint32_t to = smem_u32(act) + (uint32_t)(c * l.pitch);
+        for (int k = part * 32 + lane; k < n * 8; k += parts * 32) copy_codes<16>(to + k * 16, from + k * 16, true);
+        if (part == 0) {
+            const uint8_t *sum = p.packed + m.sums + row * m.blocks * 32 + u0 / BU * 16;
+            const uint32_t to_sum = smem_u32(act) + (uint32_t)(l.sums + c * l.sum_pitch);
+            for (int k = lane; k < sums; k += 32) {
+                copy_codes<16>(to_sum + k * 16, sum + k * 16, true);
+                copy_codes<16>(to_sum + l.sum_lo + k * 16, sum + m.blocks * 16 + k * 16, true);
+            }
+            if (lane < (padded - n) * 8)
+                reinterpret_cast<uint4 *>(act + (size_t)c * l.pitch)[n * 8 + lane] = make_uint4(0u, 0u, 0u, 0u);
+            if (lane == 0) sh.undo[c] = __ldcg(reinterpret_cast<const float *>(p.packed + m.undo) + row);
+        }
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+}
+
 // The sizes of a kernel.  TT tiles side by side share the activations that a
 // step of UU units reads from shared memory; 8 NB columns.
 template <int BITS, bool G32, bool PAIRS, int TT_, int NB_, int CTAS_>
@@ -601,6 +631,7 @@ struct Kernel {
     static constexpr int STAGES = STAGE <= 1024 ? 3 : 2, BLOCKS = STAGES;
     static constexpr int BLOCK = TT * 512;  // bytes: 16 scales and biases of 8 groups a tile
     static constexpr int RING = STAGES * STAGE + BLOCKS * BLOCK;  // a warp's
+    static constexpr bool PACKED = NB > 1 || CTAS_ == 2;  // columns from packed rows
     static constexpr bool SPLIT = BITS % 2 == 0;  // units apart in shared memory, else rows whole
     static constexpr int CTAS = BITS == 5 && CTAS_ == 3 ? 2 : CTAS_;  // an SM
     static constexpr int DYNAMIC = dynamic_bytes(CTAS);
@@ -792,7 +823,10 @@ __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, i
         if (wait) grid_dependency_wait();
         wait = false;
         __syncthreads();  // the last columns' readers are done
-        stage_columns<BITS, G32, PAIRS>(p, ncols, sh, u0, n, nq * UU, act, l);
+        if constexpr (S::PACKED)
+            copy_columns<G32, PAIRS>(p, ncols, sh, u0, n, nq * UU, act, l);
+        else
+            stage_columns<BITS, G32, PAIRS>(p, ncols, sh, u0, n, nq * UU, act, l);
         __syncthreads();
 
         uint32_t xs[NB], ss[NB];
@@ -1053,32 +1087,69 @@ cudaError_t launch_one(const MoeParams &p, cudaStream_t stream) {
     return moe_launch(kern, dim3((unsigned)(S::CTAS * num_sms())), kThreads, S::DYNAMIC, 1, stream, p);
 }
 
-// Which kernel: by the tokens a busy expert has on average and the tiles a CTA
-// gets, were all experts picked alike.
+// The kernel that moe_variant names, with its pack.
 template <int BITS, bool G32, bool PAIRS>
-cudaError_t launch_sized(const MoeParams &p, cudaStream_t stream) {
-    const double picked = (double)p.T * p.top;
-    const double busy = p.E * -std::expm1(p.T * std::log1p(-(double)(p.top < p.E ? p.top : p.E - 0.5) / p.E));
-    const double tokens = picked / busy, tiles = busy * (p.R / (PAIRS ? 8 : 16)) / (3.0 * num_sms());
-    if (p.T <= 8 || tokens <= 2.0) {
-        if (tiles <= 4.0) return launch_one<BITS, G32, PAIRS, 1, 1, 3>(p, stream);
-        // three CTAs an SM, but two with more room each where the columns of
-        // a long K would not stay
-        using S = Kernel<BITS, G32, PAIRS, 2, 1, 3>;
-        if ((tokens + 1.0) * p.K * 2.1 <= S::ROOM) return launch_one<BITS, G32, PAIRS, 2, 1, 3>(p, stream);
-        return launch_one<BITS, G32, PAIRS, 2, 1, 2>(p, stream);
+cudaError_t launch_sized(const MoeParams &p, int variant, cudaStream_t stream) {
+    switch (variant) {
+        case MOE_FEW: return launch_one<BITS, G32, PAIRS, 1, 1, 3>(p, stream);
+        case MOE_8: return launch_one<BITS, G32, PAIRS, 2, 1, 3>(p, stream);
+        case MOE_8_LONG: return launch_one<BITS, G32, PAIRS, 2, 1, 2>(p, stream);
+        case MOE_16: return launch_one<BITS, G32, PAIRS, 2, 2, 2>(p, stream);
+        default:  // (room for 32 columns)
+            return launch_one<BITS, G32, PAIRS, BITS == 5 ? 1 : 2, 4, 2>(p, stream);
     }
-    if (p.T <= 16 || tokens <= 10.0) return launch_one<BITS, G32, PAIRS, 2, 2, 2>(p, stream);
-    return launch_one<BITS, G32, PAIRS, BITS == 5 ? 1 : 2, 4, 2>(p, stream);  // (room for 32 columns)
 }
 
 template <int BITS>
-cudaError_t launch(const MoeParams &p, bool pairs, cudaStream_t stream) {
+cudaError_t launch(const MoeParams &p, bool pairs, int variant, cudaStream_t stream) {
     if (p.group == 32)
-        return pairs ? launch_sized<BITS, true, true>(p, stream)
-                     : launch_sized<BITS, true, false>(p, stream);
-    return pairs ? launch_sized<BITS, false, true>(p, stream)
-                 : launch_sized<BITS, false, false>(p, stream);
+        return pairs ? launch_sized<BITS, true, true>(p, variant, stream)
+                     : launch_sized<BITS, true, false>(p, variant, stream);
+    return pairs ? launch_sized<BITS, false, true>(p, variant, stream)
+                 : launch_sized<BITS, false, false>(p, variant, stream);
+}
+
+// Packs a source row a CTA (moe_pack): what the products' CTAs would each do for
+// the rows they need, done once.
+constexpr int kPackUnits = 256;
+template <int BITS, bool G32, bool PAIRS>
+__global__ void __launch_bounds__(kThreads) pack_kernel(const __grid_constant__ MoeParams p, uint8_t *to) {
+    constexpr int UU = kUnits<BITS>, BU = G32 ? 4 : 8;
+    __shared__ Shared sh;
+    extern __shared__ __align__(16) uint8_t act[];
+    grid_dependency_wait();
+    launch_dependents();
+    const int tid = threadIdx.x, U = p.K / 64;
+    const int64_t row = blockIdx.x;
+    const MoePack m = moe_pack(PAIRS ? p.T : (int64_t)p.T * p.top, p.K, p.group);
+    if (tid == 0) sh.list[0] = (uint16_t)(PAIRS ? row * p.top : row);
+    __syncthreads();
+    for (int u0 = 0; u0 < U; u0 += kPackUnits) {
+        const int n = U - u0 < kPackUnits ? U - u0 : kPackUnits, sums = (n + BU - 1) / BU;
+        const Layout l = layout<UU, BU>(1, n);
+        stage_columns<BITS, G32, PAIRS>(p, 1, sh, u0, n, n, act, l);
+        __syncthreads();
+        uint4 *out = reinterpret_cast<uint4 *>(to + row * p.K * 2 + (int64_t)u0 * 128);
+        for (int k = tid; k < n * 8; k += kThreads) out[k] = reinterpret_cast<const uint4 *>(act)[k];
+        uint4 *sum = reinterpret_cast<uint4 *>(to + m.sums + row * m.blocks * 32) + u0 / BU;
+        for (int k = tid; k < 2 * sums; k += kThreads) {
+            const bool low = k >= sums;
+            const int at = low ? k - sums : k;
+            sum[(low ? m.blocks : 0) + at] = reinterpret_cast<const uint4 *>(act + l.sums + (low ? l.sum_lo : 0))[at];
+        }
+        __syncthreads();
+    }
+    if (tid == 0) reinterpret_cast<float *>(to + m.undo)[row] = sh.undo[0];
+}
+
+template <int BITS>
+cudaError_t pack(const MoeParams &p, bool pairs, uint8_t *to, cudaStream_t stream) {
+    void (*kern)(MoeParams, uint8_t *) =
+        p.group == 32 ? (pairs ? pack_kernel<BITS, true, true> : pack_kernel<BITS, true, false>)
+                      : (pairs ? pack_kernel<BITS, false, true> : pack_kernel<BITS, false, false>);
+    const int units = p.K / 64 < kPackUnits ? p.K / 64 : kPackUnits;
+    const int smem = p.group == 32 ? layout_bytes<kUnits<BITS>, 4>(1, units) : layout_bytes<kUnits<BITS>, 8>(1, units);
+    return moe_launch(kern, dim3((unsigned)(pairs ? p.T : p.T * p.top)), kThreads, (size_t)smem, 1, stream, p, to);
 }
 
 }  // namespace moe_detail

@@ -44,18 +44,55 @@ struct MoeParams {
     const void *src;
     float *dst;
     int T, top, E, R, K, group, dtype;
+    const uint8_t *packed;  // the source rows as the MMA wants them (MoePack), or null
 };
-cudaError_t moe_product_b2(const MoeParams &p, bool pairs, cudaStream_t stream);
-cudaError_t moe_product_b3(const MoeParams &p, bool pairs, cudaStream_t stream);
-cudaError_t moe_product_b4(const MoeParams &p, bool pairs, cudaStream_t stream);
-cudaError_t moe_product_b5(const MoeParams &p, bool pairs, cudaStream_t stream);
-cudaError_t moe_product_b6(const MoeParams &p, bool pairs, cudaStream_t stream);
-cudaError_t moe_product_b8(const MoeParams &p, bool pairs, cudaStream_t stream);
+// The products' kernels: columns (tokens of an expert) taken at a time, and
+// whether they come from packed rows.
+enum MoeVariant {
+    MOE_FEW = 0,  // 8, one tile a step
+    MOE_8 = 1,    // 8, two tiles a step, three CTAs an SM
+    MOE_8_LONG,   // 8, packed, two CTAs an SM with more room each
+    MOE_16,       // 16, packed
+    MOE_32,       // 32, packed
+};
+inline bool moe_packed(int variant) { return variant >= MOE_8_LONG; }
+
+// Packed source rows: [rows][K] fp16 in MMA order, then the group sums, 16 bytes
+// of either part a block of 8 groups (4 of 128 and zeros), then the inverse
+// powers of two, floats, each part 256-byte aligned.
+struct MoePack {
+    int64_t sums, undo, bytes;  // byte offsets, and the whole
+    int blocks;                 // a row's
+};
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline MoePack moe_pack(int64_t rows, int64_t K, int group) {
+    MoePack m;
+    m.blocks = (int)((K / (group == 32 ? 256 : 512)) + (K % (group == 32 ? 256 : 512) != 0));
+    m.sums = (rows * K * 2 + 255) & ~(int64_t)255;
+    m.undo = m.sums + ((rows * m.blocks * 32 + 255) & ~(int64_t)255);
+    m.bytes = m.undo + ((rows * 4 + 255) & ~(int64_t)255);
+    return m;
+}
+// Packs rows of p.src (PAIRS as above: x, T rows, or h, T * top) to `to`.
+cudaError_t moe_pack_b2(const MoeParams &p, bool pairs, uint8_t *to, cudaStream_t stream);
+cudaError_t moe_pack_b3(const MoeParams &p, bool pairs, uint8_t *to, cudaStream_t stream);
+cudaError_t moe_pack_b4(const MoeParams &p, bool pairs, uint8_t *to, cudaStream_t stream);
+cudaError_t moe_pack_b5(const MoeParams &p, bool pairs, uint8_t *to, cudaStream_t stream);
+cudaError_t moe_pack_b6(const MoeParams &p, bool pairs, uint8_t *to, cudaStream_t stream);
+cudaError_t moe_pack_b8(const MoeParams &p, bool pairs, uint8_t *to, cudaStream_t stream);
+cudaError_t moe_product_b2(const MoeParams &p, bool pairs, int variant, cudaStream_t stream);
+cudaError_t moe_product_b3(const MoeParams &p, bool pairs, int variant, cudaStream_t stream);
+cudaError_t moe_product_b4(const MoeParams &p, bool pairs, int variant, cudaStream_t stream);
+cudaError_t moe_product_b5(const MoeParams &p, bool pairs, int variant, cudaStream_t stream);
+cudaError_t moe_product_b6(const MoeParams &p, bool pairs, int variant, cudaStream_t stream);
+cudaError_t moe_product_b8(const MoeParams &p, bool pairs, int variant, cudaStream_t stream);
 
 // A launch whose grid may start while the stream's last one ends.
-template <class P>
-cudaError_t moe_launch(void (*kern)(P), dim3 grid, int threads, size_t smem, int cluster,
-                       cudaStream_t stream, const P &prm) {
+template <class... P, class... A>
+cudaError_t moe_launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, int cluster,
+                       cudaStream_t stream, A... prm) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
@@ -70,7 +107,7 @@ cudaError_t moe_launch(void (*kern)(P), dim3 grid, int threads, size_t smem, int
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, prm);
+    return cudaLaunchKernelEx(&cfg, kern, prm...);
 }
 
 }  // namespace aq

@@ -4,8 +4,12 @@
 
 namespace aq {
 
-cudaError_t moe_product_b6(const MoeParams &p, bool pairs, cudaStream_t stream) {
-    return moe_detail::launch<6>(p, pairs, stream);
+cudaError_t moe_product_b6(const MoeParams &p, bool pairs, int variant, cudaStream_t stream) {
+    return moe_detail::launch<6>(p, pairs, variant, stream);
+}
+
+cudaError_t moe_pack_b6(const MoeParams &p, bool pairs, uint8_t *to, cudaStream_t stream) {
+    return moe_detail::pack<6>(p, pairs, to, stream);
 }
 
 }  // namespace aq

@@ -161,7 +161,7 @@ def test_embed_refuses():
     for bad in (dict(ids=A + 2), dict(ids=A + 4, index=8), dict(Wq=A + 2), dict(s=A + 1), dict(b=A + 1),
                 dict(out=A + 8)):
         assert call(**bad) == 3, bad
-    for bad in (dict(N=(1 << 31) + 1), dict(K=1 << 27), dict(T=1 << 36)):
+    for bad in (dict(N=(1 << 31) + 1), dict(K=1 << 25), dict(T=(1 << 31) + 1)):
         assert call(**bad) == 2, bad
     assert call(T=0, ids=None, out=None) == 0
 
