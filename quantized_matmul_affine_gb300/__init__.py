@@ -465,7 +465,7 @@ def aq_cache_workspace_bytes(n_pages: int, B: int) -> int:
     return int(load().aq_cache_workspace_bytes(n_pages, B))
 
 
-_I32 = torch.int32
+_I32, _F32 = torch.int32, torch.float32
 
 
 def _ints(t: torch.Tensor, name: str, *shape) -> int:
@@ -711,7 +711,7 @@ class AqRouter:
     [E] or None (sigmoid scores only), score "softmax" or "sigmoid".  The
     tensors stay the caller's; this object holds them and is kept for a layer."""
 
-    __slots__ = ("weight", "bias", "top_k", "_struct", "_ref")
+    __slots__ = ("weight", "bias", "top_k", "_struct", "_ref", "_index", "_dtype", "_shape")
 
     def __init__(self, weight, top_k: int, bias=None, score: str = "softmax",
                  normalize: bool = True, scale: float = 1.0):
@@ -725,6 +725,7 @@ class AqRouter:
         if bias is not None and bias.device != weight.device:
             raise ValueError("bias must be on weight's device")
         self.weight, self.bias, self.top_k = weight, bias, top_k
+        self._index, self._dtype, self._shape = weight.get_device(), weight.dtype, (E, K)
         self._struct = _RouterStruct(_dev(weight, "weight"),
                                      None if bias is None else _dev(bias, "bias"), E, K,
                                      AQ_BF16 if weight.dtype == torch.bfloat16 else AQ_F16, top_k,
@@ -739,7 +740,7 @@ class AqExperts:
     stay the caller's; this object holds them and is kept for a layer."""
 
     __slots__ = ("gate", "up", "down", "bits", "group_size", "count", "hidden", "inner", "_struct",
-                 "_ref", "_workspaces")
+                 "_ref", "_workspaces", "_index")
 
     def __init__(self, gate, up, down, bits: int, group_size: int):
         if bits not in (2, 3, 4, 5, 6, 8) or group_size not in (32, 64, 128):
@@ -768,53 +769,73 @@ class AqExperts:
         self.gate, self.up, self.down = tuple(gate), tuple(up), tuple(down)
         self.bits, self.group_size = bits, group_size
         self.count, self.hidden, self.inner = E, hidden, inner
+        self._index = gate[0].get_device()
         self._struct = _ExpertsStruct(*(_dev(t, name) for t, name in parts), E, hidden, inner, bits, group_size)
         self._ref = ctypes.addressof(self._struct)
         self._workspaces = {}
 
 
-def _moe_tokens(x, K: int, device, dtype=None) -> int:
-    if x.dtype not in _ACT or (dtype is not None and x.dtype != dtype):
+def _moe_tokens(x, K: int, index: int, dtype=None) -> int:
+    """Checks x [T, K] on the weights' device; returns T."""
+    if x.dtype not in _ACT or (dtype is not None and x.dtype is not dtype):
         raise ValueError(f"x must be {dtype or 'float16 or bfloat16'}, got {x.dtype}")
-    if x.dim() != 2 or x.shape[1] != K:
-        raise ValueError(f"x must be [T, {K}], got {list(x.shape)}")
-    if x.device != device:
-        raise ValueError(f"x must be on the weights' device {device}")
-    return x.shape[0]
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != K:
+        raise ValueError(f"x must be [T, {K}], got {list(shape)}")
+    if x.get_device() != index:
+        raise ValueError("x must be on the weights' device")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    return shape[0]
 
 
-def _moe_pair(ids, weights, T: int, top_k: int, device) -> tuple:
-    """The addresses of the experts' ids and weights, [T, top_k] each."""
-    if ids.dtype != _I32 or weights.dtype != torch.float32:
-        raise ValueError("experts must be int32 and weights float32")
-    for name, t in (("experts", ids), ("weights", weights)):
-        if tuple(t.shape) != (T, top_k):
-            raise ValueError(f"{name} must be {[T, top_k]}, got {list(t.shape)}")
-        if t.device != device:
-            raise ValueError(f"{name} must be on x's device")
-    return _dev(ids, "experts"), _dev(weights, "weights")
+def _moe_given(t, name: str, dtype, T: int, top_k: int, index: int) -> int:
+    """The address of the experts' ids or weights, [T, top_k]."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (T, top_k):
+        raise ValueError(f"{name} must be {[T, top_k]}, got {list(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on x's device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _moe_pair_out(routed, T: int, top_k: int, device, stream):
+def _moe_pair(routed, T: int, top_k: int, x, stream) -> tuple:
     if routed is None:
-        routed = (_empty((T, top_k), _I32, device, stream),
-                  _empty((T, top_k), torch.float32, device, stream))
+        shape, dev = (T, top_k), x.device
+        if stream is None:
+            ids, weights = torch.empty(shape, dtype=_I32, device=dev), torch.empty(shape, dtype=_F32, device=dev)
+        else:
+            ids, weights = _empty(shape, _I32, dev, stream), _empty(shape, _F32, dev, stream)
+        return ids, weights, ids.data_ptr(), weights.data_ptr()
     ids, weights = routed
-    return ids, weights, *_moe_pair(ids, weights, T, top_k, device)
+    index = x.get_device()
+    return (ids, weights, _moe_given(ids, "experts", _I32, T, top_k, index),
+            _moe_given(weights, "weights", _F32, T, top_k, index))
 
 
 def _moe_out(x, out, workspace, experts: AqExperts, T: int, top_k: int, stream) -> tuple:
     if out is None:
-        out = _empty(x.shape, x.dtype, x.device, stream)
-    elif tuple(out.shape) != tuple(x.shape) or out.device != x.device:
-        raise ValueError(f"out must be {list(x.shape)} on x's device")
-    _check_out(out, "out", x.numel(), x.dtype)
+        out = torch.empty_like(x) if stream is None else _empty(x.shape, x.dtype, x.device, stream)
+        to = out.data_ptr()
+    else:
+        if out.shape != x.shape or out.get_device() != x.get_device():
+            raise ValueError(f"out must be {list(x.shape)} on x's device")
+        _check_out(out, "out", x.numel(), x.dtype)
+        to = _dev(out, "out")
     if workspace is None:
         # refused sizes reach the library's checks
-        workspace = _scratch(max(aq_moe_workspace_bytes(experts, T, top_k), 256), x.device, stream)
+        n = aq_moe_workspace_bytes(experts, T, top_k) or 256
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device) if stream is None else \
+            _scratch(n, x.device, stream)
+        return out, to, workspace.data_ptr(), n, workspace
     if workspace.dtype != torch.uint8:
         raise ValueError("workspace must be a contiguous uint8 tensor")
-    return out, _dev(out, "out"), _dev(workspace, "workspace"), workspace.numel(), workspace
+    if workspace.get_device() != x.get_device():
+        raise ValueError("workspace must be on x's device")
+    return out, to, _dev(workspace, "workspace"), workspace.numel(), workspace
 
 
 def aq_moe_workspace_bytes(experts: AqExperts, T: int, top_k: int) -> int:
@@ -829,10 +850,11 @@ def aq_moe_workspace_bytes(experts: AqExperts, T: int, top_k: int) -> int:
 def aq_moe_route(x, router: AqRouter, out=None, stream=None) -> tuple:
     """The experts of each token of x [T, K]: (experts int32 [T, top_k], each
     row ascending, weights float32 [T, top_k])."""
-    T = _moe_tokens(x, router.weight.shape[1], router.weight.device, router.weight.dtype)
-    ids, weights, ip, wp = _moe_pair_out(out, T, router.top_k, x.device, stream)
-    _check(load().aq_moe_route(router._ref, _dev(x, "x"), T, ip, wp, _stream(stream)),
-           "aq_moe_route")
+    T = _moe_tokens(x, router._shape[1], router._index, router._dtype)
+    ids, weights, ip, wp = _moe_pair(out, T, router.top_k, x, stream)
+    st = _lib.aq_moe_route(router._ref, x.data_ptr(), T, ip, wp, _stream(stream))
+    if st:
+        _check(st, "aq_moe_route")
     return ids, weights
 
 
@@ -840,15 +862,18 @@ def aq_moe_experts(x, experts: AqExperts, ids, weights, out=None, workspace=None
                    stream=None) -> torch.Tensor:
     """y[t] = sum_j weights[t, j] * expert ids[t, j] of x[t]; ids int32
     [T, top_k] (outside 0..E-1: none), weights float32 [T, top_k]."""
-    T = _moe_tokens(x, experts.hidden, experts.gate[0].device)
+    index = experts._index
+    T = _moe_tokens(x, experts.hidden, index)
     if ids.dim() != 2:
         raise ValueError("experts must be [T, top_k]")
     top_k = ids.shape[1]
-    ip, wp = _moe_pair(ids, weights, T, top_k, x.device)
+    ip = _moe_given(ids, "experts", _I32, T, top_k, index)
+    wp = _moe_given(weights, "weights", _F32, T, top_k, index)
     out, op, ws, n, hold = _moe_out(x, out, workspace, experts, T, top_k, stream)
-    _check(load().aq_moe_experts(experts._ref, AQ_BF16 if x.dtype == torch.bfloat16 else AQ_F16,
-                                 _dev(x, "x"), T, top_k, ip, wp, op, ws, n, _stream(stream)),
-           "aq_moe_experts")
+    st = _lib.aq_moe_experts(experts._ref, AQ_BF16 if x.dtype is torch.bfloat16 else AQ_F16,
+                             x.data_ptr(), T, top_k, ip, wp, op, ws, n, _stream(stream))
+    if st:
+        _check(st, "aq_moe_experts")
     return out
 
 
@@ -857,16 +882,17 @@ def aq_moe(x, router: AqRouter, experts: AqExperts, out=None, routed=None, works
     """The whole layer: routes x [T, K] and runs the chosen experts.  Returns
     (y [T, K], experts int32 [T, top_k], weights float32 [T, top_k]); routed:
     tensors for the last two."""
-    T = _moe_tokens(x, experts.hidden, experts.gate[0].device, router.weight.dtype)
-    if router.weight.shape != (experts.count, experts.hidden):
-        raise ValueError(f"the router is {list(router.weight.shape)}, the experts "
+    T = _moe_tokens(x, experts.hidden, experts._index, router._dtype)
+    if router._shape != (experts.count, experts.hidden):
+        raise ValueError(f"the router is {list(router._shape)}, the experts "
                          f"{[experts.count, experts.hidden]}")
-    if router.weight.device != x.device:
+    if router._index != experts._index:
         raise ValueError("router and experts must be on one device")
-    ids, weights, ip, wp = _moe_pair_out(routed, T, router.top_k, x.device, stream)
+    ids, weights, ip, wp = _moe_pair(routed, T, router.top_k, x, stream)
     out, op, ws, n, hold = _moe_out(x, out, workspace, experts, T, router.top_k, stream)
-    _check(load().aq_moe(router._ref, experts._ref, _dev(x, "x"), T, ip, wp, op, ws, n,
-                         _stream(stream)), "aq_moe")
+    st = _lib.aq_moe(router._ref, experts._ref, x.data_ptr(), T, ip, wp, op, ws, n, _stream(stream))
+    if st:
+        _check(st, "aq_moe")
     return out, ids, weights
 
 
@@ -877,24 +903,36 @@ def aq_embed(ids, Wq, scales, biases, bits: int, group_size: int, dtype, scale: 
     [N, K*bits/32], scales and biases fp16 [N, K/group_size]."""
     if dtype not in _ACT:
         raise ValueError("dtype must be float16 or bfloat16")
-    if ids.dtype not in (_I32, torch.int64):
+    wide = ids.dtype is torch.int64
+    if not wide and ids.dtype is not _I32:
         raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
     if scales.dim() != 2:
         raise ValueError("scales must be [N, K/group_size]")
-    N, K = scales.shape[0], scales.shape[1] * group_size
+    N, G = scales.shape
+    K = G * group_size
     _check_weights(Wq, scales, biases, N, K, bits, group_size)
-    if not Wq.device == scales.device == biases.device == ids.device:
+    index = ids.get_device()
+    if index < 0:
+        raise ValueError("ids must be a CUDA tensor")
+    if not Wq.get_device() == scales.get_device() == biases.get_device() == index:
         raise ValueError("ids and the table must be on one device")
+    if not (ids.is_contiguous() and Wq.is_contiguous() and scales.is_contiguous() and biases.is_contiguous()):
+        raise ValueError("ids and the table must be contiguous")
     T = ids.numel()
     if out is None:
-        out = _empty((*ids.shape, K), dtype, ids.device, stream)
-    elif out.device != ids.device:
-        raise ValueError("out must be on ids' device")
-    _check_out(out, "out", T * K, dtype)
-    _check(load().aq_embed(AQ_BF16 if dtype == torch.bfloat16 else AQ_F16, _dev(ids, "ids"),
-                           ids.element_size(), T, _dev(Wq, "Wq"), _dev(scales, "scales"),
-                           _dev(biases, "biases"), N, K, bits, group_size, scale, _dev(out, "out"),
-                           _stream(stream)), "aq_embed")
+        shape = (*ids.shape, K)
+        out = torch.empty(shape, dtype=dtype, device=ids.device) if stream is None else \
+            _empty(shape, dtype, ids.device, stream)
+    else:
+        if out.get_device() != index:
+            raise ValueError("out must be on ids' device")
+        _check_out(out, "out", T * K, dtype)
+        _dev(out, "out")
+    st = _lib.aq_embed(AQ_BF16 if dtype is torch.bfloat16 else AQ_F16, ids.data_ptr(), 8 if wide else 4, T,
+                       Wq.data_ptr(), scales.data_ptr(), biases.data_ptr(), N, K, bits, group_size, scale,
+                       out.data_ptr(), _stream(stream))
+    if st:
+        _check(st, "aq_embed")
     return out
 
 

@@ -13,9 +13,10 @@
 //     of two 16-bit floats are exact in fp32, two-sums keep what each addition
 //     rounds off), which is good to about 2^-46 of the sum of |x w|.
 //   * weights come from the fp32 logits.
-// A cluster of 8 CTAs takes 8 or 32 tokens: its CTAs deal the experts (16 an
-// MMA tile) and, where there are fewer tiles than CTAs, slices of K; the parts
-// are sent to the CTA that chooses for the token, one warp a token.
+// A cluster of 8 CTAs takes 8 or 16 tokens: its CTAs slice K, their warps deal
+// the experts (16 an MMA tile) and, where there are fewer tiles than warps,
+// slice K further; the parts are sent to the CTA that chooses for the token,
+// one warp a token.
 #include "aq_moe.h"
 #include "aq_ptx.cuh"
 
@@ -39,8 +40,7 @@ struct RouteParams {
     float *weights;
     int T, E, K, top, score, normalize;
     float scale;
-    int tiles;   // CTAs of a cluster that take different expert tiles; the rest slice K
-    int slices;  // kCluster / tiles
+    int slices;  // of K: one a CTA of the cluster, more where there are fewer tiles than warps
 };
 
 template <bool BF16>
@@ -115,10 +115,9 @@ __device__ void choose(const RouteParams &p, int t, const float *parts, double *
     float logit[LANES], val[LANES];
     float slack = 0.f;      // the largest error bound of a value
     uint32_t open = 0u;     // experts not yet taken, by position
-    // a slice's warp adds K / (16 * slices * 8) products of 16 and then 8 warps
-    // and the slices are added: each step rounds (the MMA: truncates) to 2^-22
-    // of the partial sum at most
-    const float ulps = (float)(p.K / (16 * kWarps * p.slices) + 2 + kWarps + p.slices) * 2.384185791015625e-07f;
+    // a slice adds K / (16 * slices) products of 16, then the slices are added:
+    // each step rounds (the MMA: truncates) to 2^-22 of the partial sum at most
+    const float ulps = (float)(p.K / (16 * p.slices) + 2 + p.slices) * 2.384185791015625e-07f;
 #pragma unroll
     for (int j = 0; j < LANES; ++j) {
         logit[j] = val[j] = -INFINITY;
@@ -254,35 +253,35 @@ template <bool BF16, int NB, int LANES>
 __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteParams p) {
     constexpr int TOKENS = 8 * NB, MINE = TOKENS / kCluster;  // a CTA chooses for MINE tokens
     extern __shared__ __align__(16) uint8_t dyn[];
-    // [kWarps][NB][2][32] float4 of the CTA's own sums; [MINE][slices][2][E]
-    // parts from all CTAs; [MINE][E] doubles
-    float4 *red = reinterpret_cast<float4 *>(dyn);
-    float *parts = reinterpret_cast<float *>(red + kWarps * NB * 2 * 32);
-    double *keep = reinterpret_cast<double *>(
-        reinterpret_cast<uint8_t *>(parts) + ((MINE * p.slices * 2 * p.E * 4 + 15) & ~15));
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+    // [MINE][slices][2][E] parts from all CTAs, [MINE][E] doubles
+    float *parts = reinterpret_cast<float *>(dyn);
+    double *keep = reinterpret_cast<double *>(dyn + ((MINE * p.slices * 2 * p.E * 4 + 15) & ~15));
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0);
     const int rank = (int)cluster_ctarank();
     const int t0 = (int)(blockIdx.x / kCluster) * TOKENS;
-    const int slice = rank / p.tiles;
     launch_dependents();
     cluster_sync();  // every CTA of the cluster runs before its shared memory is written
     grid_dependency_wait();
 
-    // the warp's 32-value steps of K
-    const int steps = p.K / 32, parts_k = p.slices * kWarps, me = slice * kWarps + warp;
-    const int k_beg = (int)((int64_t)steps * me / parts_k);
-    const int k_end = (int)((int64_t)steps * (me + 1) / parts_k);
-    for (int tile = rank % p.tiles; tile * 16 < p.E; tile += p.tiles) {
+    // A warp takes tiles warp / cuts, + kWarps / cuts, .. over one slice of K, in
+    // steps of 32 values: lane (g, q) reads 8 of them of rows g and g + 8, and of
+    // token g of each block of 8.
+    const int cuts = p.slices / kCluster, slice = rank * cuts + warp % cuts;
+    const int steps = p.K / 32;
+    const int k_beg = (int)((int64_t)steps * slice / p.slices);
+    const int k_end = (int)((int64_t)steps * (slice + 1) / p.slices);
+    const uint16_t *xs[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) xs[nb] = p.x + (size_t)min(t0 + nb * 8 + g, p.T - 1) * p.K + 8 * q;
+    for (int tile = warp / cuts; tile * 16 < p.E; tile += kWarps / cuts) {
         const int ra = min(tile * 16 + g, p.E - 1), rb = min(tile * 16 + 8 + g, p.E - 1);
         const uint16_t *wa = p.w + (size_t)ra * p.K + 8 * q, *wb = p.w + (size_t)rb * p.K + 8 * q;
-        const uint16_t *xs[NB];
         float d[NB][4], m[NB][4];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            xs[nb] = p.x + (size_t)min(t0 + nb * 8 + g, p.T - 1) * p.K + 8 * q;
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[nb][i] = m[nb][i] = 0.f;
-        }
 #pragma unroll 4
         for (int k = k_beg; k < k_end; ++k) {
             const uint4 a = *reinterpret_cast<const uint4 *>(wa + 32 * k);
@@ -299,33 +298,18 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
                             x.w & kAbs);
             }
         }
+        // to the tokens' CTAs
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-            red[((warp * NB + nb) * 2) * 32 + lane] = make_float4(d[nb][0], d[nb][1], d[nb][2], d[nb][3]);
-            red[((warp * NB + nb) * 2 + 1) * 32 + lane] = make_float4(m[nb][0], m[nb][1], m[nb][2], m[nb][3]);
-        }
-        __syncthreads();
-        // add the warps' sums in order and send them to the token's CTA
-        for (int i = tid; i < NB * 2 * 32; i += kThreads) {
-            float4 s = red[i];
-            for (int w = 1; w < kWarps; ++w) {
-                const float4 v = red[w * NB * 2 * 32 + i];
-                s.x += v.x;
-                s.y += v.y;
-                s.z += v.z;
-                s.w += v.w;
-            }
-            const int ln = i & 31, which = (i >> 5) & 1, nb = i >> 6;
-            const float val[4] = {s.x, s.y, s.z, s.w};
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int e = tile * 16 + (ln >> 2) + 8 * (j >> 1), n = nb * 8 + 2 * (ln & 3) + (j & 1);
-                if (e >= p.E) continue;
-                const float *to = parts + ((size_t)((n / kCluster) * p.slices + slice) * 2 + which) * p.E + e;
-                st_dsmem_f32(map_to_rank(smem_u32(to), (uint32_t)(n % kCluster)), val[j]);
+                const int e = tile * 16 + g + 8 * (j >> 1), n = nb * 8 + 2 * q + (j & 1);
+                if (e >= p.E || t0 + n >= p.T) continue;
+                const float *to = parts + ((size_t)(n / kCluster) * p.slices + slice) * 2 * p.E + e;
+                const uint32_t at = map_to_rank(smem_u32(to), (uint32_t)(n % kCluster));
+                st_dsmem_f32(at, d[nb][j]);
+                st_dsmem_f32(at + 4u * (uint32_t)p.E, m[nb][j]);
             }
-        }
-        __syncthreads();
     }
     cluster_sync();
     if (warp < MINE) {
@@ -375,8 +359,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
 template <bool BF16, int NB, int LANES>
 cudaError_t route_run(const RouteParams &p, cudaStream_t stream) {
     const int mine = 8 * NB / kCluster;
-    const size_t smem = (size_t)kWarps * NB * 2 * 32 * 16 +
-                        (((size_t)mine * p.slices * 2 * p.E * 4 + 15) & ~(size_t)15) +
+    const size_t smem = (((size_t)mine * p.slices * 2 * p.E * 4 + 15) & ~(size_t)15) +
                         (size_t)mine * p.E * 8;
     const unsigned blocks = (unsigned)((p.T + 8 * NB - 1) / (8 * NB)) * kCluster;
     auto *kern = route_kernel<BF16, NB, LANES>;
@@ -388,11 +371,11 @@ cudaError_t route_run(const RouteParams &p, cudaStream_t stream) {
     return moe_launch(kern, dim3(blocks), kThreads, smem, kCluster, stream, p);
 }
 
-// 8 tokens a cluster while the clusters fit on the device, else 32.
+// 8 tokens a cluster, or 16 for many, so that the weights are read half as often.
 template <bool BF16>
 cudaError_t route_sized(const RouteParams &p, cudaStream_t stream) {
     if (p.T > 64)
-        return p.E <= 128 ? route_run<BF16, 4, 4>(p, stream) : route_run<BF16, 4, 16>(p, stream);
+        return p.E <= 128 ? route_run<BF16, 2, 4>(p, stream) : route_run<BF16, 2, 16>(p, stream);
     return p.E <= 128 ? route_run<BF16, 1, 4>(p, stream) : route_run<BF16, 1, 16>(p, stream);
 }
 
@@ -413,9 +396,8 @@ cudaError_t moe_route_launch(const RouteArgs &a) {
     p.score = r.score;
     p.normalize = r.normalize;
     p.scale = r.scale;
-    p.tiles = 1;
-    while (p.tiles < kCluster && p.tiles * 16 < p.E) p.tiles *= 2;
-    p.slices = kCluster / p.tiles;
+    p.slices = kCluster * kWarps;
+    for (int tiles = (p.E + 15) / 16, w = 1; w < tiles && w < kWarps; w *= 2) p.slices /= 2;
     const bool bf16 = r.dtype == AQ_BF16;
     return bf16 ? route_sized<true>(p, a.stream) : route_sized<false>(p, a.stream);
 }
