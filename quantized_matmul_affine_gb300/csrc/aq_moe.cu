@@ -5,15 +5,16 @@
 // 1 / (1 + exp(-l)), the top_k largest l (with a bias: the largest p + bias),
 // ties to the lowest index, weights p / (sum of the chosen p) or p, times a
 // factor.  The choice is that of exact arithmetic as far as 64 bits tell:
-//   * the logits are MMA sums in fp32, beside them the sums of |x w|, which
-//     bound their error;
+//   * the logits are fp32 sums of MMA steps with the additions' rounding errors
+//     carried along, beside them the sums of |x w|, which bound what the steps
+//     truncate;
 //   * experts whose value is farther from the k-th largest than the bounds
 //     are in or out for certain; where others are left to choose from, their
 //     logits are summed again with the rounding errors carried along (products
 //     of two 16-bit floats are exact in fp32, two-sums keep what each addition
 //     rounds off), which is good to about 2^-46 of the sum of |x w|.
 //   * weights come from the fp32 logits.
-// A cluster of 8 CTAs takes 8 or 16 tokens: its CTAs slice K, their warps deal
+// A cluster of 8 or 16 CTAs takes 8 or 16 tokens: its CTAs slice K, their warps deal
 // the experts (16 an MMA tile) and, where there are fewer tiles than warps,
 // slice K further; the parts are sent to the CTA that chooses for the token,
 // one warp a token.
@@ -23,13 +24,14 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cmath>
 #include <initializer_list>
 
 namespace aq {
 namespace {
 
-constexpr int kCluster = 8;
+constexpr int kOwners = 8;  // CTAs of a cluster that choose, for every eighth token each
 constexpr int kWarps = 8;
 constexpr int kThreads = 256;
 
@@ -40,7 +42,8 @@ struct RouteParams {
     float *weights;
     int T, E, K, top, score, normalize;
     float scale;
-    int slices;  // of K: one a CTA of the cluster, more where there are fewer tiles than warps
+    int cluster;  // CTAs of a cluster, 8 or 16
+    int slices;   // of K: one a CTA of the cluster, more where there are fewer tiles than warps
 };
 
 template <bool BF16>
@@ -80,7 +83,7 @@ template <bool BF16>
 __device__ __noinline__ double precise_logit(const uint16_t *x, const uint16_t *w, int K) {
     const int lane = threadIdx.x & 31;
     float s[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
+#pragma unroll 8
     for (int k = lane * 8; k < K; k += 256) {
         const uint4 a = *reinterpret_cast<const uint4 *>(x + k), b = *reinterpret_cast<const uint4 *>(w + k);
         const uint32_t xa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
@@ -105,31 +108,28 @@ __device__ __forceinline__ uint32_t ordered(float v) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// The choice for token t by one warp, of up to 32 LANES experts.  parts: [slices][2][E], sums and sums of
-// magnitudes; keep: E doubles for values summed again.
+// The choice for token t by one warp, of up to 32 LANES experts.  sums: [2][E],
+// logits and their sums of magnitudes; keep: E doubles for values summed again.
 template <bool BF16, int LANES>
-__device__ void choose(const RouteParams &p, int t, const float *parts, double *keep) {
+__device__ void choose(const RouteParams &p, int t, const float *sums, double *keep) {
     const int lane = threadIdx.x & 31;
     const int per = (p.E + 31) / 32;
     const bool sigmoid = p.score == AQ_SCORE_SIGMOID;
     float logit[LANES], val[LANES];
     float slack = 0.f;      // the largest error bound of a value
     uint32_t open = 0u;     // experts not yet taken, by position
-    // a slice adds K / (16 * slices) products of 16, then the slices are added:
-    // each step rounds (the MMA: truncates) to 2^-22 of the partial sum at most
-    const float ulps = (float)(p.K / (16 * p.slices) + 2 + p.slices) * 2.384185791015625e-07f;
+    // what the sums leave out: a step's two products truncate to 2^-22 of their
+    // magnitudes each, the last rounding is 2^-24 of the logit; what the errors'
+    // own sums and those of the magnitudes round is smaller by 2^-20
+    constexpr float kUlps = 2.5f * 2.384185791015625e-07f;
 #pragma unroll
     for (int j = 0; j < LANES; ++j) {
         logit[j] = val[j] = -INFINITY;
         const int e = j * 32 + lane;
         if (j < per && e < p.E) {
-            float s = 0.f, m = 0.f;
-            for (int k = 0; k < p.slices; ++k) {
-                s += parts[(size_t)k * 2 * p.E + e];
-                m += parts[(size_t)k * 2 * p.E + p.E + e];
-            }
+            const float s = sums[e];
             logit[j] = s;
-            float bound = ulps * m;
+            float bound = kUlps * sums[p.E + e];
             float v = s;
             if (p.bias) {
                 v = 1.f / (1.f + expf(-s)) + p.bias[e];
@@ -178,12 +178,13 @@ __device__ void choose(const RouteParams &p, int t, const float *parts, double *
     const int n_doubt = __reduce_add_sync(0xFFFFFFFFu, __popc(doubt));
     // (a border that is not finite decides nothing: the fp32 choice stands)
     if (n_sure + n_doubt > p.top && fabsf(border) < INFINITY) {
-        for (int e = 0; e < p.E; ++e) {
-            if (!(__shfl_sync(0xFFFFFFFFu, doubt, e & 31) >> (e >> 5) & 1u)) continue;
-            double d = precise_logit<BF16>(p.x + (size_t)t * p.K, p.w + (size_t)e * p.K, p.K);
-            if (p.bias) d = 1.0 / (1.0 + exp(-d)) + (double)p.bias[e];
-            if (lane == (e & 31)) keep[e] = d;
-        }
+#pragma unroll
+        for (int j = 0; j < LANES; ++j)
+            for (uint32_t m = __ballot_sync(0xFFFFFFFFu, doubt >> j & 1u); m; m &= m - 1u) {
+                const int e = j * 32 + __ffs(m) - 1;
+                double d = precise_logit<BF16>(p.x + (size_t)t * p.K, p.w + (size_t)e * p.K, p.K);
+                if (lane == (e & 31)) keep[e] = p.bias ? 1.0 / (1.0 + exp(-d)) + (double)p.bias[e] : d;
+            }
         __syncwarp();
         taken = sure;
         for (int n = n_sure; n < p.top; ++n) {
@@ -251,15 +252,15 @@ __device__ void choose(const RouteParams &p, int t, const float *parts, double *
 
 template <bool BF16, int NB, int LANES>
 __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteParams p) {
-    constexpr int TOKENS = 8 * NB, MINE = TOKENS / kCluster;  // a CTA chooses for MINE tokens
+    constexpr int TOKENS = 8 * NB, MINE = TOKENS / kOwners;  // a CTA chooses for MINE tokens
     extern __shared__ __align__(16) uint8_t dyn[];
-    // [MINE][slices][2][E] parts from all CTAs, [MINE][E] doubles
+    // [MINE][slices][3][E] parts from all CTAs, [MINE][E] doubles
     float *parts = reinterpret_cast<float *>(dyn);
-    double *keep = reinterpret_cast<double *>(dyn + ((MINE * p.slices * 2 * p.E * 4 + 15) & ~15));
+    double *keep = reinterpret_cast<double *>(dyn + ((MINE * p.slices * 3 * p.E * 4 + 15) & ~15));
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0);
     const int rank = (int)cluster_ctarank();
-    const int t0 = (int)(blockIdx.x / kCluster) * TOKENS;
+    const int t0 = (int)blockIdx.x / p.cluster * TOKENS;
     launch_dependents();
     cluster_sync();  // every CTA of the cluster runs before its shared memory is written
     grid_dependency_wait();
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
     // A warp takes tiles warp / cuts, + kWarps / cuts, .. over one slice of K, in
     // steps of 32 values: lane (g, q) reads 8 of them of rows g and g + 8, and of
     // token g of each block of 8.
-    const int cuts = p.slices / kCluster, slice = rank * cuts + warp % cuts;
+    const int cuts = p.slices / p.cluster, slice = rank * cuts + warp % cuts;
     const int steps = p.K / 32;
     const int k_beg = (int)((int64_t)steps * slice / p.slices);
     const int k_end = (int)((int64_t)steps * (slice + 1) / p.slices);
@@ -277,12 +278,14 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
     for (int tile = warp / cuts; tile * 16 < p.E; tile += kWarps / cuts) {
         const int ra = min(tile * 16 + g, p.E - 1), rb = min(tile * 16 + 8 + g, p.E - 1);
         const uint16_t *wa = p.w + (size_t)ra * p.K + 8 * q, *wb = p.w + (size_t)rb * p.K + 8 * q;
-        float d[NB][4], m[NB][4];
+        // a step's two products start from zero and are added with their rounding
+        // errors: s + r; m the sums of magnitudes
+        float s[NB][4], r[NB][4], m[NB][4];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) d[nb][i] = m[nb][i] = 0.f;
-#pragma unroll 4
+            for (int i = 0; i < 4; ++i) s[nb][i] = r[nb][i] = m[nb][i] = 0.f;
+#pragma unroll(NB == 1 ? 8 : 4)
         for (int k = k_beg; k < k_end; ++k) {
             const uint4 a = *reinterpret_cast<const uint4 *>(wa + 32 * k);
             const uint4 b = *reinterpret_cast<const uint4 *>(wb + 32 * k);
@@ -290,8 +293,11 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(xs[nb] + 32 * k);
-                mma_x<BF16>(d[nb], a.x, b.x, a.y, b.y, x.x, x.y);
-                mma_x<BF16>(d[nb], a.z, b.z, a.w, b.w, x.z, x.w);
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_x<BF16>(d, a.x, b.x, a.y, b.y, x.x, x.y);
+                mma_x<BF16>(d, a.z, b.z, a.w, b.w, x.z, x.w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) two_sum(s[nb][i], r[nb][i], d[i]);
                 mma_x<BF16>(m[nb], a.x & kAbs, b.x & kAbs, a.y & kAbs, b.y & kAbs, x.x & kAbs,
                             x.y & kAbs);
                 mma_x<BF16>(m[nb], a.z & kAbs, b.z & kAbs, a.w & kAbs, b.w & kAbs, x.z & kAbs,
@@ -305,16 +311,34 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
             for (int j = 0; j < 4; ++j) {
                 const int e = tile * 16 + g + 8 * (j >> 1), n = nb * 8 + 2 * q + (j & 1);
                 if (e >= p.E || t0 + n >= p.T) continue;
-                const float *to = parts + ((size_t)(n / kCluster) * p.slices + slice) * 2 * p.E + e;
-                const uint32_t at = map_to_rank(smem_u32(to), (uint32_t)(n % kCluster));
-                st_dsmem_f32(at, d[nb][j]);
-                st_dsmem_f32(at + 4u * (uint32_t)p.E, m[nb][j]);
+                const float *to = parts + ((size_t)(n / kOwners) * p.slices + slice) * 3 * p.E + e;
+                const uint32_t at = map_to_rank(smem_u32(to), (uint32_t)(n % kOwners));
+                st_dsmem_f32(at, s[nb][j]);
+                st_dsmem_f32(at + 4u * (uint32_t)p.E, r[nb][j]);
+                st_dsmem_f32(at + 8u * (uint32_t)p.E, m[nb][j]);
             }
     }
     cluster_sync();
+    if (rank >= kOwners) return;
+    // the slices' parts, in order, into the first slice's place
+    for (int i = threadIdx.x; i < MINE * p.E; i += kThreads) {
+        const int n = i / p.E;
+        float *from = parts + (size_t)n * p.slices * 3 * p.E + (i - n * p.E);
+        float s = 0.f, r = 0.f, m = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < p.slices; ++k) {
+            const float *f = from + (size_t)k * 3 * p.E;
+            two_sum(s, r, f[0]);
+            r += f[p.E];
+            m += f[2 * p.E];
+        }
+        from[0] = s + r;
+        from[p.E] = m;
+    }
+    __syncthreads();
     if (warp < MINE) {
-        const int t = t0 + warp * kCluster + rank;
-        if (t < p.T) choose<BF16, LANES>(p, t, parts + (size_t)warp * p.slices * 2 * p.E, keep + (size_t)warp * p.E);
+        const int t = t0 + warp * kOwners + rank;
+        if (t < p.T) choose<BF16, LANES>(p, t, parts + (size_t)warp * p.slices * 3 * p.E, keep + (size_t)warp * p.E);
     }
 }
 
@@ -357,26 +381,61 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
 }
 
 template <bool BF16, int NB, int LANES>
-cudaError_t route_run(const RouteParams &p, cudaStream_t stream) {
-    const int mine = 8 * NB / kCluster;
-    const size_t smem = (((size_t)mine * p.slices * 2 * p.E * 4 + 15) & ~(size_t)15) +
-                        (size_t)mine * p.E * 8;
-    const unsigned blocks = (unsigned)((p.T + 8 * NB - 1) / (8 * NB)) * kCluster;
+cudaError_t route_run(RouteParams p, cudaStream_t stream) {
     auto *kern = route_kernel<BF16, NB, LANES>;
+    // K in 16 slices where one cluster has much to read alone (1 token of 5120,
+    // 256 experts: WIDE us in 8 slices, WIDE16 in 16), if the device has room
+    // for such a cluster; else in 8
+    static std::atomic<int> wide{-1};
+    p.cluster = 8;
+    if (p.T <= 64 && (int64_t)p.E * p.K >= 1 << 19) {
+        int w = wide.load(std::memory_order_relaxed);
+        if (w < 0) {
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(16);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = 112 * 1024;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 16;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+            if (e != cudaSuccess) cudaGetLastError();
+            w = e == cudaSuccess && n > 0;
+            wide.store(w, std::memory_order_relaxed);
+        }
+        if (w) p.cluster = 16;
+    }
+    p.slices = p.cluster * kWarps;
+    for (int tiles = (p.E + 15) / 16, w = 1; w < tiles && w < kWarps; w *= 2) p.slices /= 2;
+    const int mine = 8 * NB / kOwners;
+    const size_t smem = (((size_t)mine * p.slices * 3 * p.E * 4 + 15) & ~(size_t)15) +
+                        (size_t)mine * p.E * 8;
     if (smem > 48 * 1024) {
         const cudaError_t e =
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
         if (e != cudaSuccess) return e;
     }
-    return moe_launch(kern, dim3(blocks), kThreads, smem, kCluster, stream, p);
+    const unsigned blocks = (unsigned)((p.T + 8 * NB - 1) / (8 * NB)) * (unsigned)p.cluster;
+    return moe_launch(kern, dim3(blocks), kThreads, smem, p.cluster, stream, p);
 }
 
 // 8 tokens a cluster, or 16 for many, so that the weights are read half as often.
 template <bool BF16>
 cudaError_t route_sized(const RouteParams &p, cudaStream_t stream) {
     if (p.T > 64)
-        return p.E <= 128 ? route_run<BF16, 2, 4>(p, stream) : route_run<BF16, 2, 16>(p, stream);
-    return p.E <= 128 ? route_run<BF16, 1, 4>(p, stream) : route_run<BF16, 1, 16>(p, stream);
+        return p.E <= 128   ? route_run<BF16, 2, 4>(p, stream)
+               : p.E <= 256 ? route_run<BF16, 2, 8>(p, stream)
+                            : route_run<BF16, 2, 16>(p, stream);
+    return p.E <= 128   ? route_run<BF16, 1, 4>(p, stream)
+           : p.E <= 256 ? route_run<BF16, 1, 8>(p, stream)
+                        : route_run<BF16, 1, 16>(p, stream);
 }
 
 }  // namespace
@@ -396,8 +455,6 @@ cudaError_t moe_route_launch(const RouteArgs &a) {
     p.score = r.score;
     p.normalize = r.normalize;
     p.scale = r.scale;
-    p.slices = kCluster * kWarps;
-    for (int tiles = (p.E + 15) / 16, w = 1; w < tiles && w < kWarps; w *= 2) p.slices /= 2;
     const bool bf16 = r.dtype == AQ_BF16;
     return bf16 ? route_sized<true>(p, a.stream) : route_sized<false>(p, a.stream);
 }
