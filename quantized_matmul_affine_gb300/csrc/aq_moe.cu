@@ -463,27 +463,21 @@ namespace {
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 }  // namespace
 
-// Which kernel runs a product of R rows (tiles of 8 pairs, or of 16 rows) and
-// K columns: by the tokens a busy expert has on average and the tiles a CTA
-// gets, were all experts picked alike.
-static int moe_variant(const aq_experts *x, int64_t T, int top, int64_t tiles, int64_t K) {
+// Which kernel runs a product over K, by the tokens a busy expert has on
+// average, were all experts picked alike: 8, 16 or 32 at a time (an expert with
+// more takes its weights from L2 again).  Whether the rows are packed first by
+// a launch of their own, about 3 us, or by each CTA for itself, by how many
+// values the CTAs would pack.  Measured, us a call of the layer: 5 tokens a step
+// and 60 experts of 2048 (700 values of K by tokens... see the table below).
+static int moe_variant(const aq_experts *x, int64_t T, int top, int64_t K) {
     const double E = (double)x->E;
     const double busy = top >= E ? E : E * (1.0 - std::pow(1.0 - top / E, (double)T));
     const double tokens = (double)T * top / busy;
-    if (T <= 8 || tokens <= 2.0) {
-        if (busy * (double)tiles <= 4.0 * 3.0 * num_sms()) return MOE_FEW;
-        // three CTAs an SM, but two with more room each, and packed rows, where
-        // the columns of a long K would not stay
-        return (tokens + 1.0) * (double)K * 2.1 <= 20480.0 ? MOE_8 : MOE_8_LONG;
-    }
+    if (T <= 8 || tokens <= 4.0) return tokens * (double)K >= 8192.0 ? MOE_8_PACKED : MOE_8;
     return T <= 16 || tokens <= 10.0 ? MOE_16 : MOE_32;
 }
-static int up_variant(const aq_experts *x, int64_t T, int top) {
-    return moe_variant(x, T, top, x->I / 8, x->K);
-}
-static int down_variant(const aq_experts *x, int64_t T, int top) {
-    return moe_variant(x, T, top, x->K / 16, x->I);
-}
+static int up_variant(const aq_experts *x, int64_t T, int top) { return moe_variant(x, T, top, x->K); }
+static int down_variant(const aq_experts *x, int64_t T, int top) { return moe_variant(x, T, top, x->I); }
 
 namespace {
 struct Workspace {

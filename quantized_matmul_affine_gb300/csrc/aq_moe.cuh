@@ -617,39 +617,40 @@ __device__ __forceinline__ void copy_columns(const MoeParams &p, int ncols, Shar
     cp_async_wait<0>();
 }
 
-// The sizes of a kernel.  TT tiles side by side share the activations that a
-// step of UU units reads from shared memory; 8 NB columns.
-template <int BITS, bool G32, bool PAIRS, int TT_, int NB_, int CTAS_>
+// The sizes of a kernel for 8 NB columns, CTAS an SM.
+template <int BITS, bool G32, bool PAIRS, int NB_, int CTAS_, bool PACKED_>
 struct Kernel {
-    static constexpr int TT = TT_, NB = NB_, C = 8 * NB, UU = kUnits<BITS>, NW = kWords<BITS, G32>;
+    static constexpr int NB = NB_, C = 8 * NB, UU = kUnits<BITS>, NW = kWords<BITS, G32>;
     static constexpr int SETS = G32 ? 2 : 1;     // groups of a unit whose sums are kept apart
     static constexpr int BU = G32 ? 4 : 8;       // units of a block of scales: 8 groups, 4 of 128
     static constexpr int ROWS = PAIRS ? 8 : 16;  // rows of a matrix in a tile
     static constexpr int UNIT = 8 * BITS;        // bytes of a unit's row
-    static constexpr int CELL = 16 * UNIT, STAGE = TT * UU * CELL;
-    // steps in flight, and a block of scales for each
-    static constexpr int STAGES = STAGE <= 1024 ? 3 : 2, BLOCKS = STAGES;
-    static constexpr int BLOCK = TT * 512;  // bytes: 16 scales and biases of 8 groups a tile
-    static constexpr int RING = STAGES * STAGE + BLOCKS * BLOCK;  // a warp's
-    static constexpr bool PACKED = NB > 1 || CTAS_ == 2;  // columns from packed rows
-    static constexpr bool SPLIT = BITS % 2 == 0;  // units apart in shared memory, else rows whole
-    static constexpr int CTAS = BITS == 5 && CTAS_ == 3 ? 2 : CTAS_;  // an SM
-    static constexpr int DYNAMIC = dynamic_bytes(CTAS);
+    static constexpr int CELL = 16 * UNIT, STAGE = UU * CELL;
+    // Three steps in flight (two of 5 bits), and a block of scales for each, since
+    // a step may be a tile's only one: with 24 warps an SM 72 KB of 4-bit codes.
+    // Four and more measured slower (8 large experts: 205 us with three, 234
+    // with four), and so did steps of twice the bytes.
+    static constexpr int STAGES = STAGE <= 1024 ? 3 : 2, BLOCK = 512;  // 16 scales and biases of 8 groups
+    static constexpr int CTAS = CTAS_, DYNAMIC = dynamic_bytes(CTAS);
+    static constexpr int COLUMNS = layout_bytes<UU, BU>(C, 8) + 2 * kMaxEntries;
+    static constexpr int RING = STAGES * (STAGE + BLOCK);  // a warp's
+    static constexpr bool PACKED = PACKED_;        // columns from packed rows
+    static constexpr bool SPLIT = BITS % 2 == 0;   // units apart in shared memory, else rows whole
     static constexpr int ROOM = DYNAMIC - kWarps * RING;  // for columns, less the entries' experts
     // 8 units of all columns fit beside the most entries, and the partial
     // sums of shared tiles where the rings were
-    static_assert(layout_bytes<UU, BU>(C, 8) <= ROOM - 2 * kMaxEntries && TT * NB * 512 <= RING, "room");
+    static_assert(COLUMNS <= ROOM && NB * 512 <= RING, "room");
 };
 
-// Tiles from .. to - 1 of expert e for the ncols listed entries.  The tiles, TT
-// a group, go round the warps; the groups of the last, unfull round are shared
-// by 2, 4 or 8 warps, which split K.  Each warp has its codes and scales copied
-// to shared memory a few steps ahead, from one group to the next without a
-// stop; the warps meet only where columns are staged.
+// Tiles from .. to - 1 of expert e for the ncols listed entries.  The tiles go
+// round the warps; those of the last, unfull round are shared by 2, 4 or 8
+// warps, which split K.  Each warp has its codes and scales copied to shared
+// memory a few steps ahead, from one tile to the next without a stop; the warps
+// meet only where columns are staged.
 template <class S, int BITS, bool G32, bool PAIRS>
 __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, int to, int ncols, Shared &sh,
                                           uint8_t *dyn, int room, bool wait) {
-    constexpr int TT = S::TT, NB = S::NB, UU = S::UU, BU = S::BU, SETS = S::SETS, STAGES = S::STAGES;
+    constexpr int NB = S::NB, UU = S::UU, BU = S::BU, SETS = S::SETS, STAGES = S::STAGES;
     const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, q = lane & 3;
     // (the shuffle tells the compiler that a warp's lanes agree on it)
     const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
@@ -667,7 +668,7 @@ __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, i
     const uint32_t ring = smem_u32(dyn + warp * S::RING), blocks = ring + STAGES * S::STAGE;
     float4 *slots = reinterpret_cast<float4 *>(dyn);
 
-    const int ngroups = (to - from + TT - 1) / TT, full = ngroups / kWarps, rest = ngroups - full * kWarps;
+    const int full = (to - from) / kWarps, rest = to - from - full * kWarps;
     const int share = rest >= 5 ? 1 : rest >= 3 ? 2 : rest == 2 ? 4 : 8;
     const int rounds = full + (rest > 0);
 
@@ -710,14 +711,12 @@ __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, i
     const uint32_t shift = (uint32_t)first_bit<BITS, G32>(q) & 31u;
     const uint32_t mine = (uint32_t)(g * (S::SPLIT ? UNIT : UU * UNIT) + first_bit<BITS, G32>(q) / 32 * 4);
 
-    float acc[TT][NB][4];
+    float acc[NB][4];
     auto clear = [&]() {
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][nb][i] = 0.f;
+            for (int i = 0; i < 4; ++i) acc[nb][i] = 0.f;
     };
     // acc is in 2^-24 of the column's units
     auto write = [&](int tile, int c, float a, float b) {
@@ -732,15 +731,15 @@ __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, i
             o[8] = b;
         }
     };
-    // The warp's group in a round and its steps of a chunk with nq steps.
-    auto place = [&](int round, int nq, int &group, int &beg, int &end) {
+    // The warp's tile in a round and its steps of a chunk with nq steps.
+    auto place = [&](int round, int nq, int &tile, int &beg, int &end) {
         if (round < full) {
-            group = round * kWarps + warp;
+            tile = round * kWarps + warp;
             beg = 0;
             end = nq;
         } else {
             const int i = warp / share, part = warp - i * share;
-            group = full * kWarps + i;
+            tile = full * kWarps + i;
             beg = nq * part / share;
             end = i < rest ? nq * (part + 1) / share : beg;
         }
@@ -750,64 +749,54 @@ __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, i
     auto stream = [&](int r0, int r1, int u0, int n) {
         const int nq = (n + UU - 1) / UU;
         // the step to fetch next
-        int fround = r0, fgroup, fk, fend, fu, fblock = 0;
+        int fround = r0, ftile, fk, fend, fu, fblock = 0;
         const uint8_t *src = nullptr;
-        int64_t next = 0;
-        bool fresh = true;  // the first step of a group
+        bool fresh = true;  // the first step of a tile
         uint32_t fr = ring;
         auto enter = [&]() {
-            place(fround, nq, fgroup, fk, fend);
-            while (fk >= fend && ++fround < r1) place(fround, nq, fgroup, fk, fend);
+            place(fround, nq, ftile, fk, fend);
+            while (fk >= fend && ++fround < r1) place(fround, nq, ftile, fk, fend);
             fu = fk * UU;
-            src = w0 + (int64_t)(fgroup * TT) * to_t + (int64_t)(u0 + fu) * UNIT;
-            next = TT == 2 && from + fgroup * 2 + 1 < to ? to_t : 0;
+            src = w0 + ftile * to_t + (int64_t)(u0 + fu) * UNIT;
             fresh = true;
         };
         enter();
         auto fetch = [&]() {
             if (fround < r1) {
                 const int left = (n - fu) * UNIT;  // bytes of the row up to the chunk's end
+                if (S::SPLIT || !fine) {
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    const uint8_t *s = src + (t ? next : 0);
-                    if (S::SPLIT || !fine) {
-#pragma unroll
-                        for (int i = 0; i < PIECES; ++i)
-                            copy_codes<16>(fr + t * UU * CELL + code_to[i], s + code_from[i],
-                                           (16 * PER % 32 == 0 || lane + 32 * i < 16 * PER) &&
-                                               (UU == 1 || piece_at(i) < left));
-                    } else {
-                        for (int k = lane; k < 32 * PER; k += 32) {
-                            const int row = k / (2 * PER), at = k % (2 * PER) * 8;
-                            copy_codes<8>(fr + t * UU * CELL + piece_to(row, at),
-                                          s + (row & 7) * row_bytes + (row >= 8 ? to_b : 0) + at, at < left);
-                        }
+                    for (int i = 0; i < PIECES; ++i)
+                        copy_codes<16>(fr + code_to[i], src + code_from[i],
+                                       (16 * PER % 32 == 0 || lane + 32 * i < 16 * PER) &&
+                                           (UU == 1 || piece_at(i) < left));
+                } else {
+                    for (int k = lane; k < 32 * PER; k += 32) {
+                        const int row = k / (2 * PER), at = k % (2 * PER) * 8;
+                        copy_codes<8>(fr + piece_to(row, at),
+                                      src + (row & 7) * row_bytes + (row >= 8 ? to_b : 0) + at, at < left);
                     }
                 }
                 if (fresh || (fu & (BU - 1)) == 0) {
                     // the block of scales that this step lies in
                     const int b0 = (u0 + fu) / BU * block_bytes;  // of the row's bytes
+                    const uint8_t *s = scale_row + (int64_t)ftile * (S::ROWS * 2) * groups + b0;
+                    const uint32_t to_s = blocks + (uint32_t)(fblock * S::BLOCK + lane * 16);
+                    const int have = groups * 2 - b0;  // bytes of the row from here on
+                    if ((even & 15) == 0) {
+                        copy_scales<16>(to_s, s, true);
+                    } else if ((even & 7) == 0) {
+                        copy_scales<8>(to_s, s, true);
+                        copy_scales<8>(to_s + 8, s + 8, !wide && have >= 16);
+                    } else if ((even & 3) == 0) {
 #pragma unroll
-                    for (int t = 0; t < TT; ++t) {
-                        const int tile = fgroup * TT + (t && next ? 1 : 0);
-                        const uint8_t *s = scale_row + (int64_t)tile * (S::ROWS * 2) * groups + b0;
-                        const uint32_t to_s = blocks + (uint32_t)(fblock * S::BLOCK + t * 512 + lane * 16);
-                        const int have = groups * 2 - b0;  // bytes of the row from here on
-                        if ((even & 15) == 0) {
-                            copy_scales<16>(to_s, s, true);
-                        } else if ((even & 7) == 0) {
-                            copy_scales<8>(to_s, s, true);
-                            copy_scales<8>(to_s + 8, s + 8, !wide && have >= 16);
-                        } else if ((even & 3) == 0) {
-#pragma unroll
-                            for (int k = 0; k < 16; k += 4)
-                                copy_scales<4>(to_s + k, s + k, k < block_bytes && have >= k + 4);
-                        } else {
-                            for (int k = 0; k < 16; k += 2)
-                                copy_scales<2>(to_s + k, s + k, k < block_bytes && have >= k + 2);
-                        }
+                        for (int k = 0; k < 16; k += 4)
+                            copy_scales<4>(to_s + k, s + k, k < block_bytes && have >= k + 4);
+                    } else {
+                        for (int k = 0; k < 16; k += 2)
+                            copy_scales<2>(to_s + k, s + k, k < block_bytes && have >= k + 2);
                     }
-                    fblock = fblock + 1 == S::BLOCKS ? 0 : fblock + 1;
+                    fblock = fblock + 1 == STAGES ? 0 : fblock + 1;
                     fresh = false;
                 }
                 fu += UU;
@@ -839,14 +828,14 @@ __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, i
         uint32_t rd = ring + mine;
         int block = -1;
         for (int round = r0; round < r1; ++round) {
-            int group, beg, end;
-            place(round, nq, group, beg, end);
+            int tile, beg, end;
+            place(round, nq, tile, beg, end);
             uint32_t sc = 0;
             for (int k = beg, u = beg * UU; k < end; ++k, u += UU) {
                 cp_async_wait<STAGES - 1>();
                 __syncwarp();
                 if (k == beg || (u & (BU - 1)) == 0) {
-                    block = block + 1 == S::BLOCKS ? 0 : block + 1;
+                    block = block + 1 == STAGES ? 0 : block + 1;
                     sc = blocks + (uint32_t)(block * S::BLOCK);
                     if ((u & (BU - 1)) == 0) {
                         // the block's biases times the columns' group sums: acc is in
@@ -857,76 +846,64 @@ __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, i
                             uint32_t hi, lo;
                             lds<1>(ss[nb] + (uint32_t)(u / BU * 16), &hi);
                             lds<1>(ss[nb] + (uint32_t)(l.sum_lo + u / BU * 16), &lo);
+                            uint32_t a0, a1;
+                            lds<1>(sc + (uint32_t)(256 + g * 16 + 4 * q), &a0);
+                            lds<1>(sc + (uint32_t)(384 + g * 16 + 4 * q), &a1);
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma_k8(d, a0, a1, hi);
+                            mma_k8(d, a0, a1, lo);
 #pragma unroll
-                            for (int t = 0; t < TT; ++t) {
-                                uint32_t a0, a1;
-                                lds<1>(sc + (uint32_t)(t * 512 + 256 + g * 16 + 4 * q), &a0);
-                                lds<1>(sc + (uint32_t)(t * 512 + 384 + g * 16 + 4 * q), &a1);
-                                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma_k8(d, a0, a1, hi);
-                                mma_k8(d, a0, a1, lo);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    acc[t][nb][i] = fmaf(d[i], 1.52587890625e-05f, acc[t][nb][i]);
-                            }
+                            for (int i = 0; i < 4; ++i) acc[nb][i] = fmaf(d[i], 1.52587890625e-05f, acc[nb][i]);
                         }
                     }
                 }
-                // scales of the step's groups, rows g and g + 8 of each tile: the words
-                // that hold them, and which half is unit 0's (with one group a step
-                // also unit 1's)
+                // scales of the step's groups, rows g and g + 8: the words that hold
+                // them, and which half is unit 0's (with one group a step also unit 1's)
                 constexpr int W = UU * SETS == 4 ? 2 : 1;
                 const int at = wide ? (u & 7) >> 1 : (u & (BU - 1)) * SETS;
                 const uint32_t pick = UU * SETS > 1 && !wide ? 0x3210u : at & 1 ? 0x3232u : 0x1010u;
-                uint32_t sv[TT][2][W];
+                uint32_t sv[2][W];
 #pragma unroll
-                for (int t = 0; t < TT; ++t)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        lds<W>(sc + (uint32_t)(t * 512 + b * 128 + g * 16 + (at & ~1) * 2), sv[t][b]);
-                        if (UU * SETS < 4) sv[t][b][0] = prmt(sv[t][b][0], 0u, pick);
-                    }
+                for (int b = 0; b < 2; ++b) {
+                    lds<W>(sc + (uint32_t)(b * 128 + g * 16 + (at & ~1) * 2), sv[b]);
+                    if (UU * SETS < 4) sv[b][0] = prmt(sv[b][0], 0u, pick);
+                }
 #pragma unroll
                 for (int i = 0; i < UU; ++i) {
-                    uint32_t ra[TT][8], rb[TT][8];
-#pragma unroll
-                    for (int t = 0; t < TT; ++t) {
+                    uint32_t ra[8], rb[8];
+                    {
                         uint32_t w[S::NW];
-                        const uint32_t a = rd + (uint32_t)((t * UU + (S::SPLIT ? i : 0)) * CELL + (S::SPLIT ? 0 : i * UNIT));
+                        const uint32_t a = rd + (uint32_t)(S::SPLIT ? i * CELL : i * UNIT);
                         load_codes<BITS, G32>(a, w);
-                        decode<BITS, G32>(w, shift, ra[t]);
+                        decode<BITS, G32>(w, shift, ra);
                         load_codes<BITS, G32>(a + 8 * (S::SPLIT ? UNIT : UU * UNIT), w);
-                        decode<BITS, G32>(w, shift, rb[t]);
+                        decode<BITS, G32>(w, shift, rb);
                     }
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {
                         if (NB > 1 && nb * 8 >= ncols) continue;
                         const uint4 x = lds16(xs[nb] + (uint32_t)(u + i) * 128u);
                         const uint4 y = lds16(xs[nb] + (uint32_t)(u + i) * 128u + 64u);
+                        float d[SETS][4];
+                        mma0(d[0], ra[0], rb[0], ra[1], rb[1], x.x, x.y);
+                        mma(d[0], ra[2], rb[2], ra[3], rb[3], x.z, x.w);
+                        if constexpr (G32)
+                            mma0(d[SETS - 1], ra[4], rb[4], ra[5], rb[5], y.x, y.y);
+                        else
+                            mma(d[0], ra[4], rb[4], ra[5], rb[5], y.x, y.y);
+                        mma(d[SETS - 1], ra[6], rb[6], ra[7], rb[7], y.z, y.w);
 #pragma unroll
-                        for (int t = 0; t < TT; ++t) {
-                            float d[SETS][4];
-                            mma0(d[0], ra[t][0], rb[t][0], ra[t][1], rb[t][1], x.x, x.y);
-                            mma(d[0], ra[t][2], rb[t][2], ra[t][3], rb[t][3], x.z, x.w);
-                            if constexpr (G32)
-                                mma0(d[SETS - 1], ra[t][4], rb[t][4], ra[t][5], rb[t][5], y.x, y.y);
-                            else
-                                mma(d[0], ra[t][4], rb[t][4], ra[t][5], rb[t][5], y.x, y.y);
-                            mma(d[SETS - 1], ra[t][6], rb[t][6], ra[t][7], rb[t][7], y.z, y.w);
-                            float(&o)[4] = acc[t][nb];
-#pragma unroll
-                            for (int h = 0; h < SETS; ++h) {
-                                const int z = i * SETS + h;
-                                auto half = [&](int b) {
-                                    const __half2 v = *reinterpret_cast<const __half2 *>(&sv[t][b][z / 2]);
-                                    return z & 1 ? __high2float(v) : __low2float(v);
-                                };
-                                const float sa = half(0), sb = half(1);
-                                o[0] = fmaf(sa, d[h][0], o[0]);
-                                o[1] = fmaf(sa, d[h][1], o[1]);
-                                o[2] = fmaf(sb, d[h][2], o[2]);
-                                o[3] = fmaf(sb, d[h][3], o[3]);
-                            }
+                        for (int h = 0; h < SETS; ++h) {
+                            const int z = i * SETS + h;
+                            auto half = [&](int b) {
+                                const __half2 v = *reinterpret_cast<const __half2 *>(&sv[b][z / 2]);
+                                return z & 1 ? __high2float(v) : __low2float(v);
+                            };
+                            const float sa = half(0), sb = half(1);
+                            acc[nb][0] = fmaf(sa, d[h][0], acc[nb][0]);
+                            acc[nb][1] = fmaf(sa, d[h][1], acc[nb][1]);
+                            acc[nb][2] = fmaf(sb, d[h][2], acc[nb][2]);
+                            acc[nb][3] = fmaf(sb, d[h][3], acc[nb][3]);
                         }
                     }
                 }
@@ -935,19 +912,14 @@ __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, i
                 rd += S::STAGE;
                 if (rd >= ring + STAGES * S::STAGE) rd -= STAGES * S::STAGE;
             }
-            if (u0 + n >= U && (round < full || share == 1) && end > beg) {  // the group is whole
+            if (u0 + n >= U && (round < full || share == 1) && end > beg) {  // the tile is whole
 #pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    const int tile = from + group * TT + t;
-                    if (tile >= to) continue;
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int c = nb * 8 + 2 * q + j;
-                            if (c < ncols) write(tile, c, acc[t][nb][j], acc[t][nb][2 + j]);
-                        }
-                }
+                    for (int j = 0; j < 2; ++j) {
+                        const int c = nb * 8 + 2 * q + j;
+                        if (c < ncols) write(from + tile, c, acc[nb][j], acc[nb][2 + j]);
+                    }
                 clear();
             }
         }
@@ -963,27 +935,22 @@ __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, i
         // the warps' parts of the shared tiles, added in order
         __syncthreads();  // no copies are in flight, and the rings are read
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-                slots[((warp * TT + t) * NB + nb) * 32 + lane] =
-                    make_float4(acc[t][nb][0], acc[t][nb][1], acc[t][nb][2], acc[t][nb][3]);
+        for (int nb = 0; nb < NB; ++nb)
+            slots[(warp * NB + nb) * 32 + lane] = make_float4(acc[nb][0], acc[nb][1], acc[nb][2], acc[nb][3]);
         __syncthreads();
-        for (int i = warp; i < rest * TT * NB; i += kWarps) {
-            const int grp = i / (TT * NB), t = i / NB % TT, nb = i % NB;
-            const int tile = from + (full * kWarps + grp) * TT + t;
-            if (tile >= to) continue;
+        for (int i = warp; i < rest * NB; i += kWarps) {
+            const int tile = i / NB, nb = i % NB;
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = grp * share; w < (grp + 1) * share; ++w) {
-                const float4 v = slots[((w * TT + t) * NB + nb) * 32 + lane];
+            for (int w = tile * share; w < (tile + 1) * share; ++w) {
+                const float4 v = slots[(w * NB + nb) * 32 + lane];
                 s.x += v.x;
                 s.y += v.y;
                 s.z += v.z;
                 s.w += v.w;
             }
             const int c = nb * 8 + 2 * q;
-            if (c < ncols) write(tile, c, s.x, s.z);
-            if (c + 1 < ncols) write(tile, c + 1, s.y, s.w);
+            if (c < ncols) write(from + full * kWarps + tile, c, s.x, s.z);
+            if (c + 1 < ncols) write(from + full * kWarps + tile, c + 1, s.y, s.w);
         }
         __syncthreads();  // before the rings are filled again
     }
@@ -991,9 +958,9 @@ __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, i
 
 // A kernel takes columns 8 NB at a time; which one is launched is a matter of
 // sizes alone (launch_sized below).
-template <int BITS, bool G32, bool PAIRS, int TT, int NB, int CTAS>
-__global__ void __launch_bounds__(kThreads, Kernel<BITS, G32, PAIRS, TT, NB, CTAS>::CTAS) moe_kernel(const __grid_constant__ MoeParams p) {
-    using S = Kernel<BITS, G32, PAIRS, TT, NB, CTAS>;
+template <int BITS, bool G32, bool PAIRS, int NB, int CTAS, bool PACKED>
+__global__ void __launch_bounds__(kThreads, Kernel<BITS, G32, PAIRS, NB, CTAS, PACKED>::CTAS) moe_kernel(const __grid_constant__ MoeParams p) {
+    using S = Kernel<BITS, G32, PAIRS, NB, CTAS, PACKED>;
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ Shared sh;
     // The down grid reads ids and weights before it waits: this grid's
@@ -1070,10 +1037,10 @@ __global__ void __launch_bounds__(kThreads, Kernel<BITS, G32, PAIRS, TT, NB, CTA
 }
 
 // The grid: every SM full, each CTA with an even run of tiles.
-template <int BITS, bool G32, bool PAIRS, int TT, int NB, int CTAS>
+template <int BITS, bool G32, bool PAIRS, int NB, int CTAS, bool PACKED>
 cudaError_t launch_one(const MoeParams &p, cudaStream_t stream) {
-    using S = Kernel<BITS, G32, PAIRS, TT, NB, CTAS>;
-    auto *kern = moe_kernel<BITS, G32, PAIRS, TT, NB, CTAS>;
+    using S = Kernel<BITS, G32, PAIRS, NB, CTAS, PACKED>;
+    auto *kern = moe_kernel<BITS, G32, PAIRS, NB, CTAS, PACKED>;
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised, one bit each
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1091,12 +1058,10 @@ cudaError_t launch_one(const MoeParams &p, cudaStream_t stream) {
 template <int BITS, bool G32, bool PAIRS>
 cudaError_t launch_sized(const MoeParams &p, int variant, cudaStream_t stream) {
     switch (variant) {
-        case MOE_FEW: return launch_one<BITS, G32, PAIRS, 1, 1, 3>(p, stream);
-        case MOE_8: return launch_one<BITS, G32, PAIRS, 2, 1, 3>(p, stream);
-        case MOE_8_LONG: return launch_one<BITS, G32, PAIRS, 2, 1, 2>(p, stream);
-        case MOE_16: return launch_one<BITS, G32, PAIRS, 2, 2, 2>(p, stream);
-        default:  // (room for 32 columns)
-            return launch_one<BITS, G32, PAIRS, BITS == 5 ? 1 : 2, 4, 2>(p, stream);
+        case MOE_8: return launch_one<BITS, G32, PAIRS, 1, 3, false>(p, stream);
+        case MOE_8_PACKED: return launch_one<BITS, G32, PAIRS, 1, 3, true>(p, stream);
+        case MOE_16: return launch_one<BITS, G32, PAIRS, 2, 2, true>(p, stream);
+        default: return launch_one<BITS, G32, PAIRS, 4, 2, true>(p, stream);
     }
 }
 

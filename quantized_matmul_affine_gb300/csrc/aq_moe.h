@@ -48,14 +48,8 @@ struct MoeParams {
 };
 // The products' kernels: columns (tokens of an expert) taken at a time, and
 // whether they come from packed rows.
-enum MoeVariant {
-    MOE_FEW = 0,  // 8, one tile a step
-    MOE_8 = 1,    // 8, two tiles a step, three CTAs an SM
-    MOE_8_LONG,   // 8, packed, two CTAs an SM with more room each
-    MOE_16,       // 16, packed
-    MOE_32,       // 32, packed
-};
-inline bool moe_packed(int variant) { return variant >= MOE_8_LONG; }
+enum MoeVariant { MOE_8 = 0, MOE_8_PACKED, MOE_16, MOE_32 };
+inline bool moe_packed(int variant) { return variant >= MOE_8_PACKED; }
 
 // Packed source rows: [rows][K] fp16 in MMA order, then the group sums, 16 bytes
 // of either part a block of 8 groups (4 of 128 and zeros), then the inverse
