@@ -906,22 +906,26 @@ def aq_embed(ids, Wq, scales, biases, bits: int, group_size: int, dtype, scale: 
     wide = ids.dtype is torch.int64
     if not wide and ids.dtype is not _I32:
         raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
-    if scales.dim() != 2:
+    shape = scales.shape
+    if len(shape) != 2:
         raise ValueError("scales must be [N, K/group_size]")
-    N, G = scales.shape
-    K = G * group_size
-    _check_weights(Wq, scales, biases, N, K, bits, group_size)
+    N, K = shape[0], shape[1] * group_size
+    if Wq.numel() * Wq.element_size() * 8 != N * K * bits or biases.shape != shape or \
+            scales.dtype is not torch.float16 or biases.dtype is not torch.float16:
+        _check_weights(Wq, scales, biases, N, K, bits, group_size)  # says which
+        if biases.shape != shape:
+            raise ValueError(f"biases must be {list(shape)}, got {list(biases.shape)}")
     index = ids.get_device()
     if index < 0:
         raise ValueError("ids must be a CUDA tensor")
-    if not Wq.get_device() == scales.get_device() == biases.get_device() == index:
+    if Wq.get_device() != index or scales.get_device() != index or biases.get_device() != index:
         raise ValueError("ids and the table must be on one device")
     if not (ids.is_contiguous() and Wq.is_contiguous() and scales.is_contiguous() and biases.is_contiguous()):
         raise ValueError("ids and the table must be contiguous")
     T = ids.numel()
     if out is None:
         shape = (*ids.shape, K)
-        out = torch.empty(shape, dtype=dtype, device=ids.device) if stream is None else \
+        out = scales.new_empty(shape, dtype=dtype) if stream is None else \
             _empty(shape, dtype, ids.device, stream)
     else:
         if out.get_device() != index:

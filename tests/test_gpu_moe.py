@@ -57,6 +57,79 @@ def test_experts_formats(bits, group, dtype):
     _run(3, 256, 128, 5, 2, bits, group, dtype)
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("bits", [2, 3, 4, 5, 6, 8])
+@pytest.mark.parametrize("T,K,inner,E,top", [
+    (3, 8192, 128, 2, 2),   # 8 columns, packed rows
+    (14, 640, 128, 3, 2),   # 16 columns
+    (50, 384, 256, 2, 1),   # 32 columns
+])
+def test_experts_packed(T, K, inner, E, top, bits, group):
+    _run(T, K, inner, E, top, bits, group, F16 if bits & 1 else BF16)
+
+
+@pytest.mark.parametrize("K", [64, 128, 192, 256, 320, 512, 576])
+@pytest.mark.parametrize("bits,group", [(3, 64), (5, 32), (4, 32), (8, 64)])
+@pytest.mark.parametrize("T", [2, 20])
+def test_experts_widths(T, K, bits, group):
+    """Rows of codes and scales that are and are not whole 16-byte pieces."""
+    _run(T, K, 64 * (K // 128 + 1), 3, 2, bits, group, F16)
+
+
+@pytest.mark.parametrize("T", [2, 20])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_experts_offsets(T, group):
+    """Scales and biases that are aligned to their elements only."""
+    mats = _layer(3, 256, 128, 4, group, 5)
+
+    def shifted(t):
+        buf = torch.zeros(t.numel() + 1, dtype=t.dtype, device=t.device)
+        buf[1:] = t.flatten()
+        return buf[1:].view(t.shape)
+
+    moved = [(w, shifted(a), shifted(b)) for w, a, b in mats]
+    assert all(a.data_ptr() % 4 == 2 for _, a, _ in moved)
+    x, ids, w = _tokens(T, 256, BF16, 6), _ids(T, 3, 2, 7), _weights(T, 2, 8)
+    y = aq.aq_moe_experts(x, aq.AqExperts(*moved, 4, group), ids, w)
+    assert torch.equal(y, aq.aq_moe_experts(x, aq.AqExperts(*mats, 4, group), ids, w))
+
+
+def test_experts_uneven():
+    """One expert with most of the tokens, others with few or none."""
+    ids = torch.full((200, 2), -1, dtype=torch.int32)
+    ids[:, 0] = 5
+    ids[3:9, 1] = 0
+    ids[100, 1] = 39
+    ids[::7, 1] = 20
+    _run(200, 512, 256, 40, 2, 4, 64, BF16, ids=ids.cuda())
+
+
+def test_written_just_before():
+    """Weights, ids and tokens written by the launches right before the call,
+    over and over: nothing is read before they are complete."""
+    E, K, inner = 6, 512, 256
+    w = [torch.randn(E * r, c, generator=_gen(i)).half().cuda() for i, (r, c) in
+         enumerate(((inner, K), (inner, K), (K, inner)))]
+    made = [tuple(t.view(E, -1, t.shape[1]) for t in aq.aq_quantize(m, 4)) for m in w]
+    live = [tuple(t.clone() for t in m) for m in made]
+    ex = aq.AqExperts(*live, 4, 64)
+    x0, ids0, wt = _tokens(4, K, F16, 1), _ids(4, E, 2, 2), _weights(4, 2, 3)
+    want = aq.aq_moe_experts(x0, aq.AqExperts(*made, 4, 64), ids0, wt)
+    x, ids = torch.zeros_like(x0), torch.zeros_like(ids0)
+    for _ in range(20):
+        for m in live:
+            for t in m:
+                t.zero_()
+        x.zero_()
+        ids.fill_(-1)
+        for a, b in zip(live, made):
+            for t, s in zip(a, b):
+                t.copy_(s)
+        ids.copy_(ids0)
+        x.copy_(x0)
+        assert torch.equal(aq.aq_moe_experts(x, ex, ids, wt), want)
+
+
 @pytest.mark.parametrize("T,K,inner,E,top,bits,group", [
     (1, 64, 64, 1, 1, 4, 64),          # the smallest
     (1, 64, 64, 1, 1, 3, 32),
@@ -271,9 +344,13 @@ def test_streams():
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in xs]
     got = []
-    for _ in range(20):
-        for x, s in zip(xs, streams):
-            got.append(aq.aq_moe(x, router, ex, stream=s)[0])
+    for i in range(20):
+        for x, s in zip(xs, streams):  # by argument, and as the current stream
+            if i & 1:
+                got.append(aq.aq_moe(x, router, ex, stream=s)[0])
+            else:
+                with torch.cuda.stream(s):
+                    got.append(aq.aq_moe(x, router, ex)[0])
     torch.cuda.synchronize()
     for i, y in enumerate(got):
         assert torch.equal(y, want[i % 2])
