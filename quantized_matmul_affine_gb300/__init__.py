@@ -847,19 +847,20 @@ def aq_moe_workspace_bytes(experts: AqExperts, T: int, top_k: int) -> int:
     return n
 
 
-def aq_moe_route(x, router: AqRouter, out=None, stream=None) -> tuple:
+def aq_moe_route(x, router: AqRouter, out=None,
+                 stream: Optional[torch.cuda.Stream] = None) -> tuple:
     """The experts of each token of x [T, K]: (experts int32 [T, top_k], each
     row ascending, weights float32 [T, top_k])."""
     T = _moe_tokens(x, router._shape[1], router._index, router._dtype)
     ids, weights, ip, wp = _moe_pair(out, T, router.top_k, x, stream)
-    st = _lib.aq_moe_route(router._ref, x.data_ptr(), T, ip, wp, _stream(stream))
+    st = load().aq_moe_route(router._ref, x.data_ptr(), T, ip, wp, _stream(stream))
     if st:
         _check(st, "aq_moe_route")
     return ids, weights
 
 
 def aq_moe_experts(x, experts: AqExperts, ids, weights, out=None, workspace=None,
-                   stream=None) -> torch.Tensor:
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """y[t] = sum_j weights[t, j] * expert ids[t, j] of x[t]; ids int32
     [T, top_k] (outside 0..E-1: none), weights float32 [T, top_k]."""
     index = experts._index
@@ -870,7 +871,7 @@ def aq_moe_experts(x, experts: AqExperts, ids, weights, out=None, workspace=None
     ip = _moe_given(ids, "experts", _I32, T, top_k, index)
     wp = _moe_given(weights, "weights", _F32, T, top_k, index)
     out, op, ws, n, hold = _moe_out(x, out, workspace, experts, T, top_k, stream)
-    st = _lib.aq_moe_experts(experts._ref, AQ_BF16 if x.dtype is torch.bfloat16 else AQ_F16,
+    st = load().aq_moe_experts(experts._ref, AQ_BF16 if x.dtype is torch.bfloat16 else AQ_F16,
                              x.data_ptr(), T, top_k, ip, wp, op, ws, n, _stream(stream))
     if st:
         _check(st, "aq_moe_experts")
@@ -878,7 +879,7 @@ def aq_moe_experts(x, experts: AqExperts, ids, weights, out=None, workspace=None
 
 
 def aq_moe(x, router: AqRouter, experts: AqExperts, out=None, routed=None, workspace=None,
-           stream=None) -> tuple:
+           stream: Optional[torch.cuda.Stream] = None) -> tuple:
     """The whole layer: routes x [T, K] and runs the chosen experts.  Returns
     (y [T, K], experts int32 [T, top_k], weights float32 [T, top_k]); routed:
     tensors for the last two."""
@@ -890,14 +891,14 @@ def aq_moe(x, router: AqRouter, experts: AqExperts, out=None, routed=None, works
         raise ValueError("router and experts must be on one device")
     ids, weights, ip, wp = _moe_pair(routed, T, router.top_k, x, stream)
     out, op, ws, n, hold = _moe_out(x, out, workspace, experts, T, router.top_k, stream)
-    st = _lib.aq_moe(router._ref, experts._ref, x.data_ptr(), T, ip, wp, op, ws, n, _stream(stream))
+    st = load().aq_moe(router._ref, experts._ref, x.data_ptr(), T, ip, wp, op, ws, n, _stream(stream))
     if st:
         _check(st, "aq_moe")
     return out, ids, weights
 
 
 def aq_embed(ids, Wq, scales, biases, bits: int, group_size: int, dtype, scale: float = 1.0,
-             out=None, stream=None) -> torch.Tensor:
+             out=None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Rows of a quantised table by token: scale * row ids[...] as dtype (fp16
     or bf16) [..., K]; ids int32 or int64, outside 0..N-1 a row of zeros.  Wq
     [N, K*bits/32], scales and biases fp16 [N, K/group_size]."""
@@ -925,14 +926,14 @@ def aq_embed(ids, Wq, scales, biases, bits: int, group_size: int, dtype, scale: 
     T = ids.numel()
     if out is None:
         shape = (*ids.shape, K)
-        out = scales.new_empty(shape, dtype=dtype) if stream is None else \
+        out = torch.empty(shape, dtype=dtype, device=ids.device) if stream is None else \
             _empty(shape, dtype, ids.device, stream)
     else:
         if out.get_device() != index:
             raise ValueError("out must be on ids' device")
         _check_out(out, "out", T * K, dtype)
         _dev(out, "out")
-    st = _lib.aq_embed(AQ_BF16 if dtype is torch.bfloat16 else AQ_F16, ids.data_ptr(), 8 if wide else 4, T,
+    st = load().aq_embed(AQ_BF16 if dtype is torch.bfloat16 else AQ_F16, ids.data_ptr(), 8 if wide else 4, T,
                        Wq.data_ptr(), scales.data_ptr(), biases.data_ptr(), N, K, bits, group_size, scale,
                        out.data_ptr(), _stream(stream))
     if st:
