@@ -518,8 +518,9 @@ aq_status aq_attention_batch(const aq_cache *cache, int64_t layer, int dtype, co
  * E experts for each token; each expert is a gated MLP whose matrices are in
  * the weight format:
  *   y[t] = sum over j of weights[t][j] * Wd_e . (silu(Wg_e . x[t]) * (Wu_e . x[t])),
- * e = experts[t][j].  Only the experts that some token picked are read, each
- * once for up to 32 of its tokens.  (The pages have no such layer; its products
+ * e = experts[t][j].  Only the experts that some token picked are read, from
+ * memory once; an expert with more tokens than a kernel takes at a time (8, 16 or
+ * 32, by the call's sizes) from L2 again.  (The pages have no such layer; its products
  * follow their gate/up with SiLU and their factored form.)
  */
 /* Largest number of tokens of a call, of experts, and of experts a token. */
@@ -575,9 +576,9 @@ typedef struct aq_experts {
  *   weights_dev  float [T][top_k], written entirely.
  * The choice is the one that logits in 64 bits give: where fp32 sums leave it
  * open, the logits in question are summed again with their rounding errors.
- * Weights come from fp32 logits.  A token whose logits are not finite gets
- * top_k distinct experts, which ones is unspecified, and weights that are not
- * finite; other tokens are not affected.
+ * Weights come from fp32 logits.  A logit that is not a number ranks last; a
+ * token with logits that are not finite still gets top_k distinct experts, but
+ * which ones and its weights are unspecified; other tokens are not affected.
  * Errors: AQ_ERR_INVALID_ARG for a bad router, T outside 1..AQ_MOE_MAX_TOKENS
  * or NULL pointers; AQ_ERR_UNSUPPORTED for a bias with softmax scores;
  * AQ_ERR_MISALIGNED; AQ_ERR_CUDA.

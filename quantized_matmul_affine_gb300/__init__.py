@@ -9,6 +9,7 @@ this package fails if libaq.so cannot be loaded.
     y = aq_matmul(x, Wq, scales, biases, bits)        # fp16 x -> fp16 y
     y = aq_matmul_bf16(x, Wq, scales, biases, bits)   # bf16 x -> bf16 y
     Wq = aq_pack(codes, bits)                         # uint8 codes -> uint32 words
+    y, ids, weights = aq_moe(x, AqRouter(...), AqExperts(...))  # experts' layer
 """
 from __future__ import annotations
 

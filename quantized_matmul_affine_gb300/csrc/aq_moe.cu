@@ -14,6 +14,11 @@
 //     of two 16-bit floats are exact in fp32, two-sums keep what each addition
 //     rounds off), which is good to about 2^-46 of the sum of |x w|.
 //   * weights come from the fp32 logits.
+// One launch, bound by latency (loads, two cluster barriers, the choice): one
+// token and 128 experts of 2048 6 us, 256 tokens and 256 experts of 5120 27 us
+// (the weights, read by 16 clusters from L2, are 42 MB of that).  The bound that
+// the sums' rounding errors allow leaves about one of 10^3 tokens to be summed
+// again; without them it was one of 25, and each costs the call 4 us and more.
 // A cluster of 8 or 16 CTAs takes 8 or 16 tokens: its CTAs slice K, their warps deal
 // the experts (16 an MMA tile) and, where there are fewer tiles than warps,
 // slice K further; the parts are sent to the CTA that chooses for the token,
@@ -383,9 +388,8 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const __grid_constant
 template <bool BF16, int NB, int LANES>
 cudaError_t route_run(RouteParams p, cudaStream_t stream) {
     auto *kern = route_kernel<BF16, NB, LANES>;
-    // K in 16 slices where one cluster has much to read alone (1 token of 5120,
-    // 256 experts: WIDE us in 8 slices, WIDE16 in 16), if the device has room
-    // for such a cluster; else in 8
+    // K in 16 slices where one cluster has much to read alone, if the device has
+    // room for such a cluster; else in 8
     static std::atomic<int> wide{-1};
     p.cluster = 8;
     if (p.T <= 64 && (int64_t)p.E * p.K >= 1 << 19) {
@@ -464,11 +468,13 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 }  // namespace
 
 // Which kernel runs a product over K, by the tokens a busy expert has on
-// average, were all experts picked alike: 8, 16 or 32 at a time (an expert with
-// more takes its weights from L2 again).  Whether the rows are packed first by
-// a launch of their own, about 3 us, or by each CTA for itself, by how many
-// values the CTAs would pack.  Measured, us a call of the layer: 5 tokens a step
-// and 60 experts of 2048 (700 values of K by tokens... see the table below).
+// average, were all experts picked alike: 8, 16 or 32 columns at a time.
+// Measured (us a layer with 8 / 16 / 32 columns): 33 tokens of 64 experts, 3.1
+// each, 219 / 228 / 223; 256 of 128, 16 each, 495 / 367 / 316.  Whether the rows
+// are packed first by a launch of their own, about 3 us, or by each CTA for
+// itself, by the values a busy expert's tokens have (packed / not): 8 tokens of
+// 8 experts of 4096, 9000 values, 205 / 228; 48 tokens of 64 experts of 2048,
+// 6300, 82 / 83; one token of 2048, 32 / 28.
 static int moe_variant(const aq_experts *x, int64_t T, int top, int64_t K) {
     const double E = (double)x->E;
     const double busy = top >= E ? E : E * (1.0 - std::pow(1.0 - top / E, (double)T));

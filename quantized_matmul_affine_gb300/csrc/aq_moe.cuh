@@ -11,17 +11,17 @@
 //
 //   * Work is the list of 16-row MMA tiles (8 gate and the same 8 up rows, or
 //     16 down rows) of all busy experts, in expert order, dealt to the CTAs in
-//     even runs.  A CTA takes its run expert by expert, up to 16 tiles a pass.
-//     Within a pass the (tile, 64-value unit) pairs, tile after tile, are
-//     dealt to the 8 warps in even runs, so no shape leaves a warp idle; a
-//     warp's part of tile t goes to slot t + warp (the pairs (tile, warp) that
-//     occur lie on a monotone path, so their sums t + warp differ), and a
-//     tile's slots are added in warp order: the result does not depend on
-//     timing.
-//   * Codes go from global memory to registers, several units ahead: lane
-//     (g, q) of the MMA layout reads the 16 codes [16q, 16q + 16) of rows g and
-//     g + 8.  The MMA's k order within a unit is whatever the decode gives
-//     (Order<BITS>): the activations are staged in that order.
+//     runs of even cost.  A CTA takes its run expert by expert; an expert's tiles
+//     go round the 8 warps, and the last, unfull round's tiles are shared by 2, 4
+//     or 8 warps that split K and add their parts in order: the result does not
+//     depend on timing.
+//   * A warp streams its tiles by itself: three steps of 128 values of K, 64
+//     bytes of 16 rows each at 4 bits, are on their way to its own ring in shared
+//     memory by asynchronous copies, with the blocks of scales they need, and the
+//     next tile's follow without a stop.  Lane (g, q) of the MMA layout reads the
+//     16 codes [16q, 16q + 16) of rows g and g + 8 of a unit.  The MMA's k order
+//     within a unit is whatever the decode gives (Order): the activations are
+//     staged, or packed, in that order.
 //   * A code masked in place in an fp16 with zero exponent is the exact
 //     subnormal q * 2^(p - 24), p its bit position; the activation paired with
 //     it carries 2^-p.  Activations are fp16 with one power of two per token
@@ -30,7 +30,20 @@
 //     2^-39 of it at most; h (fp32) is rounded to fp16's 11 bits, 2^-11 of a
 //     value at most, an eighth of what rounding it to bf16 would cost.
 //     Sums of codes, group sums and everything after them are fp32.
-//   * Tokens of an expert are MMA columns, 8, 16 or 32 at a time.
+//   * The biases enter as products of their own, 8 groups a step, with the
+//     columns' group sums, which are kept as two fp16 parts (22 bits).
+//   * Tokens of an expert are MMA columns, 8, 16 or 32 at a time; blocks of 8
+//     that are empty are skipped.  An expert with more takes its weights again,
+//     from L2.
+//
+// Bound by HBM where the experts are large: 8 experts of 4096 x 13824 at 4 bits
+// (688 MB) take 205 us for both products, 3.4 TB/s; with the arithmetic left out
+// 190 us, with the codes left out 68 us, and with the loop left out 44 us (five
+// dependent launches, plans, staged columns).  So the codes alone stream at 5.1
+// TB/s, the arithmetic is hidden, and what remains is latency at a kernel's
+// start, which is all there is for one token (128 experts of 2048 x 768: 28 us
+// for 22 MB).  24 warps of 80 registers an SM: 16 warps of 128 with two tiles a
+// step were as fast on large runs and slower on short ones.
 #pragma once
 
 #include "aq_moe.h"
