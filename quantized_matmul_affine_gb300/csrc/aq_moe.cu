@@ -17,7 +17,7 @@
 // One launch, bound by latency (loads, two cluster barriers, the choice): one
 // token and 128 experts of 2048 6 us, 256 tokens and 256 experts of 5120 27 us
 // (the weights, read by 16 clusters from L2, are 42 MB of that).  The bound that
-// the sums' rounding errors allow leaves about one of 10^3 tokens to be summed
+// the sums' rounding errors allow leaves about one of 300 tokens to be summed
 // again; without them it was one of 25, and each costs the call 4 us and more.
 // A cluster of 8 or 16 CTAs takes 8 or 16 tokens: its CTAs slice K, their warps deal
 // the experts (16 an MMA tile) and, where there are fewer tiles than warps,
@@ -123,10 +123,11 @@ __device__ void choose(const RouteParams &p, int t, const float *sums, double *k
     float logit[LANES], val[LANES];
     float slack = 0.f;      // the largest error bound of a value
     uint32_t open = 0u;     // experts not yet taken, by position
-    // what the sums leave out: a step's two products truncate to 2^-22 of their
-    // magnitudes each, the last rounding is 2^-24 of the logit; what the errors'
-    // own sums and those of the magnitudes round is smaller by 2^-20
-    constexpr float kUlps = 2.5f * 2.384185791015625e-07f;
+    // what the sums leave out: a product of 16 may truncate each of its 17 terms
+    // at 2^-24 of the largest, 4.25 * 2^-22 of the magnitudes at most, a step has
+    // two; the last rounding is 2^-24 of the logit, what the errors' own sums and
+    // those of the magnitudes round is smaller by 2^-20
+    constexpr float kUlps = 9.f * 2.384185791015625e-07f;
 #pragma unroll
     for (int j = 0; j < LANES; ++j) {
         logit[j] = val[j] = -INFINITY;
