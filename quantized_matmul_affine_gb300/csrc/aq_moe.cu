@@ -15,9 +15,9 @@
 //     rounds off), which is good to about 2^-46 of the sum of |x w|.
 //   * weights come from the fp32 logits.
 // One launch, bound by latency (loads, two cluster barriers, the choice): one
-// token and 128 experts of 2048 6 us, 256 tokens and 256 experts of 5120 27 us
+// token and 128 experts of 2048 6 us, 256 tokens and 256 experts of 5120 32 us
 // (the weights, read by 16 clusters from L2, are 42 MB of that).  The bound that
-// the sums' rounding errors allow leaves about one of 300 tokens to be summed
+// the sums' rounding errors allow leaves about one of 500 tokens to be summed
 // again; without them it was one of 25, and each costs the call 4 us and more.
 // A cluster of 8 or 16 CTAs takes 8 or 16 tokens: its CTAs slice K, their warps deal
 // the experts (16 an MMA tile) and, where there are fewer tiles than warps,
@@ -123,11 +123,11 @@ __device__ void choose(const RouteParams &p, int t, const float *sums, double *k
     float logit[LANES], val[LANES];
     float slack = 0.f;      // the largest error bound of a value
     uint32_t open = 0u;     // experts not yet taken, by position
-    // what the sums leave out: a product of 16 may truncate each of its 17 terms
-    // at 2^-24 of the largest, 4.25 * 2^-22 of the magnitudes at most, a step has
-    // two; the last rounding is 2^-24 of the logit, what the errors' own sums and
-    // those of the magnitudes round is smaller by 2^-20
-    constexpr float kUlps = 9.f * 2.384185791015625e-07f;
+    // what the sums leave out: a product of 16 may truncate each of its 16 terms
+    // at 2^-24 of the largest, 4 * 2^-22 of the magnitudes at most; the last
+    // rounding is 2^-24 of the logit, what the errors' own sums and those of the
+    // magnitudes round is smaller by 2^-20
+    constexpr float kUlps = 4.5f * 2.384185791015625e-07f;
 #pragma unroll
     for (int j = 0; j < LANES; ++j) {
         logit[j] = val[j] = -INFINITY;
@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
     for (int tile = warp / cuts; tile * 16 < p.E; tile += kWarps / cuts) {
         const int ra = min(tile * 16 + g, p.E - 1), rb = min(tile * 16 + 8 + g, p.E - 1);
         const uint16_t *wa = p.w + (size_t)ra * p.K + 8 * q, *wb = p.w + (size_t)rb * p.K + 8 * q;
-        // a step's two products start from zero and are added with their rounding
-        // errors: s + r; m the sums of magnitudes
+        // each product starts from zero and is added with the rounding error: s + r;
+        // m the sums of magnitudes
         float s[NB][4], r[NB][4], m[NB][4];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -299,11 +299,14 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(xs[nb] + 32 * k);
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_x<BF16>(d, a.x, b.x, a.y, b.y, x.x, x.y);
-                mma_x<BF16>(d, a.z, b.z, a.w, b.w, x.z, x.w);
+                float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_x<BF16>(d0, a.x, b.x, a.y, b.y, x.x, x.y);
+                mma_x<BF16>(d1, a.z, b.z, a.w, b.w, x.z, x.w);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) two_sum(s[nb][i], r[nb][i], d[i]);
+                for (int i = 0; i < 4; ++i) {
+                    two_sum(s[nb][i], r[nb][i], d0[i]);
+                    two_sum(s[nb][i], r[nb][i], d1[i]);
+                }
                 mma_x<BF16>(m[nb], a.x & kAbs, b.x & kAbs, a.y & kAbs, b.y & kAbs, x.x & kAbs,
                             x.y & kAbs);
                 mma_x<BF16>(m[nb], a.z & kAbs, b.z & kAbs, a.w & kAbs, b.w & kAbs, x.z & kAbs,
