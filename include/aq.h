@@ -576,9 +576,10 @@ typedef struct aq_experts {
  *   weights_dev  float [T][top_k], written entirely.
  * The choice is the one that logits in 64 bits give: where fp32 sums leave it
  * open, the logits in question are summed again with their rounding errors.
- * Weights come from fp32 logits.  A logit that is not a number ranks last; a
- * token with logits that are not finite still gets top_k distinct experts, but
- * which ones and its weights are unspecified; other tokens are not affected.
+ * Weights come from fp32 logits; those of a token with a logit past fp32's range
+ * are unspecified.  A logit that is not a number ranks last; a token with
+ * infinities or NaN still gets top_k distinct experts, but which ones and its
+ * weights are unspecified; other tokens are not affected.
  * Errors: AQ_ERR_INVALID_ARG for a bad router, T outside 1..AQ_MOE_MAX_TOKENS
  * or NULL pointers; AQ_ERR_UNSUPPORTED for a bias with softmax scores;
  * AQ_ERR_MISALIGNED; AQ_ERR_CUDA.

@@ -12,7 +12,8 @@
 //     are in or out for certain; where others are left to choose from, their
 //     logits are summed again with the rounding errors carried along (products
 //     of two 16-bit floats are exact in fp32, two-sums keep what each addition
-//     rounds off), which is good to about 2^-46 of the sum of |x w|.
+//     rounds off), which is good to about 2^-46 of the sum of |x w|, or in 64
+//     bits where a product or a sum passes fp32's range.
 //   * weights come from the fp32 logits.
 // One launch, bound by latency (loads, two cluster barriers, the choice): one
 // token and 128 experts of 2048 6 us, 256 tokens and 256 experts of 5120 32 us
@@ -82,6 +83,18 @@ __device__ __forceinline__ void two_sum(float &s, float &e, float v) {
     s = t;
 }
 
+// One logit in 64 bits, in every lane: finite for every finite row.
+template <bool BF16>
+__device__ __noinline__ double wide_logit(const uint16_t *x, const uint16_t *w, int K) {
+    double d = 0.0;
+    for (int k = (threadIdx.x & 31) * 8; k < K; k += 256)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d = fma((double)value<BF16>(x[k + i]), (double)value<BF16>(w[k + i]), d);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
+    return d;
+}
+
 // One logit to about 2^-46 of its sum of magnitudes, in every lane.  Four sums
 // a lane, so that the additions of one do not wait for another's.
 template <bool BF16>
@@ -103,7 +116,22 @@ __device__ __noinline__ double precise_logit(const uint16_t *x, const uint16_t *
     for (int i = 0; i < 4; ++i) d += (double)s[i] + (double)e[i];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
-    return d;
+    // (a sum that passes the largest float, though the logit may not, ends as NaN)
+    return fabs(d) < INFINITY ? d : wide_logit<BF16>(x, w, K);
+}
+
+// Whether a row has neither infinities nor NaN, in every lane.
+template <bool BF16>
+__device__ bool finite_row(const uint16_t *x, int K) {
+    constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
+    bool ok = true;
+    for (int k = (threadIdx.x & 31) * 8; k < K; k += 256) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(x + k);
+        const uint32_t v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ok = ok && (v[i] & kExp) != kExp && (v[i] >> 16 & kExp) != kExp;
+    }
+    return __all_sync(0xFFFFFFFFu, ok);
 }
 
 // Floats in the order of unsigned integers; NaN below everything.
@@ -122,6 +150,7 @@ __device__ void choose(const RouteParams &p, int t, const float *sums, double *k
     const bool sigmoid = p.score == AQ_SCORE_SIGMOID;
     float logit[LANES], val[LANES];
     float slack = 0.f;      // the largest error bound of a value
+    bool lost = false;      // an expert's sums pass fp32's range: they tell nothing
     uint32_t open = 0u;     // experts not yet taken, by position
     // what the sums leave out: a product of 16 may truncate each of its 16 terms
     // at 2^-24 of the largest, 4 * 2^-22 of the magnitudes at most; the last
@@ -136,6 +165,7 @@ __device__ void choose(const RouteParams &p, int t, const float *sums, double *k
             const float s = sums[e];
             logit[j] = s;
             float bound = kUlps * sums[p.E + e];
+            lost = lost || !(bound < INFINITY);
             float v = s;
             if (p.bias) {
                 v = 1.f / (1.f + expf(-s)) + p.bias[e];
@@ -147,6 +177,7 @@ __device__ void choose(const RouteParams &p, int t, const float *sums, double *k
         }
     }
     slack = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(slack)));
+    lost = __any_sync(0xFFFFFFFFu, lost);
 
     // the top_k of the fp32 values: the last one taken is the border
     uint32_t left = open, taken = 0u;
@@ -180,16 +211,26 @@ __device__ void choose(const RouteParams &p, int t, const float *sums, double *k
         else if (val[j] >= border - 2.f * slack)
             doubt |= 1u << j;
     }
+    if (lost) {  // the border is nowhere
+        sure = 0u;
+        doubt = open;
+    }
     const int n_sure = __reduce_add_sync(0xFFFFFFFFu, __popc(sure));
     const int n_doubt = __reduce_add_sync(0xFFFFFFFFu, __popc(doubt));
-    // (a border that is not finite decides nothing: the fp32 choice stands)
-    if (n_sure + n_doubt > p.top && fabsf(border) < INFINITY) {
+    // (The fp32 choice stands where the border is a bias that is not finite, and
+    // for a token that is not.)
+    if (lost ? finite_row<BF16>(p.x + (size_t)t * p.K, p.K)
+             : n_sure + n_doubt > p.top && fabsf(border) < INFINITY) {
 #pragma unroll
         for (int j = 0; j < LANES; ++j)
             for (uint32_t m = __ballot_sync(0xFFFFFFFFu, doubt >> j & 1u); m; m &= m - 1u) {
                 const int e = j * 32 + __ffs(m) - 1;
                 double d = precise_logit<BF16>(p.x + (size_t)t * p.K, p.w + (size_t)e * p.K, p.K);
-                if (lane == (e & 31)) keep[e] = p.bias ? 1.0 / (1.0 + exp(-d)) + (double)p.bias[e] : d;
+                if (lane == (e & 31)) {
+                    const double v = p.bias ? 1.0 / (1.0 + exp(-d)) + (double)p.bias[e] : d;
+                    keep[e] = v == v ? v : -INFINITY;  // (the lanes below agree on an order without NaN)
+                    if (lost) logit[j] = (float)d;
+                }
             }
         __syncwarp();
         taken = sure;
@@ -247,8 +288,9 @@ __device__ void choose(const RouteParams &p, int t, const float *sums, double *k
 #pragma unroll
     for (int j = 0; j < LANES; ++j) {
         const uint32_t on = __ballot_sync(0xFFFFFFFFu, taken >> j & 1u);
-        if (taken >> j & 1u) {
-            const size_t at = (size_t)t * p.top + before + __popc(on & ((1u << lane) - 1u));
+        const int place = before + __popc(on & ((1u << lane) - 1u));
+        if ((taken >> j & 1u) && place < p.top) {
+            const size_t at = (size_t)t * p.top + place;
             p.ids[at] = j * 32 + lane;
             p.weights[at] = val[j] / sum * p.scale;
         }
