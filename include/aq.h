@@ -37,7 +37,8 @@
  *   - Entry points are thread-safe when different threads use different
  *     streams; results do not depend on the thread or stream.
  *   - One device a process: what a kernel needs set on the device (its
- *     shared-memory size) is set on that of its first call.
+ *     shared-memory size) is set on that of its first call.  (The experts'
+ *     calls and the embedding lookup set it on every device they run on.)
  *   - Results are deterministic: the same inputs give bit-identical outputs,
  *     call after call (fixed-order reductions, no atomics on data; the
  *     reference counts of pages are integers, whose sums have no order).

@@ -24,13 +24,13 @@
 // the experts (16 an MMA tile) and, where there are fewer tiles than warps,
 // slice K further; the parts are sent to the CTA that chooses for the token,
 // one warp a token.
+#include "aq_device.h"
 #include "aq_moe.h"
 #include "aq_ptx.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include <atomic>
 #include <cmath>
 #include <initializer_list>
 
@@ -436,11 +436,13 @@ cudaError_t route_run(RouteParams p, cudaStream_t stream) {
     auto *kern = route_kernel<BF16, NB, LANES>;
     // K in 16 slices where one cluster has much to read alone, if the device has
     // room for such a cluster; else in 8
-    static std::atomic<int> wide{-1};
+    static PerDevice wide;
     p.cluster = 8;
     if (p.T <= 64 && (int64_t)p.E * p.K >= 1 << 19) {
-        int w = wide.load(std::memory_order_relaxed);
-        if (w < 0) {
+        int dev = 0;
+        const cudaError_t got = cudaGetDevice(&dev);
+        if (got != cudaSuccess) return got;
+        const bool w = wide(dev, [&] {
             cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
@@ -457,9 +459,8 @@ cudaError_t route_run(RouteParams p, cudaStream_t stream) {
             int n = 0;
             if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
             if (e != cudaSuccess) cudaGetLastError();
-            w = e == cudaSuccess && n > 0;
-            wide.store(w, std::memory_order_relaxed);
-        }
+            return e == cudaSuccess && n > 0;
+        });
         if (w) p.cluster = 16;
     }
     p.slices = p.cluster * kWarps;
