@@ -543,10 +543,11 @@ __device__ __forceinline__ void stage_columns(const MoeParams &p, int ncols, Sha
             }
             float v[16];
             widen16<PAIRS>(p, raw[r], v);
-            // 2^up puts the largest magnitude into [2^14, 2^15)
+            // 2^up puts the largest magnitude into [2^14, 2^15) (one below 2^-112
+            // less high: 2^-126 is the smallest inverse that is a normal float)
             const int ex = (int)(sh.peak[c] >> 23);
-            int up = ex == 0 || ex == 255 ? 0 : 14 + 127 - ex;
-            up = up > 100 ? 100 : up;
+            int up = ex == 255 ? 0 : 14 + 127 - ex;
+            up = up > 126 ? 126 : up;
             const float f = __int_as_float((127 + up) << 23);
             if (k == 0) sh.undo[c] = __int_as_float((127 - up) << 23);
             float s = 0.f, s2 = 0.f;
