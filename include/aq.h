@@ -603,7 +603,9 @@ aq_status aq_moe_route(const aq_router *router, const void *x_dev, int64_t T,
  *                calls that may overlap use distinct ones.
  * Products are fp32 sums; between the two products h is kept in fp32 and enters
  * the second rounded to fp16's 11 bits (times a power of two); y is rounded
- * once.  Deterministic.  The output must not alias weights that the next
+ * once.  A value of x or h far below its row's largest, 2^-20 of it and less at 2
+ * bits, 2^-28 at 6 and 8, is off by up to 2^-31 (2^-39) of that largest.
+ * Deterministic.  The output must not alias weights that the next
  * matmul call on the stream reads.
  * Errors: AQ_ERR_INVALID_ARG for bad experts, sizes, T outside
  * 1..AQ_MOE_MAX_TOKENS, top_k outside 1..AQ_MOE_MAX_TOP, NULL pointers or a

@@ -24,14 +24,17 @@
 //     staged, or packed, in that order.
 //   * A code masked in place in an fp16 with zero exponent is the exact
 //     subnormal q * 2^(p - 24), p its bit position; the activation paired with
-//     it carries 2^-p.  Activations are fp16 with one power of two per token
-//     that puts the row's largest magnitude into [2^14, 2^15): bf16 and fp16
-//     values above 2^-28 of it keep all their bits, smaller ones are off by
-//     2^-39 of it at most; h (fp32) is rounded to fp16's 11 bits, 2^-11 of a
-//     value at most, an eighth of what rounding it to bf16 would cost.
-//     Sums of codes, group sums and everything after them are fp32.
+//     it carries 2^-p (p is 8 at most at 2 bits, 6 at 3, 5 at 5, 4 at 4, 0 at 6
+//     and 8; with groups of 32 also 6 at 2).  Activations are fp16 with one power
+//     of two per token that puts the row's largest magnitude into [2^14, 2^15):
+//     bf16 and fp16 values above 2^(p - 28) of it keep all their bits, smaller
+//     ones are off by 2^(p - 39) of it at most (which shows only where the
+//     weights of all large values are near zero); h (fp32) is rounded to fp16's
+//     11 bits, 2^-11 of a value at most, an eighth of what rounding it to bf16
+//     would cost.  Sums of codes, group sums and everything after them are fp32.
 //   * The biases enter as products of their own, 8 groups a step, with the
-//     columns' group sums, which are kept as two fp16 parts (22 bits).
+//     columns' group sums, which are kept as two fp16 parts: 22 bits, down to
+//     2^-31 of the row's largest magnitude.
 //   * Tokens of an expert are MMA columns, 8, 16 or 32 at a time; blocks of 8
 //     that are empty are skipped.  An expert with more takes its weights again,
 //     from L2.
@@ -552,19 +555,21 @@ __device__ __forceinline__ void stage_columns(const MoeParams &p, int ncols, Sha
             if (k == 0) sh.undo[c] = __int_as_float((127 - up) << 23);
             float s = 0.f, s2 = 0.f;
 #pragma unroll
-            for (int m = 0; m < 16; ++m) {
-                v[m] *= f;
-                const float h = __half2float(__float2half_rn(v[m]));
-                if (G32 && m >= 8)
-                    s2 += h;
-                else
-                    s += h;
-            }
+            for (int m = 0; m < 16; ++m) v[m] *= f;
+            // (the sums are of the values as the codes' products see them, so that
+            // what rounds off of a value is multiplied by its weight, not by its
+            // code's part of it)
             uint32_t o[8];
 #pragma unroll
             for (int m = 0; m < 8; ++m) {
-                const float down = 1.f / (float)(1 << Ord::pre(m));
+                const float back = (float)(1 << Ord::pre(m)), down = 1.f / back;
                 o[m] = pack_half2(v[Ord::lo(m)] * down, v[Ord::hi(m)] * down);
+                const __half2 h = *reinterpret_cast<const __half2 *>(&o[m]);
+                const float both = (__low2float(h) + __high2float(h)) * back;
+                if (G32 && m >= 4)
+                    s2 += both;
+                else
+                    s += both;
             }
             dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
             dst[4] = make_uint4(o[4], o[5], o[6], o[7]);

@@ -6,7 +6,8 @@ A row of activations enters the MMAs as fp16, times 2^up, which puts its largest
 magnitude into [2^14, 2^15), or 2^126 where that is more; up to 2^-pre of that
 where a code lies pre bits up in its fp16.  So a value is off by 2^-11 of itself
 (not at all where it came from 16 bits) or by half of fp16's smallest step:
-    spread = 2^(pre - 25 - up) <= max(2^(pre - 39) * largest, 2^(pre - 151)).
+    spread = 2^(pre - 25 - up) <= max(2^(pre - 39) * largest, 2^(pre - 151)),
+in its code's product and in its group's sum alike, so times its weight.
 A group's sum enters times 2^-8 in two such parts: off by 2^-22 of itself, which
 is in the sums' own bound, or by
     floor = 2^(8 - 25 - up) <= max(2^-31 * largest, 2^-143)."""
@@ -34,7 +35,7 @@ def _off(x, part, bits, group, own):
     peak = x.abs().amax(1, keepdim=True)
     spread = torch.clamp(2.0 ** (pre(bits, group) - 39) * peak, min=2.0 ** (pre(bits, group) - 151))
     floor = torch.clamp(2.0 ** -31 * peak, min=2.0 ** -143)
-    off = _moe.steps(x.shape[1]) * (x.abs() @ mag.T) + spread * mag.sum(1) + floor * biases
+    off = _moe.steps(x.shape[1]) * (x.abs() @ mag.T) + spread * v.abs().sum(1) + floor * biases
     return off + own * (x.abs() @ v.abs().T) + 2.0 ** -149
 
 
