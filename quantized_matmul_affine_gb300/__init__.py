@@ -16,7 +16,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
-from typing import List, Optional
+from typing import List, Optional, Union
 
 import torch
 
@@ -849,7 +849,7 @@ def aq_moe_workspace_bytes(experts: AqExperts, T: int, top_k: int) -> int:
 
 
 def aq_moe_route(x, router: AqRouter, out=None,
-                 stream: Optional[torch.cuda.Stream] = None) -> tuple:
+                 stream: Union[torch.cuda.Stream, int, None] = None) -> tuple:
     """The experts of each token of x [T, K]: (experts int32 [T, top_k], each
     row ascending, weights float32 [T, top_k])."""
     T = _moe_tokens(x, router._shape[1], router._index, router._dtype)
@@ -861,7 +861,7 @@ def aq_moe_route(x, router: AqRouter, out=None,
 
 
 def aq_moe_experts(x, experts: AqExperts, ids, weights, out=None, workspace=None,
-                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+                   stream: Union[torch.cuda.Stream, int, None] = None) -> torch.Tensor:
     """y[t] = sum_j weights[t, j] * expert ids[t, j] of x[t]; ids int32
     [T, top_k] (outside 0..E-1: none), weights float32 [T, top_k]."""
     index = experts._index
@@ -880,7 +880,7 @@ def aq_moe_experts(x, experts: AqExperts, ids, weights, out=None, workspace=None
 
 
 def aq_moe(x, router: AqRouter, experts: AqExperts, out=None, routed=None, workspace=None,
-           stream: Optional[torch.cuda.Stream] = None) -> tuple:
+           stream: Union[torch.cuda.Stream, int, None] = None) -> tuple:
     """The whole layer: routes x [T, K] and runs the chosen experts.  Returns
     (y [T, K], experts int32 [T, top_k], weights float32 [T, top_k]); routed:
     tensors for the last two."""
@@ -899,7 +899,7 @@ def aq_moe(x, router: AqRouter, experts: AqExperts, out=None, routed=None, works
 
 
 def aq_embed(ids, Wq, scales, biases, bits: int, group_size: int, dtype, scale: float = 1.0,
-             out=None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+             out=None, stream: Union[torch.cuda.Stream, int, None] = None) -> torch.Tensor:
     """Rows of a quantised table by token: scale * row ids[...] as dtype (fp16
     or bf16) [..., K]; ids int32 or int64, outside 0..N-1 a row of zeros.  Wq
     [N, K*bits/32], scales and biases fp16 [N, K/group_size]."""
