@@ -707,10 +707,31 @@ class _ExpertsStruct(ctypes.Structure):
 _SCORES = {"softmax": AQ_SCORE_SOFTMAX, "sigmoid": AQ_SCORE_SIGMOID}
 
 
-class AqRouter:
+class _Fixed:
+    """An object whose attributes are those its struct was made of: the library
+    reads the struct, the binding's checks the attributes."""
+
+    __slots__ = ()
+
+    def _fix(self, **kw):
+        for name, value in kw.items():
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{name} is fixed: make another {type(self).__name__}")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{name} is fixed: make another {type(self).__name__}")
+
+    def __copy__(self):
+        return self
+
+
+class AqRouter(_Fixed):
     """A router (struct aq_router): weight [E, K] fp16 or bf16, bias float32
     [E] or None (sigmoid scores only), score "softmax" or "sigmoid".  The
-    tensors stay the caller's; this object holds them and is kept for a layer."""
+    tensors stay the caller's; this object holds them and is kept for a layer.
+    Its attributes do not change."""
 
     __slots__ = ("weight", "bias", "top_k", "_struct", "_ref", "_index", "_dtype", "_shape")
 
@@ -725,20 +746,19 @@ class AqRouter:
             raise ValueError(f"bias must be float32 [{E}]")
         if bias is not None and bias.device != weight.device:
             raise ValueError("bias must be on weight's device")
-        self.weight, self.bias, self.top_k = weight, bias, top_k
-        self._index, self._dtype, self._shape = weight.get_device(), weight.dtype, (E, K)
-        self._struct = _RouterStruct(_dev(weight, "weight"),
-                                     None if bias is None else _dev(bias, "bias"), E, K,
-                                     AQ_BF16 if weight.dtype == torch.bfloat16 else AQ_F16, top_k,
-                                     _SCORES[score], int(normalize), scale)
-        self._ref = ctypes.addressof(self._struct)
+        struct = _RouterStruct(_dev(weight, "weight"), None if bias is None else _dev(bias, "bias"), E, K,
+                               AQ_BF16 if weight.dtype == torch.bfloat16 else AQ_F16, top_k,
+                               _SCORES[score], int(normalize), scale)
+        self._fix(weight=weight, bias=bias, top_k=top_k, _index=weight.get_device(), _dtype=weight.dtype,
+                  _shape=(E, K), _struct=struct, _ref=ctypes.addressof(struct))
 
 
-class AqExperts:
+class AqExperts(_Fixed):
     """The experts of a layer (struct aq_experts): gate and up are (words
     [E, I, K*bits/32] int32, scales [E, I, K/group] fp16, biases), down the
     same with [E, K, I]; bits 2/3/4/5/6/8, groups of 32/64/128.  The tensors
-    stay the caller's; this object holds them and is kept for a layer."""
+    stay the caller's; this object holds them and is kept for a layer.  Its
+    attributes do not change."""
 
     __slots__ = ("gate", "up", "down", "bits", "group_size", "count", "hidden", "inner", "_struct",
                  "_ref", "_workspaces", "_index")
@@ -767,13 +787,10 @@ class AqExperts:
                 if t.device != gate[0].device:
                     raise ValueError("gate, up and down must be on one device")
                 parts.append((t, f"{name} {part}"))
-        self.gate, self.up, self.down = tuple(gate), tuple(up), tuple(down)
-        self.bits, self.group_size = bits, group_size
-        self.count, self.hidden, self.inner = E, hidden, inner
-        self._index = gate[0].get_device()
-        self._struct = _ExpertsStruct(*(_dev(t, name) for t, name in parts), E, hidden, inner, bits, group_size)
-        self._ref = ctypes.addressof(self._struct)
-        self._workspaces = {}
+        struct = _ExpertsStruct(*(_dev(t, name) for t, name in parts), E, hidden, inner, bits, group_size)
+        self._fix(gate=tuple(gate), up=tuple(up), down=tuple(down), bits=bits, group_size=group_size, count=E,
+                  hidden=hidden, inner=inner, _index=gate[0].get_device(), _struct=struct,
+                  _ref=ctypes.addressof(struct), _workspaces={})
 
 
 def _moe_tokens(x, K: int, index: int, dtype=None) -> int:
