@@ -120,18 +120,24 @@ __device__ __noinline__ double precise_logit(const uint16_t *x, const uint16_t *
     return fabs(d) < INFINITY ? d : wide_logit<BF16>(x, w, K);
 }
 
-// Whether a row has neither infinities nor NaN, in every lane.
+// What a row of x holds, in every lane.
+enum Row { ROW_ZEROS, ROW_FINITE, ROW_OTHER };  // zeros alone; finite numbers; infinities or NaN too
 template <bool BF16>
-__device__ bool finite_row(const uint16_t *x, int K) {
+__device__ Row row_holds(const uint16_t *x, int K) {
     constexpr uint32_t kExp = BF16 ? 0x7F80u : 0x7C00u;
-    bool ok = true;
+    bool finite = true;
+    uint32_t any = 0u;
     for (int k = (threadIdx.x & 31) * 8; k < K; k += 256) {
         const uint4 a = *reinterpret_cast<const uint4 *>(x + k);
         const uint32_t v[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ok = ok && (v[i] & kExp) != kExp && (v[i] >> 16 & kExp) != kExp;
+        for (int i = 0; i < 4; ++i) {
+            finite = finite && (v[i] & kExp) != kExp && (v[i] >> 16 & kExp) != kExp;
+            any |= v[i] & 0x7FFF7FFFu;
+        }
     }
-    return __all_sync(0xFFFFFFFFu, ok);
+    if (!__all_sync(0xFFFFFFFFu, finite)) return ROW_OTHER;
+    return __any_sync(0xFFFFFFFFu, any != 0u) ? ROW_FINITE : ROW_ZEROS;
 }
 
 // Floats in the order of unsigned integers; NaN below everything.
@@ -217,21 +223,41 @@ __device__ void choose(const RouteParams &p, int t, const float *sums, double *k
     }
     const int n_sure = __reduce_add_sync(0xFFFFFFFFu, __popc(sure));
     const int n_doubt = __reduce_add_sync(0xFFFFFFFFu, __popc(doubt));
-    // (The fp32 choice stands where the border is a bias that is not finite, and
-    // for a token that is not.)
-    if (lost ? finite_row<BF16>(p.x + (size_t)t * p.K, p.K)
-             : n_sure + n_doubt > p.top && fabsf(border) < INFINITY) {
+    const uint16_t *x = p.x + (size_t)t * p.K;
+    // (the fp32 choice stands where the border is a bias that is not finite)
+    bool again = lost || (n_sure + n_doubt > p.top && fabsf(border) < INFINITY);
+    bool zeros = false;
+    if (again) {
+        // An empty slot of a padded batch, zeros or whatever was there, is not worth
+        // E sums: the fp32 choice stands for a token that is not finite, and for
+        // zeros, whose logits are exact, as far as there are no biases to add.
+        bool some = false;
 #pragma unroll
-        for (int j = 0; j < LANES; ++j)
+        for (int j = 0; j < LANES; ++j) some = some || ((open >> j & 1u) && sums[p.E + j * 32 + lane] != 0.f);
+        if (lost || !__any_sync(0xFFFFFFFFu, some)) {
+            const Row row = row_holds<BF16>(x, p.K);
+            zeros = row == ROW_ZEROS && !lost;  // (infinite weights times zero are NaN)
+            again = row != ROW_OTHER && !(zeros && !p.bias);
+        }
+    }
+    if (again) {
+#pragma unroll
+        for (int j = 0; j < LANES; ++j) {
+            if (zeros) {
+                const int e = j * 32 + lane;
+                if (doubt >> j & 1u) keep[e] = 0.5 + (double)p.bias[e];
+                continue;
+            }
             for (uint32_t m = __ballot_sync(0xFFFFFFFFu, doubt >> j & 1u); m; m &= m - 1u) {
                 const int e = j * 32 + __ffs(m) - 1;
-                double d = precise_logit<BF16>(p.x + (size_t)t * p.K, p.w + (size_t)e * p.K, p.K);
+                const double d = precise_logit<BF16>(x, p.w + (size_t)e * p.K, p.K);
                 if (lane == (e & 31)) {
                     const double v = p.bias ? 1.0 / (1.0 + exp(-d)) + (double)p.bias[e] : d;
                     keep[e] = v == v ? v : -INFINITY;  // (the lanes below agree on an order without NaN)
                     if (lost) logit[j] = (float)d;
                 }
             }
+        }
         __syncwarp();
         taken = sure;
         for (int n = n_sure; n < p.top; ++n) {
