@@ -13,7 +13,7 @@
 //     logits are summed again with the rounding errors carried along (products
 //     of two 16-bit floats are exact in fp32, two-sums keep what each addition
 //     rounds off), which is good to about 2^-46 of the sum of |x w|, or in 64
-//     bits where a product or a sum passes fp32's range.
+//     bits where a product or a sum passes fp32's range at either end.
 //   * weights come from the fp32 logits.
 // One launch, bound by latency (loads, two cluster barriers, the choice): one
 // token and 128 experts of 2048 6 us, 256 tokens and 256 experts of 5120 32 us
@@ -96,9 +96,11 @@ __device__ __noinline__ double wide_logit(const uint16_t *x, const uint16_t *w, 
 }
 
 // One logit to about 2^-46 of its sum of magnitudes, in every lane.  Four sums
-// a lane, so that the additions of one do not wait for another's.
+// a lane, so that the additions of one do not wait for another's.  tiny: that
+// sum is so small that what products below 2^-126 lose counts.
 template <bool BF16>
-__device__ __noinline__ double precise_logit(const uint16_t *x, const uint16_t *w, int K) {
+__device__ __noinline__ double precise_logit(const uint16_t *x, const uint16_t *w, int K, bool tiny) {
+    if (tiny) return wide_logit<BF16>(x, w, K);
     const int lane = threadIdx.x & 31;
     float s[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
@@ -161,8 +163,10 @@ __device__ void choose(const RouteParams &p, int t, const float *sums, double *k
     // what the sums leave out: a product of 16 may truncate each of its 16 terms
     // at 2^-24 of the largest, 4 * 2^-22 of the magnitudes at most; the last
     // rounding is 2^-24 of the logit, what the errors' own sums and those of the
-    // magnitudes round is smaller by 2^-20
+    // magnitudes round is smaller by 2^-20.  Products and sums below 2^-126 may
+    // count as zeros.
     constexpr float kUlps = 4.5f * 2.384185791015625e-07f;
+    const float least = (float)p.K * 1.175494350822287508e-38f;
 #pragma unroll
     for (int j = 0; j < LANES; ++j) {
         logit[j] = val[j] = -INFINITY;
@@ -170,7 +174,7 @@ __device__ void choose(const RouteParams &p, int t, const float *sums, double *k
         if (j < per && e < p.E) {
             const float s = sums[e];
             logit[j] = s;
-            float bound = kUlps * sums[p.E + e];
+            float bound = fmaf(kUlps, sums[p.E + e], least);
             lost = lost || !(bound < INFINITY);
             float v = s;
             if (p.bias) {
@@ -250,7 +254,8 @@ __device__ void choose(const RouteParams &p, int t, const float *sums, double *k
             }
             for (uint32_t m = __ballot_sync(0xFFFFFFFFu, doubt >> j & 1u); m; m &= m - 1u) {
                 const int e = j * 32 + __ffs(m) - 1;
-                const double d = precise_logit<BF16>(x, p.w + (size_t)e * p.K, p.K);
+                const bool tiny = !(sums[p.E + e] > 67108864.f * least);  // 2^-46 of more is above what is lost
+                const double d = precise_logit<BF16>(x, p.w + (size_t)e * p.K, p.K, tiny);
                 if (lane == (e & 31)) {
                     const double v = p.bias ? 1.0 / (1.0 + exp(-d)) + (double)p.bias[e] : d;
                     keep[e] = v == v ? v : -INFINITY;  // (the lanes below agree on an order without NaN)
