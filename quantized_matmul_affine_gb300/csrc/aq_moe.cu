@@ -161,7 +161,8 @@ __device__ void choose(const RouteParams &p, int t, const float *sums, double *k
     bool lost = false;      // an expert's sums pass fp32's range: they tell nothing
     uint32_t open = 0u;     // experts not yet taken, by position
     // what the sums leave out: a product of 16 may truncate each of its 16 terms
-    // at 2^-24 of the largest, 4 * 2^-22 of the magnitudes at most; the last
+    // at 2^-24 of the largest, 4 * 2^-22 of the magnitudes at most (the most seen,
+    // with one term 2^23 to 2^27 times the others, is 1.5 * 2^-22); the last
     // rounding is 2^-24 of the logit, what the errors' own sums and those of the
     // magnitudes round is smaller by 2^-20.  Products and sums below 2^-126 may
     // count as zeros.
