@@ -744,7 +744,10 @@ __device__ __forceinline__ void run_tiles(const MoeParams &p, int e, int from, i
         b = b * 16777216.f * f;
         float *o = p.dst + (size_t)sh.list[c] * p.R + tile * S::ROWS + g;
         if constexpr (PAIRS) {
-            *o = a / (1.f + expf(-a)) * b;
+            // (exp(-a) passes the largest float at -88.7, where a exp(a) is still a
+            // normal one; exp(a) alone is not, so b takes half of it)
+            const float half = expf(0.5f * a);
+            *o = a < -80.f ? a * half * (b * half) : a / (1.f + expf(-a)) * b;
         } else {
             o[0] = a;
             o[8] = b;
