@@ -552,10 +552,11 @@ typedef struct aq_router {
 } aq_router;
 
 /*
- * The experts' weights: three stacks of E matrices, gate and up [E][I][K],
- * down [E][K][I], each as words uint32 [E][rows][cols*bits/32] and fp16 scales
- * and biases [E][rows][cols/group_size], device.  Words 16-byte aligned.
- *   K, I        hidden and inner size, multiples of 64 and of group_size, up to
+ * The experts' weights: three stacks of E matrices, gate and up
+ * [E][inner][K], down [E][K][inner], each as words uint32
+ * [E][rows][cols*bits/32] and fp16 scales and biases
+ * [E][rows][cols/group_size], device.  Words 16-byte aligned.
+ *   K, inner    hidden and inner size, multiples of 64 and of group_size, up to
  *               2^20.
  *   bits        2, 3, 4, 5, 6 or 8.   group_size  32, 64 or 128.
  */
@@ -566,7 +567,7 @@ typedef struct aq_experts {
     const void *up_scales_dev, *up_biases_dev;
     const uint32_t *down_words_dev;
     const void *down_scales_dev, *down_biases_dev;
-    int64_t E, K, I;
+    int64_t E, K, inner;  /* (I is a macro of complex.h) */
     int bits, group_size;
 } aq_experts;
 

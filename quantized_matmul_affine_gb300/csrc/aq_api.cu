@@ -638,10 +638,10 @@ static aq_status check_routed(const void *x_dev, int64_t T, const int32_t *exper
 
 static bool valid_experts_sizes(const aq_experts *x) {
     return x && x->E >= 1 && x->E <= AQ_MOE_MAX_EXPERTS && x->K >= 64 && x->K <= 1 << 20 &&
-           x->I >= 64 && x->I <= 1 << 20 && valid_width(x->bits) &&
+           x->inner >= 64 && x->inner <= 1 << 20 && valid_width(x->bits) &&
            (x->group_size == 32 || x->group_size == 64 || x->group_size == 128) &&
-           x->K % 64 == 0 && x->I % 64 == 0 && x->K % x->group_size == 0 &&
-           x->I % x->group_size == 0;
+           x->K % 64 == 0 && x->inner % 64 == 0 && x->K % x->group_size == 0 &&
+           x->inner % x->group_size == 0;
 }
 
 static aq_status check_experts(const aq_experts *x, int64_t T, int top_k, const void *out_dev,

@@ -562,7 +562,7 @@ static int moe_variant(const aq_experts *x, int64_t T, int top, int64_t K) {
     return T <= 16 || tokens <= 10.0 ? MOE_16 : MOE_32;
 }
 static int up_variant(const aq_experts *x, int64_t T, int top) { return moe_variant(x, T, top, x->K); }
-static int down_variant(const aq_experts *x, int64_t T, int top) { return moe_variant(x, T, top, x->I); }
+static int down_variant(const aq_experts *x, int64_t T, int top) { return moe_variant(x, T, top, x->inner); }
 
 namespace {
 struct Workspace {
@@ -571,10 +571,10 @@ struct Workspace {
 Workspace workspace(const aq_experts *x, int64_t T, int top) {
     Workspace w;
     w.h = 0;
-    w.parts = round256((size_t)T * top * x->I * 4);
+    w.parts = round256((size_t)T * top * x->inner * 4);
     w.x = w.parts + round256((size_t)T * top * x->K * 4);
     w.hp = w.x + (moe_packed(up_variant(x, T, top)) ? (size_t)moe_pack(T, x->K, x->group_size).bytes : 0);
-    w.bytes = w.hp + (moe_packed(down_variant(x, T, top)) ? (size_t)moe_pack(T * top, x->I, x->group_size).bytes : 0);
+    w.bytes = w.hp + (moe_packed(down_variant(x, T, top)) ? (size_t)moe_pack(T * top, x->inner, x->group_size).bytes : 0);
     return w;
 }
 }  // namespace
@@ -598,7 +598,7 @@ cudaError_t moe_experts_launch(const ExpertsArgs &a) {
                                                   moe_pack_b5, moe_pack_b6, moe_pack_b8}.begin()[at];
     MoeParams p = {x.gate_words_dev, x.up_words_dev, x.gate_scales_dev, x.up_scales_dev,
                    x.gate_biases_dev, x.up_biases_dev, a.ids, a.x, h, (int)a.T, a.top_k, (int)x.E,
-                   (int)x.I, (int)x.K, x.group_size, a.dtype, nullptr};
+                   (int)x.inner, (int)x.K, x.group_size, a.dtype, nullptr};
     cudaError_t e;
     int variant = up_variant(&x, a.T, a.top_k);
     if (moe_packed(variant)) {
@@ -614,7 +614,7 @@ cudaError_t moe_experts_launch(const ExpertsArgs &a) {
     p.src = h;
     p.dst = parts;
     p.R = (int)x.K;
-    p.K = (int)x.I;
+    p.K = (int)x.inner;
     p.packed = nullptr;
     variant = down_variant(&x, a.T, a.top_k);
     if (moe_packed(variant)) {
