@@ -548,11 +548,18 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Which kernel runs a product over K, by the tokens a busy expert has on
 // average, were all experts picked alike: 8, 16 or 32 columns at a time.
-// Measured (us a layer with 8 / 16 / 32 columns): 33 tokens of 64 experts, 3.1
-// each, 219 / 228 / 223; 256 of 128, 16 each, 495 / 367 / 316.  Whether the rows
-// are packed first by a launch of their own, about 3 us, or by each CTA for
-// itself, by the values a busy expert's tokens have (packed / not): 8 tokens of
-// 8 experts of 4096, 9000 values, 205 / 228; 48 tokens of 64 experts of 2048,
+// Measured, us a layer's experts with 8 / 16 / 32 columns, packed, at 4 bits:
+//   33 tokens, 6 of 64 experts of 5120 x 1536,   3.2 each  243 / 254 / 270
+//   64 tokens, 6 of 64 experts of 2048 x 1024,   6.0 each  103 /  95 / 101
+//   96 tokens, 6 of 64 experts of 5120 x 1536,   9.0 each  403 / 322 / 340
+//   256 tokens, 8 of 128 experts of 2048 x 768,   16 each  496 / 367 / 316 (6 bits)
+// and with at most 16 tokens, where an expert never has more than two blocks,
+// 12 tokens on all of 4 experts of 4096 x 1536            61 /  44 /  46.
+// The other widths choose alike (100 tokens, 6.3 each: 6 bits 231 / 189 / 204, 8
+// bits 182 / 154 / 161; 64 tokens at 3 bits, 4.3 each: 124 / 113 / 127).  Whether
+// the rows are packed first by a launch of their own, about 3 us, or by each CTA
+// for itself, by the values a busy expert's tokens have (packed / not): 8 tokens
+// of 8 experts of 4096, 9000 values, 205 / 228; 48 tokens of 64 experts of 2048,
 // 6300, 82 / 83; one token of 2048, 32 / 28.
 static int moe_variant(const aq_experts *x, int64_t T, int top, int64_t K) {
     const double E = (double)x->E;
