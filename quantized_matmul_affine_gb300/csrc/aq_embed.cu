@@ -6,8 +6,9 @@
 // values: B bytes of codes, which lie in two words at most, one 16-byte store.
 // s q + b is one fp32 fma, the product with the scale one more rounding, the
 // output type the last.  Four tokens' pieces are in flight a thread: 16,384
-// rows of 4096 at 4 bits take 42 us (55 with one), 172 MB at 4.1 TB/s; a single
-// token is a launch, 2 us.
+// rows of 4096 at 4 bits take 42 us (55 with one), 172 MB at 4.1 TB/s, three
+// narrow loads behind the id's for each 16-byte store; a single token is a
+// launch, 2 us.
 #include "aq_moe.h"
 
 #include <cuda_bf16.h>

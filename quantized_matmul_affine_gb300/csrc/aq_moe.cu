@@ -16,10 +16,12 @@
 //     bits where a product or a sum passes fp32's range at either end.
 //   * weights come from the fp32 logits.
 // One launch, bound by latency (loads, two cluster barriers, the choice): one
-// token and 128 experts of 2048 6 us, 256 tokens and 256 experts of 5120 32 us
-// (the weights, read by 16 clusters from L2, are 42 MB of that).  The bound that
-// the sums' rounding errors allow leaves about one of 500 tokens to be summed
-// again; without them it was one of 25, and each costs the call 4 us and more.
+// token and 128 experts of 2048 6 us; 256 experts of 5120 11 us for one token, 21
+// for 65 to 128, 31 for 256 (eight warps an SM, which wait for loads 43 % of the
+// time; L2 is 4 % busy).  The bound that the sums' rounding errors allow leaves
+// about one of 300 tokens of the last case to be summed again; without them it
+// was one of 25.  A call with one such token takes 36 us instead of 31, with
+// three 40, since one warp sums for its token.
 // A cluster of 8 or 16 CTAs takes 8 or 16 tokens: its CTAs slice K, their warps deal
 // the experts (16 an MMA tile) and, where there are fewer tiles than warps,
 // slice K further; the parts are sent to the CTA that chooses for the token,

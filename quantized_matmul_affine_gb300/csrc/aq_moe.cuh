@@ -39,13 +39,14 @@
 //     that are empty are skipped.  An expert with more takes its weights again,
 //     from L2.
 //
-// Bound by HBM where the experts are large: 8 experts of 4096 x 13824 at 4 bits
-// (688 MB) take 205 us for both products, 3.4 TB/s; with the arithmetic left out
-// 190 us, with the codes left out 68 us, and with the loop left out 44 us (five
-// dependent launches, plans, staged columns).  So the codes alone stream at 5.1
-// TB/s, the arithmetic is hidden, and what remains is latency at a kernel's
-// start, which is all there is for one token (128 experts of 2048 x 768: 28 us
-// for 22 MB).  24 warps of 80 registers an SM: 16 warps of 128 with two tiles a
+// Where the experts are large, bound by the copies into shared memory: 8
+// experts of 4096 x 13824 at 4 bits (688 MB) take 205 us a layer; gate and up 114
+// of them and down 74, 4.0 and 3.1 TB/s; with the arithmetic left out 190 us, so
+// it is nearly hidden; with the codes left out 68 us, and with the loop left out
+// 44 us (six dependent launches, plans, staged columns).  What limits the codes is
+// how they are copied, 16 bytes a lane with an address and a predicate each.  For
+// one token the kernels' starts are all there is (128 experts of 2048 x 768: 28
+// us for 22 MB).  24 warps of up to 80 registers an SM: 16 warps of 128 with two tiles a
 // step were as fast on large runs and slower on short ones.
 #pragma once
 
