@@ -709,19 +709,27 @@ _SCORES = {"softmax": AQ_SCORE_SOFTMAX, "sigmoid": AQ_SCORE_SIGMOID}
 
 class _Fixed:
     """An object whose attributes are those its struct was made of: the library
-    reads the struct, the binding's checks the attributes."""
+    reads the struct, the binding's checks the attributes.  (What a subclass adds
+    is its own.)"""
 
     __slots__ = ()
+    _names = frozenset()
 
     def _fix(self, **kw):
         for name, value in kw.items():
             object.__setattr__(self, name, value)
 
+    def _check_name(self, name):
+        if name in self._names:
+            raise AttributeError(f"{name} is fixed: make another {type(self).__name__}")
+
     def __setattr__(self, name, value):
-        raise AttributeError(f"{name} is fixed: make another {type(self).__name__}")
+        self._check_name(name)
+        object.__setattr__(self, name, value)
 
     def __delattr__(self, name):
-        raise AttributeError(f"{name} is fixed: make another {type(self).__name__}")
+        self._check_name(name)
+        object.__delattr__(self, name)
 
     def __copy__(self):
         return self
@@ -734,6 +742,7 @@ class AqRouter(_Fixed):
     Its attributes do not change."""
 
     __slots__ = ("weight", "bias", "top_k", "_struct", "_ref", "_index", "_dtype", "_shape")
+    _names = frozenset(__slots__)
 
     def __init__(self, weight, top_k: int, bias=None, score: str = "softmax",
                  normalize: bool = True, scale: float = 1.0):
@@ -762,6 +771,7 @@ class AqExperts(_Fixed):
 
     __slots__ = ("gate", "up", "down", "bits", "group_size", "count", "hidden", "inner", "_struct",
                  "_ref", "_workspaces", "_index")
+    _names = frozenset(__slots__)
 
     def __init__(self, gate, up, down, bits: int, group_size: int):
         if bits not in (2, 3, 4, 5, 6, 8) or group_size not in (32, 64, 128):

@@ -51,3 +51,17 @@ def test_structs_say_the_same():
     assert (s.E, s.K, s.I, s.bits, s.group_size) == (x.count, x.hidden, x.inner, x.bits, x.group_size)
     assert [s.gate_words_dev, s.up_scales_dev, s.down_biases_dev] == \
         [t.data_ptr() for t in (x.gate[0], x.up[1], x.down[2])]
+
+
+def test_subclasses_add_their_own():
+    class Named(aq.AqRouter):
+        def __init__(self, name, *args, **kw):
+            super().__init__(*args, **kw)
+            self.name = name
+
+    r = Named("first", _t(4, 128, **HALF), 2)
+    r.name = "second"
+    assert r.name == "second" and r.top_k == 2
+    del r.name
+    with pytest.raises(AttributeError, match="fixed"):
+        r.top_k = 3
